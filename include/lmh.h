@@ -17,6 +17,10 @@
  * lmh_project_partials and lmh_merge_records split step 2 over GPUs that each
  * hold a share of the vocabulary (a vocabulary-parallel head).
  *
+ * For a decode step around a model body with a 4-bit head: lmh_lookup_q4 (the
+ * input rows of token ids), lmh_project_q4 (the logits of the body's rows) and
+ * lmh_sample_from_logits (the next ids, with temperature, top-k, top-p, min-p).
+ *
  * The O(k+1) result of a row is: lse (fp32 log-sum-exp over the vocabulary),
  * the selected token's logprob, and the exact top-k (ids and logprobs),
  * sorted by logit descending with exact ties ordered by ascending token id.
@@ -443,6 +447,148 @@ lmh_status lmh_merge_records(const void* records, int32_t num_parts, int32_t row
                              float* sel_logprob, int32_t* topk_ids, float* topk_logprobs, void* workspace,
                              size_t workspace_bytes, uint32_t* dev_status, cudaStream_t stream);
 
+/*
+ * lmh_sample_from_logits -- one token per row from given logits, with
+ * temperature, top-k, top-p and min-p, and one given random number per row.
+ *
+ * The filters a serving request asks for, applied to logits in device memory
+ * (the full logits of lmh_project_logprobs, the output of lmh_project_q4, or a
+ * model's own).  The pages name the selected token as an input and have no
+ * counterpart for the filters; the definition is this one.  For row i:
+ *   z_v      = the logit widened to fp32; -inf for a token that allowed_mask
+ *              forbids (whatever value stands there) and for NaN.  zm = max z.
+ *              Rows whose zm is +inf draw among their +inf tokens alone (these
+ *              count as 0, every other token as -inf).
+ *   T        = temperature[i] (1 when NULL).  T <= 0 or NaN is greedy: the
+ *              token with the largest z, ties to the smallest id, logprob 0;
+ *              the filters do not matter.
+ *   c        = log2(e) * (1 / T) in fp32, two roundings, held in [2^-126, FLT_MAX].
+ *   t_v      = fp32(fp32(z_v - zm) * c);  w_v = rint(2^32 * exp2f(t_v)), a whole
+ *              number (exp2f is CUDA's).
+ *   order    = z descending, exact ties by ascending id.
+ *   top-k    keeps the first k tokens of the order (k <= 0 or k >= V: all); M is
+ *            the sum of their w.
+ *   top-p    keeps the shortest prefix of the order whose sum of w is at least
+ *            max(1, ceil(p * M)), the product in fp64 (p >= 1 or NaN: all).
+ *   min-p    keeps the tokens with t_v >= min(log2f(m), 0), that is of at least m
+ *            times the best token's probability (m <= 0 or NaN: all).
+ *   A token is kept when every filter keeps it; the best token always is.
+ *   sampled_ids[i] = the smallest id whose sum of kept w over the ids up to and
+ *            including it exceeds r = min(floor(u * K), K - 1): K the sum of all
+ *            kept w, u = uniforms[i] held in [0, 1 - 2^-24] (NaN: 0), the product
+ *            in fp64.
+ *   sampled_logprob[i] = t * ln 2 - ln(K / 2^32): the token's log-probability in
+ *            the distribution that it was drawn from.  (Its log-probability in
+ *            the model's own distribution: lmh_logprobs_from_logits with sel_ids.)
+ *   A row with no token above -inf gives id -1, a NaN logprob and
+ *   LMH_DS_NO_ALLOWED_TOKEN.
+ * The sums are of whole numbers, so a draw depends neither on the GPU's split of
+ * a row nor on the batch that the row is in.
+ *
+ *   logits            device [rows x V] of dtype, row stride row_stride (>= V),
+ *                     aligned to sizeof(dtype); V <= LMH_SAMPLE_V_MAX.
+ *   filters           NULL: none, temperature 1.  Its pointers are device memory.
+ *   uniforms          device fp32 [rows].
+ *   sampled_ids       device int32 [rows], out.
+ *   sampled_logprob   device fp32 [rows], out, or NULL.
+ * No workspace is needed.  Errors: LMH_ERR_INVALID_ARG (null pointers, bad sizes,
+ * mask_words < ceil(V / 32) with a mask), LMH_ERR_UNSUPPORTED (misaligned logits,
+ * V > LMH_SAMPLE_V_MAX), LMH_ERR_CUDA.  Device: LMH_DS_NO_ALLOWED_TOKEN.
+ */
+#define LMH_SAMPLE_V_MAX 393216
+
+typedef struct lmh_filters {
+  const float* temperature;     /* device fp32 [rows] or NULL (1) */
+  const int32_t* top_k;         /* device int32 [rows] or NULL (off) */
+  const float* top_p;           /* device fp32 [rows] or NULL (off) */
+  const float* min_p;           /* device fp32 [rows] or NULL (off) */
+  const uint32_t* allowed_mask; /* device u32 [rows x mask_words] or NULL, as in lmh_sampling */
+  int32_t mask_words;           /* >= ceil(V / 32) when allowed_mask is given */
+} lmh_filters;
+
+lmh_status lmh_sample_from_logits(const void* logits, lmh_dtype dtype, int32_t rows, int32_t V, int64_t row_stride,
+                                  const lmh_filters* filters, const float* uniforms, int32_t* sampled_ids,
+                                  float* sampled_logprob, uint32_t* dev_status, cudaStream_t stream);
+
+/*
+ * A [V x H] table (an LM head, or the embedding that is tied to it) held in 4
+ * bits with one scale per group of `group` consecutive entries of a row:
+ *   value[v][h] = scale[v][h / group] * (q[v][h] - zero[v][h / group])
+ * with q in 0..15 and zero = 8 when `zeros` is NULL.  The pages leave quantised
+ * heads to the model's own framework; this is the plain layout such checkpoints
+ * are brought to: two entries a byte, the even h in the low half.
+ */
+typedef struct lmh_q4_table {
+  const void* packed;       /* device u8 [V x H/2], 16-byte aligned */
+  int64_t packed_row_bytes; /* >= H/2, a multiple of 16 */
+  const void* scales;       /* device [V x H/group] of scale_dtype */
+  lmh_dtype scale_dtype;    /* any lmh_dtype */
+  int64_t scale_row_stride; /* elements, >= H/group */
+  const uint8_t* zeros;     /* device u8 [V x H/group] (the low four bits count), or NULL */
+  int64_t zero_row_stride;  /* elements, >= H/group */
+  int32_t V, H;             /* H a multiple of group */
+  int32_t group;            /* 32, 64 or 128 */
+} lmh_q4_table;
+
+/*
+ * lmh_quantize_q4 -- round a bf16 table to 4 bits (once, when weights are loaded).
+ *
+ * Writes the arrays that `table` points to (its pointers are outputs here).  Per
+ * group, in fp32 with the scale rounded once to scale_dtype (s below):
+ *   zeros NULL:  s = max|w| / 7;              q = clamp(rint(w / s), -8, 7) + 8
+ *   with zeros:  s = (max(w, 0) - min(w, 0)) / 15;  zero = clamp(rint(-min(w, 0) / s), 0, 15);
+ *                q = clamp(rint(w / s) + zero, 0, 15)
+ * A group whose s is 0 holds q = zero (8 without zeros).  Entries are finite.
+ *
+ *   W             device bf16 [V x H], row stride w_row_stride (>= H).
+ * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (a table outside the layout
+ * above), LMH_ERR_CUDA.
+ */
+lmh_status lmh_quantize_q4(const void* W, int64_t w_row_stride, const lmh_q4_table* table, cudaStream_t stream);
+
+/*
+ * lmh_project_q4 -- the head projection through a 4-bit table.
+ *
+ *   out[i][v] = logit_scale * sum_h hidden[row_idx[i]][h] * value[v][h]
+ * The products are of the 16-bit inputs and the whole numbers q - zero (exact in
+ * 16 bits); a group's sum is held in fp32, times its scale, and summed in fp32.
+ * Rounded once, to out_dtype.  For batches of few rows (decode): up to 16 rows
+ * cost one read of the table; more rows are taken 32 at a time.
+ *
+ *   hidden            device [num_tokens x H] of hidden_dtype (LMH_BF16 or
+ *                     LMH_F16), row stride hidden_row_stride (>= H), aligned to
+ *                     its elements.
+ *   row_idx           device int32 [rows] or NULL, as lmh_project_logprobs.
+ *   logit_scale       finite and > 0 (a head transform, as
+ *                     lmh_project_logprobs_scaled).
+ *   out               device [rows x V] of out_dtype (LMH_F32 or hidden_dtype),
+ *                     row stride out_row_stride (>= V).
+ * The table's 4-bit entries may be read before the kernel enqueued before this
+ * one ends (the conventions above: head weights).  No workspace is needed.
+ * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (dtypes, group, alignment),
+ * LMH_ERR_CUDA.  Device: LMH_DS_ROW_IDX_OUT_OF_RANGE (the row reads zeros).
+ */
+lmh_status lmh_project_q4(const void* hidden, lmh_dtype hidden_dtype, int64_t hidden_row_stride, int32_t num_tokens,
+                          const int32_t* row_idx, int32_t rows, const lmh_q4_table* table, float logit_scale,
+                          void* out, lmh_dtype out_dtype, int64_t out_row_stride, uint32_t* dev_status,
+                          cudaStream_t stream);
+
+/*
+ * lmh_lookup_q4 -- the embedding rows of token ids, from a tied 4-bit table.
+ *
+ *   out[i][h] = (q - zero) * table scale * scale, in fp32 (the first product is
+ *               exact for 16-bit scales), rounded once to out_dtype.
+ *   ids               device int32 [n].  -1 (no token) gives a row of zeros; any
+ *                     other id outside [0, V) does too and sets
+ *                     LMH_DS_SEL_OUT_OF_RANGE.
+ *   scale             finite (1, or a model's embedding multiplier).
+ *   out               device [n x H] of out_dtype (any), row stride
+ *                     out_row_stride (>= H).
+ * Errors: as lmh_project_q4.
+ */
+lmh_status lmh_lookup_q4(const int32_t* ids, int32_t n, const lmh_q4_table* table, float scale, void* out,
+                         lmh_dtype out_dtype, int64_t out_row_stride, uint32_t* dev_status, cudaStream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* lmh_status_string(lmh_status status);
 
@@ -459,8 +605,9 @@ int32_t lmh_version(void);
  * and total milliseconds of the named kernel ("select_rows", "gather_rows",
  * "head_logprobs", "merge_partials", "logits_reduce" (the streaming pass of
  * lmh_logprobs_from_logits), "logits_select" (its per-row selection),
- * "full_logprobs" (the pass that writes the k_max = LMH_K_FULL output)) since
- * the last reset.
+ * "full_logprobs" (the pass that writes the k_max = LMH_K_FULL output),
+ * "sample_logits", "project_q4", "lookup_q4", "quantize_q4") since the last
+ * reset.
  * lmh_trace_reset clears the totals.
  */
 lmh_status lmh_trace_enable(int32_t enable);

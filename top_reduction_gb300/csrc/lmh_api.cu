@@ -2,7 +2,8 @@
 // one-time device set-up, kernel launches and the kernel trace.
 //
 // Nothing here computes results: every step of the path runs in the kernels
-// of select_rows.cu, head_gemm.cu, logits_reduce.cu and merge_partials.cu.
+// of select_rows.cu, head_gemm.cu, logits_reduce.cu, merge_partials.cu,
+// sample_logits.cu, q4_table.cu and q4_project.cu.
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -34,6 +35,8 @@ static cudaError_t device_setup(int* num_sms) {
     if (e == cudaSuccess) e = logits_reduce_setup();
     if (e == cudaSuccess) e = merge_setup();
     if (e == cudaSuccess) e = head_setup();
+    if (e == cudaSuccess) e = sample_logits_setup();
+    if (e == cudaSuccess) e = q4_project_setup();
     if (e != cudaSuccess) return e;
     g_num_sms[dev] = sms;
     g_setup_done[dev] = true;
@@ -75,7 +78,8 @@ Partials carve_partials(void* base, int rows, int splits, int k_max) {
 // ---------------------------------------------------------------------------
 static const char* const kTraceNames[kTraceCount] = {"select_rows",    "gather_rows",   "head_logprobs",
                                                      "logits_reduce",  "merge_partials", "logits_select",
-                                                     "full_logprobs"};
+                                                     "full_logprobs", "sample_logits", "project_q4",    "lookup_q4",
+                                                     "quantize_q4"};
 
 struct TraceRecord {
   int kernel;
@@ -487,6 +491,84 @@ lmh_status lmh_merge_records(const void* records, int32_t num_parts, int32_t row
                      dev_status, stream, /*pdl=*/true, nullptr, sms);
   }
   return from_cuda(e);
+}
+
+lmh_status lmh_sample_from_logits(const void* logits, lmh_dtype dtype, int32_t rows, int32_t V, int64_t row_stride,
+                                  const lmh_filters* filters, const float* uniforms, int32_t* sampled_ids,
+                                  float* sampled_logprob, uint32_t* dev_status, cudaStream_t stream) {
+  if (rows < 0 || V <= 0 || row_stride < V) return LMH_ERR_INVALID_ARG;
+  if (dtype != LMH_BF16 && dtype != LMH_F16 && dtype != LMH_F32) return LMH_ERR_INVALID_ARG;
+  if (rows == 0) return LMH_OK;  // (an empty tensor's pointer may be null)
+  if (!logits || !uniforms || !sampled_ids) return LMH_ERR_INVALID_ARG;
+  const lmh_filters f = filters ? *filters : lmh_filters{};
+  if (f.allowed_mask && f.mask_words < (V + 31) / 32) return LMH_ERR_INVALID_ARG;
+  if (V > LMH_SAMPLE_V_MAX || !aligned(logits, dtype == LMH_F32 ? 4 : 2)) return LMH_ERR_UNSUPPORTED;
+  int sms = 0;
+  if (device_setup(&sms) != cudaSuccess) return LMH_ERR_CUDA;
+  Traced tr(kTraceSample, stream);
+  return from_cuda(launch_sample_logits(logits, dtype, rows, V, row_stride, f, uniforms, sampled_ids, sampled_logprob,
+                                        dev_status, sms, stream));
+}
+
+// The 4-bit entry points' common check of a table.
+static lmh_status check_table(const lmh_q4_table* t) {
+  if (!t || !t->packed || !t->scales || t->V <= 0 || t->H <= 0) return LMH_ERR_INVALID_ARG;
+  if (t->scale_dtype != LMH_BF16 && t->scale_dtype != LMH_F16 && t->scale_dtype != LMH_F32) return LMH_ERR_INVALID_ARG;
+  if (t->group != 32 && t->group != 64 && t->group != 128) return LMH_ERR_UNSUPPORTED;
+  if (t->H % t->group != 0) return LMH_ERR_INVALID_ARG;
+  const int groups = t->H / t->group;
+  if (t->packed_row_bytes < t->H / 2 || t->scale_row_stride < groups || (t->zeros && t->zero_row_stride < groups))
+    return LMH_ERR_INVALID_ARG;
+  if (!aligned(t->packed, 16) || t->packed_row_bytes % 16 != 0 || !aligned(t->scales, t->scale_dtype == LMH_F32 ? 4 : 2))
+    return LMH_ERR_UNSUPPORTED;
+  return LMH_OK;
+}
+
+static size_t dtype_bytes(lmh_dtype d) { return d == LMH_F32 ? 4 : 2; }
+
+lmh_status lmh_quantize_q4(const void* W, int64_t w_row_stride, const lmh_q4_table* table, cudaStream_t stream) {
+  const lmh_status st = check_table(table);
+  if (st != LMH_OK) return st;
+  if (!W || w_row_stride < table->H) return LMH_ERR_INVALID_ARG;
+  if (!aligned(W, 2)) return LMH_ERR_UNSUPPORTED;
+  int sms = 0;
+  if (device_setup(&sms) != cudaSuccess) return LMH_ERR_CUDA;
+  Traced tr(kTraceQuantizeQ4, stream);
+  return from_cuda(launch_quantize_q4(W, w_row_stride, *table, stream));
+}
+
+lmh_status lmh_project_q4(const void* hidden, lmh_dtype hidden_dtype, int64_t hidden_row_stride, int32_t num_tokens,
+                          const int32_t* row_idx, int32_t rows, const lmh_q4_table* table, float logit_scale,
+                          void* out, lmh_dtype out_dtype, int64_t out_row_stride, uint32_t* dev_status,
+                          cudaStream_t stream) {
+  const lmh_status st = check_table(table);
+  if (st != LMH_OK) return st;
+  if (rows == 0) return LMH_OK;
+  if (rows < 0 || num_tokens < 0 || !hidden || !out || hidden_row_stride < table->H || out_row_stride < table->V ||
+      !valid_scale(logit_scale) || (!row_idx && rows > num_tokens))
+    return LMH_ERR_INVALID_ARG;
+  if (hidden_dtype != LMH_BF16 && hidden_dtype != LMH_F16) return LMH_ERR_UNSUPPORTED;
+  if (out_dtype != LMH_F32 && out_dtype != hidden_dtype) return LMH_ERR_UNSUPPORTED;
+  if (!aligned(hidden, 2) || !aligned(out, dtype_bytes(out_dtype))) return LMH_ERR_UNSUPPORTED;
+  int sms = 0;
+  if (device_setup(&sms) != cudaSuccess) return LMH_ERR_CUDA;
+  Traced tr(kTraceProjectQ4, stream);
+  return from_cuda(launch_project_q4(hidden, hidden_dtype, hidden_row_stride, num_tokens, row_idx, rows, *table,
+                                     logit_scale, out, out_dtype, out_row_stride, dev_status, sms, stream));
+}
+
+lmh_status lmh_lookup_q4(const int32_t* ids, int32_t n, const lmh_q4_table* table, float scale, void* out,
+                         lmh_dtype out_dtype, int64_t out_row_stride, uint32_t* dev_status, cudaStream_t stream) {
+  const lmh_status st = check_table(table);
+  if (st != LMH_OK) return st;
+  if (n == 0) return LMH_OK;
+  if (n < 0 || !ids || !out || out_row_stride < table->H || !std::isfinite(scale)) return LMH_ERR_INVALID_ARG;
+  if (out_dtype != LMH_BF16 && out_dtype != LMH_F16 && out_dtype != LMH_F32) return LMH_ERR_INVALID_ARG;
+  if (!aligned(out, dtype_bytes(out_dtype))) return LMH_ERR_UNSUPPORTED;
+  int sms = 0;
+  if (device_setup(&sms) != cudaSuccess) return LMH_ERR_CUDA;
+  Traced tr(kTraceLookupQ4, stream);
+  return from_cuda(launch_lookup_q4(ids, n, *table, scale, out, out_dtype, out_row_stride, dev_status, sms, stream));
 }
 
 lmh_status lmh_debug_set_wait_limit(uint64_t limit_ns) {

@@ -173,6 +173,25 @@ cudaError_t launch_head(const void* A, int64_t a_stride, int rows, int H, const 
                         bool pdl = false, const RowOutputs* final_out = nullptr, float logit_scale = 1.0f,
                         const SampleArgs* samp = nullptr, bool w_hv = false, int id_off = 0);
 
+// ---- filtered sampling (sample_logits.cu) ----
+
+cudaError_t sample_logits_setup();
+cudaError_t launch_sample_logits(const void* logits, lmh_dtype dtype, int rows, int V, int64_t row_stride,
+                                 const lmh_filters& f, const float* uniforms, int32_t* ids, float* logprobs,
+                                 uint32_t* dev_status, int num_sms, cudaStream_t stream);
+
+// ---- 4-bit tables (q4_table.cu, q4_project.cu) ----
+
+cudaError_t q4_project_setup();
+cudaError_t launch_quantize_q4(const void* W, int64_t w_stride, const lmh_q4_table& t, cudaStream_t stream);
+cudaError_t launch_lookup_q4(const int32_t* ids, int n, const lmh_q4_table& t, float scale, void* out,
+                             lmh_dtype out_dtype, int64_t out_stride, uint32_t* dev_status, int num_sms,
+                             cudaStream_t stream);
+cudaError_t launch_project_q4(const void* hidden, lmh_dtype hidden_dtype, int64_t hidden_stride, int num_tokens,
+                              const int32_t* row_idx, int rows, const lmh_q4_table& t, float logit_scale, void* out,
+                              lmh_dtype out_dtype, int64_t out_stride, uint32_t* dev_status, int num_sms,
+                              cudaStream_t stream);
+
 // Launch `kernel` on `stream`; with pdl = true it carries the programmatic
 // stream serialization attribute, so it may start while its predecessor in the
 // stream finishes (the kernel calls pdl_wait() before reading that
@@ -202,6 +221,10 @@ enum TraceKernel {
   kTraceMerge,
   kTraceLogitsSelect,
   kTraceFull,
+  kTraceSample,
+  kTraceProjectQ4,
+  kTraceLookupQ4,
+  kTraceQuantizeQ4,
   kTraceCount
 };
 void trace_begin(TraceKernel k, cudaStream_t s);

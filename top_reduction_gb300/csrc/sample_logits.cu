@@ -1,0 +1,699 @@
+// sample_logits.cu -- one token per row with temperature, top-k, top-p and
+// min-p from one given uniform number (lmh_sample_from_logits).
+//
+// A row belongs to a thread-block cluster.  Its CTAs hold the row in their
+// shared memory (a contiguous slice of the ids each), so HBM is read once and
+// every later pass -- the maximum, the sum of the weights, the searches for the
+// top-k and top-p thresholds, the draw -- runs on chip.
+//
+// Weights are whole numbers, w = rint(2^32 exp2(t)) with t = (z - max) * c: their
+// sums are the same in any order, so neither the split over threads, warps and
+// CTAs nor the batch changes a draw.  A sum costs no integer conversion per
+// logit: adding 1.5 * 2^9 to p = exp2(t) leaves p rounded to 2^-14 in the
+// mantissa's low bits, the rest p - that (exact) plus 1.5 * 2^-9 leaves it
+// rounded to 2^-32 in the same way, and the two bit patterns are summed as
+// integers (the constants' bits are taken off once at the end).
+//
+// Kept tokens are described by a threshold (z, id): every token with a larger
+// logit, and those equal to it up to that id.  A threshold is the last token of a
+// prefix of the order (z descending, id ascending) that reaches a count (top-k) or
+// a mass (top-p); it is found by histograms over ever smaller intervals of z.
+#include <cmath>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "device_common.cuh"
+#include "lmh_internal.h"
+
+namespace lmh {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kBins = 256;
+constexpr float kHiAdd = 768.0f;             // 1.5 * 2^9: unit 2^-14
+constexpr float kLoAdd = 0.0029296875f;      // 1.5 * 2^-9: unit 2^-32
+constexpr uint32_t kHiBits = 0x44400000u;    // of kHiAdd
+constexpr uint32_t kLoBits = 0x3B400000u;    // of kLoAdd
+constexpr int kHiShift = 18;                 // 2^-14 in units of 2^-32
+
+// ---------------------------------------------------------------------------
+// clusters
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// All threads of all CTAs of the cluster; orders their shared-memory accesses.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.aligned.release;\n\tbarrier.cluster.wait.aligned.acquire;" ::: "memory");
+}
+// Address of `p` (this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t a) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// logits in 16-byte vectors
+// ---------------------------------------------------------------------------
+template <typename T>
+struct Vec;  // kN elements a vector; widen and narrow are exact
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ void widen(const uint4& x, float (&z)[4]) {
+    z[0] = __uint_as_float(x.x);
+    z[1] = __uint_as_float(x.y);
+    z[2] = __uint_as_float(x.z);
+    z[3] = __uint_as_float(x.w);
+  }
+  static __device__ __forceinline__ uint4 narrow(const float (&z)[4]) {
+    return make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3]));
+  }
+  static __device__ __forceinline__ float to_float(float x) { return x; }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void widen(const uint4& x, float (&z)[8]) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      z[2 * i] = __uint_as_float(u[i] << 16);
+      z[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 narrow(const float (&z)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      u[i] = (__float_as_uint(z[2 * i]) >> 16) | (__float_as_uint(z[2 * i + 1]) & 0xFFFF0000u);
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  static __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+};
+template <>
+struct Vec<__half> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void widen(const uint4& x, float (&z)[8]) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      z[2 * i] = f.x;
+      z[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ uint4 narrow(const float (&z)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(z[2 * i], z[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  static __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+};
+
+// ---------------------------------------------------------------------------
+// weights
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float tempered(float z, float zm, float c) { return __fmul_rn(__fsub_rn(z, zm), c); }
+
+// The two parts of the weight of p = exp2(t), as bit patterns to be summed.
+__device__ __forceinline__ void weight_bits(float p, uint32_t& hi, uint32_t& lo) {
+  const float h = __fadd_rn(p, kHiAdd);
+  const float rest = __fsub_rn(p, __fsub_rn(h, kHiAdd));
+  hi = __float_as_uint(h);
+  lo = __float_as_uint(__fadd_rn(rest, kLoAdd));
+}
+// Sum of n weights from the sums (mod 2^32) of their parts; n < 2^14.
+__device__ __forceinline__ long long weight_sum(uint32_t hi, uint32_t lo, uint32_t n) {
+  const long long h = static_cast<int32_t>(hi - n * kHiBits), l = static_cast<int32_t>(lo - n * kLoBits);
+  return (h << kHiShift) + l;
+}
+__device__ __forceinline__ long long weight_of(float t) {
+  uint32_t hi, lo;
+  weight_bits(ex2_approx(t), hi, lo);
+  return weight_sum(hi, lo, 1);
+}
+
+__device__ __forceinline__ long long warp_sum_i64(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+struct Params {
+  const void* logits;
+  int64_t row_stride;
+  int rows, V;
+  lmh_filters f;
+  const float* uniforms;
+  int32_t* ids;
+  float* logprobs;
+  uint32_t* dev_status;
+};
+
+// What is kept: t >= min_t, and z > z_cut or (z == z_cut and id <= id_cut).
+struct Kept {
+  float min_t;
+  float z_cut;
+  int id_cut;
+};
+
+struct Shared {
+  // read by the other CTAs of the cluster
+  uint32_t slot_u32[2][4];
+  unsigned long long slot_u64[2];
+  uint32_t hist[2][2][kBins];  // [level parity][high, low part or count][bin]
+  // this CTA's own
+  uint32_t scratch_u32[kWarps];
+  unsigned long long scratch_u64[kWarps];
+  unsigned long long warp_mass[kWarps];
+  unsigned long long bin_scan[kBins / 32];
+  unsigned long long found_above;
+  int found_bin;
+};
+
+// One row's slice in one CTA.
+template <typename T>
+struct Slice {
+  uint4* data;        // this warp's vectors: data[i], i = lane, lane + 32, ...
+  int n;              // vectors of this warp
+  int id0;            // id of element 0 of data[0] (may be below 0 in a row's first vector)
+  int lane;
+};
+
+template <typename T, typename F>
+__device__ __forceinline__ void for_each_vector(const Slice<T>& s, F&& f) {
+  for (int i = s.lane; i < s.n; i += 32) {
+    float z[Vec<T>::kN];
+    Vec<T>::widen(s.data[i], z);
+    f(z, s.id0 + i * Vec<T>::kN);
+  }
+}
+
+template <typename T>
+class RowSampler {
+ public:
+  static constexpr int kN = Vec<T>::kN;
+
+  __device__ RowSampler(const Params& p, Shared& sh, uint4* data, int row)
+      : p_(p), sh_(sh), row_(row), rank_(cluster_rank()), size_(cluster_size()) {
+    tid_ = threadIdx.x;
+    lane_ = tid_ & 31;
+    warp_ = tid_ >> 5;
+    parity_ = 0;
+    load(data);
+  }
+
+  __device__ void run();
+
+ private:
+  const Params& p_;
+  Shared& sh_;
+  int row_, tid_, lane_, warp_;
+  uint32_t rank_, size_;
+  int parity_;
+  Slice<T> s_;
+  float zm_, c_;
+
+  __device__ void load(uint4* data);
+  __device__ void sync_next() {
+    cluster_sync();
+    parity_ ^= 1;
+  }
+  // max / min / sum over the cluster (every thread gets the result)
+  __device__ uint32_t reduce_max_u32(uint32_t v);
+  __device__ unsigned long long reduce_sum_u64(unsigned long long v, unsigned long long* before);
+  __device__ float weight_p(float z) const { return ex2_approx(tempered(z, zm_, c_)); }
+  __device__ bool is_kept(float z, int id, const Kept& k) const {
+    return tempered(z, zm_, c_) >= k.min_t && (z > k.z_cut || (z == k.z_cut && id <= k.id_cut));
+  }
+  __device__ unsigned long long warp_kept_mass(const Kept& k);
+  __device__ void threshold(bool by_mass, unsigned long long target, Kept* k);
+  __device__ void draw(const Kept& k);
+  __device__ void greedy();
+};
+
+// Copies this CTA's slice into shared memory: -inf stands for tokens that are
+// not allowed, NaN, and the padding of the row's first and last vector.  A lane
+// reads back only what it wrote, so no barrier is needed.
+template <typename T>
+__device__ void RowSampler<T>::load(uint4* data) {
+  const T* row = static_cast<const T*>(p_.logits) + static_cast<int64_t>(row_) * p_.row_stride;
+  const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % kN);  // elements before the row
+  const uint4* base = reinterpret_cast<const uint4*>(row - lead);
+  const int nvec = (lead + p_.V + kN - 1) / kN;
+  const int per_cta = (nvec + static_cast<int>(size_) - 1) / static_cast<int>(size_);
+  const int cta0 = min(static_cast<int>(rank_) * per_cta, nvec), cta1 = min(cta0 + per_cta, nvec);
+  const int per_warp = (cta1 - cta0 + kWarps - 1) / kWarps;
+  const int v0 = min(cta0 + warp_ * per_warp, cta1), v1 = min(v0 + per_warp, cta1);
+  s_.data = data + (v0 - cta0);
+  s_.n = v1 - v0;
+  s_.id0 = v0 * kN - lead;
+  s_.lane = lane_;
+  const uint32_t* mask =
+      p_.f.allowed_mask ? p_.f.allowed_mask + static_cast<int64_t>(row_) * p_.f.mask_words : nullptr;
+  for (int i = lane_; i < s_.n; i += 32) {
+    const int id = s_.id0 + i * kN;
+    float z[kN];
+    if (id >= 0 && id + kN <= p_.V) {
+      Vec<T>::widen(__ldg(base + v0 + i), z);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        z[e] = (id + e >= 0 && id + e < p_.V) ? Vec<T>::to_float(row[id + e]) : -INFINITY;
+    }
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      if (z[e] != z[e]) z[e] = -INFINITY;
+      if (mask && id + e >= 0 && id + e < p_.V && !((mask[(id + e) >> 5] >> ((id + e) & 31)) & 1u)) z[e] = -INFINITY;
+    }
+    s_.data[i] = Vec<T>::narrow(z);
+  }
+}
+
+template <typename T>
+__device__ uint32_t RowSampler<T>::reduce_max_u32(uint32_t v) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if (lane_ == 0) sh_.scratch_u32[warp_] = v;
+  __syncthreads();
+  if (warp_ == 0) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, lane_ < kWarps ? sh_.scratch_u32[lane_] : 0u);
+    if (lane_ == 0) sh_.slot_u32[parity_][0] = m;
+  }
+  cluster_sync();
+  uint32_t m = 0;
+  for (uint32_t r = 0; r < size_; ++r) m = max(m, ld_cluster_u32(cluster_addr(&sh_.slot_u32[parity_][0], r)));
+  parity_ ^= 1;
+  return m;
+}
+
+// Sum over the cluster of one value per warp (lane 0's); *before: the sum over
+// the CTAs of lower rank.  Leaves the warps' values in sh_.warp_mass.
+template <typename T>
+__device__ unsigned long long RowSampler<T>::reduce_sum_u64(unsigned long long v, unsigned long long* before) {
+  __syncthreads();
+  if (lane_ == 0) sh_.warp_mass[warp_] = v;
+  __syncthreads();
+  if (warp_ == 0) {
+    const long long m = warp_sum_i64(lane_ < kWarps ? static_cast<long long>(sh_.warp_mass[lane_]) : 0);
+    if (lane_ == 0) sh_.slot_u64[parity_] = static_cast<unsigned long long>(m);
+  }
+  cluster_sync();
+  unsigned long long all = 0, b = 0;
+  for (uint32_t r = 0; r < size_; ++r) {
+    const unsigned long long m = ld_cluster_u64(cluster_addr(&sh_.slot_u64[parity_], r));
+    if (r < rank_) b += m;
+    all += m;
+  }
+  parity_ ^= 1;
+  *before = b;
+  return all;
+}
+
+template <typename T>
+__device__ unsigned long long RowSampler<T>::warp_kept_mass(const Kept& k) {
+  uint32_t hi = 0, lo = 0, n = 0;
+  for_each_vector(s_, [&](const float(&z)[kN], int id) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      uint32_t h, l;
+      weight_bits(is_kept(z[e], id + e, k) ? weight_p(z[e]) : 0.0f, h, l);
+      hi += h;
+      lo += l;
+    }
+    n += kN;
+  });
+  return static_cast<unsigned long long>(warp_sum_i64(weight_sum(hi, lo, n)));
+}
+
+// Narrows k->z_cut, k->id_cut to the shortest prefix of the order whose count (or
+// mass) reaches target >= 1.  A target above the row's total leaves k alone.
+template <typename T>
+__device__ void RowSampler<T>::threshold(bool by_mass, unsigned long long target, Kept* k) {
+  float hi = zm_;                 // the interval of z that holds the threshold: [lo, hi]
+  float lo = -INFINITY;
+  unsigned long long above = 0;   // count or mass of z > hi
+  // lo: the smallest logit above -inf
+  {
+    uint32_t m = 0;  // max of the complemented order keys
+    for_each_vector(s_, [&](const float(&z)[kN], int) {
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (z[e] > -INFINITY) m = max(m, ~f32_ord(z[e]));
+    });
+    __syncthreads();
+    lo = ord_f32(~reduce_max_u32(m));
+  }
+  for (int level = 0; lo < hi; ++level) {
+    // Bins over [lo, hi], bin 0 at the top: linear in z first, which spreads a
+    // row's logits evenly; linear in the order keys after eight levels or where
+    // the width is no ordinary number (each such level takes 8 bits off the keys).
+    const float width = __fsub_rn(hi, lo);
+    const bool linear = level < 8 && width < 1e30f && width > 1e-30f;
+    const float inv = linear ? __fdiv_rn(kBins - 1, width) : 0.0f;
+    const uint32_t ord_hi = f32_ord(hi);
+    const int shift = max(0, 32 - __clz(ord_hi - f32_ord(lo)) - 8);
+    auto bin_of = [&](float z) -> int {
+      return linear ? min(static_cast<int>(__fmul_rn(__fsub_rn(hi, z), inv)), kBins - 1)
+                    : static_cast<int>((ord_hi - f32_ord(z)) >> shift);
+    };
+    uint32_t(*hist)[kBins] = sh_.hist[parity_];
+    __syncthreads();
+    for (int b = tid_; b < 2 * kBins; b += kThreads) (&hist[0][0])[b] = 0;
+    __syncthreads();
+    for_each_vector(s_, [&](const float(&z)[kN], int) {
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (z[e] >= lo && z[e] <= hi) {
+          const int b = bin_of(z[e]);
+          if (by_mass) {
+            const unsigned long long w = static_cast<unsigned long long>(weight_of(tempered(z[e], zm_, c_)));
+            atomicAdd(&hist[0][b], static_cast<uint32_t>(w >> 16));
+            atomicAdd(&hist[1][b], static_cast<uint32_t>(w) & 0xFFFFu);
+          } else {
+            atomicAdd(&hist[0][b], 1u);
+          }
+        }
+    });
+    cluster_sync();
+    // every CTA adds the bins up and finds the one that holds the target
+    unsigned long long mine = 0, incl = 0;
+    if (tid_ < kBins) {
+      for (uint32_t r = 0; r < size_; ++r) {
+        const unsigned long long h = ld_cluster_u32(cluster_addr(&hist[0][tid_], r));
+        mine += by_mass ? (h << 16) + ld_cluster_u32(cluster_addr(&hist[1][tid_], r)) : h;
+      }
+      incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane_ >= o) incl += t;
+      }
+      if (lane_ == 31) sh_.bin_scan[warp_] = incl;
+    }
+    if (tid_ == 0) sh_.found_bin = -1;
+    __syncthreads();
+    if (tid_ < kBins) {
+      unsigned long long b = above;
+      for (int w = 0; w < warp_; ++w) b += sh_.bin_scan[w];
+      if (b + incl >= target && b + incl - mine < target) {
+        sh_.found_bin = tid_;
+        sh_.found_above = b + incl - mine;
+      }
+    }
+    __syncthreads();
+    const int bin = sh_.found_bin;
+    if (bin < 0) return;  // the row has less than the target: all of it is kept
+    above = sh_.found_above;
+    // the bin's own extremes are the next interval
+    uint32_t top = 0, bottom = 0;
+    for_each_vector(s_, [&](const float(&z)[kN], int) {
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (z[e] >= lo && z[e] <= hi && bin_of(z[e]) == bin) {
+          top = max(top, f32_ord(z[e]));
+          bottom = max(bottom, ~f32_ord(z[e]));
+        }
+    });
+    parity_ ^= 1;
+    __syncthreads();
+    const uint32_t t = reduce_max_u32(top);
+    __syncthreads();
+    const uint32_t b = reduce_max_u32(bottom);
+    hi = ord_f32(t);
+    lo = ord_f32(~b);
+  }
+  // One value left, `hi`: of the tokens equal to it the first m in id order are kept.
+  unsigned long long ties = 0, before = 0;
+  for_each_vector(s_, [&](const float(&z)[kN], int) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) ties += z[e] == hi ? 1 : 0;
+  });
+  ties = static_cast<unsigned long long>(warp_sum_i64(static_cast<long long>(ties)));
+  const unsigned long long all = reduce_sum_u64(ties, &before);
+  unsigned long long m = target - above;
+  if (by_mass) {
+    const unsigned long long w = static_cast<unsigned long long>(weight_of(tempered(hi, zm_, c_)));
+    if (w == 0) return;  // (a target above the row's total)
+    m = (m + w - 1) / w;
+  }
+  if (m > all) return;
+  // the CTA and warp that hold the m-th of them find its id
+  unsigned long long b = before;
+  for (int w = 0; w < warp_; ++w) b += sh_.warp_mass[w];
+  uint32_t found = 0;
+  if (b < m && m <= b + ties) {
+    unsigned long long left = m - b;
+    for (int i0 = 0; i0 < s_.n; i0 += 32) {
+      const int i = i0 + lane_;
+      float z[kN];
+      int cnt = 0;
+      if (i < s_.n) {
+        Vec<T>::widen(s_.data[i], z);
+#pragma unroll
+        for (int e = 0; e < kN; ++e) cnt += z[e] == hi ? 1 : 0;
+      }
+      int incl = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane_ >= o) incl += t;
+      }
+      const int total = __shfl_sync(0xffffffffu, incl, 31);
+      if (static_cast<unsigned long long>(total) >= left) {
+        int need = static_cast<int>(left) - (incl - cnt);
+        if (need >= 1 && need <= cnt) {
+#pragma unroll
+          for (int e = 0; e < kN; ++e)
+            if (z[e] == hi && --need == 0) found = static_cast<uint32_t>(s_.id0 + i * kN + e) + 1;
+        }
+        break;
+      }
+      left -= total;
+    }
+  }
+  __syncthreads();
+  const uint32_t f = reduce_max_u32(found);
+  k->z_cut = hi;
+  k->id_cut = static_cast<int>(f) - 1;
+}
+
+// The token at the given point of the kept tokens' mass, in id order.
+template <typename T>
+__device__ void RowSampler<T>::draw(const Kept& k) {
+  const unsigned long long mine = warp_kept_mass(k);
+  unsigned long long before = 0;
+  const unsigned long long total = reduce_sum_u64(mine, &before);
+  const float u = fminf(fmaxf(p_.uniforms[row_], 0.0f), 0.99999994f);
+  unsigned long long r = static_cast<unsigned long long>(
+      floor(__dmul_rn(static_cast<double>(u), static_cast<double>(static_cast<long long>(total)))));
+  if (r > total - 1) r = total - 1;
+  for (int w = 0; w < warp_; ++w) before += sh_.warp_mass[w];
+  if (r < before || r >= before + mine) return;
+  unsigned long long left = r - before;  // mass to pass within this warp's vectors
+  for (int i0 = 0; i0 < s_.n; i0 += 32) {
+    const int i = i0 + lane_;
+    float z[kN];
+    unsigned long long w[kN], sum = 0;
+#pragma unroll
+    for (int e = 0; e < kN; ++e) w[e] = 0;
+    if (i < s_.n) {
+      Vec<T>::widen(s_.data[i], z);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        if (is_kept(z[e], s_.id0 + i * kN + e, k))
+          w[e] = static_cast<unsigned long long>(weight_of(tempered(z[e], zm_, c_)));
+        sum += w[e];
+      }
+    }
+    unsigned long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane_ >= o) incl += t;
+    }
+    const unsigned long long all = __shfl_sync(0xffffffffu, incl, 31);
+    if (left < all) {
+      unsigned long long at = incl - sum;
+      if (at <= left && left < incl) {
+        int id = -1;
+        float zs = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+          if (at <= left && left < at + w[e]) {
+            id = s_.id0 + i * kN + e;
+            zs = z[e];
+          }
+          at += w[e];
+        }
+        p_.ids[row_] = id;
+        if (p_.logprobs) {
+          const float k32 = __fmul_rn(__ll2float_rn(static_cast<long long>(total)), 2.3283064365386963e-10f);
+          p_.logprobs[row_] = __fsub_rn(__fmul_rn(tempered(zs, zm_, c_), 0.6931471805599453f), logf(k32));
+        }
+      }
+      return;
+    }
+    left -= all;
+  }
+}
+
+// The first token whose logit is the row's maximum.
+template <typename T>
+__device__ void RowSampler<T>::greedy() {
+  uint32_t first = 0;  // complemented id
+  for_each_vector(s_, [&](const float(&z)[kN], int id) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e)
+      if (z[e] == zm_) first = max(first, ~static_cast<uint32_t>(id + e));
+  });
+  __syncthreads();
+  first = reduce_max_u32(first);
+  if (rank_ == 0 && tid_ == 0) {
+    p_.ids[row_] = static_cast<int32_t>(~first);
+    if (p_.logprobs) p_.logprobs[row_] = 0.0f;
+  }
+}
+
+template <typename T>
+__device__ void RowSampler<T>::run() {
+  float m = -INFINITY;
+  for_each_vector(s_, [&](const float(&z)[kN], int) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) m = fmaxf(m, z[e]);
+  });
+  zm_ = ord_f32(reduce_max_u32(f32_ord(m)));
+  if (zm_ == -INFINITY) {
+    if (rank_ == 0 && tid_ == 0) {
+      p_.ids[row_] = -1;
+      if (p_.logprobs) p_.logprobs[row_] = __int_as_float(0x7FC00000);
+      set_status(p_.dev_status, LMH_DS_NO_ALLOWED_TOKEN);
+    }
+    return;
+  }
+  if (zm_ == INFINITY) {  // only the +inf tokens are left, as equals
+    for (int i = lane_; i < s_.n; i += 32) {
+      float z[kN];
+      Vec<T>::widen(s_.data[i], z);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) z[e] = z[e] == INFINITY ? 0.0f : -INFINITY;
+      s_.data[i] = Vec<T>::narrow(z);
+    }
+    zm_ = 0.0f;
+  }
+  const float T_row = p_.f.temperature ? p_.f.temperature[row_] : 1.0f;
+  if (!(T_row > 0.0f)) {
+    greedy();
+    return;
+  }
+  c_ = fminf(fmaxf(__fmul_rn(__frcp_rn(T_row), kLog2e), 1.1754944e-38f), 3.402823466e+38f);
+
+  Kept k{-INFINITY, -INFINITY, INT32_MAX};
+  const int top_k = p_.f.top_k ? p_.f.top_k[row_] : 0;
+  const float top_p = p_.f.top_p ? p_.f.top_p[row_] : 1.0f;
+  const float min_p = p_.f.min_p ? p_.f.min_p[row_] : 0.0f;
+  if (top_k > 0 && top_k < p_.V) threshold(false, static_cast<unsigned long long>(top_k), &k);
+  if (top_p < 1.0f) {
+    unsigned long long before;
+    const unsigned long long mass = reduce_sum_u64(warp_kept_mass(k), &before);
+    const double need = ceil(__dmul_rn(static_cast<double>(top_p), static_cast<double>(static_cast<long long>(mass))));
+    threshold(true, need >= 1.0 ? static_cast<unsigned long long>(need) : 1ull, &k);
+  }
+  if (min_p > 0.0f) k.min_t = fminf(log2f(min_p), 0.0f);
+  draw(k);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) sample_logits_kernel(Params p) {
+  extern __shared__ uint4 data[];
+  __shared__ Shared sh;
+  pdl_wait();
+  pdl_launch_dependents();
+  RowSampler<T> s(p, sh, data, static_cast<int>(blockIdx.x / cluster_size()));
+  s.run();
+  cluster_sync();  // no CTA leaves while another may still read its shared memory
+}
+
+template <typename T>
+cudaError_t set_up() {
+  cudaFuncAttributes a{};
+  cudaError_t e = cudaFuncGetAttributes(&a, sample_logits_kernel<T>);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(sample_logits_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              227 * 1024 - static_cast<int>(a.sharedSizeBytes));
+}
+
+template <typename T>
+cudaError_t launch(const Params& p, int num_sms, cudaStream_t stream) {
+  // Largest slice of a row in one CTA: as many vectors as the kernel's own split.
+  auto slice_bytes = [&](int cl) {
+    const int nvec = (p.V + 2 * Vec<T>::kN - 2) / Vec<T>::kN;
+    return static_cast<size_t>((nvec + cl - 1) / cl) * 16;
+  };
+  // More CTAs per row until a slice leaves room for two or three CTAs per SM and,
+  // while the rows do not fill the GPU, until a slice is down to 8 Ki logits.
+  int cl = 1;
+  while (cl < kMaxCluster && (slice_bytes(cl) > 64 * 1024 || (p.rows * cl < num_sms && p.V / cl > 8192))) cl *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.rows) * cl);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = slice_bytes(cl);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cl;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, sample_logits_kernel<T>, p);
+}
+
+}  // namespace
+
+cudaError_t sample_logits_setup() {
+  cudaError_t e = set_up<float>();
+  if (e == cudaSuccess) e = set_up<__nv_bfloat16>();
+  if (e == cudaSuccess) e = set_up<__half>();
+  return e;
+}
+
+cudaError_t launch_sample_logits(const void* logits, lmh_dtype dtype, int rows, int V, int64_t row_stride,
+                                 const lmh_filters& f, const float* uniforms, int32_t* ids, float* logprobs,
+                                 uint32_t* dev_status, int num_sms, cudaStream_t stream) {
+  const Params p{logits, row_stride, rows, V, f, uniforms, ids, logprobs, dev_status};
+  if (dtype == LMH_F32) return launch<float>(p, num_sms, stream);
+  if (dtype == LMH_BF16) return launch<__nv_bfloat16>(p, num_sms, stream);
+  return launch<__half>(p, num_sms, stream);
+}
+
+}  // namespace lmh

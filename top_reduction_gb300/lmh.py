@@ -7,6 +7,7 @@ in the library's CUDA kernels.  There is no fallback: if liblmh.so is missing
 or no CUDA device is present, the calls raise.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -35,12 +36,28 @@ class Sampling(ctypes.Structure):
                 ("seed", ctypes.c_uint64), ("offsets", ctypes.c_void_p), ("sampled_ids", ctypes.c_void_p),
                 ("sampled_logprob", ctypes.c_void_p)]
 
+
+class Filters(ctypes.Structure):
+    """struct lmh_filters (include/lmh.h)."""
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("allowed_mask", ctypes.c_void_p), ("mask_words", ctypes.c_int32)]
+
+
+class Q4TableArg(ctypes.Structure):
+    """struct lmh_q4_table (include/lmh.h)."""
+    _fields_ = [("packed", ctypes.c_void_p), ("packed_row_bytes", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("scale_dtype", ctypes.c_int), ("scale_row_stride", ctypes.c_int64), ("zeros", ctypes.c_void_p),
+                ("zero_row_stride", ctypes.c_int64), ("V", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("group", ctypes.c_int32)]
+
+
 EXPORTS = ("lmh_select_rows", "lmh_count_selected_rows", "lmh_workspace_bytes",
            "lmh_project_logprobs", "lmh_project_logprobs_scaled", "lmh_project_logprobs_sample",
            "lmh_probe_selective",
            "lmh_logprobs_from_logits", "lmh_status_string",
            "lmh_version", "lmh_trace_enable", "lmh_trace_read", "lmh_trace_reset", "lmh_debug_set_wait_limit",
-           "lmh_record_bytes", "lmh_project_partials", "lmh_merge_workspace_bytes", "lmh_merge_records")
+           "lmh_record_bytes", "lmh_project_partials", "lmh_merge_workspace_bytes", "lmh_merge_records",
+           "lmh_sample_from_logits", "lmh_quantize_q4", "lmh_project_q4", "lmh_lookup_q4")
 
 _lib = None
 
@@ -102,6 +119,15 @@ def load():
     lib.lmh_merge_workspace_bytes.restype = u64
     lib.lmh_merge_records.argtypes = [P, i32, i32, i32, P, P, i32, P, P, P, P, P, u64, P, P]
     lib.lmh_merge_records.restype = ctypes.c_int
+    lib.lmh_sample_from_logits.argtypes = [P, ctypes.c_int, i32, i32, i64, ctypes.POINTER(Filters), P, P, P, P, P]
+    lib.lmh_sample_from_logits.restype = ctypes.c_int
+    T = ctypes.POINTER(Q4TableArg)
+    lib.lmh_quantize_q4.argtypes = [P, i64, T, P]
+    lib.lmh_quantize_q4.restype = ctypes.c_int
+    lib.lmh_project_q4.argtypes = [P, ctypes.c_int, i64, i32, P, i32, T, ctypes.c_float, P, ctypes.c_int, i64, P, P]
+    lib.lmh_project_q4.restype = ctypes.c_int
+    lib.lmh_lookup_q4.argtypes = [P, i32, T, ctypes.c_float, P, ctypes.c_int, i64, P, P]
+    lib.lmh_lookup_q4.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -308,11 +334,173 @@ def logprobs_from_logits(logits, sel=None, row_k=None, k_max=0, workspace=None, 
 
 
 # ---------------------------------------------------------------------------
+# a decode step with a 4-bit head: lookup, projection, filtered draw
+# ---------------------------------------------------------------------------
+
+def _on_stream(call):
+    """`stream=` makes the whole call on that stream: the tensors it converts and allocates, too."""
+    @functools.wraps(call)
+    def wrapper(*args, stream=None, **kwargs):
+        if stream is None:
+            return call(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return call(*args, **kwargs)
+    return wrapper
+
+
+def _current_stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _per_row(t, dtype, rows, device, name):
+    """A per-row parameter as a contiguous device tensor (as it is when it already is one)."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.is_contiguous()):
+        t = torch.as_tensor(t, dtype=dtype, device=device).contiguous()
+    if t.numel() != rows:
+        raise ValueError("%s must have %d entries" % (name, rows))
+    return t
+
+
+@_on_stream
+def sample_from_logits(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None, mask=None,
+                       dev_status=None, out=None):
+    """One token per row of logits [rows, V] (bf16, f16 or f32; rows may be strided), from one
+    given uniform number per row (lmh_sample_from_logits).
+
+    uniforms: fp32 [rows] in [0, 1).  temperature, top_p, min_p: fp32 [rows] or None; top_k: int32
+    [rows] or None; mask: int32/uint32 [rows, words] allowed-token bits or None.
+    Returns a dict with sampled_ids (int32 [rows], -1 where a row has no token) and sampled_logprob
+    (fp32 [rows], in the distribution that was drawn from).
+    """
+    assert logits.is_cuda and logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1)
+    rows, V = logits.shape
+    dev = logits.device
+    u = _per_row(uniforms, torch.float32, rows, dev, "uniforms")
+    if u is None:
+        raise ValueError("uniforms is required")
+    temp = _per_row(temperature, torch.float32, rows, dev, "temperature")
+    k = _per_row(top_k, torch.int32, rows, dev, "top_k")
+    p = _per_row(top_p, torch.float32, rows, dev, "top_p")
+    m = _per_row(min_p, torch.float32, rows, dev, "min_p")
+    words = 0
+    if mask is not None:
+        mask = torch.as_tensor(mask, device=dev).contiguous()
+        assert mask.dim() == 2 and mask.shape[0] == rows and mask.element_size() == 4
+        words = mask.shape[1]
+    if out is None:
+        out = {"sampled_ids": torch.empty(rows, dtype=torch.int32, device=dev),
+               "sampled_logprob": torch.empty(rows, dtype=torch.float32, device=dev)}
+    f = Filters(_ptr(temp), _ptr(k), _ptr(p), _ptr(m), _ptr(mask), words)
+    lp = out.get("sampled_logprob")
+    _check(load().lmh_sample_from_logits(logits.data_ptr(), _DTYPES[logits.dtype], rows, V,
+                                         logits.stride(0) if rows > 1 else V, ctypes.byref(f), u.data_ptr(),
+                                         out["sampled_ids"].data_ptr(), _ptr(lp), _ptr(dev_status), _current_stream()),
+           "lmh_sample_from_logits")
+    return out
+
+
+class Q4Table:
+    """A [V, H] table in 4 bits with group scales (struct lmh_q4_table).
+
+    packed: uint8 [V, H/2], the even entry of a pair in the low half; scales: bf16, f16 or f32
+    [V, H/group]; zeros: uint8 [V, H/group] or None (8).  value = scale * (q - zero).  Rows may
+    be strided; the object keeps the tensors alive.
+    """
+
+    def __init__(self, packed, scales, zeros=None, group=64):
+        assert packed.is_cuda and packed.dtype == torch.uint8 and packed.dim() == 2 and packed.stride(1) == 1
+        V, H = packed.shape[0], 2 * packed.shape[1]
+        if H % group or tuple(scales.shape) != (V, H // group):
+            raise ValueError("scales must be [V, H/group]")
+        assert scales.device == packed.device and (scales.stride(1) == 1 or scales.shape[1] == 1)
+        if zeros is not None:
+            if tuple(zeros.shape) != (V, H // group):
+                raise ValueError("zeros must be [V, H/group]")
+            assert zeros.dtype == torch.uint8 and zeros.device == packed.device
+            assert zeros.stride(1) == 1 or zeros.shape[1] == 1
+        self.packed, self.scales, self.zeros, self.group = packed, scales, zeros, group
+        self.V, self.H, self.device = V, H, packed.device
+
+        def stride(t, n):
+            return t.stride(0) if V > 1 else n
+        self._arg = Q4TableArg(packed.data_ptr(), stride(packed, H // 2), scales.data_ptr(), _DTYPES[scales.dtype],
+                               stride(scales, H // group), _ptr(zeros),
+                               0 if zeros is None else stride(zeros, H // group), V, H, group)
+        self._ref = ctypes.byref(self._arg)
+
+
+@_on_stream
+def quantize_q4(W, group=64, zeros=False, scale_dtype=torch.bfloat16):
+    """Round a bf16 table [V, H] to 4 bits (lmh_quantize_q4): a Q4Table."""
+    assert W.is_cuda and W.dtype == torch.bfloat16 and W.dim() == 2 and W.stride(1) == 1
+    V, H = W.shape
+    if H % group:
+        raise ValueError("H must be a multiple of the group")
+    dev = W.device
+    packed = torch.empty((V, H // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((V, H // group), dtype=scale_dtype, device=dev)
+    z = torch.empty((V, H // group), dtype=torch.uint8, device=dev) if zeros else None
+    table = Q4Table(packed, scales, z, group)
+    _check(load().lmh_quantize_q4(W.data_ptr(), W.stride(0) if V > 1 else H, table._ref, _current_stream()),
+           "lmh_quantize_q4")
+    return table
+
+
+@_on_stream
+def project_q4(hidden, table, row_idx=None, rows=None, logit_scale=1.0, out_dtype=torch.float32, out=None,
+               dev_status=None):
+    """Logits [rows, V] of hidden rows through a 4-bit head (lmh_project_q4).
+
+    hidden: bf16 or f16 [T, H] (rows may be strided); row_idx: int32 [rows] device tensor or None;
+    out_dtype: float32 or hidden's type, or give `out` (rows may be strided).
+    """
+    assert hidden.is_cuda and hidden.dim() == 2 and hidden.stride(1) == 1 and hidden.device == table.device
+    T, H = hidden.shape
+    if H != table.H:
+        raise ValueError("hidden has %d columns, the table %d" % (H, table.H))
+    if row_idx is not None:
+        assert row_idx.dtype == torch.int32 and row_idx.is_cuda and row_idx.is_contiguous()
+        rows = row_idx.numel() if rows is None else rows
+        assert rows <= row_idx.numel()
+    elif rows is None:
+        rows = T
+    if out is None:
+        out = torch.empty((rows, table.V), dtype=out_dtype, device=hidden.device)
+    assert out.is_cuda and tuple(out.shape) == (rows, table.V) and (out.stride(1) == 1 or table.V == 1)
+    _check(load().lmh_project_q4(hidden.data_ptr(), _DTYPES[hidden.dtype], hidden.stride(0) if T > 1 else H, T,
+                                 _ptr(row_idx), rows, table._ref, logit_scale, out.data_ptr(), _DTYPES[out.dtype],
+                                 out.stride(0) if rows > 1 else table.V, _ptr(dev_status), _current_stream()),
+           "lmh_project_q4")
+    return out
+
+
+@_on_stream
+def lookup_q4(ids, table, scale=1.0, out_dtype=torch.bfloat16, out=None, dev_status=None):
+    """The rows [n, H] of int32 device ids from a 4-bit table, times scale (lmh_lookup_q4); an id of
+    -1 (no token) gives zeros."""
+    assert ids.is_cuda and ids.dtype == torch.int32 and ids.dim() == 1 and ids.is_contiguous()
+    n = ids.numel()
+    if out is None:
+        out = torch.empty((n, table.H), dtype=out_dtype, device=ids.device)
+    assert out.is_cuda and tuple(out.shape) == (n, table.H) and out.stride(1) == 1
+    _check(load().lmh_lookup_q4(ids.data_ptr(), n, table._ref, scale, out.data_ptr(), _DTYPES[out.dtype],
+                                out.stride(0) if n > 1 else table.H, _ptr(dev_status), _current_stream()),
+           "lmh_lookup_q4")
+    return out
+
+
+# ---------------------------------------------------------------------------
 # kernel trace
 # ---------------------------------------------------------------------------
 
 TRACE_KERNELS = ("select_rows", "gather_rows", "head_logprobs", "logits_reduce", "merge_partials",
-                 "logits_select", "full_logprobs")
+                 "logits_select", "full_logprobs", "sample_logits", "project_q4", "lookup_q4", "quantize_q4")
 
 
 def trace_enable(on=True):
