@@ -91,6 +91,40 @@ def test_project_long_rows(lmh, rows, H, group):
     check_project(lmh.project_q4(x, table), x.double().cpu().numpy(), w, H, 1.0, "f32")
 
 
+@pytest.mark.parametrize("rows,V,H,group", [(1, 151936, 256, 32), (8, 120001, 1024, 32), (12, 90000, 512, 64),
+                                            (16, 100003, 1280, 128), (32, 60001, 768, 64), (3, 200003, 64, 32),
+                                            (20, 151936, 128, 64)])
+def test_project_many_tiles_per_sm(lmh, rows, V, H, group):
+    """Vocabularies that give every SM several tiles; repeated calls, the same bits each time."""
+    rng = np.random.default_rng(V)
+    table, w = random_table(lmh, V, H, group, group == 128, seed=rows)
+    x = torch.from_numpy(rng.standard_normal((rows, H)).astype(np.float32)).to(torch.bfloat16).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    first = lmh.project_q4(x, table, dev_status=status)
+    check_project(first, x.double().cpu().numpy(), w, H, 1.0, "f32")
+    for _ in range(20):
+        assert torch.equal(lmh.project_q4(x, table, dev_status=status), first)
+    assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_project_hidden_ranges(lmh, dtype):
+    """Rows of very large, very small, subnormal and widely spread values, and zeros."""
+    rng = np.random.default_rng(31)
+    V, H = 400, 640
+    table, w = random_table(lmh, V, H, 64, True, scale="f32", seed=9)
+    big, small = (1e30, 1e-36) if dtype == "bf16" else (3e4, 1e-7)
+    x = rng.standard_normal((12, H))
+    for i, f in enumerate([big, small, 1e-40 if dtype == "bf16" else 6e-8, 0.0]):
+        x[i] = np.clip(x[i] * f, -6e4 if dtype == "f16" else -3e38, 6e4 if dtype == "f16" else 3e38)
+    x[4] *= 10.0 ** rng.uniform(-20 if dtype == "bf16" else -4, 4, H)
+    x[5, ::2] = 0
+    x[6] = 0
+    x[6, 17] = 1.5
+    xt = torch.from_numpy(x.astype(np.float32)).to(DT[dtype]).cuda()
+    check_project(lmh.project_q4(xt, table), xt.double().cpu().numpy(), w, H, 1.0, "f32")
+
+
 def test_project_strides_and_row_index(lmh):
     """Strided hidden rows (odd strides too), strided table rows and output rows, gathered rows; an index out of range
     reads zeros and sets the status bit; nothing is written beside the output's columns."""

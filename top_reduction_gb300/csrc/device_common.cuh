@@ -279,6 +279,11 @@ __device__ __forceinline__ void named_bar_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
+// Arrive at barrier `id` without waiting (the other participants sync on it).
+__device__ __forceinline__ void named_bar_arrive(int id, int n) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
 // Barrier that also returns the OR of every participating thread's `pred`.
 __device__ __forceinline__ bool named_bar_or(int id, int n, bool pred) {
   uint32_t r;

@@ -8,7 +8,6 @@
 // token's logprob and the exact top-k, returned as an O(k+1) result; for
 // finite k the [rows x vocab] logits are never written to memory.
 
-#include <mutex>
 #include <type_traits>
 
 #include "head_kernel.cuh"
@@ -96,36 +95,10 @@ HeadPlan head_plan(int rows, int H, int V, int k_max, int num_sms) {
   return p;
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-static std::once_flag g_encode_once;
-
-static cudaError_t get_encode(PFN_cuTensorMapEncodeTiled_v12000* fn) {
-  std::call_once(g_encode_once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  *fn = g_encode;
-  return g_encode ? cudaSuccess : cudaErrorNotSupported;
-}
-
 // 2-D bf16 tensor map over a row-major [outer x inner] matrix with `pitch` elements per row.
 static cudaError_t make_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch,
                              uint32_t box_inner, uint32_t box_outer) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc;
-  cudaError_t e = get_encode(&enc);
-  if (e != cudaSuccess) return e;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {pitch * 2};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return make_tensor_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, pitch * 2, box_inner, box_outer);
 }
 
 cudaError_t head_setup() {
