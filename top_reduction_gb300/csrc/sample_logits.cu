@@ -14,10 +14,20 @@
 // rounded to 2^-32 in the same way, and the two bit patterns are summed as
 // integers (the constants' bits are taken off once at the end).
 //
-// Kept tokens are described by a threshold (z, id): every token with a larger
-// logit, and those equal to it up to that id.  A threshold is the last token of a
-// prefix of the order (z descending, id ascending) that reaches a count (top-k) or
-// a mass (top-p); it is found by histograms over ever smaller intervals of z.
+// Two ways to the kept tokens of a row with top-k or top-p:
+// - A list.  Every lane knows the largest of its own logits.  A histogram of these
+//   maxima over t gives a bound that at least k tokens reach (128 for top-p alone),
+//   few more than that do, and only lanes whose maximum reaches it look at their
+//   logits again.  The tokens that reach it go to the cluster's first CTA, which ranks
+//   them by counting: with n tokens, n^2 comparisons give every token its rank and the
+//   mass before it.  This holds for k up to kListTarget, and for top-p wherever the
+//   listed tokens have the mass that is asked for.
+// - A threshold (z, id) otherwise: every token with a larger logit is kept, and those
+//   equal to it up to that id.  It is the last token of the prefix of the order (z
+//   descending, id ascending) that reaches a count (top-k) or a mass (top-p), and is
+//   found by histograms of all logits over ever smaller intervals of z.
+// Tokens of weight 0 (t < -33) can be left out of either: no draw falls on them and no
+// sum changes.
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -33,7 +43,13 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 256;
+constexpr int kBins = 256;             // of a threshold search
+constexpr int kListBins = 512;         // of the lanes' maxima
+constexpr int kListCap = 512;          // tokens in a list, and in one CTA's part of it
+constexpr int kListTarget = 384;       // largest k that is tried with a list
+constexpr int kListTargetTopP = 128;   // tokens asked for with top-p alone
+constexpr float kMinT = -33.0f;        // below: weight 0
+constexpr int kUnroll = 4;             // vectors of a lane in flight while a row is loaded
 constexpr float kHiAdd = 768.0f;             // 1.5 * 2^9: unit 2^-14
 constexpr float kLoAdd = 0.0029296875f;      // 1.5 * 2^-9: unit 2^-32
 constexpr uint32_t kHiBits = 0x44400000u;    // of kHiAdd
@@ -54,9 +70,17 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 // All threads of all CTAs of the cluster; orders their shared-memory accesses.
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.aligned.release;\n\tbarrier.cluster.wait.aligned.acquire;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.aligned.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned.acquire;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
 }
 // Address of `p` (this CTA's shared memory) in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
@@ -93,7 +117,43 @@ struct Vec<float> {
     return make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3]));
   }
   static __device__ __forceinline__ float to_float(float x) { return x; }
+  // NaN becomes -inf
+  static __device__ __forceinline__ uint4 clean(const uint4& x) {
+    auto f = [](uint32_t u) { return __float_as_uint(fmaxf(__uint_as_float(u), -INFINITY)); };
+    return make_uint4(f(x.x), f(x.y), f(x.z), f(x.w));
+  }
+  static __device__ __forceinline__ float max_of(const uint4& x) {
+    return fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)), fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
+  }
+  // -inf in element e where bit e of `allowed` is clear
+  static __device__ __forceinline__ uint4 masked(const uint4& x, uint32_t allowed) {
+    return make_uint4((allowed & 1) ? x.x : 0xFF800000u, (allowed & 2) ? x.y : 0xFF800000u,
+                      (allowed & 4) ? x.z : 0xFF800000u, (allowed & 8) ? x.w : 0xFF800000u);
+  }
 };
+// The same for the 16-bit types: kNegInf twice in a word, packed maxima.
+template <uint32_t kNegInf, typename Max2>
+__device__ __forceinline__ uint4 clean16(const uint4& x, Max2 max2) {
+  return make_uint4(max2(x.x, kNegInf), max2(x.y, kNegInf), max2(x.z, kNegInf), max2(x.w, kNegInf));
+}
+template <uint32_t kNegInf>
+__device__ __forceinline__ uint4 masked16(const uint4& x, uint32_t allowed) {
+  auto one = [&](uint32_t u, uint32_t bits) {
+    const uint32_t keep = ((bits & 1) ? 0x0000FFFFu : 0u) | ((bits & 2) ? 0xFFFF0000u : 0u);
+    return (u & keep) | (kNegInf & ~keep);
+  };
+  return make_uint4(one(x.x, allowed), one(x.y, allowed >> 2), one(x.z, allowed >> 4), one(x.w, allowed >> 6));
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int kN = 8;
@@ -113,6 +173,14 @@ struct Vec<__nv_bfloat16> {
     return make_uint4(u[0], u[1], u[2], u[3]);
   }
   static __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ uint4 clean(const uint4& x) { return clean16<0xFF80FF80u>(x, max_bf16x2); }
+  static __device__ __forceinline__ uint4 masked(const uint4& x, uint32_t allowed) {
+    return masked16<0xFF80FF80u>(x, allowed);
+  }
+  static __device__ __forceinline__ float max_of(const uint4& x) {
+    const uint32_t m = max_bf16x2(max_bf16x2(x.x, x.y), max_bf16x2(x.z, x.w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
 };
 template <>
 struct Vec<__half> {
@@ -136,6 +204,15 @@ struct Vec<__half> {
     return make_uint4(u[0], u[1], u[2], u[3]);
   }
   static __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+  static __device__ __forceinline__ uint4 clean(const uint4& x) { return clean16<0xFC00FC00u>(x, max_f16x2); }
+  static __device__ __forceinline__ uint4 masked(const uint4& x, uint32_t allowed) {
+    return masked16<0xFC00FC00u>(x, allowed);
+  }
+  static __device__ __forceinline__ float max_of(const uint4& x) {
+    const uint32_t m = max_f16x2(max_f16x2(x.x, x.y), max_f16x2(x.z, x.w));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    return fmaxf(f.x, f.y);
+  }
 };
 
 // ---------------------------------------------------------------------------
@@ -185,18 +262,33 @@ struct Kept {
   int id_cut;
 };
 
+// A listed token: its key (z, id) as in device_common.cuh, and its weight.
+struct __align__(16) Listed {
+  unsigned long long key;
+  unsigned long long w;
+};
+
 struct Shared {
   // read by the other CTAs of the cluster
-  uint32_t slot_u32[2][4];
+  uint32_t slot_u32[2];
   unsigned long long slot_u64[2];
-  uint32_t hist[2][2][kBins];  // [level parity][high, low part or count][bin]
+  uint32_t list_hist[kListBins];
+  uint32_t list_n;
+  int list_ok;
+  union {
+    uint32_t hist[2][2][kBins];            // [level parity][high, low part or count][bin]
+    unsigned long long part[kListCap];     // this CTA's part of the list: keys
+  };
   // this CTA's own
+  Listed list[kListCap];
   uint32_t scratch_u32[kWarps];
   unsigned long long scratch_u64[kWarps];
   unsigned long long warp_mass[kWarps];
   unsigned long long bin_scan[kBins / 32];
   unsigned long long found_above;
+  unsigned long long winner_w;
   int found_bin;
+  uint32_t count;
 };
 
 // One row's slice in one CTA.
@@ -228,10 +320,13 @@ class RowSampler {
     lane_ = tid_ & 31;
     warp_ = tid_ >> 5;
     parity_ = 0;
+    for (int b = tid_; b < kListBins; b += kThreads) sh_.list_hist[b] = 0;
+    if (tid_ == 0) sh_.list_n = 0;
     load(data);
   }
 
-  __device__ void run();
+  // True: no CTA but the first has anything left to do or to be read.
+  __device__ bool run();
 
  private:
   const Params& p_;
@@ -241,12 +336,9 @@ class RowSampler {
   int parity_;
   Slice<T> s_;
   float zm_, c_;
+  float lane_max_;  // of this lane's logits
 
   __device__ void load(uint4* data);
-  __device__ void sync_next() {
-    cluster_sync();
-    parity_ ^= 1;
-  }
   // max / min / sum over the cluster (every thread gets the result)
   __device__ uint32_t reduce_max_u32(uint32_t v);
   __device__ unsigned long long reduce_sum_u64(unsigned long long v, unsigned long long* before);
@@ -258,6 +350,14 @@ class RowSampler {
   __device__ void threshold(bool by_mass, unsigned long long target, Kept* k);
   __device__ void draw(const Kept& k);
   __device__ void greedy();
+  __device__ unsigned long long block_sum_u64(unsigned long long v);
+  __device__ bool from_list(int top_k, float top_p, float min_t, unsigned long long* mass);
+  __device__ void draw_from_list(int n, int top_k, unsigned long long need, float min_t);
+  __device__ void write(int id, float z, unsigned long long total);
+  __device__ int list_bin(float z) const {
+    const float t = tempered(z, zm_, c_);
+    return t >= kMinT ? min(static_cast<int>(__fmul_rn(t, (kListBins - 1) / kMinT)), kListBins - 1) : kListBins;
+  }
 };
 
 // Copies this CTA's slice into shared memory: -inf stands for tokens that are
@@ -279,22 +379,42 @@ __device__ void RowSampler<T>::load(uint4* data) {
   s_.lane = lane_;
   const uint32_t* mask =
       p_.f.allowed_mask ? p_.f.allowed_mask + static_cast<int64_t>(row_) * p_.f.mask_words : nullptr;
-  for (int i = lane_; i < s_.n; i += 32) {
-    const int id = s_.id0 + i * kN;
-    float z[kN];
-    if (id >= 0 && id + kN <= p_.V) {
-      Vec<T>::widen(__ldg(base + v0 + i), z);
-    } else {
+  lane_max_ = -INFINITY;
+  for (int i0 = lane_; i0 < s_.n; i0 += 32 * kUnroll) {
+    uint4 x[kUnroll];
+    uint32_t allowed[kUnroll];
 #pragma unroll
-      for (int e = 0; e < kN; ++e)
-        z[e] = (id + e >= 0 && id + e < p_.V) ? Vec<T>::to_float(row[id + e]) : -INFINITY;
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + 32 * u;
+      const int id = s_.id0 + i * kN;
+      allowed[u] = 0xFFFFFFFFu;
+      if (i >= s_.n) continue;
+      if (id >= 0 && id + kN <= p_.V) {
+        x[u] = __ldg(base + v0 + i);
+        if (mask) {
+          const int w = id >> 5;
+          allowed[u] = __funnelshift_r(mask[w], (id & 31) + kN > 32 ? mask[w + 1] : 0u, id & 31);
+        }
+      } else {  // the row's first or last vector
+        float z[kN];
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+          const int v = id + e;
+          z[e] = -INFINITY;
+          if (v >= 0 && v < p_.V && (!mask || ((mask[v >> 5] >> (v & 31)) & 1u))) z[e] = Vec<T>::to_float(row[v]);
+        }
+        x[u] = Vec<T>::narrow(z);
+      }
     }
 #pragma unroll
-    for (int e = 0; e < kN; ++e) {
-      if (z[e] != z[e]) z[e] = -INFINITY;
-      if (mask && id + e >= 0 && id + e < p_.V && !((mask[(id + e) >> 5] >> ((id + e) & 31)) & 1u)) z[e] = -INFINITY;
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + 32 * u;
+      if (i >= s_.n) continue;
+      if (mask) x[u] = Vec<T>::masked(x[u], allowed[u]);
+      x[u] = Vec<T>::clean(x[u]);
+      lane_max_ = fmaxf(lane_max_, Vec<T>::max_of(x[u]));
+      s_.data[i] = x[u];
     }
-    s_.data[i] = Vec<T>::narrow(z);
   }
 }
 
@@ -305,11 +425,11 @@ __device__ uint32_t RowSampler<T>::reduce_max_u32(uint32_t v) {
   __syncthreads();
   if (warp_ == 0) {
     const uint32_t m = __reduce_max_sync(0xffffffffu, lane_ < kWarps ? sh_.scratch_u32[lane_] : 0u);
-    if (lane_ == 0) sh_.slot_u32[parity_][0] = m;
+    if (lane_ == 0) sh_.slot_u32[parity_] = m;
   }
   cluster_sync();
   uint32_t m = 0;
-  for (uint32_t r = 0; r < size_; ++r) m = max(m, ld_cluster_u32(cluster_addr(&sh_.slot_u32[parity_][0], r)));
+  for (uint32_t r = 0; r < size_; ++r) m = max(m, ld_cluster_u32(cluster_addr(&sh_.slot_u32[parity_], r)));
   parity_ ^= 1;
   return m;
 }
@@ -505,16 +625,184 @@ __device__ void RowSampler<T>::threshold(bool by_mass, unsigned long long target
   k->id_cut = static_cast<int>(f) - 1;
 }
 
+template <typename T>
+__device__ void RowSampler<T>::write(int id, float z, unsigned long long total) {
+  p_.ids[row_] = id;
+  if (p_.logprobs) {
+    const float k32 = __fmul_rn(__ll2float_rn(static_cast<long long>(total)), 2.3283064365386963e-10f);  // 2^-32
+    p_.logprobs[row_] = __fsub_rn(__fmul_rn(tempered(z, zm_, c_), 0.6931471805599453f), logf(k32));
+  }
+}
+
+// The point of a draw: floor(u * total), below total.
+__device__ __forceinline__ unsigned long long draw_point(float uniform, unsigned long long total) {
+  const float u = fminf(fmaxf(uniform, 0.0f), 0.99999994f);
+  const unsigned long long r = static_cast<unsigned long long>(
+      floor(__dmul_rn(static_cast<double>(u), static_cast<double>(static_cast<long long>(total)))));
+  return r < total ? r : total - 1;
+}
+
+// Sum over this CTA of every thread's value.
+template <typename T>
+__device__ unsigned long long RowSampler<T>::block_sum_u64(unsigned long long v) {
+  v = static_cast<unsigned long long>(warp_sum_i64(static_cast<long long>(v)));
+  __syncthreads();
+  if (lane_ == 0) sh_.scratch_u64[warp_] = v;
+  __syncthreads();
+  return static_cast<unsigned long long>(
+      warp_sum_i64(lane_ < kWarps ? static_cast<long long>(sh_.scratch_u64[lane_]) : 0));
+}
+
+// Draws from a list, if one can be made: true when the row is done.  With top-p alone
+// *mass becomes the row's mass.
+template <typename T>
+__device__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, unsigned long long* mass) {
+  const unsigned target = top_k > 0 ? top_k : kListTargetTopP;
+  const int my_bin = list_bin(lane_max_);
+  if (my_bin < kListBins) atomicAdd(&sh_.list_hist[my_bin], 1u);
+  unsigned long long before;
+  if (top_k == 0) {
+    *mass = reduce_sum_u64(warp_kept_mass(Kept{-INFINITY, -INFINITY, INT32_MAX}), &before);
+  } else {
+    cluster_sync();
+  }
+  // The last bin that is listed: the first at which the lanes' maxima reach the target.
+  static_assert(kListBins <= kThreads, "one bin per thread");
+  uint32_t n = 0;
+  if (tid_ < kListBins)
+    for (uint32_t r = 0; r < size_; ++r) n += ld_cluster_u32(cluster_addr(&sh_.list_hist[tid_], r));
+  uint32_t incl = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane_ >= o) incl += t;
+  }
+  if (lane_ == 31) sh_.scratch_u32[warp_] = incl;
+  if (tid_ == 0) sh_.found_bin = kListBins - 1;
+  __syncthreads();
+  for (int w = 0; w < warp_; ++w) incl += sh_.scratch_u32[w];
+  if (incl >= target && incl - n < target) sh_.found_bin = tid_;
+  __syncthreads();
+  const int last_bin = sh_.found_bin;
+  if (my_bin <= last_bin) {
+    for_each_vector(s_, [&](const float(&z)[kN], int id) {
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (list_bin(z[e]) <= last_bin) {
+          const uint32_t at = atomicAdd(&sh_.list_n, 1u);
+          if (at < kListCap) sh_.part[at] = make_key(z[e], id + e);
+        }
+    });
+  }
+  cluster_sync();
+  // The first CTA fetches the parts and says whether they will do.
+  unsigned long long need = 0;
+  int total = 0;
+  if (rank_ == 0) {
+    bool ok = true;
+    for (uint32_t r = 0; r < size_; ++r) {
+      const uint32_t m = ld_cluster_u32(cluster_addr(&sh_.list_n, r));
+      if (m > kListCap || total + m > kListCap) {
+        ok = false;
+        break;
+      }
+      for (uint32_t i = tid_; i < m; i += kThreads) {
+        const unsigned long long key = ld_cluster_u64(cluster_addr(&sh_.part[i], r));
+        sh_.list[total + i] =
+            Listed{key, static_cast<unsigned long long>(weight_of(tempered(key_value(key), zm_, c_)))};
+      }
+      total += m;
+    }
+    if (ok && top_k == 0) {
+      const double x = ceil(__dmul_rn(static_cast<double>(top_p), static_cast<double>(static_cast<long long>(*mass))));
+      need = x >= 1.0 ? static_cast<unsigned long long>(x) : 1ull;
+      unsigned long long have = 0;
+      __syncthreads();
+      for (int i = tid_; i < total; i += kThreads) have += sh_.list[i].w;
+      ok = block_sum_u64(have) >= need;
+    }
+    if (tid_ == 0) sh_.list_ok = ok;
+  }
+  cluster_sync();
+  const bool ok = ld_cluster_u32(cluster_addr(&sh_.list_ok, 0)) != 0;
+  if (ok && rank_ == 0) draw_from_list(total, top_k, need, min_t);
+  return ok;
+}
+
+// The draw from the first CTA's list of n tokens.  top_k > 0: `need` is worked out here.
+template <typename T>
+__device__ void RowSampler<T>::draw_from_list(int n, int top_k, unsigned long long need, float min_t) {
+  const float top_p = p_.f.top_p ? p_.f.top_p[row_] : 1.0f;
+  constexpr int kGroup = 8;  // threads per token
+  static_assert(kListCap <= kThreads, "one thread per listed token at the end");
+  const int sub = tid_ % kGroup;
+  if (tid_ == 0) sh_.count = 0;
+  __syncthreads();
+  // every token's rank (bits 48..) and the mass before it in the order (below 2^48)
+  for (int i0 = 0; i0 < n; i0 += kThreads / kGroup) {
+    const int i = i0 + tid_ / kGroup;
+    unsigned long long above = 0;
+    if (i < n) {
+      const unsigned long long key = sh_.list[i].key;
+      for (int j = sub; j < n; j += kGroup) {
+        const Listed o = sh_.list[j];
+        if (o.key > key) above += o.w + (1ull << 48);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < kGroup; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+    if (i < n && sub == 0) sh_.part[i] = above;
+  }
+  __syncthreads();
+  Listed mine{0, 0};
+  int rank = 0;
+  unsigned long long above = 0;
+  if (tid_ < n) {
+    mine = sh_.list[tid_];
+    rank = static_cast<int>(sh_.part[tid_] >> 48);
+    above = sh_.part[tid_] & 0xFFFFFFFFFFFFull;
+  }
+  if (top_k > 0) {
+    const unsigned long long mass = block_sum_u64(rank < top_k ? mine.w : 0);
+    need = mass;
+    if (top_p < 1.0f) {
+      const double x = ceil(__dmul_rn(static_cast<double>(top_p), static_cast<double>(static_cast<long long>(mass))));
+      need = x >= 1.0 ? static_cast<unsigned long long>(x) : 1ull;
+    }
+  }
+  // the kept ones, closed up (their order does not matter), and their mass
+  const bool keep = mine.w > 0 && above < need && (top_k == 0 || rank < top_k) &&
+                    tempered(key_value(mine.key), zm_, c_) >= min_t;
+  const unsigned long long kept = block_sum_u64(keep ? mine.w : 0);  // (and every thread has read the list)
+  if (keep) sh_.list[atomicAdd(&sh_.count, 1u)] = mine;
+  __syncthreads();
+  const int m = static_cast<int>(sh_.count);
+  const unsigned long long r = draw_point(p_.uniforms[row_], kept);
+  for (int i0 = 0; i0 < m; i0 += kThreads / kGroup) {
+    const int i = i0 + tid_ / kGroup;
+    unsigned long long before = 0;
+    Listed it{0, 0};
+    if (i < m) {
+      it = sh_.list[i];
+      for (int j = sub; j < m; j += kGroup) {
+        const Listed o = sh_.list[j];
+        // ids are complemented in the keys' low words
+        if (static_cast<uint32_t>(o.key) > static_cast<uint32_t>(it.key)) before += o.w;
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < kGroup; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    if (i < m && sub == 0 && before <= r && r < before + it.w) write(key_id(it.key), key_value(it.key), kept);
+  }
+}
+
 // The token at the given point of the kept tokens' mass, in id order.
 template <typename T>
 __device__ void RowSampler<T>::draw(const Kept& k) {
   const unsigned long long mine = warp_kept_mass(k);
   unsigned long long before = 0;
   const unsigned long long total = reduce_sum_u64(mine, &before);
-  const float u = fminf(fmaxf(p_.uniforms[row_], 0.0f), 0.99999994f);
-  unsigned long long r = static_cast<unsigned long long>(
-      floor(__dmul_rn(static_cast<double>(u), static_cast<double>(static_cast<long long>(total)))));
-  if (r > total - 1) r = total - 1;
+  const unsigned long long r = draw_point(p_.uniforms[row_], total);
   for (int w = 0; w < warp_; ++w) before += sh_.warp_mass[w];
   if (r < before || r >= before + mine) return;
   unsigned long long left = r - before;  // mass to pass within this warp's vectors
@@ -553,11 +841,7 @@ __device__ void RowSampler<T>::draw(const Kept& k) {
           }
           at += w[e];
         }
-        p_.ids[row_] = id;
-        if (p_.logprobs) {
-          const float k32 = __fmul_rn(__ll2float_rn(static_cast<long long>(total)), 2.3283064365386963e-10f);
-          p_.logprobs[row_] = __fsub_rn(__fmul_rn(tempered(zs, zm_, c_), 0.6931471805599453f), logf(k32));
-        }
+        write(id, zs, total);
       }
       return;
     }
@@ -583,20 +867,15 @@ __device__ void RowSampler<T>::greedy() {
 }
 
 template <typename T>
-__device__ void RowSampler<T>::run() {
-  float m = -INFINITY;
-  for_each_vector(s_, [&](const float(&z)[kN], int) {
-#pragma unroll
-    for (int e = 0; e < kN; ++e) m = fmaxf(m, z[e]);
-  });
-  zm_ = ord_f32(reduce_max_u32(f32_ord(m)));
+__device__ bool RowSampler<T>::run() {
+  zm_ = ord_f32(reduce_max_u32(f32_ord(lane_max_)));
   if (zm_ == -INFINITY) {
     if (rank_ == 0 && tid_ == 0) {
       p_.ids[row_] = -1;
       if (p_.logprobs) p_.logprobs[row_] = __int_as_float(0x7FC00000);
       set_status(p_.dev_status, LMH_DS_NO_ALLOWED_TOKEN);
     }
-    return;
+    return false;
   }
   if (zm_ == INFINITY) {  // only the +inf tokens are left, as equals
     for (int i = lane_; i < s_.n; i += 32) {
@@ -607,38 +886,51 @@ __device__ void RowSampler<T>::run() {
       s_.data[i] = Vec<T>::narrow(z);
     }
     zm_ = 0.0f;
+    lane_max_ = lane_max_ == INFINITY ? 0.0f : -INFINITY;
   }
   const float T_row = p_.f.temperature ? p_.f.temperature[row_] : 1.0f;
   if (!(T_row > 0.0f)) {
     greedy();
-    return;
+    return false;
   }
   c_ = fminf(fmaxf(__fmul_rn(__frcp_rn(T_row), kLog2e), 1.1754944e-38f), 3.402823466e+38f);
 
   Kept k{-INFINITY, -INFINITY, INT32_MAX};
-  const int top_k = p_.f.top_k ? p_.f.top_k[row_] : 0;
+  int top_k = p_.f.top_k ? p_.f.top_k[row_] : 0;
+  if (top_k < 0 || top_k >= p_.V) top_k = 0;
   const float top_p = p_.f.top_p ? p_.f.top_p[row_] : 1.0f;
   const float min_p = p_.f.min_p ? p_.f.min_p[row_] : 0.0f;
-  if (top_k > 0 && top_k < p_.V) threshold(false, static_cast<unsigned long long>(top_k), &k);
+  const float min_t = min_p > 0.0f ? fminf(log2f(min_p), 0.0f) : -INFINITY;
+  unsigned long long mass = 0;
+  bool have_mass = false;
+  if (top_k > 0 ? top_k <= kListTarget : top_p < 1.0f) {
+    if (from_list(top_k, top_p, min_t, &mass)) return true;
+    have_mass = top_k == 0;
+  }
+  if (top_k > 0) threshold(false, static_cast<unsigned long long>(top_k), &k);
   if (top_p < 1.0f) {
     unsigned long long before;
-    const unsigned long long mass = reduce_sum_u64(warp_kept_mass(k), &before);
+    if (!have_mass) mass = reduce_sum_u64(warp_kept_mass(k), &before);
     const double need = ceil(__dmul_rn(static_cast<double>(top_p), static_cast<double>(static_cast<long long>(mass))));
     threshold(true, need >= 1.0 ? static_cast<unsigned long long>(need) : 1ull, &k);
   }
-  if (min_p > 0.0f) k.min_t = fminf(log2f(min_p), 0.0f);
+  k.min_t = min_t;
   draw(k);
+  return false;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_logits_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(Params p) {
   extern __shared__ uint4 data[];
   __shared__ Shared sh;
   pdl_wait();
   pdl_launch_dependents();
   RowSampler<T> s(p, sh, data, static_cast<int>(blockIdx.x / cluster_size()));
-  s.run();
-  cluster_sync();  // no CTA leaves while another may still read its shared memory
+  const bool first_only = s.run();
+  // No CTA leaves while another may still read its shared memory; after a draw from a
+  // list the others need not wait for the first, and make room for the next row.
+  cluster_arrive();
+  if (!first_only || cluster_rank() == 0) cluster_wait();
 }
 
 template <typename T>
