@@ -24,8 +24,11 @@
 //   listed tokens have the mass that is asked for.
 // - A threshold (z, id) otherwise: every token with a larger logit is kept, and those
 //   equal to it up to that id.  It is the last token of the prefix of the order (z
-//   descending, id ascending) that reaches a count (top-k) or a mass (top-p), and is
-//   found by histograms of all logits over ever smaller intervals of z.
+//   descending, id ascending) that reaches a count (top-k) or a mass (top-p): a
+//   histogram of all logits over t, one of the bin that holds the end over its 512th
+//   parts, and a list of what is left there.  Where that is too long (many equal
+//   logits), histograms over ever smaller intervals of z go on until one value is left,
+//   whose tokens are counted off in id order.
 // Tokens of weight 0 (t < -33) can be left out of either: no draw falls on them and no
 // sum changes.
 #include <cmath>
@@ -43,8 +46,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 256;             // of a threshold search
-constexpr int kListBins = 512;         // of the lanes' maxima
+constexpr int kBins = 512;             // of every histogram: one per thread
 constexpr int kListCap = 512;          // tokens in a list, and in one CTA's part of it
 constexpr int kListTarget = 384;       // largest k that is tried with a list
 constexpr int kListTargetTopP = 128;   // tokens asked for with top-p alone
@@ -272,21 +274,22 @@ struct Shared {
   // read by the other CTAs of the cluster
   uint32_t slot_u32[2];
   unsigned long long slot_u64[2];
-  uint32_t list_hist[kListBins];
+  uint32_t list_hist[kBins];
   uint32_t list_n;
   int list_ok;
+  unsigned long long list_key;
   union {
     uint32_t hist[2][2][kBins];            // [level parity][high, low part or count][bin]
-    unsigned long long part[kListCap];     // this CTA's part of the list: keys
+    struct {
+      unsigned long long part[kListCap];   // this CTA's part of a list: keys (over hist[0])
+      Listed list[kListCap];               // the first CTA's list (over hist[1])
+    };
   };
   // this CTA's own
-  Listed list[kListCap];
   uint32_t scratch_u32[kWarps];
   unsigned long long scratch_u64[kWarps];
   unsigned long long warp_mass[kWarps];
-  unsigned long long bin_scan[kBins / 32];
   unsigned long long found_above;
-  unsigned long long winner_w;
   int found_bin;
   uint32_t count;
 };
@@ -320,8 +323,14 @@ class RowSampler {
     lane_ = tid_ & 31;
     warp_ = tid_ >> 5;
     parity_ = 0;
-    for (int b = tid_; b < kListBins; b += kThreads) sh_.list_hist[b] = 0;
+    for (int b = tid_; b < kBins; b += kThreads) sh_.list_hist[b] = 0;
     if (tid_ == 0) sh_.list_n = 0;
+    // (in flight while the row is loaded)
+    temperature_ = p.f.temperature ? __ldg(p.f.temperature + row) : 1.0f;
+    top_k_ = p.f.top_k ? __ldg(p.f.top_k + row) : 0;
+    top_p_ = p.f.top_p ? __ldg(p.f.top_p + row) : 1.0f;
+    min_p_ = p.f.min_p ? __ldg(p.f.min_p + row) : 0.0f;
+    uniform_ = __ldg(p.uniforms + row);
     load(data);
   }
 
@@ -337,16 +346,25 @@ class RowSampler {
   Slice<T> s_;
   float zm_, c_;
   float lane_max_;  // of this lane's logits
+  float temperature_, top_p_, min_p_, uniform_;
+  int top_k_;
 
   __device__ void load(uint4* data);
   // max / min / sum over the cluster (every thread gets the result)
   __device__ uint32_t reduce_max_u32(uint32_t v);
   __device__ unsigned long long reduce_sum_u64(unsigned long long v, unsigned long long* before);
-  __device__ float weight_p(float z) const { return ex2_approx(tempered(z, zm_, c_)); }
   __device__ bool is_kept(float z, int id, const Kept& k) const {
     return tempered(z, zm_, c_) >= k.min_t && (z > k.z_cut || (z == k.z_cut && id <= k.id_cut));
   }
+  enum { kAll, kMinTOnly, kThreshold };
+  template <int kCase>
+  __device__ unsigned long long warp_mass_case(const Kept& k);
   __device__ unsigned long long warp_kept_mass(const Kept& k);
+  __device__ int find_bin(const uint32_t (*hist)[kBins], bool by_mass, unsigned long long target,
+                          unsigned long long* above);
+  __device__ void count_into(uint32_t (*hist)[kBins], int bin, bool by_mass, float z);
+  __device__ int fetch_list();
+  __device__ unsigned long long rank_list(int n);
   __device__ void threshold(bool by_mass, unsigned long long target, Kept* k);
   __device__ void draw(const Kept& k);
   __device__ void greedy();
@@ -354,10 +372,13 @@ class RowSampler {
   __device__ bool from_list(int top_k, float top_p, float min_t, unsigned long long* mass);
   __device__ void draw_from_list(int n, int top_k, unsigned long long need, float min_t);
   __device__ void write(int id, float z, unsigned long long total);
-  __device__ int list_bin(float z) const {
+  // Place of z on the scale of t = 0 .. kMinT, cut into kBins parts (kBins and more:
+  // no weight), and its part.
+  __device__ float list_place(float z) const {
     const float t = tempered(z, zm_, c_);
-    return t >= kMinT ? min(static_cast<int>(__fmul_rn(t, (kListBins - 1) / kMinT)), kListBins - 1) : kListBins;
+    return t >= kMinT ? __fmul_rn(t, (kBins - 1) / kMinT) : kBins;
   }
+  __device__ int list_bin(float z) const { return static_cast<int>(list_place(z)); }
 };
 
 // Copies this CTA's slice into shared memory: -inf stands for tokens that are
@@ -457,101 +478,236 @@ __device__ unsigned long long RowSampler<T>::reduce_sum_u64(unsigned long long v
   return all;
 }
 
+// Sum of the weights of this warp's kept tokens.  Two logits an instruction where the
+// arithmetic allows; the three cases differ in what has to be compared.
 template <typename T>
-__device__ unsigned long long RowSampler<T>::warp_kept_mass(const Kept& k) {
+template <int kCase>
+__device__ unsigned long long RowSampler<T>::warp_mass_case(const Kept& k) {
   uint32_t hi = 0, lo = 0, n = 0;
-  for_each_vector(s_, [&](const float(&z)[kN], int id) {
+  const float2 zm2 = make_float2(-zm_, -zm_), c2 = make_float2(c_, c_);
+  const float2 minus = make_float2(-1.0f, -1.0f), add_hi = make_float2(kHiAdd, kHiAdd),
+               sub_hi = make_float2(-kHiAdd, -kHiAdd), add_lo = make_float2(kLoAdd, kLoAdd);
+#pragma unroll 2
+  for (int i = lane_; i < s_.n; i += 32) {
+    float z[kN];
+    Vec<T>::widen(s_.data[i], z);
+    const int id = s_.id0 + i * kN;
 #pragma unroll
-    for (int e = 0; e < kN; ++e) {
-      uint32_t h, l;
-      weight_bits(is_kept(z[e], id + e, k) ? weight_p(z[e]) : 0.0f, h, l);
-      hi += h;
-      lo += l;
+    for (int e = 0; e < kN; e += 2) {
+      const float2 t = __fmul2_rn(__fadd2_rn(make_float2(z[e], z[e + 1]), zm2), c2);
+      float2 w = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+      if (kCase >= kMinTOnly) {
+        if (!(t.x >= k.min_t)) w.x = 0.0f;
+        if (!(t.y >= k.min_t)) w.y = 0.0f;
+      }
+      if (kCase == kThreshold) {
+        if (!(z[e] > k.z_cut || (z[e] == k.z_cut && id + e <= k.id_cut))) w.x = 0.0f;
+        if (!(z[e + 1] > k.z_cut || (z[e + 1] == k.z_cut && id + e + 1 <= k.id_cut))) w.y = 0.0f;
+      }
+      // weight_bits() of both
+      const float2 h = __fadd2_rn(w, add_hi);
+      const float2 l = __fadd2_rn(__ffma2_rn(__fadd2_rn(h, sub_hi), minus, w), add_lo);
+      hi += __float_as_uint(h.x) + __float_as_uint(h.y);
+      lo += __float_as_uint(l.x) + __float_as_uint(l.y);
     }
     n += kN;
-  });
+  }
   return static_cast<unsigned long long>(warp_sum_i64(weight_sum(hi, lo, n)));
 }
 
+template <typename T>
+__device__ unsigned long long RowSampler<T>::warp_kept_mass(const Kept& k) {
+  if (k.z_cut > -INFINITY) return warp_mass_case<kThreshold>(k);
+  return k.min_t > -INFINITY ? warp_mass_case<kMinTOnly>(k) : warp_mass_case<kAll>(k);
+}
+
+// The bin of the cluster's histograms at which `above` and the bins' counts (or
+// masses) first reach the target, or -1; *above grows by the bins before it.  For all
+// threads of all CTAs, each CTA for itself.
+template <typename T>
+__device__ int RowSampler<T>::find_bin(const uint32_t (*hist)[kBins], bool by_mass, unsigned long long target,
+                                       unsigned long long* above) {
+  static_assert(kBins == kThreads, "one bin per thread");
+  unsigned long long mine = 0;
+  for (uint32_t r = 0; r < size_; ++r) {
+    const unsigned long long h = ld_cluster_u32(cluster_addr(&hist[0][tid_], r));
+    mine += by_mass ? (h << 16) + ld_cluster_u32(cluster_addr(&hist[1][tid_], r)) : h;
+  }
+  unsigned long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane_ >= o) incl += t;
+  }
+  if (lane_ == 31) sh_.scratch_u64[warp_] = incl;
+  if (tid_ == 0) sh_.found_bin = -1;
+  __syncthreads();
+  incl += *above;
+  for (int w = 0; w < warp_; ++w) incl += sh_.scratch_u64[w];
+  if (incl >= target && incl - mine < target) {
+    sh_.found_bin = tid_;
+    sh_.found_above = incl - mine;
+  }
+  __syncthreads();
+  if (sh_.found_bin >= 0) *above = sh_.found_above;
+  return sh_.found_bin;
+}
+
+template <typename T>
+__device__ void RowSampler<T>::count_into(uint32_t (*hist)[kBins], int bin, bool by_mass, float z) {
+  if (by_mass) {
+    const unsigned long long w = static_cast<unsigned long long>(weight_of(tempered(z, zm_, c_)));
+    atomicAdd(&hist[0][bin], static_cast<uint32_t>(w >> 16));
+    atomicAdd(&hist[1][bin], static_cast<uint32_t>(w) & 0xFFFFu);
+  } else {
+    atomicAdd(&hist[0][bin], 1u);
+  }
+}
+
+// The first CTA fetches the CTAs' parts of a list: their tokens' number, or -1 if they
+// are too many.  (Part of a longer agreement: a cluster barrier before and after.)
+template <typename T>
+__device__ int RowSampler<T>::fetch_list() {
+  int total = 0;
+  for (uint32_t r = 0; r < size_; ++r) {
+    const uint32_t m = ld_cluster_u32(cluster_addr(&sh_.list_n, r));
+    if (total + m > kListCap) return -1;
+    for (uint32_t i = tid_; i < m; i += kThreads) {
+      const unsigned long long key = ld_cluster_u64(cluster_addr(&sh_.part[i], r));
+      sh_.list[total + i] = Listed{key, static_cast<unsigned long long>(weight_of(tempered(key_value(key), zm_, c_)))};
+    }
+    total += static_cast<int>(m);
+  }
+  return total;
+}
+
+// Every listed token's rank (bits 48..) and the mass before it in the order (below
+// 2^48), by comparing all with all: eight threads per token.  Token i's to its thread i.
+constexpr int kPerToken = 8;
+template <typename T>
+__device__ unsigned long long RowSampler<T>::rank_list(int n) {
+  static_assert(kListCap <= kThreads, "one thread per listed token at the end");
+  const int sub = tid_ % kPerToken;
+  __syncthreads();
+  for (int i0 = 0; i0 < n; i0 += kThreads / kPerToken) {
+    const int i = i0 + tid_ / kPerToken;
+    unsigned long long above = 0;
+    if (i < n) {
+      const unsigned long long key = sh_.list[i].key;
+      for (int j = sub; j < n; j += kPerToken) {
+        const Listed o = sh_.list[j];
+        if (o.key > key) above += o.w + (1ull << 48);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < kPerToken; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+    if (i < n && sub == 0) sh_.part[i] = above;
+  }
+  __syncthreads();
+  return tid_ < n ? sh_.part[tid_] : 0;
+}
+
 // Narrows k->z_cut, k->id_cut to the shortest prefix of the order whose count (or
-// mass) reaches target >= 1.  A target above the row's total leaves k alone.
+// mass) reaches target >= 1.  A target above the total of the tokens with a weight
+// leaves k alone.
 template <typename T>
 __device__ void RowSampler<T>::threshold(bool by_mass, unsigned long long target, Kept* k) {
-  float hi = zm_;                 // the interval of z that holds the threshold: [lo, hi]
-  float lo = -INFINITY;
-  unsigned long long above = 0;   // count or mass of z > hi
-  // lo: the smallest logit above -inf
+  unsigned long long above = 0;  // count or mass of the bins before
+  int bin[2] = {0, 0};
+  // the part of bin bin[0] that z lies in, or kBins
+  auto part_bin = [&](float z) -> int {
+    const float x = list_place(z);
+    return static_cast<int>(x) == bin[0] ? min(static_cast<int>((x - bin[0]) * kBins), kBins - 1) : kBins;
+  };
+#pragma unroll
+  for (int level = 0; level < 2; ++level) {
+    uint32_t(*hist)[kBins] = sh_.hist[level];
+    __syncthreads();
+    hist[0][tid_] = 0;
+    hist[1][tid_] = 0;
+    if (tid_ == 0) sh_.list_n = 0;
+    __syncthreads();
+    for_each_vector(s_, [&](const float(&z)[kN], int) {
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        const int b = level == 0 ? list_bin(z[e]) : part_bin(z[e]);
+        if (b < kBins) count_into(hist, b, by_mass, z[e]);
+      }
+    });
+    cluster_sync();
+    bin[level] = find_bin(hist, by_mass, target, &above);
+    if (bin[level] < 0) return;
+  }
+  for_each_vector(s_, [&](const float(&z)[kN], int id) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e)
+      if (part_bin(z[e]) == bin[1]) {
+        const uint32_t at = atomicAdd(&sh_.list_n, 1u);
+        if (at < kListCap) sh_.part[at] = make_key(z[e], id + e);
+      }
+  });
+  cluster_sync();
+  if (rank_ == 0) {
+    const int n = fetch_list();
+    if (n >= 0) {
+      const unsigned long long r = rank_list(n);
+      if (tid_ < n) {
+        const unsigned long long before = above + (by_mass ? r & 0xFFFFFFFFFFFFull : r >> 48);
+        if (before < target && before + (by_mass ? sh_.list[tid_].w : 1) >= target) sh_.list_key = sh_.list[tid_].key;
+      }
+    }
+    if (tid_ == 0) sh_.list_ok = n >= 0;
+  }
+  cluster_sync();
+  if (ld_cluster_u32(cluster_addr(&sh_.list_ok, 0)) != 0) {
+    const unsigned long long key = ld_cluster_u64(cluster_addr(&sh_.list_key, 0));
+    k->z_cut = key_value(key);
+    k->id_cut = key_id(key);
+    return;
+  }
+  // Too many in one part of a bin: go on with its extremes.
+  float hi, lo;
   {
-    uint32_t m = 0;  // max of the complemented order keys
+    uint32_t top = 0, bottom = 0;  // of the order keys, and of their complements
     for_each_vector(s_, [&](const float(&z)[kN], int) {
 #pragma unroll
       for (int e = 0; e < kN; ++e)
-        if (z[e] > -INFINITY) m = max(m, ~f32_ord(z[e]));
+        if (part_bin(z[e]) == bin[1]) {
+          top = max(top, f32_ord(z[e]));
+          bottom = max(bottom, ~f32_ord(z[e]));
+        }
     });
     __syncthreads();
-    lo = ord_f32(~reduce_max_u32(m));
+    hi = ord_f32(reduce_max_u32(top));
+    __syncthreads();
+    lo = ord_f32(~reduce_max_u32(bottom));
   }
   for (int level = 0; lo < hi; ++level) {
     // Bins over [lo, hi], bin 0 at the top: linear in z first, which spreads a
     // row's logits evenly; linear in the order keys after eight levels or where
-    // the width is no ordinary number (each such level takes 8 bits off the keys).
+    // the width is no ordinary number (each such level takes 9 bits off the keys).
     const float width = __fsub_rn(hi, lo);
     const bool linear = level < 8 && width < 1e30f && width > 1e-30f;
     const float inv = linear ? __fdiv_rn(kBins - 1, width) : 0.0f;
     const uint32_t ord_hi = f32_ord(hi);
-    const int shift = max(0, 32 - __clz(ord_hi - f32_ord(lo)) - 8);
+    const int shift = max(0, 32 - __clz(ord_hi - f32_ord(lo)) - 9);
     auto bin_of = [&](float z) -> int {
       return linear ? min(static_cast<int>(__fmul_rn(__fsub_rn(hi, z), inv)), kBins - 1)
                     : static_cast<int>((ord_hi - f32_ord(z)) >> shift);
     };
     uint32_t(*hist)[kBins] = sh_.hist[parity_];
     __syncthreads();
-    for (int b = tid_; b < 2 * kBins; b += kThreads) (&hist[0][0])[b] = 0;
+    hist[0][tid_] = 0;
+    hist[1][tid_] = 0;
     __syncthreads();
     for_each_vector(s_, [&](const float(&z)[kN], int) {
 #pragma unroll
       for (int e = 0; e < kN; ++e)
-        if (z[e] >= lo && z[e] <= hi) {
-          const int b = bin_of(z[e]);
-          if (by_mass) {
-            const unsigned long long w = static_cast<unsigned long long>(weight_of(tempered(z[e], zm_, c_)));
-            atomicAdd(&hist[0][b], static_cast<uint32_t>(w >> 16));
-            atomicAdd(&hist[1][b], static_cast<uint32_t>(w) & 0xFFFFu);
-          } else {
-            atomicAdd(&hist[0][b], 1u);
-          }
-        }
+        if (z[e] >= lo && z[e] <= hi) count_into(hist, bin_of(z[e]), by_mass, z[e]);
     });
     cluster_sync();
-    // every CTA adds the bins up and finds the one that holds the target
-    unsigned long long mine = 0, incl = 0;
-    if (tid_ < kBins) {
-      for (uint32_t r = 0; r < size_; ++r) {
-        const unsigned long long h = ld_cluster_u32(cluster_addr(&hist[0][tid_], r));
-        mine += by_mass ? (h << 16) + ld_cluster_u32(cluster_addr(&hist[1][tid_], r)) : h;
-      }
-      incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane_ >= o) incl += t;
-      }
-      if (lane_ == 31) sh_.bin_scan[warp_] = incl;
-    }
-    if (tid_ == 0) sh_.found_bin = -1;
-    __syncthreads();
-    if (tid_ < kBins) {
-      unsigned long long b = above;
-      for (int w = 0; w < warp_; ++w) b += sh_.bin_scan[w];
-      if (b + incl >= target && b + incl - mine < target) {
-        sh_.found_bin = tid_;
-        sh_.found_above = b + incl - mine;
-      }
-    }
-    __syncthreads();
-    const int bin = sh_.found_bin;
-    if (bin < 0) return;  // the row has less than the target: all of it is kept
-    above = sh_.found_above;
+    const int bin = find_bin(hist, by_mass, target, &above);
+    if (bin < 0) return;  // (not reached: the target lies in [lo, hi])
     // the bin's own extremes are the next interval
     uint32_t top = 0, bottom = 0;
     for_each_vector(s_, [&](const float(&z)[kN], int) {
@@ -659,7 +815,7 @@ template <typename T>
 __device__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, unsigned long long* mass) {
   const unsigned target = top_k > 0 ? top_k : kListTargetTopP;
   const int my_bin = list_bin(lane_max_);
-  if (my_bin < kListBins) atomicAdd(&sh_.list_hist[my_bin], 1u);
+  if (my_bin < kBins) atomicAdd(&sh_.list_hist[my_bin], 1u);
   unsigned long long before;
   if (top_k == 0) {
     *mass = reduce_sum_u64(warp_kept_mass(Kept{-INFINITY, -INFINITY, INT32_MAX}), &before);
@@ -667,9 +823,9 @@ __device__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, un
     cluster_sync();
   }
   // The last bin that is listed: the first at which the lanes' maxima reach the target.
-  static_assert(kListBins <= kThreads, "one bin per thread");
+  static_assert(kBins <= kThreads, "one bin per thread");
   uint32_t n = 0;
-  if (tid_ < kListBins)
+  if (tid_ < kBins)
     for (uint32_t r = 0; r < size_; ++r) n += ld_cluster_u32(cluster_addr(&sh_.list_hist[tid_], r));
   uint32_t incl = n;
 #pragma unroll
@@ -678,7 +834,7 @@ __device__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, un
     if (lane_ >= o) incl += t;
   }
   if (lane_ == 31) sh_.scratch_u32[warp_] = incl;
-  if (tid_ == 0) sh_.found_bin = kListBins - 1;
+  if (tid_ == 0) sh_.found_bin = kBins - 1;
   __syncthreads();
   for (int w = 0; w < warp_; ++w) incl += sh_.scratch_u32[w];
   if (incl >= target && incl - n < target) sh_.found_bin = tid_;
@@ -699,20 +855,8 @@ __device__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, un
   unsigned long long need = 0;
   int total = 0;
   if (rank_ == 0) {
-    bool ok = true;
-    for (uint32_t r = 0; r < size_; ++r) {
-      const uint32_t m = ld_cluster_u32(cluster_addr(&sh_.list_n, r));
-      if (m > kListCap || total + m > kListCap) {
-        ok = false;
-        break;
-      }
-      for (uint32_t i = tid_; i < m; i += kThreads) {
-        const unsigned long long key = ld_cluster_u64(cluster_addr(&sh_.part[i], r));
-        sh_.list[total + i] =
-            Listed{key, static_cast<unsigned long long>(weight_of(tempered(key_value(key), zm_, c_)))};
-      }
-      total += m;
-    }
+    total = fetch_list();
+    bool ok = total >= 0;
     if (ok && top_k == 0) {
       const double x = ceil(__dmul_rn(static_cast<double>(top_p), static_cast<double>(static_cast<long long>(*mass))));
       need = x >= 1.0 ? static_cast<unsigned long long>(x) : 1ull;
@@ -732,35 +876,16 @@ __device__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, un
 // The draw from the first CTA's list of n tokens.  top_k > 0: `need` is worked out here.
 template <typename T>
 __device__ void RowSampler<T>::draw_from_list(int n, int top_k, unsigned long long need, float min_t) {
-  const float top_p = p_.f.top_p ? p_.f.top_p[row_] : 1.0f;
-  constexpr int kGroup = 8;  // threads per token
-  static_assert(kListCap <= kThreads, "one thread per listed token at the end");
-  const int sub = tid_ % kGroup;
+  const float top_p = top_p_;
   if (tid_ == 0) sh_.count = 0;
-  __syncthreads();
-  // every token's rank (bits 48..) and the mass before it in the order (below 2^48)
-  for (int i0 = 0; i0 < n; i0 += kThreads / kGroup) {
-    const int i = i0 + tid_ / kGroup;
-    unsigned long long above = 0;
-    if (i < n) {
-      const unsigned long long key = sh_.list[i].key;
-      for (int j = sub; j < n; j += kGroup) {
-        const Listed o = sh_.list[j];
-        if (o.key > key) above += o.w + (1ull << 48);
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < kGroup; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
-    if (i < n && sub == 0) sh_.part[i] = above;
-  }
-  __syncthreads();
+  const unsigned long long place = rank_list(n);
   Listed mine{0, 0};
   int rank = 0;
   unsigned long long above = 0;
   if (tid_ < n) {
     mine = sh_.list[tid_];
-    rank = static_cast<int>(sh_.part[tid_] >> 48);
-    above = sh_.part[tid_] & 0xFFFFFFFFFFFFull;
+    rank = static_cast<int>(place >> 48);
+    above = place & 0xFFFFFFFFFFFFull;
   }
   if (top_k > 0) {
     const unsigned long long mass = block_sum_u64(rank < top_k ? mine.w : 0);
@@ -777,21 +902,22 @@ __device__ void RowSampler<T>::draw_from_list(int n, int top_k, unsigned long lo
   if (keep) sh_.list[atomicAdd(&sh_.count, 1u)] = mine;
   __syncthreads();
   const int m = static_cast<int>(sh_.count);
-  const unsigned long long r = draw_point(p_.uniforms[row_], kept);
-  for (int i0 = 0; i0 < m; i0 += kThreads / kGroup) {
-    const int i = i0 + tid_ / kGroup;
+  const unsigned long long r = draw_point(uniform_, kept);
+  const int sub = tid_ % kPerToken;
+  for (int i0 = 0; i0 < m; i0 += kThreads / kPerToken) {
+    const int i = i0 + tid_ / kPerToken;
     unsigned long long before = 0;
     Listed it{0, 0};
     if (i < m) {
       it = sh_.list[i];
-      for (int j = sub; j < m; j += kGroup) {
+      for (int j = sub; j < m; j += kPerToken) {
         const Listed o = sh_.list[j];
         // ids are complemented in the keys' low words
         if (static_cast<uint32_t>(o.key) > static_cast<uint32_t>(it.key)) before += o.w;
       }
     }
 #pragma unroll
-    for (int o = 1; o < kGroup; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    for (int o = 1; o < kPerToken; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     if (i < m && sub == 0 && before <= r && r < before + it.w) write(key_id(it.key), key_value(it.key), kept);
   }
 }
@@ -802,7 +928,7 @@ __device__ void RowSampler<T>::draw(const Kept& k) {
   const unsigned long long mine = warp_kept_mass(k);
   unsigned long long before = 0;
   const unsigned long long total = reduce_sum_u64(mine, &before);
-  const unsigned long long r = draw_point(p_.uniforms[row_], total);
+  const unsigned long long r = draw_point(uniform_, total);
   for (int w = 0; w < warp_; ++w) before += sh_.warp_mass[w];
   if (r < before || r >= before + mine) return;
   unsigned long long left = r - before;  // mass to pass within this warp's vectors
@@ -868,6 +994,8 @@ __device__ void RowSampler<T>::greedy() {
 
 template <typename T>
 __device__ bool RowSampler<T>::run() {
+  int top_k = top_k_;
+  const float T_row = temperature_, min_p = min_p_;
   zm_ = ord_f32(reduce_max_u32(f32_ord(lane_max_)));
   if (zm_ == -INFINITY) {
     if (rank_ == 0 && tid_ == 0) {
@@ -888,7 +1016,6 @@ __device__ bool RowSampler<T>::run() {
     zm_ = 0.0f;
     lane_max_ = lane_max_ == INFINITY ? 0.0f : -INFINITY;
   }
-  const float T_row = p_.f.temperature ? p_.f.temperature[row_] : 1.0f;
   if (!(T_row > 0.0f)) {
     greedy();
     return false;
@@ -896,10 +1023,8 @@ __device__ bool RowSampler<T>::run() {
   c_ = fminf(fmaxf(__fmul_rn(__frcp_rn(T_row), kLog2e), 1.1754944e-38f), 3.402823466e+38f);
 
   Kept k{-INFINITY, -INFINITY, INT32_MAX};
-  int top_k = p_.f.top_k ? p_.f.top_k[row_] : 0;
   if (top_k < 0 || top_k >= p_.V) top_k = 0;
-  const float top_p = p_.f.top_p ? p_.f.top_p[row_] : 1.0f;
-  const float min_p = p_.f.min_p ? p_.f.min_p[row_] : 0.0f;
+  const float top_p = top_p_;
   const float min_t = min_p > 0.0f ? fminf(log2f(min_p), 0.0f) : -INFINITY;
   unsigned long long mass = 0;
   bool have_mass = false;
