@@ -132,6 +132,16 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 // the phase completes and so outlast a limit shorter than its own window.
 constexpr uint64_t kPollLimitNs = 1000000ull;
 
+// Wait for a phase with the given limit (below kPollLimitNs: polled); false when it ran out.
+__device__ __forceinline__ bool mbar_wait_limit(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const bool poll = limit_ns < kPollLimitNs;
+  if (poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!(poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)))
+    if (global_timer_ns() - t0 > limit_ns) return false;
+  return true;
+}
+
 // Wait on an mbarrier unless the CTA has aborted (another thread gave up
 // first); after limit_ns, mark the abort and report LMH_DS_TIMEOUT.  The
 // kernels pass the library's wait limit (2 s unless a test shortened it);

@@ -51,7 +51,7 @@ constexpr int kListCap = 512;          // tokens in a list, and in one CTA's par
 constexpr int kListTarget = 384;       // largest k that is tried with a list
 constexpr int kListTargetTopP = 128;   // tokens asked for with top-p alone
 constexpr float kMinT = -33.0f;        // below: weight 0
-constexpr int kUnroll = 4;             // vectors of a lane in flight while a row is loaded
+constexpr int kUnroll = 4;             // vectors of a lane whose mask words are in flight at once
 constexpr float kHiAdd = 768.0f;             // 1.5 * 2^9: unit 2^-14
 constexpr float kLoAdd = 0.0029296875f;      // 1.5 * 2^-9: unit 2^-32
 constexpr uint32_t kHiBits = 0x44400000u;    // of kHiAdd
@@ -99,6 +99,29 @@ __device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t a) {
   unsigned long long v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
+}
+
+// f(rank, *p in CTA `rank`) for every CTA of the cluster, in rank order; all the loads
+// are in flight before the first is used.
+template <typename F>
+__device__ __forceinline__ void for_each_cta(const uint32_t* p, uint32_t size, F&& f) {
+  uint32_t v[kMaxCluster];
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    if (r < static_cast<int>(size)) v[r] = ld_cluster_u32(cluster_addr(p, r));
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    if (r < static_cast<int>(size)) f(static_cast<uint32_t>(r), v[r]);
+}
+template <typename F>
+__device__ __forceinline__ void for_each_cta(const unsigned long long* p, uint32_t size, F&& f) {
+  unsigned long long v[kMaxCluster];
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    if (r < static_cast<int>(size)) v[r] = ld_cluster_u64(cluster_addr(p, r));
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    if (r < static_cast<int>(size)) f(static_cast<uint32_t>(r), v[r]);
 }
 
 // ---------------------------------------------------------------------------
@@ -246,6 +269,16 @@ __device__ __forceinline__ long long warp_sum_i64(long long v) {
   return v;
 }
 
+__device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
+  return static_cast<unsigned long long>(warp_sum_i64(static_cast<long long>(v)));
+}
+
+// The mass that top-p asks for: max(1, ceil(p * mass)).
+__device__ __forceinline__ unsigned long long mass_wanted(float top_p, unsigned long long mass) {
+  const double x = ceil(__dmul_rn(static_cast<double>(top_p), static_cast<double>(static_cast<long long>(mass))));
+  return x >= 1.0 ? static_cast<unsigned long long>(x) : 1ull;
+}
+
 struct Params {
   const void* logits;
   int64_t row_stride;
@@ -255,6 +288,7 @@ struct Params {
   int32_t* ids;
   float* logprobs;
   uint32_t* dev_status;
+  uint64_t wait_ns;  // limit of the wait for a row's copies
 };
 
 // What is kept: t >= min_t, and z > z_cut or (z == z_cut and id <= id_cut).
@@ -292,6 +326,8 @@ struct Shared {
   unsigned long long found_above;
   int found_bin;
   uint32_t count;
+  unsigned long long kept, point;
+  uint64_t arrived[kWarps];  // barriers: a warp's part of the row is there
 };
 
 // One row's slice in one CTA.
@@ -382,8 +418,8 @@ class RowSampler {
 };
 
 // Copies this CTA's slice into shared memory: -inf stands for tokens that are
-// not allowed, NaN, and the padding of the row's first and last vector.  A lane
-// reads back only what it wrote, so no barrier is needed.
+// not allowed, NaN, and the padding of the row's first and last vector.  A warp works
+// on its own part of the slice alone, and a lane writes only what it reads back itself.
 template <typename T>
 __device__ void RowSampler<T>::load(uint4* data) {
   const T* row = static_cast<const T*>(p_.logits) + static_cast<int64_t>(row_) * p_.row_stride;
@@ -400,23 +436,52 @@ __device__ void RowSampler<T>::load(uint4* data) {
   s_.lane = lane_;
   const uint32_t* mask =
       p_.f.allowed_mask ? p_.f.allowed_mask + static_cast<int64_t>(row_) * p_.f.mask_words : nullptr;
+  // The vectors that lie in the row whole come by one bulk copy per warp, the first and
+  // the last of a row by element.
+  const int whole0 = max(v0, lead > 0 ? 1 : 0), whole1 = min(v1, (lead + p_.V) / kN);
+  const uint32_t bytes = whole1 > whole0 ? static_cast<uint32_t>(whole1 - whole0) * 16u : 0u;
+  uint64_t* arrived = &sh_.arrived[warp_];
+  if (bytes > 0) {
+    if (lane_ == 0) {
+      mbar_init(arrived, 1);
+      mbar_init_fence();
+      mbar_arrive_expect_tx(arrived, bytes);
+      bulk_load(s_.data + (whole0 - v0), base + whole0, bytes, arrived);
+    }
+    __syncwarp();
+  }
   lane_max_ = -INFINITY;
+  bool waited = bytes == 0;
   for (int i0 = lane_; i0 < s_.n; i0 += 32 * kUnroll) {
-    uint4 x[kUnroll];
-    uint32_t allowed[kUnroll];
+    uint32_t allowed[kUnroll];  // the mask's words are in flight beside the logits
+    if (mask) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + 32 * u;
+        const int id = s_.id0 + i * kN, w = id >> 5;
+        allowed[u] = 0xFFFFFFFFu;
+        if (i < s_.n && id >= 0 && id + kN <= p_.V)
+          allowed[u] = __funnelshift_r(mask[w], (id & 31) + kN > 32 ? mask[w + 1] : 0u, id & 31);
+      }
+    }
+    if (!waited) {
+      if (!mbar_wait_limit(arrived, 0, p_.wait_ns)) {
+        set_status(p_.dev_status, LMH_DS_TIMEOUT);
+        mbar_wait(arrived, 0);  // (the copy lands before the CTA may leave)
+      }
+      waited = true;
+    }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int i = i0 + 32 * u;
-      const int id = s_.id0 + i * kN;
-      allowed[u] = 0xFFFFFFFFu;
       if (i >= s_.n) continue;
+      const int id = s_.id0 + i * kN;
+      uint4 x, y;
       if (id >= 0 && id + kN <= p_.V) {
-        x[u] = __ldg(base + v0 + i);
-        if (mask) {
-          const int w = id >> 5;
-          allowed[u] = __funnelshift_r(mask[w], (id & 31) + kN > 32 ? mask[w + 1] : 0u, id & 31);
-        }
-      } else {  // the row's first or last vector
+        x = s_.data[i];
+        y = Vec<T>::clean(mask ? Vec<T>::masked(x, allowed[u]) : x);
+        if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) s_.data[i] = y;
+      } else {
         float z[kN];
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
@@ -424,17 +489,10 @@ __device__ void RowSampler<T>::load(uint4* data) {
           z[e] = -INFINITY;
           if (v >= 0 && v < p_.V && (!mask || ((mask[v >> 5] >> (v & 31)) & 1u))) z[e] = Vec<T>::to_float(row[v]);
         }
-        x[u] = Vec<T>::narrow(z);
+        y = Vec<T>::clean(Vec<T>::narrow(z));
+        s_.data[i] = y;
       }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + 32 * u;
-      if (i >= s_.n) continue;
-      if (mask) x[u] = Vec<T>::masked(x[u], allowed[u]);
-      x[u] = Vec<T>::clean(x[u]);
-      lane_max_ = fmaxf(lane_max_, Vec<T>::max_of(x[u]));
-      s_.data[i] = x[u];
+      lane_max_ = fmaxf(lane_max_, Vec<T>::max_of(y));
     }
   }
 }
@@ -450,7 +508,7 @@ __device__ uint32_t RowSampler<T>::reduce_max_u32(uint32_t v) {
   }
   cluster_sync();
   uint32_t m = 0;
-  for (uint32_t r = 0; r < size_; ++r) m = max(m, ld_cluster_u32(cluster_addr(&sh_.slot_u32[parity_], r)));
+  for_each_cta(&sh_.slot_u32[parity_], size_, [&](uint32_t, uint32_t v) { m = max(m, v); });
   parity_ ^= 1;
   return m;
 }
@@ -468,11 +526,10 @@ __device__ unsigned long long RowSampler<T>::reduce_sum_u64(unsigned long long v
   }
   cluster_sync();
   unsigned long long all = 0, b = 0;
-  for (uint32_t r = 0; r < size_; ++r) {
-    const unsigned long long m = ld_cluster_u64(cluster_addr(&sh_.slot_u64[parity_], r));
+  for_each_cta(&sh_.slot_u64[parity_], size_, [&](uint32_t r, unsigned long long m) {
     if (r < rank_) b += m;
     all += m;
-  }
+  });
   parity_ ^= 1;
   *before = b;
   return all;
@@ -512,7 +569,7 @@ __device__ unsigned long long RowSampler<T>::warp_mass_case(const Kept& k) {
     }
     n += kN;
   }
-  return static_cast<unsigned long long>(warp_sum_i64(weight_sum(hi, lo, n)));
+  return warp_sum_u64(static_cast<unsigned long long>(weight_sum(hi, lo, n)));
 }
 
 template <typename T>
@@ -529,10 +586,10 @@ __device__ int RowSampler<T>::find_bin(const uint32_t (*hist)[kBins], bool by_ma
                                        unsigned long long* above) {
   static_assert(kBins == kThreads, "one bin per thread");
   unsigned long long mine = 0;
-  for (uint32_t r = 0; r < size_; ++r) {
-    const unsigned long long h = ld_cluster_u32(cluster_addr(&hist[0][tid_], r));
-    mine += by_mass ? (h << 16) + ld_cluster_u32(cluster_addr(&hist[1][tid_], r)) : h;
-  }
+  for_each_cta(&hist[0][tid_], size_, [&](uint32_t, uint32_t h) {
+    mine += by_mass ? static_cast<unsigned long long>(h) << 16 : h;
+  });
+  if (by_mass) for_each_cta(&hist[1][tid_], size_, [&](uint32_t, uint32_t h) { mine += h; });
   unsigned long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -568,17 +625,21 @@ __device__ void RowSampler<T>::count_into(uint32_t (*hist)[kBins], int bin, bool
 // are too many.  (Part of a longer agreement: a cluster barrier before and after.)
 template <typename T>
 __device__ int RowSampler<T>::fetch_list() {
-  int total = 0;
-  for (uint32_t r = 0; r < size_; ++r) {
-    const uint32_t m = ld_cluster_u32(cluster_addr(&sh_.list_n, r));
-    if (total + m > kListCap) return -1;
-    for (uint32_t i = tid_; i < m; i += kThreads) {
-      const unsigned long long key = ld_cluster_u64(cluster_addr(&sh_.part[i], r));
-      sh_.list[total + i] = Listed{key, static_cast<unsigned long long>(weight_of(tempered(key_value(key), zm_, c_)))};
+  static_assert(kListCap <= kThreads, "one thread per listed token");
+  uint32_t total = 0, cta = 0, at = 0;  // where this thread's token lies
+  for_each_cta(&sh_.list_n, size_, [&](uint32_t r, uint32_t m) {
+    if (static_cast<uint32_t>(tid_) >= total && static_cast<uint32_t>(tid_) - total < m) {
+      cta = r;
+      at = tid_ - total;
     }
-    total += static_cast<int>(m);
+    total += min(m, kListCap + 1u);
+  });
+  if (total > kListCap) return -1;
+  if (static_cast<uint32_t>(tid_) < total) {
+    const unsigned long long key = ld_cluster_u64(cluster_addr(&sh_.part[at], cta));
+    sh_.list[tid_] = Listed{key, static_cast<unsigned long long>(weight_of(tempered(key_value(key), zm_, c_)))};
   }
-  return total;
+  return static_cast<int>(total);
 }
 
 // Every listed token's rank (bits 48..) and the mass before it in the order (below
@@ -589,8 +650,8 @@ __device__ unsigned long long RowSampler<T>::rank_list(int n) {
   static_assert(kListCap <= kThreads, "one thread per listed token at the end");
   const int sub = tid_ % kPerToken;
   __syncthreads();
-  for (int i0 = 0; i0 < n; i0 += kThreads / kPerToken) {
-    const int i = i0 + tid_ / kPerToken;
+  for (int i0 = warp_ * (32 / kPerToken); i0 < n; i0 += kThreads / kPerToken) {  // (a warp's share is its own)
+    const int i = i0 + lane_ / kPerToken;
     unsigned long long above = 0;
     if (i < n) {
       const unsigned long long key = sh_.list[i].key;
@@ -823,10 +884,8 @@ __device__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, un
     cluster_sync();
   }
   // The last bin that is listed: the first at which the lanes' maxima reach the target.
-  static_assert(kBins <= kThreads, "one bin per thread");
   uint32_t n = 0;
-  if (tid_ < kBins)
-    for (uint32_t r = 0; r < size_; ++r) n += ld_cluster_u32(cluster_addr(&sh_.list_hist[tid_], r));
+  for_each_cta(&sh_.list_hist[tid_], size_, [&](uint32_t, uint32_t h) { n += h; });
   uint32_t incl = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -841,14 +900,18 @@ __device__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, un
   __syncthreads();
   const int last_bin = sh_.found_bin;
   if (my_bin <= last_bin) {
-    for_each_vector(s_, [&](const float(&z)[kN], int id) {
+    for (int i = lane_; i < s_.n; i += 32) {
+      const uint4 x = s_.data[i];
+      if (list_bin(Vec<T>::max_of(x)) > last_bin) continue;
+      float z[kN];
+      Vec<T>::widen(x, z);
 #pragma unroll
       for (int e = 0; e < kN; ++e)
         if (list_bin(z[e]) <= last_bin) {
           const uint32_t at = atomicAdd(&sh_.list_n, 1u);
-          if (at < kListCap) sh_.part[at] = make_key(z[e], id + e);
+          if (at < kListCap) sh_.part[at] = make_key(z[e], s_.id0 + i * kN + e);
         }
-    });
+    }
   }
   cluster_sync();
   // The first CTA fetches the parts and says whether they will do.
@@ -858,8 +921,7 @@ __device__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, un
     total = fetch_list();
     bool ok = total >= 0;
     if (ok && top_k == 0) {
-      const double x = ceil(__dmul_rn(static_cast<double>(top_p), static_cast<double>(static_cast<long long>(*mass))));
-      need = x >= 1.0 ? static_cast<unsigned long long>(x) : 1ull;
+      need = mass_wanted(top_p, *mass);
       unsigned long long have = 0;
       __syncthreads();
       for (int i = tid_; i < total; i += kThreads) have += sh_.list[i].w;
@@ -876,36 +938,49 @@ __device__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, un
 // The draw from the first CTA's list of n tokens.  top_k > 0: `need` is worked out here.
 template <typename T>
 __device__ void RowSampler<T>::draw_from_list(int n, int top_k, unsigned long long need, float min_t) {
-  const float top_p = top_p_;
-  if (tid_ == 0) sh_.count = 0;
-  const unsigned long long place = rank_list(n);
-  Listed mine{0, 0};
-  int rank = 0;
-  unsigned long long above = 0;
-  if (tid_ < n) {
-    mine = sh_.list[tid_];
-    rank = static_cast<int>(place >> 48);
-    above = place & 0xFFFFFFFFFFFFull;
-  }
-  if (top_k > 0) {
-    const unsigned long long mass = block_sum_u64(rank < top_k ? mine.w : 0);
-    need = mass;
-    if (top_p < 1.0f) {
-      const double x = ceil(__dmul_rn(static_cast<double>(top_p), static_cast<double>(static_cast<long long>(mass))));
-      need = x >= 1.0 ? static_cast<unsigned long long>(x) : 1ull;
+  rank_list(n);
+  if (warp_ == 0) {
+    if (top_k > 0) {
+      unsigned long long mass = 0;
+      for (int i = lane_; i < n; i += 32)
+        if (static_cast<int>(sh_.part[i] >> 48) < top_k) mass += sh_.list[i].w;
+      mass = warp_sum_u64(mass);
+      need = top_p_ < 1.0f ? mass_wanted(top_p_, mass) : mass;
+    }
+    // the kept ones, closed up (each to a place at or before its own), and their mass
+    unsigned long long kept = 0;
+    int m = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane_;
+      Listed it{0, 0};
+      bool keep = false;
+      if (i < n) {
+        it = sh_.list[i];
+        const unsigned long long place = sh_.part[i];
+        keep = it.w > 0 && (place & 0xFFFFFFFFFFFFull) < need &&
+               (top_k == 0 || static_cast<int>(place >> 48) < top_k) &&
+               tempered(key_value(it.key), zm_, c_) >= min_t;
+      }
+      const unsigned ones = __ballot_sync(0xffffffffu, keep);  // (every lane has read its token)
+      if (keep) {
+        kept += it.w;
+        sh_.list[m + __popc(ones & ((1u << lane_) - 1u))] = it;
+      }
+      m += __popc(ones);
+    }
+    kept = warp_sum_u64(kept);
+    if (lane_ == 0) {
+      sh_.count = m;
+      sh_.kept = kept;
+      sh_.point = draw_point(uniform_, kept);
     }
   }
-  // the kept ones, closed up (their order does not matter), and their mass
-  const bool keep = mine.w > 0 && above < need && (top_k == 0 || rank < top_k) &&
-                    tempered(key_value(mine.key), zm_, c_) >= min_t;
-  const unsigned long long kept = block_sum_u64(keep ? mine.w : 0);  // (and every thread has read the list)
-  if (keep) sh_.list[atomicAdd(&sh_.count, 1u)] = mine;
   __syncthreads();
   const int m = static_cast<int>(sh_.count);
-  const unsigned long long r = draw_point(uniform_, kept);
+  const unsigned long long r = sh_.point;
   const int sub = tid_ % kPerToken;
-  for (int i0 = 0; i0 < m; i0 += kThreads / kPerToken) {
-    const int i = i0 + tid_ / kPerToken;
+  for (int i0 = warp_ * (32 / kPerToken); i0 < m; i0 += kThreads / kPerToken) {
+    const int i = i0 + lane_ / kPerToken;
     unsigned long long before = 0;
     Listed it{0, 0};
     if (i < m) {
@@ -918,7 +993,7 @@ __device__ void RowSampler<T>::draw_from_list(int n, int top_k, unsigned long lo
     }
 #pragma unroll
     for (int o = 1; o < kPerToken; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-    if (i < m && sub == 0 && before <= r && r < before + it.w) write(key_id(it.key), key_value(it.key), kept);
+    if (i < m && sub == 0 && before <= r && r < before + it.w) write(key_id(it.key), key_value(it.key), sh_.kept);
   }
 }
 
@@ -1036,8 +1111,7 @@ __device__ bool RowSampler<T>::run() {
   if (top_p < 1.0f) {
     unsigned long long before;
     if (!have_mass) mass = reduce_sum_u64(warp_kept_mass(k), &before);
-    const double need = ceil(__dmul_rn(static_cast<double>(top_p), static_cast<double>(static_cast<long long>(mass))));
-    threshold(true, need >= 1.0 ? static_cast<unsigned long long>(need) : 1ull, &k);
+    threshold(true, mass_wanted(top_p, mass), &k);
   }
   k.min_t = min_t;
   draw(k);
@@ -1107,7 +1181,7 @@ cudaError_t sample_logits_setup() {
 cudaError_t launch_sample_logits(const void* logits, lmh_dtype dtype, int rows, int V, int64_t row_stride,
                                  const lmh_filters& f, const float* uniforms, int32_t* ids, float* logprobs,
                                  uint32_t* dev_status, int num_sms, cudaStream_t stream) {
-  const Params p{logits, row_stride, rows, V, f, uniforms, ids, logprobs, dev_status};
+  const Params p{logits, row_stride, rows, V, f, uniforms, ids, logprobs, dev_status, wait_limit_ns()};
   if (dtype == LMH_F32) return launch<float>(p, num_sms, stream);
   if (dtype == LMH_BF16) return launch<__nv_bfloat16>(p, num_sms, stream);
   return launch<__half>(p, num_sms, stream);
