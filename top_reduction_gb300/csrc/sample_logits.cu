@@ -3,8 +3,8 @@
 //
 // A row belongs to a thread-block cluster.  Its CTAs hold the row in their
 // shared memory (a contiguous slice of the ids each), so HBM is read once and
-// every later pass -- the maximum, the sum of the weights, the searches for the
-// top-k and top-p thresholds, the draw -- runs on chip.
+// every later pass -- the sum of the weights, the searches for the top-k and
+// top-p thresholds, the draw -- runs on chip.
 //
 // Weights are whole numbers, w = rint(2^32 exp2(t)) with t = (z - max) * c: their
 // sums are the same in any order, so neither the split over threads, warps and
@@ -31,6 +31,12 @@
 //   whose tokens are counted off in id order.
 // Tokens of weight 0 (t < -33) can be left out of either: no draw falls on them and no
 // sum changes.
+//
+// A row's work is a chain of short steps, each run once by a CTA, so instructions come
+// from far away more often than not: written out for every element of a vector in every
+// pass, the kernel had 300 KB of them and spent most of its time fetching them.  Only
+// the passes over all logits are unrolled; the steps of the searches take one element
+// per lane, and what does not depend on the logits' type is a function of its own.
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -57,6 +63,8 @@ constexpr float kLoAdd = 0.0029296875f;      // 1.5 * 2^-9: unit 2^-32
 constexpr uint32_t kHiBits = 0x44400000u;    // of kHiAdd
 constexpr uint32_t kLoBits = 0x3B400000u;    // of kLoAdd
 constexpr int kHiShift = 18;                 // 2^-14 in units of 2^-32
+
+using u64 = unsigned long long;
 
 // ---------------------------------------------------------------------------
 // clusters
@@ -90,45 +98,25 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
+__device__ __forceinline__ void st_cluster_u64(uint32_t a, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t a) {
-  unsigned long long v;
+__device__ __forceinline__ u64 ld_cluster_u64(uint32_t a) {
+  u64 v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
-}
-
-// f(rank, *p in CTA `rank`) for every CTA of the cluster, in rank order; all the loads
-// are in flight before the first is used.
-template <typename F>
-__device__ __forceinline__ void for_each_cta(const uint32_t* p, uint32_t size, F&& f) {
-  uint32_t v[kMaxCluster];
-#pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r)
-    if (r < static_cast<int>(size)) v[r] = ld_cluster_u32(cluster_addr(p, r));
-#pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r)
-    if (r < static_cast<int>(size)) f(static_cast<uint32_t>(r), v[r]);
-}
-template <typename F>
-__device__ __forceinline__ void for_each_cta(const unsigned long long* p, uint32_t size, F&& f) {
-  unsigned long long v[kMaxCluster];
-#pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r)
-    if (r < static_cast<int>(size)) v[r] = ld_cluster_u64(cluster_addr(p, r));
-#pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r)
-    if (r < static_cast<int>(size)) f(static_cast<uint32_t>(r), v[r]);
 }
 
 // ---------------------------------------------------------------------------
 // logits in 16-byte vectors
 // ---------------------------------------------------------------------------
 template <typename T>
-struct Vec;  // kN elements a vector; widen and narrow are exact
+struct Vec;  // kN elements a vector; to_float and widen are exact
 template <>
 struct Vec<float> {
   static constexpr int kN = 4;
@@ -138,10 +126,8 @@ struct Vec<float> {
     z[2] = __uint_as_float(x.z);
     z[3] = __uint_as_float(x.w);
   }
-  static __device__ __forceinline__ uint4 narrow(const float (&z)[4]) {
-    return make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3]));
-  }
   static __device__ __forceinline__ float to_float(float x) { return x; }
+  static __device__ __forceinline__ float from_float(float x) { return x; }
   // NaN becomes -inf
   static __device__ __forceinline__ uint4 clean(const uint4& x) {
     auto f = [](uint32_t u) { return __float_as_uint(fmaxf(__uint_as_float(u), -INFINITY)); };
@@ -190,14 +176,8 @@ struct Vec<__nv_bfloat16> {
       z[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
     }
   }
-  static __device__ __forceinline__ uint4 narrow(const float (&z)[8]) {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      u[i] = (__float_as_uint(z[2 * i]) >> 16) | (__float_as_uint(z[2 * i + 1]) & 0xFFFF0000u);
-    return make_uint4(u[0], u[1], u[2], u[3]);
-  }
   static __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
   static __device__ __forceinline__ uint4 clean(const uint4& x) { return clean16<0xFF80FF80u>(x, max_bf16x2); }
   static __device__ __forceinline__ uint4 masked(const uint4& x, uint32_t allowed) {
     return masked16<0xFF80FF80u>(x, allowed);
@@ -219,16 +199,8 @@ struct Vec<__half> {
       z[2 * i + 1] = f.y;
     }
   }
-  static __device__ __forceinline__ uint4 narrow(const float (&z)[8]) {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 h = __floats2half2_rn(z[2 * i], z[2 * i + 1]);
-      u[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(u[0], u[1], u[2], u[3]);
-  }
   static __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+  static __device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
   static __device__ __forceinline__ uint4 clean(const uint4& x) { return clean16<0xFC00FC00u>(x, max_f16x2); }
   static __device__ __forceinline__ uint4 masked(const uint4& x, uint32_t allowed) {
     return masked16<0xFC00FC00u>(x, allowed);
@@ -253,30 +225,33 @@ __device__ __forceinline__ void weight_bits(float p, uint32_t& hi, uint32_t& lo)
   lo = __float_as_uint(__fadd_rn(rest, kLoAdd));
 }
 // Sum of n weights from the sums (mod 2^32) of their parts; n < 2^14.
-__device__ __forceinline__ long long weight_sum(uint32_t hi, uint32_t lo, uint32_t n) {
+__device__ __forceinline__ u64 weight_sum(uint32_t hi, uint32_t lo, uint32_t n) {
   const long long h = static_cast<int32_t>(hi - n * kHiBits), l = static_cast<int32_t>(lo - n * kLoBits);
-  return (h << kHiShift) + l;
+  return static_cast<u64>((h << kHiShift) + l);
 }
-__device__ __forceinline__ long long weight_of(float t) {
+__device__ __forceinline__ u64 weight_of(float t) {
   uint32_t hi, lo;
   weight_bits(ex2_approx(t), hi, lo);
   return weight_sum(hi, lo, 1);
 }
 
-__device__ __forceinline__ long long warp_sum_i64(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// f * mass for 0 < f < 1 and mass < 2^53, rounded to fp64, then down or up to a whole
+// number.
+__device__ __noinline__ u64 fp64_product(float f, u64 mass, bool up) {
+  const double x = __dmul_rn(static_cast<double>(f), static_cast<double>(static_cast<long long>(mass)));
+  return up ? __double2ull_ru(x) : __double2ull_rd(x);
 }
 
-__device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
-  return static_cast<unsigned long long>(warp_sum_i64(static_cast<long long>(v)));
+// The mass that top-p asks for: max(1, ceil(p * mass)), p < 1.
+__device__ __forceinline__ u64 mass_wanted(float top_p, u64 mass) {
+  return top_p > 0.0f ? max(1ull, fp64_product(top_p, mass, true)) : 1ull;
 }
 
-// The mass that top-p asks for: max(1, ceil(p * mass)).
-__device__ __forceinline__ unsigned long long mass_wanted(float top_p, unsigned long long mass) {
-  const double x = ceil(__dmul_rn(static_cast<double>(top_p), static_cast<double>(static_cast<long long>(mass))));
-  return x >= 1.0 ? static_cast<unsigned long long>(x) : 1ull;
+// The point of a draw: floor(u * total), below total.
+__device__ __forceinline__ u64 draw_point(float uniform, u64 total) {
+  const float u = fminf(fmaxf(uniform, 0.0f), 0.99999994f);
+  const u64 r = fp64_product(u, total, false);
+  return r < total ? r : total - 1;
 }
 
 struct Params {
@@ -300,167 +275,429 @@ struct Kept {
 
 // A listed token: its key (z, id) as in device_common.cuh, and its weight.
 struct __align__(16) Listed {
-  unsigned long long key;
-  unsigned long long w;
+  u64 key;
+  u64 w;
 };
 
 struct Shared {
-  // read by the other CTAs of the cluster
-  uint32_t slot_u32[2];
-  unsigned long long slot_u64[2];
+  // read or written by the other CTAs of the cluster
+  u64 slot[2][kMaxCluster];  // of a reduction: each CTA's value
   uint32_t list_hist[kBins];
   uint32_t list_n;
   int list_ok;
-  unsigned long long list_key;
+  u64 list_key;
   union {
-    uint32_t hist[2][2][kBins];            // [level parity][high, low part or count][bin]
+    uint32_t hist[2][2][kBins];  // [which][high, low part or count][bin]
     struct {
-      unsigned long long part[kListCap];   // this CTA's part of a list: keys (over hist[0])
-      Listed list[kListCap];               // the first CTA's list (over hist[1])
+      u64 part[kListCap];        // this CTA's part of a list: keys (over hist[0])
+      Listed list[kListCap];     // the first CTA's list (over hist[1])
     };
   };
   // this CTA's own
-  uint32_t scratch_u32[kWarps];
-  unsigned long long scratch_u64[kWarps];
-  unsigned long long warp_mass[kWarps];
-  unsigned long long found_above;
+  u64 scratch[kWarps];
+  u64 warp_mass[kWarps];
+  u64 found_above;
   int found_bin;
-  uint32_t count;
-  unsigned long long kept, point;
+  int count;
+  u64 kept, point;
   uint64_t arrived[kWarps];  // barriers: a warp's part of the row is there
 };
 
-// One row's slice in one CTA.
-template <typename T>
-struct Slice {
-  uint4* data;        // this warp's vectors: data[i], i = lane, lane + 32, ...
-  int n;              // vectors of this warp
-  int id0;            // id of element 0 of data[0] (may be below 0 in a row's first vector)
-  int lane;
-};
+__shared__ Shared sh;
+extern __shared__ uint4 row_data[];
 
-template <typename T, typename F>
-__device__ __forceinline__ void for_each_vector(const Slice<T>& s, F&& f) {
-  for (int i = s.lane; i < s.n; i += 32) {
-    float z[Vec<T>::kN];
-    Vec<T>::widen(s.data[i], z);
-    f(z, s.id0 + i * Vec<T>::kN);
+// ---------------------------------------------------------------------------
+// steps that do not depend on the logits' type
+// ---------------------------------------------------------------------------
+__device__ __noinline__ u64 warp_sum_u64(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Inclusive sum over a warp's lanes.
+__device__ __noinline__ u64 warp_scan_u64(u64 v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
+
+// Sum over this CTA of every thread's value.
+__device__ __noinline__ u64 block_sum_u64(u64 v) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_sum_u64(v);
+  __syncthreads();
+  if (lane == 0) sh.scratch[warp] = v;
+  __syncthreads();
+  return warp_sum_u64(lane < kWarps ? sh.scratch[lane] : 0);
+}
+
+// The reductions over the cluster: one warp gives this CTA's value to every CTA, so
+// that behind the barrier each reads its own shared memory.  `parity` alternates from
+// one reduction to the next.
+__device__ __noinline__ uint32_t cluster_max(uint32_t v, int parity) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int size = static_cast<int>(cluster_size());
+  v = __reduce_max_sync(0xffffffffu, v);
+  __syncthreads();
+  if (lane == 0) sh.scratch[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, lane < kWarps ? static_cast<uint32_t>(sh.scratch[lane]) : 0u);
+    if (lane < size) st_cluster_u64(cluster_addr(&sh.slot[parity][cluster_rank()], lane), m);
+  }
+  cluster_sync();
+  return __reduce_max_sync(0xffffffffu, lane < size ? static_cast<uint32_t>(sh.slot[parity][lane]) : 0u);
+}
+
+// Sum over the cluster of one value per warp (the same in its lanes), and the sum over
+// the CTAs before this one.  Leaves the warps' values in sh.warp_mass.
+struct Sum {
+  u64 all, before;
+};
+__device__ __noinline__ Sum cluster_sum(u64 v, int parity) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  __syncthreads();
+  if (lane == 0) sh.warp_mass[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    const u64 m = warp_sum_u64(lane < kWarps ? sh.warp_mass[lane] : 0);
+    if (lane < size) st_cluster_u64(cluster_addr(&sh.slot[parity][rank], lane), m);
+  }
+  cluster_sync();
+  Sum s{0, 0};
+  for (int r = 0; r < size; ++r) {
+    const u64 m = sh.slot[parity][r];
+    s.all += m;
+    if (r < rank) s.before += m;
+  }
+  return s;
+}
+
+// This thread's bin, summed over the cluster's CTAs: hist0 counts, or with hist1 the high
+// and low parts of masses.
+__device__ __noinline__ u64 gather_bin(const uint32_t* hist0, const uint32_t* hist1) {
+  const int size = static_cast<int>(cluster_size());
+  uint32_t a[kMaxCluster], b[kMaxCluster];
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) {  // (all loads in flight before the first is used)
+    a[r] = b[r] = 0;
+    if (r < size) {
+      a[r] = ld_cluster_u32(cluster_addr(hist0 + threadIdx.x, r));
+      if (hist1) b[r] = ld_cluster_u32(cluster_addr(hist1 + threadIdx.x, r));
+    }
+  }
+  u64 s = 0;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) s += hist1 ? (static_cast<u64>(a[r]) << 16) + b[r] : a[r];
+  return s;
+}
+
+// The bin at which `above` and the bins' sums (one per thread, `mine`) first reach the
+// target, or -1; its sum from the bins before it is in sh.found_above.
+__device__ __noinline__ int find_bin(u64 mine, u64 target, u64 above) {
+  static_assert(kBins == kThreads, "one bin per thread");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u64 incl = warp_scan_u64(mine);
+  __syncthreads();
+  if (lane == 31) sh.scratch[warp] = incl;
+  if (threadIdx.x == 0) sh.found_bin = -1;
+  __syncthreads();
+  incl += above;
+#pragma unroll 1
+  for (int w = 0; w < warp; ++w) incl += sh.scratch[w];
+  if (incl >= target && incl - mine < target) {
+    sh.found_bin = threadIdx.x;
+    sh.found_above = incl - mine;
+  }
+  __syncthreads();
+  return sh.found_bin;
+}
+
+// The first CTA fetches the CTAs' parts of a list: their tokens' number, or -1 if they
+// are too many.  (Part of a longer agreement: a cluster barrier before and after.)
+__device__ __noinline__ int fetch_list(float zm, float c) {
+  static_assert(kListCap <= kThreads, "one thread per listed token");
+  const int size = static_cast<int>(cluster_size()), tid = threadIdx.x;
+  uint32_t n[kMaxCluster];
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) n[r] = r < size ? ld_cluster_u32(cluster_addr(&sh.list_n, r)) : 0;
+  int total = 0, cta = 0, at = 0;  // where this thread's token lies
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) {
+    const int m = static_cast<int>(min(n[r], kListCap + 1u));
+    if (tid >= total && tid - total < m) {
+      cta = r;
+      at = tid - total;
+    }
+    total += m;
+  }
+  if (total > kListCap) return -1;
+  if (tid < total) {
+    const u64 key = ld_cluster_u64(cluster_addr(&sh.part[at], cta));
+    sh.list[tid] = Listed{key, weight_of(tempered(key_value(key), zm, c))};
+  }
+  return total;
+}
+
+// Every listed token's rank (bits 48..) and the mass before it in the order (below
+// 2^48) into sh.part, by comparing all with all, eight threads per token.
+constexpr int kPerToken = 8;
+__device__ __noinline__ void rank_list(int n) {
+  const int lane = threadIdx.x & 31, sub = lane % kPerToken;
+  __syncthreads();
+#pragma unroll 1
+  for (int i0 = (threadIdx.x >> 5) * (32 / kPerToken); i0 < n; i0 += kThreads / kPerToken) {  // (a warp's own share)
+    const int i = i0 + lane / kPerToken;
+    u64 above = 0;
+    if (i < n) {
+      const u64 key = sh.list[i].key;
+#pragma unroll 4
+      for (int j = sub; j < n; j += kPerToken) {
+        const Listed o = sh.list[j];
+        if (o.key > key) above += o.w + (1ull << 48);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < kPerToken; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+    if (i < n && sub == 0) sh.part[i] = above;
+  }
+  __syncthreads();
+}
+
+__device__ __noinline__ void write_token(const Params& p, int row, int id, float t, u64 total) {
+  p.ids[row] = id;
+  if (p.logprobs) {
+    const float k32 = __fmul_rn(__ll2float_rn(static_cast<long long>(total)), 2.3283064365386963e-10f);  // 2^-32
+    p.logprobs[row] = __fsub_rn(__fmul_rn(t, 0.6931471805599453f), logf(k32));
   }
 }
 
+// The draw from the first CTA's list of n tokens.  top_k > 0: the mass that is wanted is
+// worked out here, else it is `need`.
+__device__ __noinline__ void draw_from_list(const Params& p, int row, int n, int top_k, float top_p, u64 need,
+                                            float min_t, float uniform, float zm, float c) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  rank_list(n);
+  if (warp == 0) {
+    if (top_k > 0) {
+      u64 mass = 0;
+#pragma unroll 1
+      for (int i = lane; i < n; i += 32)
+        if (static_cast<int>(sh.part[i] >> 48) < top_k) mass += sh.list[i].w;
+      mass = warp_sum_u64(mass);
+      need = top_p < 1.0f ? mass_wanted(top_p, mass) : mass;
+    }
+    // the kept ones, closed up (each to a place at or before its own), and their mass
+    u64 kept = 0;
+    int m = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      Listed it{0, 0};
+      bool keep = false;
+      if (i < n) {
+        it = sh.list[i];
+        const u64 place = sh.part[i];
+        keep = it.w > 0 && (place & 0xFFFFFFFFFFFFull) < need &&
+               (top_k == 0 || static_cast<int>(place >> 48) < top_k) && tempered(key_value(it.key), zm, c) >= min_t;
+      }
+      const unsigned ones = __ballot_sync(0xffffffffu, keep);  // (every lane has read its token)
+      if (keep) {
+        kept += it.w;
+        sh.list[m + __popc(ones & ((1u << lane) - 1u))] = it;
+      }
+      m += __popc(ones);
+    }
+    kept = warp_sum_u64(kept);
+    const u64 r = draw_point(uniform, kept);
+    if (lane == 0) {
+      sh.count = m;
+      sh.kept = kept;
+      sh.point = r;
+    }
+  }
+  __syncthreads();
+  const int m = sh.count;
+  const u64 r = sh.point;
+  const int sub = lane % kPerToken;
+#pragma unroll 1
+  for (int i0 = warp * (32 / kPerToken); i0 < m; i0 += kThreads / kPerToken) {
+    const int i = i0 + lane / kPerToken;
+    u64 before = 0;
+    Listed it{0, 0};
+    if (i < m) {
+      it = sh.list[i];
+#pragma unroll 4
+      for (int j = sub; j < m; j += kPerToken) {
+        const Listed o = sh.list[j];
+        // ids are complemented in the keys' low words
+        if (static_cast<uint32_t>(o.key) > static_cast<uint32_t>(it.key)) before += o.w;
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < kPerToken; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    if (i < m && sub == 0 && before <= r && r < before + it.w)
+      write_token(p, row, key_id(it.key), tempered(key_value(it.key), zm, c), sh.kept);
+  }
+}
+
+// Adds a logit to a histogram: its weight in two parts, or a count.
+__device__ __forceinline__ void count_into(uint32_t (*hist)[kBins], int bin, bool by_mass, float t) {
+  if (by_mass) {
+    const u64 w = weight_of(t);
+    atomicAdd(&hist[0][bin], static_cast<uint32_t>(w >> 16));
+    atomicAdd(&hist[1][bin], static_cast<uint32_t>(w) & 0xFFFFu);
+  } else {
+    atomicAdd(&hist[0][bin], 1u);
+  }
+}
+
+__device__ __forceinline__ void clear_hist(uint32_t (*hist)[kBins]) {
+  __syncthreads();
+  hist[0][threadIdx.x] = 0;
+  hist[1][threadIdx.x] = 0;
+  if (threadIdx.x == 0) sh.list_n = 0;
+  __syncthreads();
+}
+
+// ---------------------------------------------------------------------------
+// one row
+// ---------------------------------------------------------------------------
 template <typename T>
 class RowSampler {
  public:
   static constexpr int kN = Vec<T>::kN;
 
-  __device__ RowSampler(const Params& p, Shared& sh, uint4* data, int row)
-      : p_(p), sh_(sh), row_(row), rank_(cluster_rank()), size_(cluster_size()) {
-    tid_ = threadIdx.x;
-    lane_ = tid_ & 31;
-    warp_ = tid_ >> 5;
+  __device__ __forceinline__ RowSampler(const Params& p, int row) : p_(p), row_(row) {
+    lane_ = threadIdx.x & 31;
+    warp_ = threadIdx.x >> 5;
     parity_ = 0;
-    for (int b = tid_; b < kBins; b += kThreads) sh_.list_hist[b] = 0;
-    if (tid_ == 0) sh_.list_n = 0;
+    cluster_arrive();  // (waited for before the first word goes to another CTA)
+    sh.list_hist[threadIdx.x] = 0;
+    if (threadIdx.x == 0) sh.list_n = 0;
     // (in flight while the row is loaded)
     temperature_ = p.f.temperature ? __ldg(p.f.temperature + row) : 1.0f;
     top_k_ = p.f.top_k ? __ldg(p.f.top_k + row) : 0;
     top_p_ = p.f.top_p ? __ldg(p.f.top_p + row) : 1.0f;
     min_p_ = p.f.min_p ? __ldg(p.f.min_p + row) : 0.0f;
     uniform_ = __ldg(p.uniforms + row);
-    load(data);
+    load();
   }
 
   // True: no CTA but the first has anything left to do or to be read.
-  __device__ bool run();
+  __device__ __forceinline__ bool run();
 
  private:
   const Params& p_;
-  Shared& sh_;
-  int row_, tid_, lane_, warp_;
-  uint32_t rank_, size_;
-  int parity_;
-  Slice<T> s_;
+  int row_, lane_, warp_, parity_;
+  // this warp's part of the row: n_ vectors from data_, id0_ the id of their first element
+  // (below 0 in a row's first vector)
+  uint4* data_;
+  int n_, id0_;
   float zm_, c_;
   float lane_max_;  // of this lane's logits
   float temperature_, top_p_, min_p_, uniform_;
   int top_k_;
 
-  __device__ void load(uint4* data);
-  // max / min / sum over the cluster (every thread gets the result)
-  __device__ uint32_t reduce_max_u32(uint32_t v);
-  __device__ unsigned long long reduce_sum_u64(unsigned long long v, unsigned long long* before);
-  __device__ bool is_kept(float z, int id, const Kept& k) const {
-    return tempered(z, zm_, c_) >= k.min_t && (z > k.z_cut || (z == k.z_cut && id <= k.id_cut));
+  __device__ __forceinline__ void load();
+  __device__ __forceinline__ float element(int j) const { return Vec<T>::to_float(reinterpret_cast<const T*>(data_)[j]); }
+  __device__ __forceinline__ float t_of(float z) const { return tempered(z, zm_, c_); }
+  __device__ __forceinline__ uint32_t max_over(uint32_t v) {
+    parity_ ^= 1;
+    return cluster_max(v, parity_);
   }
-  enum { kAll, kMinTOnly, kThreshold };
-  template <int kCase>
-  __device__ unsigned long long warp_mass_case(const Kept& k);
-  __device__ unsigned long long warp_kept_mass(const Kept& k);
-  __device__ int find_bin(const uint32_t (*hist)[kBins], bool by_mass, unsigned long long target,
-                          unsigned long long* above);
-  __device__ void count_into(uint32_t (*hist)[kBins], int bin, bool by_mass, float z);
-  __device__ int fetch_list();
-  __device__ unsigned long long rank_list(int n);
-  __device__ void threshold(bool by_mass, unsigned long long target, Kept* k);
-  __device__ void draw(const Kept& k);
-  __device__ void greedy();
-  __device__ unsigned long long block_sum_u64(unsigned long long v);
-  __device__ bool from_list(int top_k, float top_p, float min_t, unsigned long long* mass);
-  __device__ void draw_from_list(int n, int top_k, unsigned long long need, float min_t);
-  __device__ void write(int id, float z, unsigned long long total);
-  // Place of z on the scale of t = 0 .. kMinT, cut into kBins parts (kBins and more:
-  // no weight), and its part.
-  __device__ float list_place(float z) const {
-    const float t = tempered(z, zm_, c_);
+  __device__ __forceinline__ Sum sum_over(u64 v) {
+    parity_ ^= 1;
+    return cluster_sum(v, parity_);
+  }
+  __device__ __forceinline__ bool is_kept(float z, int id, const Kept& k) const {
+    return t_of(z) >= k.min_t && (z > k.z_cut || (z == k.z_cut && id <= k.id_cut));
+  }
+  template <bool kEvery>
+  __device__ __forceinline__ u64 warp_mass(const Kept& k);
+  __device__ __forceinline__ void threshold(bool by_mass, u64 target, Kept* k);
+  __device__ __forceinline__ void draw(const Kept& k);
+  __device__ __forceinline__ void greedy();
+  __device__ __forceinline__ bool from_list(int top_k, float top_p, float min_t, u64* mass);
+  // Place of t on the scale of 0 .. kMinT, cut into kBins bins (kBins: no weight).
+  __device__ __forceinline__ float place(float t) const {
     return t >= kMinT ? __fmul_rn(t, (kBins - 1) / kMinT) : kBins;
   }
-  __device__ int list_bin(float z) const { return static_cast<int>(list_place(z)); }
+  // f(z, j) for this warp's elements j, one per lane at a time
+  template <typename F>
+  __device__ __forceinline__ void for_each_element(F&& f) const {
+    const int m = n_ * kN;
+#pragma unroll 2
+    for (int j = lane_; j < m; j += 32) f(element(j), j);
+  }
 };
 
 // Copies this CTA's slice into shared memory: -inf stands for tokens that are
 // not allowed, NaN, and the padding of the row's first and last vector.  A warp works
-// on its own part of the slice alone, and a lane writes only what it reads back itself.
+// on its own part of the slice alone.
 template <typename T>
-__device__ void RowSampler<T>::load(uint4* data) {
+__device__ __forceinline__ void RowSampler<T>::load() {
+  const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const T* row = static_cast<const T*>(p_.logits) + static_cast<int64_t>(row_) * p_.row_stride;
   const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % kN);  // elements before the row
   const uint4* base = reinterpret_cast<const uint4*>(row - lead);
   const int nvec = (lead + p_.V + kN - 1) / kN;
-  const int per_cta = (nvec + static_cast<int>(size_) - 1) / static_cast<int>(size_);
-  const int cta0 = min(static_cast<int>(rank_) * per_cta, nvec), cta1 = min(cta0 + per_cta, nvec);
+  const int per_cta = (nvec + size - 1) / size;
+  const int cta0 = min(rank * per_cta, nvec), cta1 = min(cta0 + per_cta, nvec);
   const int per_warp = (cta1 - cta0 + kWarps - 1) / kWarps;
   const int v0 = min(cta0 + warp_ * per_warp, cta1), v1 = min(v0 + per_warp, cta1);
-  s_.data = data + (v0 - cta0);
-  s_.n = v1 - v0;
-  s_.id0 = v0 * kN - lead;
-  s_.lane = lane_;
+  data_ = row_data + (v0 - cta0);
+  n_ = v1 - v0;
+  id0_ = v0 * kN - lead;
   const uint32_t* mask =
       p_.f.allowed_mask ? p_.f.allowed_mask + static_cast<int64_t>(row_) * p_.f.mask_words : nullptr;
-  // The vectors that lie in the row whole come by one bulk copy per warp, the first and
-  // the last of a row by element.
-  const int whole0 = max(v0, lead > 0 ? 1 : 0), whole1 = min(v1, (lead + p_.V) / kN);
-  const uint32_t bytes = whole1 > whole0 ? static_cast<uint32_t>(whole1 - whole0) * 16u : 0u;
-  uint64_t* arrived = &sh_.arrived[warp_];
-  if (bytes > 0) {
+  // The vectors that lie in the row whole, [w0, w1) of this warp's, come by one bulk copy,
+  // the first and the last of a row by element.
+  const int w0 = lead > 0 && v0 == 0 ? 1 : 0, w1 = min(v1, (lead + p_.V) / kN) - v0;
+  uint64_t* arrived = &sh.arrived[warp_];
+  if (w1 > w0) {
     if (lane_ == 0) {
+      const uint32_t bytes = static_cast<uint32_t>(w1 - w0) * 16u;
       mbar_init(arrived, 1);
       mbar_init_fence();
       mbar_arrive_expect_tx(arrived, bytes);
-      bulk_load(s_.data + (whole0 - v0), base + whole0, bytes, arrived);
+      bulk_load(data_ + w0, base + v0 + w0, bytes, arrived);
     }
     __syncwarp();
   }
+  auto by_element = [&](int j) {
+    const int v = id0_ + j;
+    float z = -INFINITY;
+    if (v >= 0 && v < p_.V && (!mask || ((mask[v >> 5] >> (v & 31)) & 1u))) z = Vec<T>::to_float(row[v]);
+    reinterpret_cast<T*>(data_)[j] = Vec<T>::from_float(fmaxf(z, -INFINITY));  // (NaN becomes -inf)
+  };
+  const int after = max(w0, w1);  // vectors [w0, after) are whole, at most two are not
+  if (lane_ < w0 * kN) by_element(lane_);
+  if (after * kN + lane_ < n_ * kN) by_element(after * kN + lane_);
+  __syncwarp();
+  // A lane's maximum is that of its vectors: lane_, lane_ + 32, ...
   lane_max_ = -INFINITY;
-  bool waited = bytes == 0;
-  for (int i0 = lane_; i0 < s_.n; i0 += 32 * kUnroll) {
+  if (lane_ < w0) lane_max_ = Vec<T>::max_of(data_[lane_]);
+#pragma unroll 1
+  for (int i = after; i < n_; ++i)
+    if (i % 32 == lane_) lane_max_ = fmaxf(lane_max_, Vec<T>::max_of(data_[i]));
+  if (w1 <= w0) return;
+  bool waited = false;
+#pragma unroll 1
+  for (int i0 = lane_; i0 < w1; i0 += 32 * kUnroll) {
     uint32_t allowed[kUnroll];  // the mask's words are in flight beside the logits
     if (mask) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + 32 * u;
-        const int id = s_.id0 + i * kN, w = id >> 5;
-        allowed[u] = 0xFFFFFFFFu;
-        if (i < s_.n && id >= 0 && id + kN <= p_.V)
+        const int id = id0_ + (i0 + 32 * u) * kN, w = id >> 5;
+        allowed[u] = 0;
+        if (i0 + 32 * u >= w0 && i0 + 32 * u < w1)
           allowed[u] = __funnelshift_r(mask[w], (id & 31) + kN > 32 ? mask[w + 1] : 0u, id & 31);
       }
     }
@@ -474,92 +711,37 @@ __device__ void RowSampler<T>::load(uint4* data) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int i = i0 + 32 * u;
-      if (i >= s_.n) continue;
-      const int id = s_.id0 + i * kN;
-      uint4 x, y;
-      if (id >= 0 && id + kN <= p_.V) {
-        x = s_.data[i];
-        y = Vec<T>::clean(mask ? Vec<T>::masked(x, allowed[u]) : x);
-        if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) s_.data[i] = y;
-      } else {
-        float z[kN];
-#pragma unroll
-        for (int e = 0; e < kN; ++e) {
-          const int v = id + e;
-          z[e] = -INFINITY;
-          if (v >= 0 && v < p_.V && (!mask || ((mask[v >> 5] >> (v & 31)) & 1u))) z[e] = Vec<T>::to_float(row[v]);
-        }
-        y = Vec<T>::clean(Vec<T>::narrow(z));
-        s_.data[i] = y;
-      }
+      if (i < w0 || i >= w1) continue;
+      const uint4 x = data_[i];
+      const uint4 y = Vec<T>::clean(mask ? Vec<T>::masked(x, allowed[u]) : x);
+      if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) data_[i] = y;
       lane_max_ = fmaxf(lane_max_, Vec<T>::max_of(y));
     }
   }
+  __syncwarp();
 }
 
+// Sum of the weights of this warp's kept tokens (kEvery: of all), two logits an
+// instruction where the arithmetic allows.
 template <typename T>
-__device__ uint32_t RowSampler<T>::reduce_max_u32(uint32_t v) {
-  v = __reduce_max_sync(0xffffffffu, v);
-  if (lane_ == 0) sh_.scratch_u32[warp_] = v;
-  __syncthreads();
-  if (warp_ == 0) {
-    const uint32_t m = __reduce_max_sync(0xffffffffu, lane_ < kWarps ? sh_.scratch_u32[lane_] : 0u);
-    if (lane_ == 0) sh_.slot_u32[parity_] = m;
-  }
-  cluster_sync();
-  uint32_t m = 0;
-  for_each_cta(&sh_.slot_u32[parity_], size_, [&](uint32_t, uint32_t v) { m = max(m, v); });
-  parity_ ^= 1;
-  return m;
-}
-
-// Sum over the cluster of one value per warp (lane 0's); *before: the sum over
-// the CTAs of lower rank.  Leaves the warps' values in sh_.warp_mass.
-template <typename T>
-__device__ unsigned long long RowSampler<T>::reduce_sum_u64(unsigned long long v, unsigned long long* before) {
-  __syncthreads();
-  if (lane_ == 0) sh_.warp_mass[warp_] = v;
-  __syncthreads();
-  if (warp_ == 0) {
-    const long long m = warp_sum_i64(lane_ < kWarps ? static_cast<long long>(sh_.warp_mass[lane_]) : 0);
-    if (lane_ == 0) sh_.slot_u64[parity_] = static_cast<unsigned long long>(m);
-  }
-  cluster_sync();
-  unsigned long long all = 0, b = 0;
-  for_each_cta(&sh_.slot_u64[parity_], size_, [&](uint32_t r, unsigned long long m) {
-    if (r < rank_) b += m;
-    all += m;
-  });
-  parity_ ^= 1;
-  *before = b;
-  return all;
-}
-
-// Sum of the weights of this warp's kept tokens.  Two logits an instruction where the
-// arithmetic allows; the three cases differ in what has to be compared.
-template <typename T>
-template <int kCase>
-__device__ unsigned long long RowSampler<T>::warp_mass_case(const Kept& k) {
+template <bool kEvery>
+__device__ __forceinline__ u64 RowSampler<T>::warp_mass(const Kept& k) {
   uint32_t hi = 0, lo = 0, n = 0;
   const float2 zm2 = make_float2(-zm_, -zm_), c2 = make_float2(c_, c_);
   const float2 minus = make_float2(-1.0f, -1.0f), add_hi = make_float2(kHiAdd, kHiAdd),
                sub_hi = make_float2(-kHiAdd, -kHiAdd), add_lo = make_float2(kLoAdd, kLoAdd);
-#pragma unroll 2
-  for (int i = lane_; i < s_.n; i += 32) {
+#pragma unroll 1
+  for (int i = lane_; i < n_; i += 32) {
     float z[kN];
-    Vec<T>::widen(s_.data[i], z);
-    const int id = s_.id0 + i * kN;
+    Vec<T>::widen(data_[i], z);
+    const int id = id0_ + i * kN;
 #pragma unroll
     for (int e = 0; e < kN; e += 2) {
       const float2 t = __fmul2_rn(__fadd2_rn(make_float2(z[e], z[e + 1]), zm2), c2);
       float2 w = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-      if (kCase >= kMinTOnly) {
-        if (!(t.x >= k.min_t)) w.x = 0.0f;
-        if (!(t.y >= k.min_t)) w.y = 0.0f;
-      }
-      if (kCase == kThreshold) {
-        if (!(z[e] > k.z_cut || (z[e] == k.z_cut && id + e <= k.id_cut))) w.x = 0.0f;
-        if (!(z[e + 1] > k.z_cut || (z[e + 1] == k.z_cut && id + e + 1 <= k.id_cut))) w.y = 0.0f;
+      if (!kEvery) {
+        if (!(t.x >= k.min_t && (z[e] > k.z_cut || (z[e] == k.z_cut && id + e <= k.id_cut)))) w.x = 0.0f;
+        if (!(t.y >= k.min_t && (z[e + 1] > k.z_cut || (z[e + 1] == k.z_cut && id + e + 1 <= k.id_cut)))) w.y = 0.0f;
       }
       // weight_bits() of both
       const float2 h = __fadd2_rn(w, add_hi);
@@ -569,159 +751,57 @@ __device__ unsigned long long RowSampler<T>::warp_mass_case(const Kept& k) {
     }
     n += kN;
   }
-  return warp_sum_u64(static_cast<unsigned long long>(weight_sum(hi, lo, n)));
-}
-
-template <typename T>
-__device__ unsigned long long RowSampler<T>::warp_kept_mass(const Kept& k) {
-  if (k.z_cut > -INFINITY) return warp_mass_case<kThreshold>(k);
-  return k.min_t > -INFINITY ? warp_mass_case<kMinTOnly>(k) : warp_mass_case<kAll>(k);
-}
-
-// The bin of the cluster's histograms at which `above` and the bins' counts (or
-// masses) first reach the target, or -1; *above grows by the bins before it.  For all
-// threads of all CTAs, each CTA for itself.
-template <typename T>
-__device__ int RowSampler<T>::find_bin(const uint32_t (*hist)[kBins], bool by_mass, unsigned long long target,
-                                       unsigned long long* above) {
-  static_assert(kBins == kThreads, "one bin per thread");
-  unsigned long long mine = 0;
-  for_each_cta(&hist[0][tid_], size_, [&](uint32_t, uint32_t h) {
-    mine += by_mass ? static_cast<unsigned long long>(h) << 16 : h;
-  });
-  if (by_mass) for_each_cta(&hist[1][tid_], size_, [&](uint32_t, uint32_t h) { mine += h; });
-  unsigned long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane_ >= o) incl += t;
-  }
-  if (lane_ == 31) sh_.scratch_u64[warp_] = incl;
-  if (tid_ == 0) sh_.found_bin = -1;
-  __syncthreads();
-  incl += *above;
-  for (int w = 0; w < warp_; ++w) incl += sh_.scratch_u64[w];
-  if (incl >= target && incl - mine < target) {
-    sh_.found_bin = tid_;
-    sh_.found_above = incl - mine;
-  }
-  __syncthreads();
-  if (sh_.found_bin >= 0) *above = sh_.found_above;
-  return sh_.found_bin;
-}
-
-template <typename T>
-__device__ void RowSampler<T>::count_into(uint32_t (*hist)[kBins], int bin, bool by_mass, float z) {
-  if (by_mass) {
-    const unsigned long long w = static_cast<unsigned long long>(weight_of(tempered(z, zm_, c_)));
-    atomicAdd(&hist[0][bin], static_cast<uint32_t>(w >> 16));
-    atomicAdd(&hist[1][bin], static_cast<uint32_t>(w) & 0xFFFFu);
-  } else {
-    atomicAdd(&hist[0][bin], 1u);
-  }
-}
-
-// The first CTA fetches the CTAs' parts of a list: their tokens' number, or -1 if they
-// are too many.  (Part of a longer agreement: a cluster barrier before and after.)
-template <typename T>
-__device__ int RowSampler<T>::fetch_list() {
-  static_assert(kListCap <= kThreads, "one thread per listed token");
-  uint32_t total = 0, cta = 0, at = 0;  // where this thread's token lies
-  for_each_cta(&sh_.list_n, size_, [&](uint32_t r, uint32_t m) {
-    if (static_cast<uint32_t>(tid_) >= total && static_cast<uint32_t>(tid_) - total < m) {
-      cta = r;
-      at = tid_ - total;
-    }
-    total += min(m, kListCap + 1u);
-  });
-  if (total > kListCap) return -1;
-  if (static_cast<uint32_t>(tid_) < total) {
-    const unsigned long long key = ld_cluster_u64(cluster_addr(&sh_.part[at], cta));
-    sh_.list[tid_] = Listed{key, static_cast<unsigned long long>(weight_of(tempered(key_value(key), zm_, c_)))};
-  }
-  return static_cast<int>(total);
-}
-
-// Every listed token's rank (bits 48..) and the mass before it in the order (below
-// 2^48), by comparing all with all: eight threads per token.  Token i's to its thread i.
-constexpr int kPerToken = 8;
-template <typename T>
-__device__ unsigned long long RowSampler<T>::rank_list(int n) {
-  static_assert(kListCap <= kThreads, "one thread per listed token at the end");
-  const int sub = tid_ % kPerToken;
-  __syncthreads();
-  for (int i0 = warp_ * (32 / kPerToken); i0 < n; i0 += kThreads / kPerToken) {  // (a warp's share is its own)
-    const int i = i0 + lane_ / kPerToken;
-    unsigned long long above = 0;
-    if (i < n) {
-      const unsigned long long key = sh_.list[i].key;
-      for (int j = sub; j < n; j += kPerToken) {
-        const Listed o = sh_.list[j];
-        if (o.key > key) above += o.w + (1ull << 48);
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < kPerToken; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
-    if (i < n && sub == 0) sh_.part[i] = above;
-  }
-  __syncthreads();
-  return tid_ < n ? sh_.part[tid_] : 0;
+  return warp_sum_u64(weight_sum(hi, lo, n));
 }
 
 // Narrows k->z_cut, k->id_cut to the shortest prefix of the order whose count (or
 // mass) reaches target >= 1.  A target above the total of the tokens with a weight
 // leaves k alone.
 template <typename T>
-__device__ void RowSampler<T>::threshold(bool by_mass, unsigned long long target, Kept* k) {
-  unsigned long long above = 0;  // count or mass of the bins before
-  int bin[2] = {0, 0};
-  // the part of bin bin[0] that z lies in, or kBins
-  auto part_bin = [&](float z) -> int {
-    const float x = list_place(z);
-    return static_cast<int>(x) == bin[0] ? min(static_cast<int>((x - bin[0]) * kBins), kBins - 1) : kBins;
+__device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 target, Kept* k) {
+  u64 above = 0;  // count or mass of what comes before the bin
+  int bin = -1, part = -1;
+  auto part_of = [&](float x) {
+    return static_cast<int>(x) == bin ? min(static_cast<int>((x - bin) * kBins), kBins - 1) : kBins;
   };
-#pragma unroll
+#pragma unroll 1
   for (int level = 0; level < 2; ++level) {
-    uint32_t(*hist)[kBins] = sh_.hist[level];
-    __syncthreads();
-    hist[0][tid_] = 0;
-    hist[1][tid_] = 0;
-    if (tid_ == 0) sh_.list_n = 0;
-    __syncthreads();
-    for_each_vector(s_, [&](const float(&z)[kN], int) {
-#pragma unroll
-      for (int e = 0; e < kN; ++e) {
-        const int b = level == 0 ? list_bin(z[e]) : part_bin(z[e]);
-        if (b < kBins) count_into(hist, b, by_mass, z[e]);
-      }
+    uint32_t(*hist)[kBins] = sh.hist[level];
+    clear_hist(hist);
+    for_each_element([&](float z, int) {
+      const float t = t_of(z), x = place(t);
+      const int b = level == 0 ? static_cast<int>(x) : part_of(x);
+      if (b < kBins) count_into(hist, b, by_mass, t);
     });
     cluster_sync();
-    bin[level] = find_bin(hist, by_mass, target, &above);
-    if (bin[level] < 0) return;
+    part = find_bin(gather_bin(hist[0], by_mass ? hist[1] : nullptr), target, above);
+    if (part < 0) return;
+    above = sh.found_above;
+    if (level == 0) bin = part;
   }
-  for_each_vector(s_, [&](const float(&z)[kN], int id) {
-#pragma unroll
-    for (int e = 0; e < kN; ++e)
-      if (part_bin(z[e]) == bin[1]) {
-        const uint32_t at = atomicAdd(&sh_.list_n, 1u);
-        if (at < kListCap) sh_.part[at] = make_key(z[e], id + e);
-      }
+  for_each_element([&](float z, int j) {
+    if (part_of(place(t_of(z))) == part) {
+      const uint32_t at = atomicAdd(&sh.list_n, 1u);
+      if (at < kListCap) sh.part[at] = make_key(z, id0_ + j);
+    }
   });
   cluster_sync();
-  if (rank_ == 0) {
-    const int n = fetch_list();
+  if (cluster_rank() == 0) {
+    const int n = fetch_list(zm_, c_);
     if (n >= 0) {
-      const unsigned long long r = rank_list(n);
-      if (tid_ < n) {
-        const unsigned long long before = above + (by_mass ? r & 0xFFFFFFFFFFFFull : r >> 48);
-        if (before < target && before + (by_mass ? sh_.list[tid_].w : 1) >= target) sh_.list_key = sh_.list[tid_].key;
+      rank_list(n);
+      if (static_cast<int>(threadIdx.x) < n) {
+        const u64 r = sh.part[threadIdx.x];
+        const Listed it = sh.list[threadIdx.x];
+        const u64 before = above + (by_mass ? r & 0xFFFFFFFFFFFFull : r >> 48);
+        if (before < target && before + (by_mass ? it.w : 1) >= target) sh.list_key = it.key;
       }
     }
-    if (tid_ == 0) sh_.list_ok = n >= 0;
+    if (threadIdx.x == 0) sh.list_ok = n >= 0;
   }
   cluster_sync();
-  if (ld_cluster_u32(cluster_addr(&sh_.list_ok, 0)) != 0) {
-    const unsigned long long key = ld_cluster_u64(cluster_addr(&sh_.list_key, 0));
+  if (ld_cluster_u32(cluster_addr(&sh.list_ok, 0)) != 0) {
+    const u64 key = ld_cluster_u64(cluster_addr(&sh.list_key, 0));
     k->z_cut = key_value(key);
     k->id_cut = key_id(key);
     return;
@@ -730,19 +810,16 @@ __device__ void RowSampler<T>::threshold(bool by_mass, unsigned long long target
   float hi, lo;
   {
     uint32_t top = 0, bottom = 0;  // of the order keys, and of their complements
-    for_each_vector(s_, [&](const float(&z)[kN], int) {
-#pragma unroll
-      for (int e = 0; e < kN; ++e)
-        if (part_bin(z[e]) == bin[1]) {
-          top = max(top, f32_ord(z[e]));
-          bottom = max(bottom, ~f32_ord(z[e]));
-        }
+    for_each_element([&](float z, int) {
+      if (part_of(place(t_of(z))) == part) {
+        top = max(top, f32_ord(z));
+        bottom = max(bottom, ~f32_ord(z));
+      }
     });
-    __syncthreads();
-    hi = ord_f32(reduce_max_u32(top));
-    __syncthreads();
-    lo = ord_f32(~reduce_max_u32(bottom));
+    hi = ord_f32(max_over(top));
+    lo = ord_f32(~max_over(bottom));
   }
+#pragma unroll 1
   for (int level = 0; lo < hi; ++level) {
     // Bins over [lo, hi], bin 0 at the top: linear in z first, which spreads a
     // row's logits evenly; linear in the order keys after eight levels or where
@@ -756,293 +833,144 @@ __device__ void RowSampler<T>::threshold(bool by_mass, unsigned long long target
       return linear ? min(static_cast<int>(__fmul_rn(__fsub_rn(hi, z), inv)), kBins - 1)
                     : static_cast<int>((ord_hi - f32_ord(z)) >> shift);
     };
-    uint32_t(*hist)[kBins] = sh_.hist[parity_];
-    __syncthreads();
-    hist[0][tid_] = 0;
-    hist[1][tid_] = 0;
-    __syncthreads();
-    for_each_vector(s_, [&](const float(&z)[kN], int) {
-#pragma unroll
-      for (int e = 0; e < kN; ++e)
-        if (z[e] >= lo && z[e] <= hi) count_into(hist, bin_of(z[e]), by_mass, z[e]);
+    uint32_t(*hist)[kBins] = sh.hist[level & 1];
+    clear_hist(hist);
+    for_each_element([&](float z, int) {
+      if (z >= lo && z <= hi) count_into(hist, bin_of(z), by_mass, t_of(z));
     });
     cluster_sync();
-    const int bin = find_bin(hist, by_mass, target, &above);
-    if (bin < 0) return;  // (not reached: the target lies in [lo, hi])
+    const int b = find_bin(gather_bin(hist[0], by_mass ? hist[1] : nullptr), target, above);
+    if (b < 0) return;  // (not reached: the target lies in [lo, hi])
+    above = sh.found_above;
     // the bin's own extremes are the next interval
     uint32_t top = 0, bottom = 0;
-    for_each_vector(s_, [&](const float(&z)[kN], int) {
-#pragma unroll
-      for (int e = 0; e < kN; ++e)
-        if (z[e] >= lo && z[e] <= hi && bin_of(z[e]) == bin) {
-          top = max(top, f32_ord(z[e]));
-          bottom = max(bottom, ~f32_ord(z[e]));
-        }
+    for_each_element([&](float z, int) {
+      if (z >= lo && z <= hi && bin_of(z) == b) {
+        top = max(top, f32_ord(z));
+        bottom = max(bottom, ~f32_ord(z));
+      }
     });
-    parity_ ^= 1;
-    __syncthreads();
-    const uint32_t t = reduce_max_u32(top);
-    __syncthreads();
-    const uint32_t b = reduce_max_u32(bottom);
-    hi = ord_f32(t);
-    lo = ord_f32(~b);
+    hi = ord_f32(max_over(top));
+    lo = ord_f32(~max_over(bottom));
   }
   // One value left, `hi`: of the tokens equal to it the first m in id order are kept.
-  unsigned long long ties = 0, before = 0;
-  for_each_vector(s_, [&](const float(&z)[kN], int) {
-#pragma unroll
-    for (int e = 0; e < kN; ++e) ties += z[e] == hi ? 1 : 0;
-  });
-  ties = static_cast<unsigned long long>(warp_sum_i64(static_cast<long long>(ties)));
-  const unsigned long long all = reduce_sum_u64(ties, &before);
-  unsigned long long m = target - above;
+  uint32_t mine = 0;
+  for_each_element([&](float z, int) { mine += z == hi ? 1 : 0; });
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  const Sum ties = sum_over(mine);
+  u64 m = target - above;
   if (by_mass) {
-    const unsigned long long w = static_cast<unsigned long long>(weight_of(tempered(hi, zm_, c_)));
+    const u64 w = weight_of(t_of(hi));
     if (w == 0) return;  // (a target above the row's total)
     m = (m + w - 1) / w;
   }
-  if (m > all) return;
-  // the CTA and warp that hold the m-th of them find its id
-  unsigned long long b = before;
-  for (int w = 0; w < warp_; ++w) b += sh_.warp_mass[w];
+  if (m > ties.all) return;
+  // the warp that holds the m-th of them finds its id
+  u64 before = ties.before;
+#pragma unroll 1
+  for (int w = 0; w < warp_; ++w) before += sh.warp_mass[w];
   uint32_t found = 0;
-  if (b < m && m <= b + ties) {
-    unsigned long long left = m - b;
-    for (int i0 = 0; i0 < s_.n; i0 += 32) {
-      const int i = i0 + lane_;
-      float z[kN];
-      int cnt = 0;
-      if (i < s_.n) {
-        Vec<T>::widen(s_.data[i], z);
-#pragma unroll
-        for (int e = 0; e < kN; ++e) cnt += z[e] == hi ? 1 : 0;
-      }
-      int incl = cnt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane_ >= o) incl += t;
-      }
-      const int total = __shfl_sync(0xffffffffu, incl, 31);
-      if (static_cast<unsigned long long>(total) >= left) {
-        int need = static_cast<int>(left) - (incl - cnt);
-        if (need >= 1 && need <= cnt) {
-#pragma unroll
-          for (int e = 0; e < kN; ++e)
-            if (z[e] == hi && --need == 0) found = static_cast<uint32_t>(s_.id0 + i * kN + e) + 1;
-        }
-        break;
-      }
-      left -= total;
+  if (before < m && m <= before + mine) {
+    int left = static_cast<int>(m - before);
+#pragma unroll 1
+    for (int j0 = 0; j0 < n_ * kN; j0 += 32) {
+      const bool tie = j0 + lane_ < n_ * kN && element(j0 + lane_) == hi;
+      const unsigned ones = __ballot_sync(0xffffffffu, tie);
+      if (tie && __popc(ones & ((2u << lane_) - 1u)) == left) found = static_cast<uint32_t>(id0_ + j0 + lane_) + 1;
+      left -= __popc(ones);
+      if (left <= 0) break;
     }
   }
-  __syncthreads();
-  const uint32_t f = reduce_max_u32(found);
   k->z_cut = hi;
-  k->id_cut = static_cast<int>(f) - 1;
-}
-
-template <typename T>
-__device__ void RowSampler<T>::write(int id, float z, unsigned long long total) {
-  p_.ids[row_] = id;
-  if (p_.logprobs) {
-    const float k32 = __fmul_rn(__ll2float_rn(static_cast<long long>(total)), 2.3283064365386963e-10f);  // 2^-32
-    p_.logprobs[row_] = __fsub_rn(__fmul_rn(tempered(z, zm_, c_), 0.6931471805599453f), logf(k32));
-  }
-}
-
-// The point of a draw: floor(u * total), below total.
-__device__ __forceinline__ unsigned long long draw_point(float uniform, unsigned long long total) {
-  const float u = fminf(fmaxf(uniform, 0.0f), 0.99999994f);
-  const unsigned long long r = static_cast<unsigned long long>(
-      floor(__dmul_rn(static_cast<double>(u), static_cast<double>(static_cast<long long>(total)))));
-  return r < total ? r : total - 1;
-}
-
-// Sum over this CTA of every thread's value.
-template <typename T>
-__device__ unsigned long long RowSampler<T>::block_sum_u64(unsigned long long v) {
-  v = static_cast<unsigned long long>(warp_sum_i64(static_cast<long long>(v)));
-  __syncthreads();
-  if (lane_ == 0) sh_.scratch_u64[warp_] = v;
-  __syncthreads();
-  return static_cast<unsigned long long>(
-      warp_sum_i64(lane_ < kWarps ? static_cast<long long>(sh_.scratch_u64[lane_]) : 0));
+  k->id_cut = static_cast<int>(max_over(found)) - 1;
 }
 
 // Draws from a list, if one can be made: true when the row is done.  With top-p alone
 // *mass becomes the row's mass.
 template <typename T>
-__device__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, unsigned long long* mass) {
-  const unsigned target = top_k > 0 ? top_k : kListTargetTopP;
-  const int my_bin = list_bin(lane_max_);
-  if (my_bin < kBins) atomicAdd(&sh_.list_hist[my_bin], 1u);
-  unsigned long long before;
-  if (top_k == 0) {
-    *mass = reduce_sum_u64(warp_kept_mass(Kept{-INFINITY, -INFINITY, INT32_MAX}), &before);
-  } else {
+__device__ __forceinline__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, u64* mass) {
+  const u64 target = top_k > 0 ? top_k : kListTargetTopP;
+  const int my_bin = static_cast<int>(place(t_of(lane_max_)));
+  if (my_bin < kBins) atomicAdd(&sh.list_hist[my_bin], 1u);
+  if (top_k == 0)
+    *mass = sum_over(warp_mass<true>(Kept{})).all;
+  else
     cluster_sync();
-  }
   // The last bin that is listed: the first at which the lanes' maxima reach the target.
-  uint32_t n = 0;
-  for_each_cta(&sh_.list_hist[tid_], size_, [&](uint32_t, uint32_t h) { n += h; });
-  uint32_t incl = n;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane_ >= o) incl += t;
-  }
-  if (lane_ == 31) sh_.scratch_u32[warp_] = incl;
-  if (tid_ == 0) sh_.found_bin = kBins - 1;
-  __syncthreads();
-  for (int w = 0; w < warp_; ++w) incl += sh_.scratch_u32[w];
-  if (incl >= target && incl - n < target) sh_.found_bin = tid_;
-  __syncthreads();
-  const int last_bin = sh_.found_bin;
+  int last_bin = find_bin(gather_bin(sh.list_hist, nullptr), target, 0);
+  if (last_bin < 0) last_bin = kBins - 1;
   if (my_bin <= last_bin) {
-    for (int i = lane_; i < s_.n; i += 32) {
-      const uint4 x = s_.data[i];
-      if (list_bin(Vec<T>::max_of(x)) > last_bin) continue;
-      float z[kN];
-      Vec<T>::widen(x, z);
-#pragma unroll
-      for (int e = 0; e < kN; ++e)
-        if (list_bin(z[e]) <= last_bin) {
-          const uint32_t at = atomicAdd(&sh_.list_n, 1u);
-          if (at < kListCap) sh_.part[at] = make_key(z[e], s_.id0 + i * kN + e);
+#pragma unroll 1
+    for (int i = lane_; i < n_; i += 32) {
+      if (static_cast<int>(place(t_of(Vec<T>::max_of(data_[i])))) > last_bin) continue;
+#pragma unroll 1
+      for (int j = i * kN; j < (i + 1) * kN; ++j) {
+        const float z = element(j);
+        if (static_cast<int>(place(t_of(z))) <= last_bin) {
+          const uint32_t at = atomicAdd(&sh.list_n, 1u);
+          if (at < kListCap) sh.part[at] = make_key(z, id0_ + j);
         }
+      }
     }
   }
   cluster_sync();
   // The first CTA fetches the parts and says whether they will do.
-  unsigned long long need = 0;
+  u64 need = 0;
   int total = 0;
-  if (rank_ == 0) {
-    total = fetch_list();
+  if (cluster_rank() == 0) {
+    total = fetch_list(zm_, c_);
     bool ok = total >= 0;
     if (ok && top_k == 0) {
       need = mass_wanted(top_p, *mass);
-      unsigned long long have = 0;
-      __syncthreads();
-      for (int i = tid_; i < total; i += kThreads) have += sh_.list[i].w;
-      ok = block_sum_u64(have) >= need;
+      // (a thread's token is the one that it fetched)
+      ok = block_sum_u64(static_cast<int>(threadIdx.x) < total ? sh.list[threadIdx.x].w : 0) >= need;
     }
-    if (tid_ == 0) sh_.list_ok = ok;
+    if (threadIdx.x == 0) sh.list_ok = ok;
   }
   cluster_sync();
-  const bool ok = ld_cluster_u32(cluster_addr(&sh_.list_ok, 0)) != 0;
-  if (ok && rank_ == 0) draw_from_list(total, top_k, need, min_t);
+  const bool ok = ld_cluster_u32(cluster_addr(&sh.list_ok, 0)) != 0;
+  if (ok && cluster_rank() == 0)
+    draw_from_list(p_, row_, total, top_k, top_p, need, min_t, uniform_, zm_, c_);
   return ok;
-}
-
-// The draw from the first CTA's list of n tokens.  top_k > 0: `need` is worked out here.
-template <typename T>
-__device__ void RowSampler<T>::draw_from_list(int n, int top_k, unsigned long long need, float min_t) {
-  rank_list(n);
-  if (warp_ == 0) {
-    if (top_k > 0) {
-      unsigned long long mass = 0;
-      for (int i = lane_; i < n; i += 32)
-        if (static_cast<int>(sh_.part[i] >> 48) < top_k) mass += sh_.list[i].w;
-      mass = warp_sum_u64(mass);
-      need = top_p_ < 1.0f ? mass_wanted(top_p_, mass) : mass;
-    }
-    // the kept ones, closed up (each to a place at or before its own), and their mass
-    unsigned long long kept = 0;
-    int m = 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + lane_;
-      Listed it{0, 0};
-      bool keep = false;
-      if (i < n) {
-        it = sh_.list[i];
-        const unsigned long long place = sh_.part[i];
-        keep = it.w > 0 && (place & 0xFFFFFFFFFFFFull) < need &&
-               (top_k == 0 || static_cast<int>(place >> 48) < top_k) &&
-               tempered(key_value(it.key), zm_, c_) >= min_t;
-      }
-      const unsigned ones = __ballot_sync(0xffffffffu, keep);  // (every lane has read its token)
-      if (keep) {
-        kept += it.w;
-        sh_.list[m + __popc(ones & ((1u << lane_) - 1u))] = it;
-      }
-      m += __popc(ones);
-    }
-    kept = warp_sum_u64(kept);
-    if (lane_ == 0) {
-      sh_.count = m;
-      sh_.kept = kept;
-      sh_.point = draw_point(uniform_, kept);
-    }
-  }
-  __syncthreads();
-  const int m = static_cast<int>(sh_.count);
-  const unsigned long long r = sh_.point;
-  const int sub = tid_ % kPerToken;
-  for (int i0 = warp_ * (32 / kPerToken); i0 < m; i0 += kThreads / kPerToken) {
-    const int i = i0 + lane_ / kPerToken;
-    unsigned long long before = 0;
-    Listed it{0, 0};
-    if (i < m) {
-      it = sh_.list[i];
-      for (int j = sub; j < m; j += kPerToken) {
-        const Listed o = sh_.list[j];
-        // ids are complemented in the keys' low words
-        if (static_cast<uint32_t>(o.key) > static_cast<uint32_t>(it.key)) before += o.w;
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < kPerToken; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-    if (i < m && sub == 0 && before <= r && r < before + it.w) write(key_id(it.key), key_value(it.key), sh_.kept);
-  }
 }
 
 // The token at the given point of the kept tokens' mass, in id order.
 template <typename T>
-__device__ void RowSampler<T>::draw(const Kept& k) {
-  const unsigned long long mine = warp_kept_mass(k);
-  unsigned long long before = 0;
-  const unsigned long long total = reduce_sum_u64(mine, &before);
-  const unsigned long long r = draw_point(uniform_, total);
-  for (int w = 0; w < warp_; ++w) before += sh_.warp_mass[w];
+__device__ __forceinline__ void RowSampler<T>::draw(const Kept& k) {
+  const u64 mine =
+      k.z_cut > -INFINITY || k.min_t > -INFINITY ? warp_mass<false>(k) : warp_mass<true>(k);
+  const Sum sum = sum_over(mine);
+  const u64 r = draw_point(uniform_, sum.all);
+  u64 before = sum.before;
+#pragma unroll 1
+  for (int w = 0; w < warp_; ++w) before += sh.warp_mass[w];
   if (r < before || r >= before + mine) return;
-  unsigned long long left = r - before;  // mass to pass within this warp's vectors
-  for (int i0 = 0; i0 < s_.n; i0 += 32) {
+  u64 left = r - before;  // mass to pass within this warp's vectors
+#pragma unroll 1
+  for (int i0 = 0; i0 < n_; i0 += 32) {
     const int i = i0 + lane_;
-    float z[kN];
-    unsigned long long w[kN], sum = 0;
-#pragma unroll
-    for (int e = 0; e < kN; ++e) w[e] = 0;
-    if (i < s_.n) {
-      Vec<T>::widen(s_.data[i], z);
-#pragma unroll
-      for (int e = 0; e < kN; ++e) {
-        if (is_kept(z[e], s_.id0 + i * kN + e, k))
-          w[e] = static_cast<unsigned long long>(weight_of(tempered(z[e], zm_, c_)));
-        sum += w[e];
+    u64 w = 0;
+    if (i < n_)
+#pragma unroll 2
+      for (int j = i * kN; j < (i + 1) * kN; ++j) {
+        const float z = element(j);
+        if (is_kept(z, id0_ + j, k)) w += weight_of(t_of(z));
       }
-    }
-    unsigned long long incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane_ >= o) incl += t;
-    }
-    const unsigned long long all = __shfl_sync(0xffffffffu, incl, 31);
+    const u64 incl = warp_scan_u64(w);
+    const u64 all = __shfl_sync(0xffffffffu, incl, 31);
     if (left < all) {
-      unsigned long long at = incl - sum;
-      if (at <= left && left < incl) {
-        int id = -1;
-        float zs = 0.0f;
-#pragma unroll
-        for (int e = 0; e < kN; ++e) {
-          if (at <= left && left < at + w[e]) {
-            id = s_.id0 + i * kN + e;
-            zs = z[e];
+      if (incl - w <= left && left < incl) {
+        u64 at = incl - w;
+#pragma unroll 1
+        for (int j = i * kN; j < (i + 1) * kN; ++j) {
+          const float z = element(j);
+          if (!is_kept(z, id0_ + j, k)) continue;
+          at += weight_of(t_of(z));
+          if (left < at) {
+            write_token(p_, row_, id0_ + j, t_of(z), sum.all);
+            break;
           }
-          at += w[e];
         }
-        write(id, zs, total);
       }
       return;
     }
@@ -1052,28 +980,30 @@ __device__ void RowSampler<T>::draw(const Kept& k) {
 
 // The first token whose logit is the row's maximum.
 template <typename T>
-__device__ void RowSampler<T>::greedy() {
+__device__ __forceinline__ void RowSampler<T>::greedy() {
   uint32_t first = 0;  // complemented id
-  for_each_vector(s_, [&](const float(&z)[kN], int id) {
-#pragma unroll
-    for (int e = 0; e < kN; ++e)
-      if (z[e] == zm_) first = max(first, ~static_cast<uint32_t>(id + e));
-  });
-  __syncthreads();
-  first = reduce_max_u32(first);
-  if (rank_ == 0 && tid_ == 0) {
+  if (lane_max_ == zm_) {
+#pragma unroll 1
+    for (int i = lane_; i < n_ && first == 0; i += 32) {
+      if (Vec<T>::max_of(data_[i]) != zm_) continue;
+#pragma unroll 1
+      for (int j = (i + 1) * kN - 1; j >= i * kN; --j)
+        if (element(j) == zm_) first = ~static_cast<uint32_t>(id0_ + j);
+    }
+  }
+  first = max_over(first);
+  if (cluster_rank() == 0 && threadIdx.x == 0) {
     p_.ids[row_] = static_cast<int32_t>(~first);
     if (p_.logprobs) p_.logprobs[row_] = 0.0f;
   }
 }
 
 template <typename T>
-__device__ bool RowSampler<T>::run() {
-  int top_k = top_k_;
-  const float T_row = temperature_, min_p = min_p_;
-  zm_ = ord_f32(reduce_max_u32(f32_ord(lane_max_)));
+__device__ __forceinline__ bool RowSampler<T>::run() {
+  cluster_wait();  // every CTA of the cluster has started
+  zm_ = ord_f32(max_over(f32_ord(lane_max_)));
   if (zm_ == -INFINITY) {
-    if (rank_ == 0 && tid_ == 0) {
+    if (cluster_rank() == 0 && threadIdx.x == 0) {
       p_.ids[row_] = -1;
       if (p_.logprobs) p_.logprobs[row_] = __int_as_float(0x7FC00000);
       set_status(p_.dev_status, LMH_DS_NO_ALLOWED_TOKEN);
@@ -1081,37 +1011,36 @@ __device__ bool RowSampler<T>::run() {
     return false;
   }
   if (zm_ == INFINITY) {  // only the +inf tokens are left, as equals
-    for (int i = lane_; i < s_.n; i += 32) {
-      float z[kN];
-      Vec<T>::widen(s_.data[i], z);
-#pragma unroll
-      for (int e = 0; e < kN; ++e) z[e] = z[e] == INFINITY ? 0.0f : -INFINITY;
-      s_.data[i] = Vec<T>::narrow(z);
-    }
+    float m = -INFINITY;
+    for_each_element([&](float z, int j) {
+      const float y = z == INFINITY ? 0.0f : -INFINITY;
+      reinterpret_cast<T*>(data_)[j] = Vec<T>::from_float(y);
+      m = fmaxf(m, y);
+    });
+    __syncwarp();
+    // (the lanes of a warp that holds one may all look for it)
+    lane_max_ = __any_sync(0xffffffffu, m == 0.0f) ? 0.0f : -INFINITY;
     zm_ = 0.0f;
-    lane_max_ = lane_max_ == INFINITY ? 0.0f : -INFINITY;
   }
-  if (!(T_row > 0.0f)) {
+  if (!(temperature_ > 0.0f)) {
     greedy();
     return false;
   }
-  c_ = fminf(fmaxf(__fmul_rn(__frcp_rn(T_row), kLog2e), 1.1754944e-38f), 3.402823466e+38f);
+  c_ = fminf(fmaxf(__fmul_rn(__frcp_rn(temperature_), kLog2e), 1.1754944e-38f), 3.402823466e+38f);
 
   Kept k{-INFINITY, -INFINITY, INT32_MAX};
-  if (top_k < 0 || top_k >= p_.V) top_k = 0;
-  const float top_p = top_p_;
-  const float min_t = min_p > 0.0f ? fminf(log2f(min_p), 0.0f) : -INFINITY;
-  unsigned long long mass = 0;
+  const int top_k = top_k_ > 0 && top_k_ < p_.V ? top_k_ : 0;
+  const float min_t = min_p_ > 0.0f ? fminf(log2f(min_p_), 0.0f) : -INFINITY;
+  u64 mass = 0;
   bool have_mass = false;
-  if (top_k > 0 ? top_k <= kListTarget : top_p < 1.0f) {
-    if (from_list(top_k, top_p, min_t, &mass)) return true;
+  if (top_k > 0 ? top_k <= kListTarget : top_p_ < 1.0f) {
+    if (from_list(top_k, top_p_, min_t, &mass)) return true;
     have_mass = top_k == 0;
   }
-  if (top_k > 0) threshold(false, static_cast<unsigned long long>(top_k), &k);
-  if (top_p < 1.0f) {
-    unsigned long long before;
-    if (!have_mass) mass = reduce_sum_u64(warp_kept_mass(k), &before);
-    threshold(true, mass_wanted(top_p, mass), &k);
+#pragma unroll 1
+  for (int by_mass = top_k > 0 ? 0 : 1; by_mass < (top_p_ < 1.0f ? 2 : 1); ++by_mass) {
+    if (by_mass && !have_mass) mass = sum_over(warp_mass<false>(k)).all;
+    threshold(by_mass != 0, by_mass ? mass_wanted(top_p_, mass) : static_cast<u64>(top_k), &k);
   }
   k.min_t = min_t;
   draw(k);
@@ -1119,12 +1048,10 @@ __device__ bool RowSampler<T>::run() {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(Params p) {
-  extern __shared__ uint4 data[];
-  __shared__ Shared sh;
+__global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const __grid_constant__ Params p) {
   pdl_wait();
   pdl_launch_dependents();
-  RowSampler<T> s(p, sh, data, static_cast<int>(blockIdx.x / cluster_size()));
+  RowSampler<T> s(p, static_cast<int>(blockIdx.x / cluster_size()));
   const bool first_only = s.run();
   // No CTA leaves while another may still read its shared memory; after a draw from a
   // list the others need not wait for the first, and make room for the next row.

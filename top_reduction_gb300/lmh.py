@@ -7,7 +7,6 @@ in the library's CUDA kernels.  There is no fallback: if liblmh.so is missing
 or no CUDA device is present, the calls raise.
 """
 import ctypes
-import functools
 import os
 
 import torch
@@ -337,19 +336,12 @@ def logprobs_from_logits(logits, sel=None, row_k=None, k_max=0, workspace=None, 
 # a decode step with a 4-bit head: lookup, projection, filtered draw
 # ---------------------------------------------------------------------------
 
-def _on_stream(call):
-    """`stream=` makes the whole call on that stream: the tensors it converts and allocates, too."""
-    @functools.wraps(call)
-    def wrapper(*args, stream=None, **kwargs):
-        if stream is None:
-            return call(*args, **kwargs)
-        with torch.cuda.stream(stream):
-            return call(*args, **kwargs)
-    return wrapper
+# These calls are made once or more per token of a stream, so the host's share is kept small:
+# one look-up of the raw stream, no conversions of tensors that are already right.
 
-
-def _current_stream():
-    return torch.cuda.current_stream().cuda_stream
+def _raw_stream(device):
+    """The current stream of `device`, as the C ABI takes it."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _ptr(t):
@@ -367,23 +359,27 @@ def _per_row(t, dtype, rows, device, name):
     return t
 
 
-@_on_stream
 def sample_from_logits(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None, mask=None,
-                       dev_status=None, out=None):
+                       dev_status=None, out=None, stream=None):
     """One token per row of logits [rows, V] (bf16, f16 or f32; rows may be strided), from one
     given uniform number per row (lmh_sample_from_logits).
 
     uniforms: fp32 [rows] in [0, 1).  temperature, top_p, min_p: fp32 [rows] or None; top_k: int32
-    [rows] or None; mask: int32/uint32 [rows, words] allowed-token bits or None.
+    [rows] or None; mask: int32/uint32 [rows, words] allowed-token bits or None.  stream: the call
+    is made on it, conversions and allocations included.
     Returns a dict with sampled_ids (int32 [rows], -1 where a row has no token) and sampled_logprob
     (fp32 [rows], in the distribution that was drawn from).
     """
-    assert logits.is_cuda and logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return sample_from_logits(logits, uniforms, temperature, top_k, top_p, min_p, mask, dev_status, out)
     rows, V = logits.shape
+    pitch, step = logits.stride()
     dev = logits.device
-    u = _per_row(uniforms, torch.float32, rows, dev, "uniforms")
-    if u is None:
+    assert logits.is_cuda and (step == 1 or V == 1)
+    if uniforms is None:
         raise ValueError("uniforms is required")
+    u = _per_row(uniforms, torch.float32, rows, dev, "uniforms")
     temp = _per_row(temperature, torch.float32, rows, dev, "temperature")
     k = _per_row(top_k, torch.int32, rows, dev, "top_k")
     p = _per_row(top_p, torch.float32, rows, dev, "top_p")
@@ -397,11 +393,11 @@ def sample_from_logits(logits, uniforms, temperature=None, top_k=None, top_p=Non
         out = {"sampled_ids": torch.empty(rows, dtype=torch.int32, device=dev),
                "sampled_logprob": torch.empty(rows, dtype=torch.float32, device=dev)}
     f = Filters(_ptr(temp), _ptr(k), _ptr(p), _ptr(m), _ptr(mask), words)
-    lp = out.get("sampled_logprob")
-    _check(load().lmh_sample_from_logits(logits.data_ptr(), _DTYPES[logits.dtype], rows, V,
-                                         logits.stride(0) if rows > 1 else V, ctypes.byref(f), u.data_ptr(),
-                                         out["sampled_ids"].data_ptr(), _ptr(lp), _ptr(dev_status), _current_stream()),
-           "lmh_sample_from_logits")
+    st = (_lib or load()).lmh_sample_from_logits(
+        logits.data_ptr(), _DTYPES[logits.dtype], rows, V, pitch if rows > 1 else V, f, u.data_ptr(),
+        out["sampled_ids"].data_ptr(), _ptr(out.get("sampled_logprob")), _ptr(dev_status), _raw_stream(dev))
+    if st != OK:
+        raise LMHError(st, "lmh_sample_from_logits")
     return out
 
 
@@ -432,12 +428,13 @@ class Q4Table:
         self._arg = Q4TableArg(packed.data_ptr(), stride(packed, H // 2), scales.data_ptr(), _DTYPES[scales.dtype],
                                stride(scales, H // group), _ptr(zeros),
                                0 if zeros is None else stride(zeros, H // group), V, H, group)
-        self._ref = ctypes.byref(self._arg)
 
 
-@_on_stream
-def quantize_q4(W, group=64, zeros=False, scale_dtype=torch.bfloat16):
+def quantize_q4(W, group=64, zeros=False, scale_dtype=torch.bfloat16, stream=None):
     """Round a bf16 table [V, H] to 4 bits (lmh_quantize_q4): a Q4Table."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantize_q4(W, group, zeros, scale_dtype)
     assert W.is_cuda and W.dtype == torch.bfloat16 and W.dim() == 2 and W.stride(1) == 1
     V, H = W.shape
     if H % group:
@@ -447,21 +444,27 @@ def quantize_q4(W, group=64, zeros=False, scale_dtype=torch.bfloat16):
     scales = torch.empty((V, H // group), dtype=scale_dtype, device=dev)
     z = torch.empty((V, H // group), dtype=torch.uint8, device=dev) if zeros else None
     table = Q4Table(packed, scales, z, group)
-    _check(load().lmh_quantize_q4(W.data_ptr(), W.stride(0) if V > 1 else H, table._ref, _current_stream()),
+    _check(load().lmh_quantize_q4(W.data_ptr(), W.stride(0) if V > 1 else H, table._arg, _raw_stream(dev)),
            "lmh_quantize_q4")
     return table
 
 
-@_on_stream
 def project_q4(hidden, table, row_idx=None, rows=None, logit_scale=1.0, out_dtype=torch.float32, out=None,
-               dev_status=None):
+               dev_status=None, stream=None):
     """Logits [rows, V] of hidden rows through a 4-bit head (lmh_project_q4).
 
     hidden: bf16 or f16 [T, H] (rows may be strided); row_idx: int32 [rows] device tensor or None;
-    out_dtype: float32 or hidden's type, or give `out` (rows may be strided).
+    out_dtype: float32 or hidden's type, or give `out` (rows may be strided); stream: as
+    sample_from_logits.
     """
-    assert hidden.is_cuda and hidden.dim() == 2 and hidden.stride(1) == 1 and hidden.device == table.device
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return project_q4(hidden, table, row_idx, rows, logit_scale, out_dtype, out, dev_status)
     T, H = hidden.shape
+    V = table.V
+    pitch, step = hidden.stride()
+    dev = hidden.device
+    assert step == 1 and dev == table.device
     if H != table.H:
         raise ValueError("hidden has %d columns, the table %d" % (H, table.H))
     if row_idx is not None:
@@ -471,27 +474,39 @@ def project_q4(hidden, table, row_idx=None, rows=None, logit_scale=1.0, out_dtyp
     elif rows is None:
         rows = T
     if out is None:
-        out = torch.empty((rows, table.V), dtype=out_dtype, device=hidden.device)
-    assert out.is_cuda and tuple(out.shape) == (rows, table.V) and (out.stride(1) == 1 or table.V == 1)
-    _check(load().lmh_project_q4(hidden.data_ptr(), _DTYPES[hidden.dtype], hidden.stride(0) if T > 1 else H, T,
-                                 _ptr(row_idx), rows, table._ref, logit_scale, out.data_ptr(), _DTYPES[out.dtype],
-                                 out.stride(0) if rows > 1 else table.V, _ptr(dev_status), _current_stream()),
-           "lmh_project_q4")
+        out = torch.empty((rows, V), dtype=out_dtype, device=dev)
+        out_pitch = V
+    else:
+        assert out.is_cuda and out.shape == (rows, V) and (out.stride(1) == 1 or V == 1)
+        out_pitch = out.stride(0) if rows > 1 else V
+    st = (_lib or load()).lmh_project_q4(
+        hidden.data_ptr(), _DTYPES[hidden.dtype], pitch if T > 1 else H, T, _ptr(row_idx), rows, table._arg,
+        logit_scale, out.data_ptr(), _DTYPES[out.dtype], out_pitch, _ptr(dev_status), _raw_stream(dev))
+    if st != OK:
+        raise LMHError(st, "lmh_project_q4")
     return out
 
 
-@_on_stream
-def lookup_q4(ids, table, scale=1.0, out_dtype=torch.bfloat16, out=None, dev_status=None):
+def lookup_q4(ids, table, scale=1.0, out_dtype=torch.bfloat16, out=None, dev_status=None, stream=None):
     """The rows [n, H] of int32 device ids from a 4-bit table, times scale (lmh_lookup_q4); an id of
-    -1 (no token) gives zeros."""
-    assert ids.is_cuda and ids.dtype == torch.int32 and ids.dim() == 1 and ids.is_contiguous()
-    n = ids.numel()
+    -1 (no token) gives zeros.  stream: as sample_from_logits."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return lookup_q4(ids, table, scale, out_dtype, out, dev_status)
+    n, = ids.shape
+    H = table.H
+    dev = ids.device
+    assert dev == table.device and ids.dtype == torch.int32 and ids.is_contiguous()
     if out is None:
-        out = torch.empty((n, table.H), dtype=out_dtype, device=ids.device)
-    assert out.is_cuda and tuple(out.shape) == (n, table.H) and out.stride(1) == 1
-    _check(load().lmh_lookup_q4(ids.data_ptr(), n, table._ref, scale, out.data_ptr(), _DTYPES[out.dtype],
-                                out.stride(0) if n > 1 else table.H, _ptr(dev_status), _current_stream()),
-           "lmh_lookup_q4")
+        out = torch.empty((n, H), dtype=out_dtype, device=dev)
+        out_pitch = H
+    else:
+        assert out.is_cuda and out.shape == (n, H) and out.stride(1) == 1
+        out_pitch = out.stride(0) if n > 1 else H
+    st = (_lib or load()).lmh_lookup_q4(ids.data_ptr(), n, table._arg, scale, out.data_ptr(), _DTYPES[out.dtype],
+                                        out_pitch, _ptr(dev_status), _raw_stream(dev))
+    if st != OK:
+        raise LMHError(st, "lmh_lookup_q4")
     return out
 
 
