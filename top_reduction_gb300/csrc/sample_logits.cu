@@ -17,8 +17,8 @@
 // Two ways to the kept tokens of a row with top-k or top-p:
 // - A list.  Every lane knows the largest of its own logits.  A histogram of these
 //   maxima over t gives a bound that at least k tokens reach (128 for top-p alone),
-//   few more than that do, and only lanes whose maximum reaches it look at their
-//   logits again.  The tokens that reach it go to the cluster's first CTA, which ranks
+//   few more than that do, and only warps with such a lane look at their logits
+//   again.  The tokens that reach it go to the cluster's first CTA, which ranks
 //   them by counting: with n tokens, n^2 comparisons give every token its rank and the
 //   mass before it.  This holds for k up to kListTarget, and for top-p wherever the
 //   listed tokens have the mass that is asked for.
@@ -28,7 +28,10 @@
 //   histogram of all logits over t, one of the bin that holds the end over its 512th
 //   parts, and a list of what is left there.  Where that is too long (many equal
 //   logits), histograms over ever smaller intervals of z go on until one value is left,
-//   whose tokens are counted off in id order.
+//   whose tokens are counted off in id order.  The bins that the second histogram cuts
+//   up come from a sample of the row, with a margin, in place of the first histogram: an
+//   addition in shared memory for every logit costs more than all arithmetic on it.
+//   Sums stay exact, so a sample that misses costs time, not the result.
 // Tokens of weight 0 (t < -33) can be left out of either: no draw falls on them and no
 // sum changes.
 //
@@ -57,6 +60,7 @@ constexpr int kListCap = 512;          // tokens in a list, and in one CTA's par
 constexpr int kListTarget = 384;       // largest k that is tried with a list
 constexpr int kListTargetTopP = 128;   // tokens asked for with top-p alone
 constexpr float kMinT = -33.0f;        // below: weight 0
+constexpr int kSampleFromV = 16384;    // vocabularies whose threshold searches begin with a sample
 constexpr int kUnroll = 4;             // vectors of a lane whose mask words are in flight at once
 constexpr float kHiAdd = 768.0f;             // 1.5 * 2^9: unit 2^-14
 constexpr float kLoAdd = 0.0029296875f;      // 1.5 * 2^-9: unit 2^-32
@@ -100,6 +104,9 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
 }
 __device__ __forceinline__ void st_cluster_u64(uint32_t a, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t a) {
   uint32_t v;
@@ -285,7 +292,7 @@ struct Shared {
   uint32_t list_hist[kBins];
   uint32_t list_n;
   int list_ok;
-  u64 list_key;
+  u64 list_key, list_mass;
   union {
     uint32_t hist[2][2][kBins];  // [which][high, low part or count][bin]
     struct {
@@ -297,7 +304,7 @@ struct Shared {
   u64 scratch[kWarps];
   u64 warp_mass[kWarps];
   u64 found_above;
-  int found_bin;
+  int found_bin, found_hi;
   int count;
   u64 kept, point;
   uint64_t arrived[kWarps];  // barriers: a warp's part of the row is there
@@ -417,6 +424,33 @@ __device__ __noinline__ int find_bin(u64 mine, u64 target, u64 above) {
   }
   __syncthreads();
   return sh.found_bin;
+}
+
+// The bins, sh.found_bin to sh.found_hi, between which a prefix of the row should end by
+// a sample's histogram (`mine` this thread's bin of it): where the sample's sums are
+// within `margin` of `share` of its whole sum, or of `share` itself where it is above 1.
+__device__ __noinline__ void find_bracket(u64 mine, float share, float margin, int first) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  u64 incl = warp_scan_u64(mine);
+  __syncthreads();
+  if (lane == 31) sh.scratch[warp] = incl;
+  if (tid == 0) {
+    sh.found_bin = first;
+    sh.found_hi = kBins - 1;
+  }
+  __syncthreads();
+  u64 all = 0;
+#pragma unroll 1
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) incl += sh.scratch[w];
+    all += sh.scratch[w];
+  }
+  const float unit = share > 1.0f ? 1.0f : static_cast<float>(all);
+  const float from = (share - margin) * unit, to = (share + margin) * unit;
+  const float below = static_cast<float>(incl - mine), upto = static_cast<float>(incl);
+  if (tid > first && below < from && upto >= from) sh.found_bin = tid;
+  if (tid >= first && below < to && upto >= to) sh.found_hi = tid;
+  __syncthreads();
 }
 
 // The first CTA fetches the CTAs' parts of a list: their tokens' number, or -1 if they
@@ -616,25 +650,41 @@ class RowSampler {
     parity_ ^= 1;
     return cluster_sum(v, parity_);
   }
-  __device__ __forceinline__ bool is_kept(float z, int id, const Kept& k) const {
-    return t_of(z) >= k.min_t && (z > k.z_cut || (z == k.z_cut && id <= k.id_cut));
+  // (no short cuts: these would be branches for every logit)
+  static __device__ __forceinline__ bool kept_by(const Kept& k, float t, float z, int id) {
+    return (t >= k.min_t) & ((z > k.z_cut) | ((z == k.z_cut) & (id <= k.id_cut)));
   }
+  __device__ __forceinline__ bool is_kept(float z, int id, const Kept& k) const { return kept_by(k, t_of(z), z, id); }
   template <bool kEvery>
   __device__ __forceinline__ u64 warp_mass(const Kept& k);
-  __device__ __forceinline__ void threshold(bool by_mass, u64 target, Kept* k);
+  __device__ __forceinline__ void threshold(bool by_mass, u64 target, u64 total, int listed_bin, u64 listed_mass,
+                                            Kept* k);
   __device__ __forceinline__ void draw(const Kept& k);
   __device__ __forceinline__ void greedy();
-  __device__ __forceinline__ bool from_list(int top_k, float top_p, float min_t, u64* mass);
+  __device__ __forceinline__ bool from_list(int top_k, float top_p, float min_t, u64* mass, int* listed_bin,
+                                            u64* listed_mass);
   // Place of t on the scale of 0 .. kMinT, cut into kBins bins (kBins: no weight).
   __device__ __forceinline__ float place(float t) const {
     return t >= kMinT ? __fmul_rn(t, (kBins - 1) / kMinT) : kBins;
   }
-  // f(z, j) for this warp's elements j, one per lane at a time
-  template <typename F>
+  __device__ __forceinline__ int bin_of(float z) const { return static_cast<int>(place(t_of(z))); }
+  // f(z, j) for this warp's elements j, one per lane at a time; `kAtOnce` of them side by side
+  template <int kAtOnce, typename F>
   __device__ __forceinline__ void for_each_element(F&& f) const {
     const int m = n_ * kN;
-#pragma unroll 2
-    for (int j = lane_; j < m; j += 32) f(element(j), j);
+    int j = lane_;
+    if (kAtOnce > 1) {
+#pragma unroll 1
+      for (; j + 32 * (kAtOnce - 1) < m; j += 32 * kAtOnce) {
+        float z[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) z[u] = element(j + 32 * u);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) f(z[u], j + 32 * u);
+      }
+    }
+#pragma unroll 1
+    for (; j < m; j += 32) f(element(j), j);
   }
 };
 
@@ -740,8 +790,8 @@ __device__ __forceinline__ u64 RowSampler<T>::warp_mass(const Kept& k) {
       const float2 t = __fmul2_rn(__fadd2_rn(make_float2(z[e], z[e + 1]), zm2), c2);
       float2 w = make_float2(ex2_approx(t.x), ex2_approx(t.y));
       if (!kEvery) {
-        if (!(t.x >= k.min_t && (z[e] > k.z_cut || (z[e] == k.z_cut && id + e <= k.id_cut)))) w.x = 0.0f;
-        if (!(t.y >= k.min_t && (z[e + 1] > k.z_cut || (z[e + 1] == k.z_cut && id + e + 1 <= k.id_cut)))) w.y = 0.0f;
+        w.x = kept_by(k, t.x, z[e], id + e) ? w.x : 0.0f;
+        w.y = kept_by(k, t.y, z[e + 1], id + e + 1) ? w.y : 0.0f;
       }
       // weight_bits() of both
       const float2 h = __fadd2_rn(w, add_hi);
@@ -756,30 +806,68 @@ __device__ __forceinline__ u64 RowSampler<T>::warp_mass(const Kept& k) {
 
 // Narrows k->z_cut, k->id_cut to the shortest prefix of the order whose count (or
 // mass) reaches target >= 1.  A target above the total of the tokens with a weight
-// leaves k alone.
+// leaves k alone.  By mass: `total` is the row's, of which the tokens of bins 0 ..
+// listed_bin have listed_mass (-1 and 0: not known).
 template <typename T>
-__device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 target, Kept* k) {
-  u64 above = 0;  // count or mass of what comes before the bin
-  int bin = -1, part = -1;
-  auto part_of = [&](float x) {
-    return static_cast<int>(x) == bin ? min(static_cast<int>((x - bin) * kBins), kBins - 1) : kBins;
+__device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 target, u64 total, int listed_bin,
+                                                         u64 listed_mass, Kept* k) {
+  // The prefix ends in one of the bins [lo_bin, hi_bin] of t, whose range is cut into
+  // kBins parts.
+  int lo_bin = 0, hi_bin = 0, part = -1;
+  float per_bin = 0.0f;
+  u64 above = 0;  // count or mass of what comes before the part
+  auto part_of = [&](float x) -> int {
+    const int b = min(static_cast<int>((x - lo_bin) * per_bin), kBins - 1);
+    return ((x >= lo_bin) & (x < hi_bin + 1) & (x < kBins)) ? b : kBins;
   };
+  // The bins come from a sample, one logit of every vector, with a margin; where that was
+  // not enough (or the row is short), from all logits.
 #pragma unroll 1
-  for (int level = 0; level < 2; ++level) {
-    uint32_t(*hist)[kBins] = sh.hist[level];
-    clear_hist(hist);
-    for_each_element([&](float z, int) {
-      const float t = t_of(z), x = place(t);
-      const int b = level == 0 ? static_cast<int>(x) : part_of(x);
-      if (b < kBins) count_into(hist, b, by_mass, t);
-    });
+  for (int attempt = p_.V >= kSampleFromV ? 0 : 1; attempt < 2 && part < 0; ++attempt) {
+    clear_hist(sh.hist[0]);
+    const int step = attempt == 0 ? kN : 1;
+#pragma unroll 1
+    for (int j = lane_ * step; j < n_ * kN; j += 32 * step) {
+      const float t = t_of(element(j));
+      const int b = static_cast<int>(place(t));
+      if (b < kBins && (attempt > 0 || b > listed_bin)) count_into(sh.hist[0], b, by_mass, t);
+    }
     cluster_sync();
-    part = find_bin(gather_bin(hist[0], by_mass ? hist[1] : nullptr), target, above);
-    if (part < 0) return;
-    above = sh.found_above;
-    if (level == 0) bin = part;
+    const u64 mine = gather_bin(sh.hist[0][0], by_mass ? sh.hist[0][1] : nullptr);
+    if (attempt == 0) {
+      const float share = by_mass ? static_cast<float>(target - listed_mass) / static_cast<float>(total - listed_mass)
+                                  : 1.0f + static_cast<float>(target) / kN;
+      find_bracket(mine, share, by_mass ? 0.08f : 16.0f + 0.05f * share, listed_bin + 1);
+      lo_bin = sh.found_bin;
+      hi_bin = max(sh.found_hi, lo_bin);
+    } else {
+      lo_bin = hi_bin = find_bin(mine, target, 0);
+      if (lo_bin < 0) return;
+    }
+    per_bin = static_cast<float>(kBins) / static_cast<float>(hi_bin - lo_bin + 1);
+    // The bins' parts, and the sum of what comes before the bins.
+    clear_hist(sh.hist[1]);
+    uint32_t hi = 0, lo = 0, n = 0;
+    for_each_element<4>([&](float z, int) {
+      const float t = t_of(z), x = place(t);
+      uint32_t h, l;
+      weight_bits(x < lo_bin ? (by_mass ? ex2_approx(t) : 1.0f) : 0.0f, h, l);
+      hi += h;
+      lo += l;
+      ++n;
+      const int b = part_of(x);
+      if (b < kBins) count_into(sh.hist[1], b, by_mass, t);
+    });
+    u64 sum = weight_sum(hi, lo, n);
+    if (!by_mass) sum >>= 32;
+    above = sum_over(warp_sum_u64(sum)).all;
+    if (above < target) {
+      part = find_bin(gather_bin(sh.hist[1][0], by_mass ? sh.hist[1][1] : nullptr), target, above);
+      if (part >= 0) above = sh.found_above;
+    }
   }
-  for_each_element([&](float z, int j) {
+  if (part < 0) return;
+  for_each_element<4>([&](float z, int j) {
     if (part_of(place(t_of(z))) == part) {
       const uint32_t at = atomicAdd(&sh.list_n, 1u);
       if (at < kListCap) sh.part[at] = make_key(z, id0_ + j);
@@ -810,7 +898,7 @@ __device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 targe
   float hi, lo;
   {
     uint32_t top = 0, bottom = 0;  // of the order keys, and of their complements
-    for_each_element([&](float z, int) {
+    for_each_element<1>([&](float z, int) {
       if (part_of(place(t_of(z))) == part) {
         top = max(top, f32_ord(z));
         bottom = max(bottom, ~f32_ord(z));
@@ -829,14 +917,14 @@ __device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 targe
     const float inv = linear ? __fdiv_rn(kBins - 1, width) : 0.0f;
     const uint32_t ord_hi = f32_ord(hi);
     const int shift = max(0, 32 - __clz(ord_hi - f32_ord(lo)) - 9);
-    auto bin_of = [&](float z) -> int {
+    auto interval_bin = [&](float z) -> int {
       return linear ? min(static_cast<int>(__fmul_rn(__fsub_rn(hi, z), inv)), kBins - 1)
                     : static_cast<int>((ord_hi - f32_ord(z)) >> shift);
     };
     uint32_t(*hist)[kBins] = sh.hist[level & 1];
     clear_hist(hist);
-    for_each_element([&](float z, int) {
-      if (z >= lo && z <= hi) count_into(hist, bin_of(z), by_mass, t_of(z));
+    for_each_element<1>([&](float z, int) {
+      if (z >= lo && z <= hi) count_into(hist, interval_bin(z), by_mass, t_of(z));
     });
     cluster_sync();
     const int b = find_bin(gather_bin(hist[0], by_mass ? hist[1] : nullptr), target, above);
@@ -844,8 +932,8 @@ __device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 targe
     above = sh.found_above;
     // the bin's own extremes are the next interval
     uint32_t top = 0, bottom = 0;
-    for_each_element([&](float z, int) {
-      if (z >= lo && z <= hi && bin_of(z) == b) {
+    for_each_element<1>([&](float z, int) {
+      if (z >= lo && z <= hi && interval_bin(z) == b) {
         top = max(top, f32_ord(z));
         bottom = max(bottom, ~f32_ord(z));
       }
@@ -855,7 +943,7 @@ __device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 targe
   }
   // One value left, `hi`: of the tokens equal to it the first m in id order are kept.
   uint32_t mine = 0;
-  for_each_element([&](float z, int) { mine += z == hi ? 1 : 0; });
+  for_each_element<1>([&](float z, int) { mine += z == hi ? 1 : 0; });
   mine = __reduce_add_sync(0xffffffffu, mine);
   const Sum ties = sum_over(mine);
   u64 m = target - above;
@@ -886,11 +974,13 @@ __device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 targe
 }
 
 // Draws from a list, if one can be made: true when the row is done.  With top-p alone
-// *mass becomes the row's mass.
+// *mass becomes the row's mass, and *listed_mass that of the tokens in the bins up to
+// *listed_bin (-1 and 0 when there are too many).
 template <typename T>
-__device__ __forceinline__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, u64* mass) {
+__device__ __forceinline__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, u64* mass,
+                                                         int* listed_bin, u64* listed_mass) {
   const u64 target = top_k > 0 ? top_k : kListTargetTopP;
-  const int my_bin = static_cast<int>(place(t_of(lane_max_)));
+  const int my_bin = bin_of(lane_max_);
   if (my_bin < kBins) atomicAdd(&sh.list_hist[my_bin], 1u);
   if (top_k == 0)
     *mass = sum_over(warp_mass<true>(Kept{})).all;
@@ -899,39 +989,56 @@ __device__ __forceinline__ bool RowSampler<T>::from_list(int top_k, float top_p,
   // The last bin that is listed: the first at which the lanes' maxima reach the target.
   int last_bin = find_bin(gather_bin(sh.list_hist, nullptr), target, 0);
   if (last_bin < 0) last_bin = kBins - 1;
-  if (my_bin <= last_bin) {
+  if (__any_sync(0xffffffffu, my_bin <= last_bin)) {
+    // vectors whose maximum reaches it, then their elements side by side
 #pragma unroll 1
-    for (int i = lane_; i < n_; i += 32) {
-      if (static_cast<int>(place(t_of(Vec<T>::max_of(data_[i])))) > last_bin) continue;
+    for (int i0 = 0; i0 < n_; i0 += 32) {
+      const int i = i0 + lane_;
+      unsigned hits = __ballot_sync(0xffffffffu, i < n_ && bin_of(i < n_ ? Vec<T>::max_of(data_[i]) : 0.0f) <= last_bin);
 #pragma unroll 1
-      for (int j = i * kN; j < (i + 1) * kN; ++j) {
+      for (; hits != 0; hits &= hits - 1) {
+        const int j = (i0 + __ffs(hits) - 1) * kN + lane_;
+        if (lane_ >= kN) continue;
         const float z = element(j);
-        if (static_cast<int>(place(t_of(z))) <= last_bin) {
-          const uint32_t at = atomicAdd(&sh.list_n, 1u);
-          if (at < kListCap) sh.part[at] = make_key(z, id0_ + j);
-        }
+        if (bin_of(z) > last_bin) continue;
+        const uint32_t at = atomicAdd(&sh.list_n, 1u);
+        if (at < kListCap) sh.part[at] = make_key(z, id0_ + j);
       }
     }
   }
   cluster_sync();
   // The first CTA fetches the parts and says whether they will do.
-  u64 need = 0;
-  int total = 0;
   if (cluster_rank() == 0) {
-    total = fetch_list(zm_, c_);
+    u64 need = 0, have = 0;
+    const int total = fetch_list(zm_, c_);
     bool ok = total >= 0;
     if (ok && top_k == 0) {
       need = mass_wanted(top_p, *mass);
       // (a thread's token is the one that it fetched)
-      ok = block_sum_u64(static_cast<int>(threadIdx.x) < total ? sh.list[threadIdx.x].w : 0) >= need;
+      have = block_sum_u64(static_cast<int>(threadIdx.x) < total ? sh.list[threadIdx.x].w : 0);
+      ok = have >= need;
     }
-    if (threadIdx.x == 0) sh.list_ok = ok;
+    // its word to every CTA; it does not wait for them where they have nothing left to do
+    const int said = ok ? 1 : total < 0 ? 0 : 2;
+    if (threadIdx.x < cluster_size()) {
+      st_cluster_u64(cluster_addr(&sh.list_mass, threadIdx.x), have);
+      st_cluster_u32(cluster_addr(&sh.list_ok, threadIdx.x), said);
+    }
+    cluster_arrive();
+    if (ok) {
+      draw_from_list(p_, row_, total, top_k, top_p, need, min_t, uniform_, zm_, c_);
+      cluster_wait();
+      return true;
+    }
+    cluster_wait();
+  } else {
+    cluster_sync();
   }
-  cluster_sync();
-  const bool ok = ld_cluster_u32(cluster_addr(&sh.list_ok, 0)) != 0;
-  if (ok && cluster_rank() == 0)
-    draw_from_list(p_, row_, total, top_k, top_p, need, min_t, uniform_, zm_, c_);
-  return ok;
+  if (sh.list_ok == 2) {
+    *listed_bin = last_bin;
+    *listed_mass = sh.list_mass;
+  }
+  return sh.list_ok == 1;
 }
 
 // The token at the given point of the kept tokens' mass, in id order.
@@ -1012,7 +1119,7 @@ __device__ __forceinline__ bool RowSampler<T>::run() {
   }
   if (zm_ == INFINITY) {  // only the +inf tokens are left, as equals
     float m = -INFINITY;
-    for_each_element([&](float z, int j) {
+    for_each_element<1>([&](float z, int j) {
       const float y = z == INFINITY ? 0.0f : -INFINITY;
       reinterpret_cast<T*>(data_)[j] = Vec<T>::from_float(y);
       m = fmaxf(m, y);
@@ -1031,16 +1138,18 @@ __device__ __forceinline__ bool RowSampler<T>::run() {
   Kept k{-INFINITY, -INFINITY, INT32_MAX};
   const int top_k = top_k_ > 0 && top_k_ < p_.V ? top_k_ : 0;
   const float min_t = min_p_ > 0.0f ? fminf(log2f(min_p_), 0.0f) : -INFINITY;
-  u64 mass = 0;
+  u64 mass = 0, listed_mass = 0;
+  int listed_bin = -1;
   bool have_mass = false;
   if (top_k > 0 ? top_k <= kListTarget : top_p_ < 1.0f) {
-    if (from_list(top_k, top_p_, min_t, &mass)) return true;
+    if (from_list(top_k, top_p_, min_t, &mass, &listed_bin, &listed_mass)) return true;
     have_mass = top_k == 0;
   }
 #pragma unroll 1
   for (int by_mass = top_k > 0 ? 0 : 1; by_mass < (top_p_ < 1.0f ? 2 : 1); ++by_mass) {
     if (by_mass && !have_mass) mass = sum_over(warp_mass<false>(k)).all;
-    threshold(by_mass != 0, by_mass ? mass_wanted(top_p_, mass) : static_cast<u64>(top_k), &k);
+    threshold(by_mass != 0, by_mass ? mass_wanted(top_p_, mass) : static_cast<u64>(top_k), mass, listed_bin,
+              listed_mass, &k);
   }
   k.min_t = min_t;
   draw(k);
