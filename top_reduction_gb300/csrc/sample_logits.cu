@@ -16,7 +16,7 @@
 //
 // Two ways to the kept tokens of a row with top-k or top-p:
 // - A list.  Every lane knows the largest of its own logits.  A histogram of these
-//   maxima over t gives a bound that at least k tokens reach (128 for top-p alone),
+//   maxima over z gives a bound that at least k tokens reach (128 for top-p alone),
 //   few more than that do, and only warps with such a lane look at their logits
 //   again.  The tokens that reach it go to the cluster's first CTA, which ranks
 //   them by counting: with n tokens, n^2 comparisons give every token its rank and the
@@ -60,6 +60,8 @@ constexpr int kListCap = 512;          // tokens in a list, and in one CTA's par
 constexpr int kListTarget = 384;       // largest k that is tried with a list
 constexpr int kListTargetTopP = 128;   // tokens asked for with top-p alone
 constexpr float kMinT = -33.0f;        // below: weight 0
+constexpr float kMaxBinsTop = 64.0f;   // the lanes' maxima: bins from this z down,
+constexpr float kMaxBinsPer = 4.0f;    // so many to a unit
 constexpr int kSampleFromV = 16384;    // vocabularies whose threshold searches begin with a sample
 constexpr int kUnroll = 4;             // vectors of a lane whose mask words are in flight at once
 constexpr float kHiAdd = 768.0f;             // 1.5 * 2^9: unit 2^-14
@@ -127,6 +129,7 @@ struct Vec;  // kN elements a vector; to_float and widen are exact
 template <>
 struct Vec<float> {
   static constexpr int kN = 4;
+  static constexpr int kZeroBits = 0;  // low bits of a widened value that are always 0
   static __device__ __forceinline__ void widen(const uint4& x, float (&z)[4]) {
     z[0] = __uint_as_float(x.x);
     z[1] = __uint_as_float(x.y);
@@ -175,6 +178,7 @@ __device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int kN = 8;
+  static constexpr int kZeroBits = 16;
   static __device__ __forceinline__ void widen(const uint4& x, float (&z)[8]) {
     const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -197,6 +201,7 @@ struct Vec<__nv_bfloat16> {
 template <>
 struct Vec<__half> {
   static constexpr int kN = 8;
+  static constexpr int kZeroBits = 13;
   static __device__ __forceinline__ void widen(const uint4& x, float (&z)[8]) {
     const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -293,6 +298,7 @@ struct Shared {
   uint32_t list_n;
   int list_ok;
   u64 list_key, list_mass;
+  u64 part_n[kMaxCluster], part_ends[kMaxCluster];  // each CTA's, as `slot`
   union {
     uint32_t hist[2][2][kBins];  // [which][high, low part or count][bin]
     struct {
@@ -305,6 +311,7 @@ struct Shared {
   u64 warp_mass[kWarps];
   u64 found_above;
   int found_bin, found_hi;
+  uint32_t extremes[2];
   int count;
   u64 kept, point;
   uint64_t arrived[kWarps];  // barriers: a warp's part of the row is there
@@ -429,13 +436,13 @@ __device__ __noinline__ int find_bin(u64 mine, u64 target, u64 above) {
 // The bins, sh.found_bin to sh.found_hi, between which a prefix of the row should end by
 // a sample's histogram (`mine` this thread's bin of it): where the sample's sums are
 // within `margin` of `share` of its whole sum, or of `share` itself where it is above 1.
-__device__ __noinline__ void find_bracket(u64 mine, float share, float margin, int first) {
+__device__ __noinline__ void find_bracket(u64 mine, float share, float margin) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
   u64 incl = warp_scan_u64(mine);
   __syncthreads();
   if (lane == 31) sh.scratch[warp] = incl;
   if (tid == 0) {
-    sh.found_bin = first;
+    sh.found_bin = 0;
     sh.found_hi = kBins - 1;
   }
   __syncthreads();
@@ -445,11 +452,13 @@ __device__ __noinline__ void find_bracket(u64 mine, float share, float margin, i
     if (w < warp) incl += sh.scratch[w];
     all += sh.scratch[w];
   }
+  // (not so far up that a share near 1 takes in the whole tail)
   const float unit = share > 1.0f ? 1.0f : static_cast<float>(all);
-  const float from = (share - margin) * unit, to = (share + margin) * unit;
+  const float from = (share - margin) * unit;
+  const float to = (share > 1.0f ? share + margin : fminf(share + margin, 1.0f - 0.125f * (1.0f - share))) * unit;
   const float below = static_cast<float>(incl - mine), upto = static_cast<float>(incl);
-  if (tid > first && below < from && upto >= from) sh.found_bin = tid;
-  if (tid >= first && below < to && upto >= to) sh.found_hi = tid;
+  if (below < from && upto >= from) sh.found_bin = tid;
+  if (below < to && upto >= to) sh.found_hi = tid;
   __syncthreads();
 }
 
@@ -596,7 +605,7 @@ __device__ __forceinline__ void clear_hist(uint32_t (*hist)[kBins]) {
   __syncthreads();
   hist[0][threadIdx.x] = 0;
   hist[1][threadIdx.x] = 0;
-  if (threadIdx.x == 0) sh.list_n = 0;
+  if (threadIdx.x == 0) sh.list_n = sh.extremes[0] = sh.extremes[1] = 0;
   __syncthreads();
 }
 
@@ -612,9 +621,9 @@ class RowSampler {
     lane_ = threadIdx.x & 31;
     warp_ = threadIdx.x >> 5;
     parity_ = 0;
-    cluster_arrive();  // (waited for before the first word goes to another CTA)
     sh.list_hist[threadIdx.x] = 0;
     if (threadIdx.x == 0) sh.list_n = 0;
+    cluster_arrive();  // (waited for before these are counted up, or a word goes to another CTA)
     // (in flight while the row is loaded)
     temperature_ = p.f.temperature ? __ldg(p.f.temperature + row) : 1.0f;
     top_k_ = p.f.top_k ? __ldg(p.f.top_k + row) : 0;
@@ -657,17 +666,31 @@ class RowSampler {
   __device__ __forceinline__ bool is_kept(float z, int id, const Kept& k) const { return kept_by(k, t_of(z), z, id); }
   template <bool kEvery>
   __device__ __forceinline__ u64 warp_mass(const Kept& k);
-  __device__ __forceinline__ void threshold(bool by_mass, u64 target, u64 total, int listed_bin, u64 listed_mass,
+  __device__ __forceinline__ void threshold(bool by_mass, u64 target, u64 total, float listed_t, u64 listed_mass,
                                             Kept* k);
   __device__ __forceinline__ void draw(const Kept& k);
   __device__ __forceinline__ void greedy();
-  __device__ __forceinline__ bool from_list(int top_k, float top_p, float min_t, u64* mass, int* listed_bin,
+  __device__ __forceinline__ bool from_list(int top_k, float top_p, float min_t, u64* mass, float* listed_t,
                                             u64* listed_mass);
   // Place of t on the scale of 0 .. kMinT, cut into kBins bins (kBins: no weight).
   __device__ __forceinline__ float place(float t) const {
     return t >= kMinT ? __fmul_rn(t, (kBins - 1) / kMinT) : kBins;
   }
-  __device__ __forceinline__ int bin_of(float z) const { return static_cast<int>(place(t_of(z))); }
+  // Bin of a lane's maximum: over z itself, so that the histogram needs no maximum of the
+  // row; the ends take what lies outside (kBins: -inf).
+  static __device__ __forceinline__ int max_bin(float z) {
+    const float x = fminf(fmaxf(kMaxBinsTop - z, 0.0f) * kMaxBinsPer, kBins - 1.0f);
+    return z > -INFINITY ? static_cast<int>(x) : kBins;
+  }
+  __device__ __forceinline__ void count_max() {
+    const int b = max_bin(lane_max_);
+    if (b < kBins && (top_k_ > 0 || top_p_ < 1.0f)) atomicAdd(&sh.list_hist[b], 1u);
+  }
+  // The value whose order key without its constant low bits (kZeroBits) is `high`.
+  static __device__ __forceinline__ float key_value_of(uint32_t high) {
+    const uint32_t low = (1u << Vec<T>::kZeroBits) - 1u, key = high << Vec<T>::kZeroBits;
+    return ord_f32(key & 0x80000000u ? key : key | low);
+  }
   // f(z, j) for this warp's elements j, one per lane at a time; `kAtOnce` of them side by side
   template <int kAtOnce, typename F>
   __device__ __forceinline__ void for_each_element(F&& f) const {
@@ -806,22 +829,27 @@ __device__ __forceinline__ u64 RowSampler<T>::warp_mass(const Kept& k) {
 
 // Narrows k->z_cut, k->id_cut to the shortest prefix of the order whose count (or
 // mass) reaches target >= 1.  A target above the total of the tokens with a weight
-// leaves k alone.  By mass: `total` is the row's, of which the tokens of bins 0 ..
-// listed_bin have listed_mass (-1 and 0: not known).
+// leaves k alone.  By mass: `total` is the row's, of which the tokens above listed_t
+// (there or thereabouts: it is the sample that leaves them out) have listed_mass.
 template <typename T>
-__device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 target, u64 total, int listed_bin,
+__device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 target, u64 total, float listed_t,
                                                          u64 listed_mass, Kept* k) {
-  // The prefix ends in one of the bins [lo_bin, hi_bin] of t, whose range is cut into
-  // kBins parts.
-  int lo_bin = 0, hi_bin = 0, part = -1;
-  float per_bin = 0.0f;
+  // The prefix ends at a t of [t0, t1], which is cut into kBins parts: by distinct values
+  // where a 16-bit type has no more of them there, so that a part's mass is its count
+  // times one weight, else linear in t.
+  float t1 = INFINITY, t0 = kMinT, per_t = 0.0f;
+  uint32_t key_top = 0;
+  bool by_key = false;
+  int part = -1;
   u64 above = 0;  // count or mass of what comes before the part
-  auto part_of = [&](float x) -> int {
-    const int b = min(static_cast<int>((x - lo_bin) * per_bin), kBins - 1);
-    return ((x >= lo_bin) & (x < hi_bin + 1) & (x < kBins)) ? b : kBins;
+  auto inside = [&](float t) { return (t <= t1) & (t >= t0); };
+  auto part_of = [&](float z, float t) -> int {
+    const int b = by_key ? static_cast<int>(key_top - (f32_ord(z) >> Vec<T>::kZeroBits))
+                         : static_cast<int>((fminf(t1, 0.0f) - t) * per_t);
+    return min(max(b, 0), kBins - 1);
   };
-  // The bins come from a sample, one logit of every vector, with a margin; where that was
-  // not enough (or the row is short), from all logits.
+  // The interval comes from a sample, one logit of every vector, with a margin; where that
+  // was not enough (or the row is short), from all logits.
 #pragma unroll 1
   for (int attempt = p_.V >= kSampleFromV ? 0 : 1; attempt < 2 && part < 0; ++attempt) {
     clear_hist(sh.hist[0]);
@@ -830,83 +858,144 @@ __device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 targe
     for (int j = lane_ * step; j < n_ * kN; j += 32 * step) {
       const float t = t_of(element(j));
       const int b = static_cast<int>(place(t));
-      if (b < kBins && (attempt > 0 || b > listed_bin)) count_into(sh.hist[0], b, by_mass, t);
+      if (b < kBins && (attempt > 0 || t <= listed_t)) count_into(sh.hist[0], b, by_mass, t);
     }
     cluster_sync();
-    const u64 mine = gather_bin(sh.hist[0][0], by_mass ? sh.hist[0][1] : nullptr);
+    const u64 bin_sum = gather_bin(sh.hist[0][0], by_mass ? sh.hist[0][1] : nullptr);
+    int lo_bin, hi_bin;
     if (attempt == 0) {
       const float share = by_mass ? static_cast<float>(target - listed_mass) / static_cast<float>(total - listed_mass)
                                   : 1.0f + static_cast<float>(target) / kN;
-      find_bracket(mine, share, by_mass ? 0.08f : 16.0f + 0.05f * share, listed_bin + 1);
+      find_bracket(bin_sum, share, by_mass ? 0.08f : 16.0f + 0.05f * share);
       lo_bin = sh.found_bin;
       hi_bin = max(sh.found_hi, lo_bin);
     } else {
-      lo_bin = hi_bin = find_bin(mine, target, 0);
+      lo_bin = hi_bin = find_bin(bin_sum, target, 0);
       if (lo_bin < 0) return;
     }
-    per_bin = static_cast<float>(kBins) / static_cast<float>(hi_bin - lo_bin + 1);
-    // The bins' parts, and the sum of what comes before the bins.
+    // (a bin more on either side: the ends are not the bins' to the last bit)
+    t1 = lo_bin <= 1 ? INFINITY : static_cast<float>(lo_bin - 1) * (kMinT / (kBins - 1));
+    t0 = fmaxf(kMinT, static_cast<float>(hi_bin + 2) * (kMinT / (kBins - 1)));
+    per_t = static_cast<float>(kBins) / (fminf(t1, 0.0f) - t0);
+    if (Vec<T>::kZeroBits > 0) {
+      // the interval in z, with room for the roundings of t: no z inside may miss the parts
+      const float z1 = zm_ + fminf(t1, 0.0f) / c_, z0 = zm_ + t0 / c_;
+      const float from = z0 - 1e-6f * (fabsf(zm_) + fabsf(z0));
+      key_top = (f32_ord(z1 + 1e-6f * (fabsf(zm_) + fabsf(z1))) >> Vec<T>::kZeroBits) + 1;
+      by_key = from > -INFINITY && key_top - (f32_ord(from) >> Vec<T>::kZeroBits) + 1 < kBins;
+    }
+    // The interval's parts, and the sum of what comes before it.
     clear_hist(sh.hist[1]);
     uint32_t hi = 0, lo = 0, n = 0;
-    for_each_element<4>([&](float z, int) {
-      const float t = t_of(z), x = place(t);
-      uint32_t h, l;
-      weight_bits(x < lo_bin ? (by_mass ? ex2_approx(t) : 1.0f) : 0.0f, h, l);
-      hi += h;
-      lo += l;
-      ++n;
-      const int b = part_of(x);
-      if (b < kBins) count_into(sh.hist[1], b, by_mass, t);
-    });
+#pragma unroll 1
+    for (int i = lane_; i < n_; i += 32) {
+      float z[kN];
+      Vec<T>::widen(data_[i], z);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        const float t = t_of(z[e]);
+        const float w = by_mass ? ex2_approx(t) : 1.0f;
+        uint32_t h, l;
+        weight_bits(t > t1 ? w : 0.0f, h, l);
+        hi += h;
+        lo += l;
+        if (inside(t)) {
+          const int b = part_of(z[e], t);
+          if (by_mass && !by_key) {
+            weight_bits(w, h, l);
+            const u64 one = weight_sum(h, l, 1);
+            atomicAdd(&sh.hist[1][0][b], static_cast<uint32_t>(one >> 16));
+            atomicAdd(&sh.hist[1][1][b], static_cast<uint32_t>(one) & 0xFFFFu);
+          } else {
+            atomicAdd(&sh.hist[1][0][b], 1u);
+          }
+        }
+      }
+      n += kN;
+    }
     u64 sum = weight_sum(hi, lo, n);
     if (!by_mass) sum >>= 32;
     above = sum_over(warp_sum_u64(sum)).all;
     if (above < target) {
-      part = find_bin(gather_bin(sh.hist[1][0], by_mass ? sh.hist[1][1] : nullptr), target, above);
+      u64 mine = gather_bin(sh.hist[1][0], by_mass && !by_key ? sh.hist[1][1] : nullptr);
+      if (by_mass && by_key) mine *= weight_of(t_of(key_value_of(key_top - threadIdx.x)));
+      part = find_bin(mine, target, above);
       if (part >= 0) above = sh.found_above;
     }
   }
   if (part < 0) return;
-  for_each_element<4>([&](float z, int j) {
-    if (part_of(place(t_of(z))) == part) {
-      const uint32_t at = atomicAdd(&sh.list_n, 1u);
-      if (at < kListCap) sh.part[at] = make_key(z, id0_ + j);
+  // The part's tokens: their number and extremes, and a list where they are not equals.
+  uint32_t mine = 0, top = 0, bottom = 0;  // of the order keys, and of their complements
+  if (by_key) {
+    const float v = key_value_of(key_top - part);
+#pragma unroll 1
+    for (int i = lane_; i < n_; i += 32) {
+      float z[kN];
+      Vec<T>::widen(data_[i], z);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) mine += z[e] == v ? 1 : 0;
     }
-  });
+    top = f32_ord(v);
+    bottom = ~top;
+  } else {
+    for_each_element<4>([&](float z, int j) {
+      const float t = t_of(z);
+      if (inside(t) && part_of(z, t) == part) {
+        ++mine;
+        top = max(top, f32_ord(z));
+        bottom = max(bottom, ~f32_ord(z));
+        const uint32_t at = atomicAdd(&sh.list_n, 1u);
+        if (at < kListCap) sh.part[at] = make_key(z, id0_ + j);
+      }
+    });
+  }
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  top = __reduce_max_sync(0xffffffffu, top);
+  bottom = __reduce_max_sync(0xffffffffu, bottom);
+  if (lane_ == 0) {
+    sh.warp_mass[warp_] = mine;
+    if (by_key) atomicAdd(&sh.list_n, mine);
+    atomicMax(&sh.extremes[0], top);
+    atomicMax(&sh.extremes[1], bottom);
+  }
+  __syncthreads();
+  const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  if (static_cast<int>(threadIdx.x) < size) {
+    st_cluster_u64(cluster_addr(&sh.part_n[rank], threadIdx.x), sh.list_n);
+    st_cluster_u64(cluster_addr(&sh.part_ends[rank], threadIdx.x),
+                   (static_cast<u64>(sh.extremes[0]) << 32) | sh.extremes[1]);
+  }
   cluster_sync();
-  if (cluster_rank() == 0) {
-    const int n = fetch_list(zm_, c_);
-    if (n >= 0) {
+  u64 n_all = 0, n_before = 0;
+  top = bottom = 0;
+#pragma unroll 1
+  for (int r = 0; r < size; ++r) {
+    n_all += sh.part_n[r];
+    if (r < rank) n_before += sh.part_n[r];
+    top = max(top, static_cast<uint32_t>(sh.part_ends[r] >> 32));
+    bottom = max(bottom, static_cast<uint32_t>(sh.part_ends[r]));
+  }
+  float hi = ord_f32(top), lo = ord_f32(~bottom);
+  if (lo < hi && n_all <= kListCap) {
+    // The first CTA ranks the list and tells every CTA the last token of the prefix.
+    if (rank == 0) {
+      const int n = fetch_list(zm_, c_);
       rank_list(n);
       if (static_cast<int>(threadIdx.x) < n) {
         const u64 r = sh.part[threadIdx.x];
         const Listed it = sh.list[threadIdx.x];
         const u64 before = above + (by_mass ? r & 0xFFFFFFFFFFFFull : r >> 48);
-        if (before < target && before + (by_mass ? it.w : 1) >= target) sh.list_key = it.key;
+        if (before < target && before + (by_mass ? it.w : 1) >= target)
+          for (int q = 0; q < size; ++q) st_cluster_u64(cluster_addr(&sh.list_key, q), it.key);
       }
     }
-    if (threadIdx.x == 0) sh.list_ok = n >= 0;
-  }
-  cluster_sync();
-  if (ld_cluster_u32(cluster_addr(&sh.list_ok, 0)) != 0) {
-    const u64 key = ld_cluster_u64(cluster_addr(&sh.list_key, 0));
-    k->z_cut = key_value(key);
-    k->id_cut = key_id(key);
+    cluster_sync();
+    k->z_cut = key_value(sh.list_key);
+    k->id_cut = key_id(sh.list_key);
     return;
   }
-  // Too many in one part of a bin: go on with its extremes.
-  float hi, lo;
-  {
-    uint32_t top = 0, bottom = 0;  // of the order keys, and of their complements
-    for_each_element<1>([&](float z, int) {
-      if (part_of(place(t_of(z))) == part) {
-        top = max(top, f32_ord(z));
-        bottom = max(bottom, ~f32_ord(z));
-      }
-    });
-    hi = ord_f32(max_over(top));
-    lo = ord_f32(~max_over(bottom));
-  }
+  // Too many: go on with the interval of z between the extremes, or count off equals.
+  const bool counted = !(lo < hi);
 #pragma unroll 1
   for (int level = 0; lo < hi; ++level) {
     // Bins over [lo, hi], bin 0 at the top: linear in z first, which spreads a
@@ -931,7 +1020,7 @@ __device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 targe
     if (b < 0) return;  // (not reached: the target lies in [lo, hi])
     above = sh.found_above;
     // the bin's own extremes are the next interval
-    uint32_t top = 0, bottom = 0;
+    top = bottom = 0;
     for_each_element<1>([&](float z, int) {
       if (z >= lo && z <= hi && interval_bin(z) == b) {
         top = max(top, f32_ord(z));
@@ -942,10 +1031,13 @@ __device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 targe
     lo = ord_f32(~max_over(bottom));
   }
   // One value left, `hi`: of the tokens equal to it the first m in id order are kept.
-  uint32_t mine = 0;
-  for_each_element<1>([&](float z, int) { mine += z == hi ? 1 : 0; });
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  const Sum ties = sum_over(mine);
+  Sum ties{n_all, n_before};
+  if (!counted) {
+    mine = 0;
+    for_each_element<1>([&](float z, int) { mine += z == hi ? 1 : 0; });
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    ties = sum_over(mine);
+  }
   u64 m = target - above;
   if (by_mass) {
     const u64 w = weight_of(t_of(hi));
@@ -974,33 +1066,29 @@ __device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 targe
 }
 
 // Draws from a list, if one can be made: true when the row is done.  With top-p alone
-// *mass becomes the row's mass, and *listed_mass that of the tokens in the bins up to
-// *listed_bin (-1 and 0 when there are too many).
+// *mass becomes the row's mass, and *listed_mass that of the tokens down to *listed_t
+// (+inf and 0 when there are too many).
 template <typename T>
 __device__ __forceinline__ bool RowSampler<T>::from_list(int top_k, float top_p, float min_t, u64* mass,
-                                                         int* listed_bin, u64* listed_mass) {
+                                                         float* listed_t, u64* listed_mass) {
   const u64 target = top_k > 0 ? top_k : kListTargetTopP;
-  const int my_bin = bin_of(lane_max_);
-  if (my_bin < kBins) atomicAdd(&sh.list_hist[my_bin], 1u);
-  if (top_k == 0)
-    *mass = sum_over(warp_mass<true>(Kept{})).all;
-  else
-    cluster_sync();
+  const int my_bin = max_bin(lane_max_);
+  if (top_k == 0) *mass = sum_over(warp_mass<true>(Kept{})).all;
   // The last bin that is listed: the first at which the lanes' maxima reach the target.
   int last_bin = find_bin(gather_bin(sh.list_hist, nullptr), target, 0);
-  if (last_bin < 0) last_bin = kBins - 1;
+  if (last_bin < 0) last_bin = kBins - 1;  // (all there are)
   if (__any_sync(0xffffffffu, my_bin <= last_bin)) {
     // vectors whose maximum reaches it, then their elements side by side
 #pragma unroll 1
     for (int i0 = 0; i0 < n_; i0 += 32) {
       const int i = i0 + lane_;
-      unsigned hits = __ballot_sync(0xffffffffu, i < n_ && bin_of(i < n_ ? Vec<T>::max_of(data_[i]) : 0.0f) <= last_bin);
+      unsigned hits = __ballot_sync(0xffffffffu, i < n_ && max_bin(i < n_ ? Vec<T>::max_of(data_[i]) : 0.0f) <= last_bin);
 #pragma unroll 1
       for (; hits != 0; hits &= hits - 1) {
         const int j = (i0 + __ffs(hits) - 1) * kN + lane_;
         if (lane_ >= kN) continue;
         const float z = element(j);
-        if (bin_of(z) > last_bin) continue;
+        if (max_bin(z) > last_bin) continue;
         const uint32_t at = atomicAdd(&sh.list_n, 1u);
         if (at < kListCap) sh.part[at] = make_key(z, id0_ + j);
       }
@@ -1035,7 +1123,7 @@ __device__ __forceinline__ bool RowSampler<T>::from_list(int top_k, float top_p,
     cluster_sync();
   }
   if (sh.list_ok == 2) {
-    *listed_bin = last_bin;
+    *listed_t = t_of(kMaxBinsTop - static_cast<float>(last_bin + 1) / kMaxBinsPer);
     *listed_mass = sh.list_mass;
   }
   return sh.list_ok == 1;
@@ -1108,6 +1196,7 @@ __device__ __forceinline__ void RowSampler<T>::greedy() {
 template <typename T>
 __device__ __forceinline__ bool RowSampler<T>::run() {
   cluster_wait();  // every CTA of the cluster has started
+  count_max();
   zm_ = ord_f32(max_over(f32_ord(lane_max_)));
   if (zm_ == -INFINITY) {
     if (cluster_rank() == 0 && threadIdx.x == 0) {
@@ -1128,6 +1217,11 @@ __device__ __forceinline__ bool RowSampler<T>::run() {
     // (the lanes of a warp that holds one may all look for it)
     lane_max_ = __any_sync(0xffffffffu, m == 0.0f) ? 0.0f : -INFINITY;
     zm_ = 0.0f;
+    __syncthreads();
+    sh.list_hist[threadIdx.x] = 0;
+    __syncthreads();
+    count_max();
+    cluster_sync();
   }
   if (!(temperature_ > 0.0f)) {
     greedy();
@@ -1139,16 +1233,16 @@ __device__ __forceinline__ bool RowSampler<T>::run() {
   const int top_k = top_k_ > 0 && top_k_ < p_.V ? top_k_ : 0;
   const float min_t = min_p_ > 0.0f ? fminf(log2f(min_p_), 0.0f) : -INFINITY;
   u64 mass = 0, listed_mass = 0;
-  int listed_bin = -1;
+  float listed_t = INFINITY;
   bool have_mass = false;
   if (top_k > 0 ? top_k <= kListTarget : top_p_ < 1.0f) {
-    if (from_list(top_k, top_p_, min_t, &mass, &listed_bin, &listed_mass)) return true;
+    if (from_list(top_k, top_p_, min_t, &mass, &listed_t, &listed_mass)) return true;
     have_mass = top_k == 0;
   }
 #pragma unroll 1
   for (int by_mass = top_k > 0 ? 0 : 1; by_mass < (top_p_ < 1.0f ? 2 : 1); ++by_mass) {
     if (by_mass && !have_mass) mass = sum_over(warp_mass<false>(k)).all;
-    threshold(by_mass != 0, by_mass ? mass_wanted(top_p_, mass) : static_cast<u64>(top_k), mass, listed_bin,
+    threshold(by_mass != 0, by_mass ? mass_wanted(top_p_, mass) : static_cast<u64>(top_k), mass, listed_t,
               listed_mass, &k);
   }
   k.min_t = min_t;
