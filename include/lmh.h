@@ -493,7 +493,8 @@ lmh_status lmh_merge_records(const void* records, int32_t num_parts, int32_t row
  *   sampled_logprob   device fp32 [rows], out, or NULL.
  * No workspace is needed.  Errors: LMH_ERR_INVALID_ARG (null pointers, bad sizes,
  * mask_words < ceil(V / 32) with a mask), LMH_ERR_UNSUPPORTED (misaligned logits,
- * V > LMH_SAMPLE_V_MAX), LMH_ERR_CUDA.  Device: LMH_DS_NO_ALLOWED_TOKEN.
+ * V > LMH_SAMPLE_V_MAX), LMH_ERR_CUDA.  Device: LMH_DS_NO_ALLOWED_TOKEN,
+ * LMH_DS_TIMEOUT.
  */
 #define LMH_SAMPLE_V_MAX 393216
 
@@ -550,10 +551,12 @@ lmh_status lmh_quantize_q4(const void* W, int64_t w_row_stride, const lmh_q4_tab
  * lmh_project_q4 -- the head projection through a 4-bit table.
  *
  *   out[i][v] = logit_scale * sum_h hidden[row_idx[i]][h] * value[v][h]
- * The products are of the 16-bit inputs and the whole numbers q - zero (exact in
- * 16 bits); a group's sum is held in fp32, times its scale, and summed in fp32.
- * Rounded once, to out_dtype.  For batches of few rows (decode): up to 16 rows
- * cost one read of the table; more rows are taken 32 at a time.
+ * The products are of the 16-bit inputs and whole numbers (exact); a group's sum
+ * is held in fp32, times its scale, and summed in fp32.  Rounded once, to
+ * out_dtype.  Entries of a hidden row smaller than 2^-28 of the row's largest are
+ * rounded to 2^-39 of it.  A row with an infinity or NaN gives infinities and NaN.
+ * For batches of few rows (decode): 16 rows cost one read of the table, 32 too
+ * where H is at most about 2800; more rows are taken in passes.
  *
  *   hidden            device [num_tokens x H] of hidden_dtype (LMH_BF16 or
  *                     LMH_F16), row stride hidden_row_stride (>= H), aligned to
@@ -565,9 +568,11 @@ lmh_status lmh_quantize_q4(const void* W, int64_t w_row_stride, const lmh_q4_tab
  *                     row stride out_row_stride (>= V).
  * The table's 4-bit entries may be read before the kernel enqueued before this
  * one ends (the conventions above: head weights).  No workspace is needed.
- * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (dtypes, group, alignment),
- * LMH_ERR_CUDA.  Device: LMH_DS_ROW_IDX_OUT_OF_RANGE (the row reads zeros).
+ * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (dtypes, group, alignment,
+ * H > LMH_Q4_H_MAX), LMH_ERR_CUDA.  Device: LMH_DS_ROW_IDX_OUT_OF_RANGE (the row
+ * reads zeros), LMH_DS_TIMEOUT.
  */
+#define LMH_Q4_H_MAX 65536
 lmh_status lmh_project_q4(const void* hidden, lmh_dtype hidden_dtype, int64_t hidden_row_stride, int32_t num_tokens,
                           const int32_t* row_idx, int32_t rows, const lmh_q4_table* table, float logit_scale,
                           void* out, lmh_dtype out_dtype, int64_t out_row_stride, uint32_t* dev_status,

@@ -360,7 +360,12 @@ __global__ void __launch_bounds__(q4_threads(NT), 1)
   int box = kw;  // this warp's next box within the tile (boxes and more: in a later tile)
   int s = kw;    // its stage
   uint32_t ph = 0;
+  bool later_lap = false;
   bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {  // (the whole warp agrees)
+    return __all_sync(0xffffffffu, mbar_test_wait(bar, parity) ||
+                                       wait_or_abort(bar, parity, abort_flag, a.dev_status, a.wait_ns));
+  };
   int it = 0;  // tiles done
   int finisher = 0;
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++it) {
@@ -391,7 +396,11 @@ __global__ void __launch_bounds__(q4_threads(NT), 1)
           }
         next_box += KW;
         next_scales();
-        if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&full[s], ph, abort_flag, a.dev_status, a.wait_ns));
+        // A stage's last box was another warp's where the ring is no multiple of KW: that one
+        // has to be over first, or a wait for this one's parity would take the one before
+        // the last for it.  (All row groups have left a box before the next is loaded.)
+        if (ok && later_lap) ok = wait(&empty[s], ph ^ 1u);
+        if (ok) ok = wait(&full[s], ph);
         if (ok) {
           const uint32_t rows = my_word + s * kQ4StageBytes;
           const uint4* x = xs + (box - b0) * kQ4BoxBlocks * NT * 32 + lane;
@@ -449,6 +458,7 @@ __global__ void __launch_bounds__(q4_threads(NT), 1)
         if (s >= a.stages) {
           s -= a.stages;
           ph ^= 1u;
+          later_lap = true;
         }
       }
     }
