@@ -258,3 +258,18 @@ def test_decode_loop(lmh):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("H,group", [(32, 32), (96, 32), (320, 64), (128, 128)])
+@pytest.mark.parametrize("scale", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows", [1, 12, 20])
+def test_project_infinite_scale_of_the_last_group(lmh, rows, scale, H, group):
+    """The entries that fill a row's last 256 up count for nothing, whatever the last scale is."""
+    V, G = 200, H // group
+    packed = torch.full((V, H // 2), 0xFF, dtype=torch.uint8, device="cuda")  # every entry 15 - 8 = 7
+    scales = torch.ones(V, G, dtype=DT[scale], device="cuda")
+    scales[5, -1], scales[130, -1] = float("inf"), float("-inf")
+    x = torch.ones(rows, H, dtype=torch.bfloat16, device="cuda")
+    want = torch.full((rows, V), 7.0 * H, device="cuda")
+    want[:, 5], want[:, 130] = float("inf"), float("-inf")
+    assert torch.equal(lmh.project_q4(x, lmh.Q4Table(packed, scales, None, group)), want)  # whole numbers: exact

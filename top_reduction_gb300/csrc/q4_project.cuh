@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(q4_threads(NT), 1)
   auto load_scales = [&]() {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      const int g = min(next_box * kGroups + c % kGroups + 4 * j, groups - 1);  // (a group past the last multiplies 0)
+      const int g = min(next_box * kGroups + c % kGroups + 4 * j, groups - 1);
       const int at = g << scale_shift;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -394,6 +394,14 @@ __global__ void __launch_bounds__(q4_threads(NT), 1)
                                     : __half2float(__ushort_as_half(static_cast<unsigned short>(raw_s[i][j])));
             if (ZP) zv[i][j] = raw_z[i][j];
           }
+        if ((box + 1) * kGroups > groups) {
+          // A group past the last one sums to 0, and its scale is 0 too: the last group's may be infinite.
+#pragma unroll
+          for (int j = 0; j < kLoads; ++j)
+            if (box * kGroups + c % kGroups + 4 * j >= groups)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sv[i][j] = 0.0f;
+        }
         next_box += KW;
         next_scales();
         // A stage's last box was another warp's where the ring is no multiple of KW: that one
