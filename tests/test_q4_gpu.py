@@ -273,3 +273,24 @@ def test_project_infinite_scale_of_the_last_group(lmh, rows, scale, H, group):
     want = torch.full((rows, V), 7.0 * H, device="cuda")
     want[:, 5], want[:, 130] = float("inf"), float("-inf")
     assert torch.equal(lmh.project_q4(x, lmh.Q4Table(packed, scales, None, group)), want)  # whole numbers: exact
+
+
+def test_project_reads_the_table_made_just_before(lmh):
+    """No synchronisation between making a table and projecting through it."""
+    V, H = 20011, 1024
+    ws = [torch.randn(V, H, generator=torch.Generator("cuda").manual_seed(i), device="cuda").to(torch.bfloat16)
+          for i in range(2)]
+    x = torch.randn(8, H, device="cuda").to(torch.bfloat16)
+    want = []
+    for w in ws:
+        t = lmh.quantize_q4(w, 64)
+        torch.cuda.synchronize()
+        want.append(lmh.project_q4(x, t))
+    del t  # (its memory holds the next tables: the allocator gives it out again)
+    got = []
+    for i in range(8):
+        t = lmh.quantize_q4(ws[i & 1], 64)
+        got.append(lmh.project_q4(x, t))
+        del t
+    for i in range(8):
+        assert torch.equal(got[i], want[i & 1]), i

@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(q4_threads(NT), 1)
     // ------------------------- producer -------------------------
     if (lane == 0) {
       prefetch_tmap(&map);
+      pdl_wait();  // (the kernel before this one may be quantize_q4_kernel, whose table this is)
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
