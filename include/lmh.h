@@ -555,8 +555,9 @@ lmh_status lmh_quantize_q4(const void* W, int64_t w_row_stride, const lmh_q4_tab
  * is held in fp32, times its scale, and summed in fp32.  Rounded once, to
  * out_dtype.  Entries of a hidden row smaller than 2^-28 of the row's largest are
  * rounded to 2^-39 of it.  A row with an infinity or NaN gives infinities and NaN.
- * For batches of few rows (decode): 16 rows cost one read of the table, 32 too
- * where H is at most about 2800; more rows are taken in passes.
+ * For batches of few rows (decode): the rows are taken in passes, each of which
+ * reads the table once, of up to 32 rows where H is at most 2560, 16 up to 5120, 8
+ * above.
  *
  *   hidden            device [num_tokens x H] of hidden_dtype (LMH_BF16 or
  *                     LMH_F16), row stride hidden_row_stride (>= H), aligned to
@@ -566,13 +567,12 @@ lmh_status lmh_quantize_q4(const void* W, int64_t w_row_stride, const lmh_q4_tab
  *                     lmh_project_logprobs_scaled).
  *   out               device [rows x V] of out_dtype (LMH_F32 or hidden_dtype),
  *                     row stride out_row_stride (>= V).
- * The table's 4-bit entries may be read before the kernel enqueued before this
- * one ends (the conventions above: head weights).  No workspace is needed.
- * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (dtypes, group, alignment,
- * H > LMH_Q4_H_MAX), LMH_ERR_CUDA.  Device: LMH_DS_ROW_IDX_OUT_OF_RANGE (the row
+ * The table is read only after the kernel enqueued before this one has ended, so
+ * that may be the one that makes it.  No workspace is needed.
+ * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (dtypes, group, alignment),
+ * LMH_ERR_CUDA.  Device: LMH_DS_ROW_IDX_OUT_OF_RANGE (the row
  * reads zeros), LMH_DS_TIMEOUT.
  */
-#define LMH_Q4_H_MAX 65536
 lmh_status lmh_project_q4(const void* hidden, lmh_dtype hidden_dtype, int64_t hidden_row_stride, int32_t num_tokens,
                           const int32_t* row_idx, int32_t rows, const lmh_q4_table* table, float logit_scale,
                           void* out, lmh_dtype out_dtype, int64_t out_row_stride, uint32_t* dev_status,

@@ -294,3 +294,12 @@ def test_project_reads_the_table_made_just_before(lmh):
         del t
     for i in range(8):
         assert torch.equal(got[i], want[i & 1]), i
+
+
+def test_project_very_long_rows(lmh):
+    """The hidden rows in many pieces; no limit on H."""
+    rng = np.random.default_rng(4)
+    H = 81920 + 96
+    table, w = random_table(lmh, 130, H, 32, True, seed=4)
+    x = torch.from_numpy(rng.standard_normal((9, H)).astype(np.float32)).to(torch.bfloat16).cuda()
+    check_project(lmh.project_q4(x, table), x.double().cpu().numpy(), w, H, 1.0, "f32")
