@@ -70,3 +70,43 @@ def test_sampling_wait_runs_out_then_recovers(lmh):
     st.zero_()
     assert torch.equal(lmh.sample_from_logits(logits, u, top_p=p, dev_status=st)["sampled_ids"], want)
     assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("rows,V", [(4, 151936), (32, 50000), (64, 8000)])
+def test_logprobs_follow_the_projection_and_the_draw(lmh, rows, V):
+    """logprobs_from_logits reads its first chunks and the selected ids ahead of the stream's order,
+    unless the kernel before has to end first: it does after project_q4 and after a draw."""
+    table, _, _ = _tables(lmh, 1, V, 256)
+    gen = torch.Generator("cuda").manual_seed(V)
+    xs = [torch.randn(rows, 256, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(12)]
+    us = torch.rand(12, rows, generator=gen, device="cuda")
+    p = torch.full((rows,), 0.95, device="cuda")
+    z = torch.empty(rows, V, device="cuda")
+    draw = {"sampled_ids": torch.empty(rows, dtype=torch.int32, device="cuda"),
+            "sampled_logprob": torch.empty(rows, device="cuda")}
+
+    def steps(sync):
+        got = []
+        for x, u in zip(xs, us):
+            lmh.project_q4(x, table, out=z)
+            if sync:
+                torch.cuda.synchronize()
+            lse = lmh.logprobs_from_logits(z)["lse"]
+            lmh.sample_from_logits(z, u, top_p=p, out=draw)
+            if sync:
+                torch.cuda.synchronize()
+            sel = lmh.logprobs_from_logits(z, sel=draw["sampled_ids"])["sel_logprob"]
+            got.append((lse.clone(), sel.clone()))
+        if sync:
+            torch.cuda.synchronize()
+        return got
+    want = steps(True)
+    graph = torch.cuda.CUDAGraph()  # (a graph's kernels follow one another at once)
+    with torch.cuda.graph(graph):
+        got = steps(False)
+    for replay in range(5):
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(want, got)):
+            assert torch.equal(a[0], b[0]), "projection, step %d" % i
+            assert torch.equal(a[1], b[1]), "draw, step %d" % i

@@ -6,12 +6,16 @@
 // For the batches of a decode step (up to a few dozen rows) the table is the
 // traffic: V * H/2 bytes and its scales, read once.  The products run on mma.sync
 // m16n8k16 (f16) with 16 table rows as the A operand and 8 hidden rows as the B
-// operand, so a single hidden row costs the same instructions as eight.  (tcgen05
-// would take the 16-bit table rows through shared memory: four times the bytes of
-// the packed ones, written and read again, for products that are not the bound here.)
+// operand, so a single hidden row costs the same instructions as eight.
 //
-// What bounds it beside the reads is the unpacking: some 13 entries a nanosecond and
-// SM.  An f16 holds two nibbles' places in its ten mantissa bits: with exponent bits
+// Measured with cold L2 (2560 x 151936, group 64): 53 us for 1 row, of which the table's
+// 207 MB at the copy rate are 30.5, and 129 us for 32 rows; 4096 x 128256, group 128 with
+// zero points, 16 rows: 92 us (41 at the copy rate).  For one row the issue slots are busy
+// 57% and the ALU 43%: what bounds it beside the reads is the unpacking.  For 32 rows it is
+// the tensor pipe (34%) and the issue (32%) of the 8 warps whose sums fit in registers, with
+// loads that stay in flight only as far as the 3 stages go that the hidden rows leave.
+//
+// An f16 holds two nibbles' places in its ten mantissa bits: with exponent bits
 // for 1024 put in, bits 0..3 make it 1024 + q and bits 4..7 make it 1024 + 16q.  One
 // logic operation and one packed f16 operation give an operand of two entries
 // q - zero, exact whole numbers: nine operations for a word of eight entries (in bf16,
@@ -27,6 +31,11 @@
 //   their operands' exponents, and with the leading zeros of a subnormal in the operand
 //   it drops seven bits of every product: errors of 6e-6 of the sum of magnitudes.
 //
+// - Measured and dropped: tcgen05, with the unpacked entries put into tensor memory as
+//   the A operand, an accumulator per group, and warps that take these out, scale and
+//   add them.  Right, but slower at every size measured: with so few hidden rows an MMA is
+//   all issue (95 cycles each), and each 128 entries change hands four times.
+//
 // Work: a CTA takes tiles of 128 table rows.  Its producer warp streams a tile as
 // boxes of 128 rows x 128 bytes (256 entries) into a ring of shared-memory stages
 // (TMA, 128-byte swizzle).  A row group of 32 rows has KW consumer warps that take
@@ -35,6 +44,11 @@
 // entries.  At the end of a tile one of the KW warps, each in its turn, gets the
 // others' sums through shared memory, adds them up in a fixed order and writes the
 // logits; the others go on to the next tile at once.
+// Measured and dropped, where the hidden rows leave few stages (16 rows of 4096 / 32 of
+// 2560; kept: 92 / 129 us): pairs of CTAs that share a tile's entries, and so have half of
+// the hidden rows each (113 / 147); no producer, the last reader of a stage loads its next
+// box (96 / 127, and 2 us more for small calls); boxes of 64 bytes a row, for twice the
+// stages (104 / 137); 16 table rows a warp and twice the warps (98 / 139).
 //
 // The order of a block's entries within an MMA is free as long as A and B agree:
 // lane c of a row's four lanes takes word c of the block's four words (entries 8c
@@ -235,7 +249,7 @@ __global__ void __launch_bounds__(q4_threads(NT), 1)
   const bool resident = a.slab >= boxes;
   const bool scale32 = a.t.scale_dtype == LMH_F32, scale_bf16 = a.t.scale_dtype == LMH_BF16;
   pdl_wait();
-  pdl_launch_dependents();
+  // (no early launch of the next kernel: it may read the logits ahead of its wait, as logprobs_from_logits does)
 
   // named barriers: all consumers; per row group, a tile's sums are there, and are read
   // (of even and of odd tiles: the finisher skips the wait at the next tile, and may be

@@ -121,7 +121,6 @@ __global__ void __launch_bounds__(kThreads)
     lookup_q4_kernel(const int32_t* __restrict__ ids, int n, Q4View t, int group_shift, float scale, T* __restrict__ out,
                      int64_t out_stride, bool vec, uint32_t* dev_status) {
   pdl_wait();
-  pdl_launch_dependents();
   // The grid has fewer than 2^31 threads, so a thread's first word is found by one
   // 32-bit division, and the next ones by adding the step's rows and words.
   const uint32_t words = t.H / 8;

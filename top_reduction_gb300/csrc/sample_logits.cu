@@ -1253,7 +1253,7 @@ __device__ __forceinline__ bool RowSampler<T>::run() {
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const __grid_constant__ Params p) {
   pdl_wait();
-  pdl_launch_dependents();
+  // (no early launch of the next kernel: it may read the ids ahead of its wait, as logprobs_from_logits does)
   RowSampler<T> s(p, static_cast<int>(blockIdx.x / cluster_size()));
   const bool first_only = s.run();
   // No CTA leaves while another may still read its shared memory; after a draw from a
