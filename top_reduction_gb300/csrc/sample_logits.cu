@@ -35,6 +35,18 @@
 // Tokens of weight 0 (t < -33) can be left out of either: no draw falls on them and no
 // sum changes.
 //
+// What bounds it is latency: a row is a chain of steps, each a pass over what a thread
+// holds (a microsecond or two) or an agreement of the cluster (one), and a decode batch is
+// one wave of rows.  Measured with cold L2: 20 us for one row of 128256 f32 with top-k and
+// top-p, 45 for 32 rows of 151936 f32 with mixed filters (half of them are done after 19
+// us in the kernel; the longest chain, 43, is a top-p row whose tokens do not fit a list:
+// loading 6 us, the list that does not do 12, the bracket 7, the parts 8, their list 5, the
+// draw 6), 27 for 64 rows of 128256 bf16 with min-p and a mask, 147 for 256 rows of 248320
+// bf16 (127 MB; 2048 CTAs, two to an SM).  HBM is not the bound in any of them: 13% of its
+// time for the largest.  Half the CTAs per row there, with twice the logits each, were
+// slower (205 us where an earlier state of this kernel took 166).
+// The next kernel is not let in early: it may read the ids ahead of its wait.
+//
 // A row's work is a chain of short steps, each run once by a CTA, so instructions come
 // from far away more often than not: written out for every element of a vector in every
 // pass, the kernel had 300 KB of them and spent most of its time fetching them.  Only
@@ -63,6 +75,7 @@ constexpr float kMinT = -33.0f;        // below: weight 0
 constexpr float kMaxBinsTop = 64.0f;   // the lanes' maxima: bins from this z down,
 constexpr float kMaxBinsPer = 4.0f;    // so many to a unit
 constexpr int kSampleFromV = 16384;    // vocabularies whose threshold searches begin with a sample
+constexpr int kSampleStep = 16;        // of which one logit in so many is (8 and 32: no difference)
 constexpr int kUnroll = 4;             // vectors of a lane whose mask words are in flight at once
 constexpr float kHiAdd = 768.0f;             // 1.5 * 2^9: unit 2^-14
 constexpr float kLoAdd = 0.0029296875f;      // 1.5 * 2^-9: unit 2^-32
@@ -848,12 +861,12 @@ __device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 targe
                          : static_cast<int>((fminf(t1, 0.0f) - t) * per_t);
     return min(max(b, 0), kBins - 1);
   };
-  // The interval comes from a sample, one logit of every vector, with a margin; where that
+  // The interval comes from a sample of the logits, with a margin; where that
   // was not enough (or the row is short), from all logits.
 #pragma unroll 1
   for (int attempt = p_.V >= kSampleFromV ? 0 : 1; attempt < 2 && part < 0; ++attempt) {
     clear_hist(sh.hist[0]);
-    const int step = attempt == 0 ? kN : 1;
+    const int step = attempt == 0 ? kSampleStep : 1;
 #pragma unroll 1
     for (int j = lane_ * step; j < n_ * kN; j += 32 * step) {
       const float t = t_of(element(j));
@@ -865,7 +878,7 @@ __device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 targe
     int lo_bin, hi_bin;
     if (attempt == 0) {
       const float share = by_mass ? static_cast<float>(target - listed_mass) / static_cast<float>(total - listed_mass)
-                                  : 1.0f + static_cast<float>(target) / kN;
+                                  : 1.0f + static_cast<float>(target) / kSampleStep;
       find_bracket(bin_sum, share, by_mass ? 0.08f : 16.0f + 0.05f * share);
       lo_bin = sh.found_bin;
       hi_bin = max(sh.found_hi, lo_bin);
