@@ -556,8 +556,8 @@ lmh_status lmh_quantize_q4(const void* W, int64_t w_row_stride, const lmh_q4_tab
  * out_dtype.  Entries of a hidden row smaller than 2^-28 of the row's largest are
  * rounded to 2^-39 of it.  A row with an infinity or NaN gives infinities and NaN.
  * For batches of few rows (decode): the rows are taken in passes, each of which
- * reads the table once, of up to 32 rows where H is at most 2560, 16 up to 5120, 8
- * above.
+ * reads the table once, of up to 32 rows where H is at most 2816 (with zero points
+ * 2560), 16 up to 5120, 8 above.
  *
  *   hidden            device [num_tokens x H] of hidden_dtype (LMH_BF16 or
  *                     LMH_F16), row stride hidden_row_stride (>= H), aligned to

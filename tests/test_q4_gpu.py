@@ -303,3 +303,19 @@ def test_project_very_long_rows(lmh):
     table, w = random_table(lmh, 130, H, 32, True, seed=4)
     x = torch.from_numpy(rng.standard_normal((9, H)).astype(np.float32)).to(torch.bfloat16).cuda()
     check_project(lmh.project_q4(x, table), x.double().cpu().numpy(), w, H, 1.0, "f32")
+
+
+@pytest.mark.parametrize("rows,V,H,group", [(32, 60000, 896, 64), (20, 151936, 128, 32), (17, 50003, 384, 128),
+                                            (24, 40000, 2816, 64), (24, 2000, 2848, 32), (32, 90000, 32, 32),
+                                            (25, 70001, 1120, 32), (64, 30000, 640, 128), (41, 25000, 192, 64)])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_project_wide_many_tiles(lmh, rows, V, H, group, zeros):
+    """More than 16 rows: odd numbers of 128 entries, long and short rings, several tiles per SM, and
+    hidden rows that just fit and just do not."""
+    rng = np.random.default_rng(H)
+    table, w = random_table(lmh, V, H, group, zeros, seed=H)
+    x = torch.from_numpy(rng.standard_normal((rows, H)).astype(np.float32)).to(torch.bfloat16).cuda()
+    out = lmh.project_q4(x, table)
+    check_project(out, x.double().cpu().numpy(), w, H, 1.0, "f32")
+    for _ in range(3):
+        assert torch.equal(lmh.project_q4(x, table), out)

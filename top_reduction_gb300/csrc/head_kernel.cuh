@@ -37,6 +37,7 @@
 
 #include "device_common.cuh"
 #include "lmh_internal.h"
+#include "tcgen05.cuh"
 #include "tma.cuh"
 
 namespace lmh {
@@ -108,19 +109,6 @@ struct HeadArgs {
 // PTX wrappers: tcgen05
 // ---------------------------------------------------------------------------
 
-// Shared-memory matrix descriptor: K-major operand, 128-byte swizzle, rows of
-// 128 bytes, 8-row groups 1024 bytes apart (stride byte offset), descriptor
-// version 1, leading byte offset unused for this layout (set to 16 bytes).
-__device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(16u >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-
 // Shared-memory matrix descriptor: vocabulary-major (MN-major) W slice of a
 // [H x V] head, 128-byte swizzle.  The slice is 4 blocks of 64 vocabulary
 // columns (128-byte rows) x 64 hidden rows, 8 KB apart; within a block, groups
@@ -155,14 +143,6 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t adesc, uint6
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // Load 64 consecutive fp32 columns of this thread's TMEM lane and wait for
 // them in the same asm statement, so no use of the registers can be scheduled

@@ -1,5 +1,7 @@
-// q4_project.cuh -- the head projection through a 4-bit table (lmh_project_q4):
-// the kernel, instantiated per type of the hidden rows in q4_project_*.cu.
+// q4_project.cuh -- the head projection through a 4-bit table (lmh_project_q4): the kernel
+// for up to 16 hidden rows a read of the table, and for more where there are zero points or
+// the hidden rows are long (the others: q4_project_wide.cuh); the choice between the two.
+// Instantiated per type of the hidden rows in q4_project_*.cu.
 //
 //   out[n][v] = logit_scale * sum_g scale[v][g] * sum_{h in g} (q[v][h] - zero[v][g]) * x[n][h]
 //
@@ -9,11 +11,12 @@
 // operand, so a single hidden row costs the same instructions as eight.
 //
 // Measured with cold L2 (2560 x 151936, group 64): 53 us for 1 row, of which the table's
-// 207 MB at the copy rate are 30.5, and 129 us for 32 rows; 4096 x 128256, group 128 with
-// zero points, 16 rows: 92 us (41 at the copy rate).  For one row the issue slots are busy
-// 57% and the ALU 43%: what bounds it beside the reads is the unpacking.  For 32 rows it is
-// the tensor pipe (34%) and the issue (32%) of the 8 warps whose sums fit in registers, with
-// loads that stay in flight only as far as the 3 stages go that the hidden rows leave.
+// 207 MB at the copy rate are 30.5, 70 us for 16 rows (80 with zero points), 150 for 32 with
+// zero points; 4096 x 128256, group 128 with zero points, 16 rows: 92 us (41 at the copy
+// rate).  For one row the issue slots are busy 57% and the ALU 43%: what bounds it beside
+// the reads is the unpacking.  For 16 and 32 rows it is the latency that the 12 or 8 warps
+// whose sums fit in registers cannot cover, and loads that stay in flight only as far as
+// the few stages go that the hidden rows leave.
 //
 // An f16 holds two nibbles' places in its ten mantissa bits: with exponent bits
 // for 1024 put in, bits 0..3 make it 1024 + q and bits 4..7 make it 1024 + 16q.  One
@@ -31,11 +34,9 @@
 //   their operands' exponents, and with the leading zeros of a subnormal in the operand
 //   it drops seven bits of every product: errors of 6e-6 of the sum of magnitudes.
 //
-// - Measured and dropped: tcgen05, with the unpacked entries put into tensor memory as
-//   the A operand, an accumulator per group, and warps that take these out, scale and
-//   add them.  Right in the tests; 84, 49 and 123 us for 1, 8 and 16 rows where this kernel
-//   takes 53, 33 and 92 (with so few hidden rows an MMA is all issue, 95 cycles each, and
-//   each 128 entries change hands four times), but 102 for 32 rows where this took 121.
+// - tcgen05 (the other kernel's way) with 16 hidden rows an MMA was measured and dropped for
+//   up to 16 rows: 84, 49 and 123 us where this kernel took 53, 33 and 92 (1 row of 2560 and 8
+//   of 1024 x 151936, 16 of 4096 x 128256).
 //
 // Work: a CTA takes tiles of 128 table rows.  Its producer warp streams a tile as
 // boxes of 128 rows x 128 bytes (256 entries) into a ring of shared-memory stages
@@ -46,7 +47,7 @@
 // others' sums through shared memory, adds them up in a fixed order and writes the
 // logits; the others go on to the next tile at once.
 // Measured and dropped, where the hidden rows leave few stages (16 rows of 4096 / 32 of
-// 2560; kept: 92 / 129 us): pairs of CTAs that share a tile's entries, and so have half of
+// 2560 without zero points; as it is: 92 / 129 us): pairs of CTAs that share a tile's entries, and so have half of
 // the hidden rows each (113 / 147); no producer, the last reader of a stage loads its next
 // box (96 / 127, and 2 us more for small calls); boxes of 64 bytes a row, for twice the
 // stages (104 / 137); 16 table rows a warp and twice the warps (98 / 139).
@@ -59,43 +60,13 @@
 // lane and block.
 #pragma once
 
-#include <cmath>
-
-#include "device_common.cuh"
-#include "lmh_internal.h"
-#include "q4_common.cuh"
-#include "tma.cuh"
+#include "q4_operands.cuh"
+#include "q4_project_wide.cuh"
 
 namespace lmh {
 
-constexpr int kQ4TileRows = 128;
-constexpr int kQ4RowGroups = kQ4TileRows / 32;
-constexpr int kQ4BoxBytes = 128;                       // of a row
-constexpr int kQ4BoxEntries = 2 * kQ4BoxBytes;
-constexpr int kQ4BoxBlocks = kQ4BoxEntries / 32;
-constexpr int kQ4StageBytes = kQ4TileRows * kQ4BoxBytes;
-constexpr int kQ4MaxStages = 12;
 // The shortest ring: a warp's next box must not wrap the ring twice.
 constexpr int q4_min_stages(int nt) { return nt == 1 ? 4 : 3; }
-constexpr size_t kQ4SmemMax = 227 * 1024;
-
-struct Q4ProjectArgs {
-  const void* hidden;
-  int64_t hidden_stride;
-  int num_tokens;
-  const int32_t* row_idx;
-  int rows;
-  bool vec;  // hidden rows can be read 16 bytes at a time
-  Q4View t;
-  float logit_scale;
-  void* out;
-  bool out_f32;
-  int64_t out_stride;
-  uint32_t* dev_status;
-  int stages;       // of the ring
-  int slab;         // boxes of hidden rows in shared memory at once
-  uint64_t wait_ns;
-};
 
 // Consumer warps per row group for NT tiles of 8 hidden rows: as many as the
 // registers that the sums need allow (96, 128 and 168 a thread).
@@ -146,33 +117,6 @@ __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
-
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-
-// Eight hidden values (from 16-byte vectors, or one by one).
-template <typename T>
-__device__ __forceinline__ void load_hidden(const T* src, bool vec, float (&x)[8]) {
-  alignas(16) T v[8];
-  if (vec) {
-    *reinterpret_cast<uint4*>(v) = __ldg(reinterpret_cast<const uint4*>(src));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = src[e];
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = to_f32(v[e]);
-}
-
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// 2^e for e in [-149, 127]
-__device__ __forceinline__ float pow2(int e) {
-  return e >= -126 ? __int_as_float((e + 127) << 23) : __int_as_float(1 << (e + 149));
 }
 
 // G: entries per group.  NT: tiles of 8 hidden rows per pass (blockIdx.y counts
@@ -570,14 +514,19 @@ cudaError_t q4_launch_one(Q4ProjectArgs a, int num_sms, cudaStream_t stream) {
 
 // Hidden rows per pass: 8, 16 or 32, the fewest passes whose rows stay in shared
 // memory (a second pass reads the table again; restaging the hidden rows at every
-// tile reads them again from L2, and stops the tile for it).
+// tile reads them again from L2, and stops the tile for it).  32 without zero points
+// are the other kernel's: 98 us for 32 rows of 2560 x 151936 where four tiles here took 129.
 template <typename T, int G, bool ZP>
 cudaError_t q4_launch_rows(const Q4ProjectArgs& a, int num_sms, cudaStream_t stream) {
   const int boxes = (a.t.H + kQ4BoxEntries - 1) / kQ4BoxEntries;
   auto fits = [&](int nt) {
     return kQ4FixedBytes + q4_sums_bytes(nt) + q4_hidden_bytes(boxes, nt) + q4_min_stages(nt) * kQ4StageBytes <= kQ4SmemMax;
   };
-  if (a.rows > 16 && fits(4)) return q4_launch_one<T, G, 4, ZP>(a, num_sms, stream);
+  if constexpr (ZP) {
+    if (a.rows > 16 && fits(4)) return q4_launch_one<T, G, 4, ZP>(a, num_sms, stream);
+  } else {
+    if (a.rows > 16 && q4_wide_fits(a.t.H)) return q4_wide_launch<T, G>(a, num_sms, stream);
+  }
   if (a.rows > 8 && fits(2)) return q4_launch_one<T, G, 2, ZP>(a, num_sms, stream);
   return q4_launch_one<T, G, 1, ZP>(a, num_sms, stream);
 }
@@ -592,20 +541,19 @@ cudaError_t q4_launch(const Q4ProjectArgs& a, int group, int num_sms, cudaStream
   return zp ? q4_launch_rows<T, 128, true>(a, num_sms, stream) : q4_launch_rows<T, 128, false>(a, num_sms, stream);
 }
 
-template <typename T, int G, int NT>
+template <typename T, int G, int NT, bool ZP>
 cudaError_t q4_attr() {
-  cudaError_t e = cudaFuncSetAttribute(project_q4_kernel<T, G, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kQ4SmemMax));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(project_q4_kernel<T, G, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kQ4SmemMax));
-  return e;
+  return cudaFuncSetAttribute(project_q4_kernel<T, G, NT, ZP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kQ4SmemMax));
 }
 template <typename T, int G>
 cudaError_t q4_attr_group() {
-  cudaError_t e = q4_attr<T, G, 1>();
-  if (e == cudaSuccess) e = q4_attr<T, G, 2>();
-  if (e == cudaSuccess) e = q4_attr<T, G, 4>();
+  cudaError_t e = q4_attr<T, G, 1, false>();
+  if (e == cudaSuccess) e = q4_attr<T, G, 1, true>();
+  if (e == cudaSuccess) e = q4_attr<T, G, 2, false>();
+  if (e == cudaSuccess) e = q4_attr<T, G, 2, true>();
+  if (e == cudaSuccess) e = q4_attr<T, G, 4, true>();
+  if (e == cudaSuccess) e = q4_wide_attr<T, G>();
   return e;
 }
 template <typename T>
