@@ -47,10 +47,11 @@
 // others' sums through shared memory, adds them up in a fixed order and writes the
 // logits; the others go on to the next tile at once.
 // Measured and dropped, where the hidden rows leave few stages (16 rows of 4096 / 32 of
-// 2560 without zero points; as it is: 92 / 129 us): pairs of CTAs that share a tile's entries, and so have half of
-// the hidden rows each (113 / 147); no producer, the last reader of a stage loads its next
-// box (96 / 127, and 2 us more for small calls); boxes of 64 bytes a row, for twice the
-// stages (104 / 137); 16 table rows a warp and twice the warps (98 / 139).
+// 2560 without zero points; as it is: 92 / 129 us): pairs of CTAs that share a tile's
+// entries, and so have half of the hidden rows each (113 / 147); no producer, the last
+// reader of a stage loads its next box (96 / 127, and 2 us more for small calls); boxes of
+// 64 bytes a row, for twice the stages (104 / 137); 16 table rows a warp and twice the
+// warps (98 / 139).
 //
 // The order of a block's entries within an MMA is free as long as A and B agree:
 // lane c of a row's four lanes takes word c of the block's four words (entries 8c
