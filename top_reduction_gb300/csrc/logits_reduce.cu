@@ -711,7 +711,8 @@ __global__ void __launch_bounds__(kTThreads, kTCtasPerSm) logits_stream_tma_kern
     const uint64_t policy = l2_evict_first_policy();  // logits are read once; the block maxima stay in L2
     int sel_row = -1, sel_id = -1;
     // Stage s <- chunk c (false: c is past the end, and stage s gets the end marker).
-    auto issue = [&](int s, int64_t c) {
+    // `early`: without the selected token (the consumers see to it).
+    auto issue = [&](int s, int64_t c, bool early) {
       StreamDesc& d = desc[s];
       if (c >= total) {
         d.row = -1;
@@ -722,9 +723,9 @@ __global__ void __launch_bounds__(kTThreads, kTCtasPerSm) logits_stream_tma_kern
       const int ci = static_cast<int>(c - static_cast<int64_t>(row) * a.cpr);
       const int lb = ci * CH;
       const int nbk = min(CH, a.nblk - lb);
-      if (row != sel_row) {
+      if (!early && row != sel_row) {
         sel_row = row;
-        sel_id = a.sel ? a.sel[row] : -1;
+        sel_id = a.sel ? __ldcg(a.sel + row) : -1;  // (through L2, as the ticket below)
       }
       const int ne = min(nbk * kBlock, a.V - lb * kBlock);
       d.row = row;
@@ -732,7 +733,7 @@ __global__ void __launch_bounds__(kTThreads, kTCtasPerSm) logits_stream_tma_kern
       d.nbk = nbk;
       d.ne = ne;
       d.slot = static_cast<int64_t>(row) * a.P + static_cast<int64_t>(ci) * kTConsumerWarps;
-      d.sel_rel = sel_id - lb * kBlock;
+      d.sel_rel = early ? -1 : sel_id - lb * kBlock;
       const char* src = a.logits + (static_cast<int64_t>(row) * a.row_stride + static_cast<int64_t>(lb) * kBlock) * ES;
       mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(ne * ES));
       bulk_load_hint(stages + static_cast<size_t>(s) * kTChunkBytes, src, static_cast<uint32_t>(ne * ES), &full[s],
@@ -741,13 +742,16 @@ __global__ void __launch_bounds__(kTThreads, kTCtasPerSm) logits_stream_tma_kern
     };
     // A CTA's first S chunks are fixed: they go out before the grid-dependency wait, so
     // they stream while the kernel before this one (the previous call's select kernel)
-    // still runs.  They read only the call's inputs, which were complete before that
-    // kernel left its own wait; the workspace (the ticket, the partials) is touched
-    // only after this kernel's wait, and the consumers wait too before writing it.
+    // still runs.  They read only the logits, which were complete before that kernel left
+    // its own wait.  All else follows this kernel's wait: the selected ids, which may be that
+    // kernel's last results (a head's merge writes its sampled ids after it lets this kernel
+    // start), and the workspace (the ticket, the partials), which the consumers wait for too
+    // before writing it.  (Handing the first stages over with the ids in, or taking their
+    // selected logits at this thread's end, cost 0.7 us of a call of 26.)
     uint32_t issued = 0;
     bool ended = false;
     for (; issued < static_cast<uint32_t>(S) && !ended; ++issued)
-      ended = !issue(static_cast<int>(issued), blockIdx.x + static_cast<int64_t>(issued) * gridDim.x);
+      ended = !issue(static_cast<int>(issued), blockIdx.x + static_cast<int64_t>(issued) * gridDim.x, true);
     pdl_wait();
     // Read through L2 (another kernel wrote them; an L1 line of an earlier call could be stale).
     TicketState* tk = a.parts.ticket;
@@ -763,7 +767,7 @@ __global__ void __launch_bounds__(kTThreads, kTCtasPerSm) logits_stream_tma_kern
       if (!wait_or_abort(&empty[s], ((issued / S) & 1u) ^ 1u, abort_flag, a.dev_status, a.wait_ns)) break;
       const int64_t c = next;
       if (c < total) next = draw(issued + 1);
-      ended = !issue(s, c);
+      ended = !issue(s, c, false);
     }
     // Copies still in flight (only after an abort) land before the CTA exits;
     // these waits keep the full limit whatever a.wait_ns is.
@@ -780,7 +784,20 @@ __global__ void __launch_bounds__(kTThreads, kTCtasPerSm) logits_stream_tma_kern
   const uint64_t keep_policy = l2_evict_last_policy();
   const int bi = c / TPB;
   const float L = kLog2e;
+  // The selected tokens of the CTA's first S chunks, which go out before the ids may be read:
+  // thread j looks up chunk j's while the first chunk is worked on, and takes its logit from memory.
+  int early_row = -1, early_v0 = 0, early_id = -1;
+  bool early_hit = false;
+  float early_z = 0.0f;
+  if (a.sel && c < S) {
+    const int64_t chunk = blockIdx.x + static_cast<int64_t>(c) * gridDim.x;
+    if (chunk < static_cast<int64_t>(a.rows) * a.cpr) {
+      early_row = static_cast<int>(chunk / a.cpr);
+      early_v0 = static_cast<int>(chunk - static_cast<int64_t>(early_row) * a.cpr) * CH * kBlock;
+    }
+  }
   pdl_wait();  // the stages may fill before the kernel before this one ends; the workspace may not be written
+  if (early_row >= 0) early_id = __ldcg(a.sel + early_row);
   for (uint32_t i = 0;; ++i) {
     const int s = static_cast<int>(i % S);
     const bool ok = wait_or_abort(&full[s], (i / S) & 1u, abort_flag, a.dev_status, a.wait_ns);
@@ -835,7 +852,12 @@ __global__ void __launch_bounds__(kTThreads, kTCtasPerSm) logits_stream_tma_kern
     const float M = warp_max(vm);
     const float sc = warp_sum(vm == -INFINITY ? 0.0f : ts * ex2_approx((vm - M) * L));
     if (lane == 0) a.parts.part_ms[d.slot + warp] = make_float2(M, M == -INFINITY ? 0.0f : sc);
+    if (i == 0 && early_id >= early_v0 && early_id < min(early_v0 + CH * kBlock, a.V)) {
+      early_hit = true;
+      early_z = VT::at(a.logits + static_cast<int64_t>(early_row) * a.row_stride * ES, early_id);
+    }
   }
+  if (early_hit) a.parts.sel_logit[early_row] = early_z;
 }
 
 // ---------------------------------------------------------------------------

@@ -45,7 +45,8 @@
 // bf16 (127 MB; 2048 CTAs, two to an SM).  HBM is not the bound in any of them: 13% of its
 // time for the largest.  Half the CTAs per row there, with twice the logits each, were
 // slower (205 us where an earlier state of this kernel took 166).
-// The next kernel is not let in early: it may read the ids ahead of its wait.
+// The next kernel is not let in early, although none of this library's reads ids ahead of its
+// wait any more: that would let draws in a row overlap, and has not been measured in this form.
 //
 // A row's work is a chain of short steps, each run once by a CTA, so instructions come
 // from far away more often than not: written out for every element of a vector in every
@@ -1266,7 +1267,7 @@ __device__ __forceinline__ bool RowSampler<T>::run() {
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_logits_kernel(const __grid_constant__ Params p) {
   pdl_wait();
-  // (no early launch of the next kernel: it may read the ids ahead of its wait, as logprobs_from_logits does)
+  // (no early launch of the next kernel)
   RowSampler<T> s(p, static_cast<int>(blockIdx.x / cluster_size()));
   const bool first_only = s.run();
   // No CTA leaves while another may still read its shared memory; after a draw from a
