@@ -80,3 +80,19 @@ def test_selected_ids_of_the_logits_reduction(lmh, producer, rows, V, H):
             sync()
         return out
     _replays_equal_single_calls(steps, xs)
+
+
+@pytest.mark.parametrize("producer,rows,V,H", PRODUCERS)
+def test_selected_ids_of_the_projection(lmh, producer, rows, V, H):
+    xs, W = _producer(lmh, producer, rows, V, H)
+    y, head = _randn(9, rows, 256).to(torch.bfloat16), _randn(10, V, 256).to(torch.bfloat16)
+
+    def steps(sync):
+        out = []
+        for i, x in enumerate(xs):
+            ids = _ids(lmh, producer, x, W, i)
+            sync()
+            out += [ids, lmh.project_logprobs(y, head, sel=ids)["sel_logprob"]]
+            sync()
+        return out
+    _replays_equal_single_calls(steps, xs)

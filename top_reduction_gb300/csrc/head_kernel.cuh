@@ -582,6 +582,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     }
   } else {
     // ------------------------- epilogue -------------------------
+    pdl_wait();  // the rows' selected ids and settings may be the last results of the kernel before
     const int q = warp & 3;  // TMEM lane quarter of this warp
     // column split (small batches): this warp's row copy and its first 64-column block
     const int n_rep = Cfg::kRepOk ? a.rep : 1;
