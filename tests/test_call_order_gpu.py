@@ -96,3 +96,26 @@ def test_selected_ids_of_the_projection(lmh, producer, rows, V, H):
             sync()
         return out
     _replays_equal_single_calls(steps, xs)
+
+
+@pytest.mark.parametrize("rows,V,H", [(128, 256, 4096), (16, 256, 8192), (5, 40, 2048), (64, 20000, 512)])
+def test_logits_that_the_projection_writes(lmh, rows, V, H):
+    """The head's own logits (from one vocabulary range and from several), reduced and drawn from."""
+    xs = [_randn(i, rows, H).to(torch.bfloat16) for i in range(STEPS)]
+    W = (_randn(77, V, H) * H ** -0.5).to(torch.bfloat16)
+    u = torch.rand(rows, generator=torch.Generator("cuda").manual_seed(5), device="cuda")
+    z = torch.empty(rows, V, device="cuda")
+
+    def steps(sync):
+        out = []
+        for x in xs:
+            lmh.project_logprobs(x, W, logits_out=z)
+            sync()
+            out.append(lmh.logprobs_from_logits(z)["lse"])
+            sync()
+            lmh.project_logprobs(x, W, logits_out=z)
+            sync()
+            out.append(lmh.sample_from_logits(z, u)["sampled_ids"])
+            sync()
+        return out
+    _replays_equal_single_calls(steps, xs)

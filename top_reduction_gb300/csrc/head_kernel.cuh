@@ -412,7 +412,9 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_launch_dependents();  // the merge may be scheduled; it waits for this grid's partials
+  // The merge may be scheduled; it waits for this grid's partials.  Where this kernel ends the
+  // call and writes logits, the next kernel may read those ahead of its wait: it starts after.
+  if (!(kMaterialize && a.final_out)) pdl_launch_dependents();
 
   if (warp == 0) {
     // ------------------------- TMA producer -------------------------
