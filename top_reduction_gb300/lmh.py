@@ -348,6 +348,36 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _other_device(device):
+    """True where `device` is not the calling thread's current one: the library launches on that."""
+    return device.index != torch._C._cuda_getDevice()
+
+
+def _on_stream(stream, device):
+    """Context of a call on `stream`, which has to be one of the tensors' device."""
+    if stream.device != device:
+        raise ValueError("stream is of %s, the tensors of %s" % (stream.device, device))
+    return torch.cuda.stream(stream)
+
+
+def _written(t, dtypes, n, device, name):
+    """The address of a tensor that the kernels write `n` entries of (it may have more)."""
+    if t is None:
+        return None
+    if t.device != device or t.dtype not in dtypes or not t.is_contiguous() or t.numel() < n:
+        raise ValueError("%s must be a contiguous %s tensor on %s with %d entries"
+                         % (name, " or ".join(str(d)[6:] for d in dtypes), device, n))
+    return t.data_ptr()
+
+
+_WORDS = (torch.int32, torch.uint32)
+_FLOATS = (torch.float32,)
+
+
+def _status_word(t, device):
+    return None if t is None else _written(t, _WORDS, 1, device, "dev_status")
+
+
 def _per_row(t, dtype, rows, device, name):
     """A per-row parameter as a contiguous device tensor (as it is when it already is one)."""
     if t is None:
@@ -368,15 +398,19 @@ def sample_from_logits(logits, uniforms, temperature=None, top_k=None, top_p=Non
     [rows] or None; mask: int32/uint32 [rows, words] allowed-token bits or None.  stream: the call
     is made on it, conversions and allocations included.
     Returns a dict with sampled_ids (int32 [rows], -1 where a row has no token) and sampled_logprob
-    (fp32 [rows], in the distribution that was drawn from).
+    (fp32 [rows], in the distribution that was drawn from).  out: such a dict, filled (contiguous
+    tensors on the logits' device; without sampled_logprob, or None there, none is written).
     """
+    dev = logits.device
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, dev):
             return sample_from_logits(logits, uniforms, temperature, top_k, top_p, min_p, mask, dev_status, out)
     rows, V = logits.shape
     pitch, step = logits.stride()
-    dev = logits.device
     assert logits.is_cuda and (step == 1 or V == 1)
+    if _other_device(dev):
+        with torch.cuda.device(dev):
+            return sample_from_logits(logits, uniforms, temperature, top_k, top_p, min_p, mask, dev_status, out)
     if uniforms is None:
         raise ValueError("uniforms is required")
     u = _per_row(uniforms, torch.float32, rows, dev, "uniforms")
@@ -387,7 +421,8 @@ def sample_from_logits(logits, uniforms, temperature=None, top_k=None, top_p=Non
     words = 0
     if mask is not None:
         mask = torch.as_tensor(mask, device=dev).contiguous()
-        assert mask.dim() == 2 and mask.shape[0] == rows and mask.element_size() == 4
+        if mask.dtype not in _WORDS or mask.dim() != 2 or mask.shape[0] != rows:
+            raise ValueError("mask must be int32 or uint32 [%d, words]" % rows)
         words = mask.shape[1]
     if out is None:
         out = {"sampled_ids": torch.empty(rows, dtype=torch.int32, device=dev),
@@ -395,7 +430,9 @@ def sample_from_logits(logits, uniforms, temperature=None, top_k=None, top_p=Non
     f = Filters(_ptr(temp), _ptr(k), _ptr(p), _ptr(m), _ptr(mask), words)
     st = (_lib or load()).lmh_sample_from_logits(
         logits.data_ptr(), _DTYPES[logits.dtype], rows, V, pitch if rows > 1 else V, f, u.data_ptr(),
-        out["sampled_ids"].data_ptr(), _ptr(out.get("sampled_logprob")), _ptr(dev_status), _raw_stream(dev))
+        _written(out["sampled_ids"], _WORDS, rows, dev, "sampled_ids"),
+        _written(out.get("sampled_logprob"), _FLOATS, rows, dev, "sampled_logprob"), _status_word(dev_status, dev),
+        _raw_stream(dev))
     if st != OK:
         raise LMHError(st, "lmh_sample_from_logits")
     return out
@@ -432,14 +469,17 @@ class Q4Table:
 
 def quantize_q4(W, group=64, zeros=False, scale_dtype=torch.bfloat16, stream=None):
     """Round a bf16 table [V, H] to 4 bits (lmh_quantize_q4): a Q4Table."""
+    dev = W.device
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, dev):
             return quantize_q4(W, group, zeros, scale_dtype)
     assert W.is_cuda and W.dtype == torch.bfloat16 and W.dim() == 2 and W.stride(1) == 1
+    if _other_device(dev):
+        with torch.cuda.device(dev):
+            return quantize_q4(W, group, zeros, scale_dtype)
     V, H = W.shape
     if H % group:
         raise ValueError("H must be a multiple of the group")
-    dev = W.device
     packed = torch.empty((V, H // 2), dtype=torch.uint8, device=dev)
     scales = torch.empty((V, H // group), dtype=scale_dtype, device=dev)
     z = torch.empty((V, H // group), dtype=torch.uint8, device=dev) if zeros else None
@@ -457,18 +497,21 @@ def project_q4(hidden, table, row_idx=None, rows=None, logit_scale=1.0, out_dtyp
     out_dtype: float32 or hidden's type, or give `out` (rows may be strided); stream: as
     sample_from_logits.
     """
+    dev = hidden.device
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, dev):
             return project_q4(hidden, table, row_idx, rows, logit_scale, out_dtype, out, dev_status)
     T, H = hidden.shape
     V = table.V
     pitch, step = hidden.stride()
-    dev = hidden.device
     assert step == 1 and dev == table.device
+    if _other_device(dev):
+        with torch.cuda.device(dev):
+            return project_q4(hidden, table, row_idx, rows, logit_scale, out_dtype, out, dev_status)
     if H != table.H:
         raise ValueError("hidden has %d columns, the table %d" % (H, table.H))
     if row_idx is not None:
-        assert row_idx.dtype == torch.int32 and row_idx.is_cuda and row_idx.is_contiguous()
+        assert row_idx.dtype == torch.int32 and row_idx.device == dev and row_idx.is_contiguous()
         rows = row_idx.numel() if rows is None else rows
         assert rows <= row_idx.numel()
     elif rows is None:
@@ -477,11 +520,11 @@ def project_q4(hidden, table, row_idx=None, rows=None, logit_scale=1.0, out_dtyp
         out = torch.empty((rows, V), dtype=out_dtype, device=dev)
         out_pitch = V
     else:
-        assert out.is_cuda and out.shape == (rows, V) and (out.stride(1) == 1 or V == 1)
+        assert out.device == dev and out.shape == (rows, V) and (out.stride(1) == 1 or V == 1)
         out_pitch = out.stride(0) if rows > 1 else V
     st = (_lib or load()).lmh_project_q4(
         hidden.data_ptr(), _DTYPES[hidden.dtype], pitch if T > 1 else H, T, _ptr(row_idx), rows, table._arg,
-        logit_scale, out.data_ptr(), _DTYPES[out.dtype], out_pitch, _ptr(dev_status), _raw_stream(dev))
+        logit_scale, out.data_ptr(), _DTYPES[out.dtype], out_pitch, _status_word(dev_status, dev), _raw_stream(dev))
     if st != OK:
         raise LMHError(st, "lmh_project_q4")
     return out
@@ -490,21 +533,24 @@ def project_q4(hidden, table, row_idx=None, rows=None, logit_scale=1.0, out_dtyp
 def lookup_q4(ids, table, scale=1.0, out_dtype=torch.bfloat16, out=None, dev_status=None, stream=None):
     """The rows [n, H] of int32 device ids from a 4-bit table, times scale (lmh_lookup_q4); an id of
     -1 (no token) gives zeros.  stream: as sample_from_logits."""
+    dev = ids.device
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, dev):
             return lookup_q4(ids, table, scale, out_dtype, out, dev_status)
     n, = ids.shape
     H = table.H
-    dev = ids.device
     assert dev == table.device and ids.dtype == torch.int32 and ids.is_contiguous()
+    if _other_device(dev):
+        with torch.cuda.device(dev):
+            return lookup_q4(ids, table, scale, out_dtype, out, dev_status)
     if out is None:
         out = torch.empty((n, H), dtype=out_dtype, device=dev)
         out_pitch = H
     else:
-        assert out.is_cuda and out.shape == (n, H) and out.stride(1) == 1
+        assert out.device == dev and out.shape == (n, H) and out.stride(1) == 1
         out_pitch = out.stride(0) if n > 1 else H
     st = (_lib or load()).lmh_lookup_q4(ids.data_ptr(), n, table._arg, scale, out.data_ptr(), _DTYPES[out.dtype],
-                                        out_pitch, _ptr(dev_status), _raw_stream(dev))
+                                        out_pitch, _status_word(dev_status, dev), _raw_stream(dev))
     if st != OK:
         raise LMHError(st, "lmh_lookup_q4")
     return out
