@@ -22,18 +22,28 @@ cudaError_t launch_project_q4(const void* hidden, lmh_dtype hidden_dtype, int64_
   a.hidden = hidden;
   a.hidden_stride = hidden_stride;
   a.num_tokens = num_tokens;
-  a.row_idx = row_idx;
-  a.rows = rows;
   a.vec = reinterpret_cast<uintptr_t>(hidden) % 16 == 0 && hidden_stride % 8 == 0;
   a.t = q4_view(t);
   a.logit_scale = logit_scale;
-  a.out = out;
   a.out_f32 = out_dtype == LMH_F32;
   a.out_stride = out_stride;
   a.dev_status = dev_status;
   a.wait_ns = wait_limit_ns();
-  return hidden_dtype == LMH_BF16 ? q4_launch_bf16(a, t.group, num_sms, stream)
-                                  : q4_launch_f16(a, t.group, num_sms, stream);
+  // The passes are the grid's second dimension: 65535 at most, of at least 8 rows each.
+  constexpr int kRowsPerLaunch = 65504 * 8;  // (whole passes of 8, 16 and 32)
+  for (int first = 0; first < rows; first += a.rows) {
+    a.rows = rows - first < kRowsPerLaunch ? rows - first : kRowsPerLaunch;
+    a.row_idx = row_idx ? row_idx + first : nullptr;
+    if (!row_idx) {
+      a.hidden = static_cast<const char*>(hidden) + static_cast<int64_t>(first) * hidden_stride * 2;
+      a.num_tokens = num_tokens - first;
+    }
+    a.out = static_cast<char*>(out) + static_cast<int64_t>(first) * out_stride * (a.out_f32 ? 4 : 2);
+    const cudaError_t e = hidden_dtype == LMH_BF16 ? q4_launch_bf16(a, t.group, num_sms, stream)
+                                                   : q4_launch_f16(a, t.group, num_sms, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace lmh
