@@ -568,9 +568,9 @@ lmh_status lmh_quantize_q4(const void* W, int64_t w_row_stride, const lmh_q4_tab
  *                     row stride out_row_stride (>= V).
  * The table is read only after the kernel enqueued before this one has ended, so
  * that may be the one that makes it.  No workspace is needed.
- * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (dtypes, group, alignment),
- * LMH_ERR_CUDA.  Device: LMH_DS_ROW_IDX_OUT_OF_RANGE (the row
- * reads zeros), LMH_DS_TIMEOUT.
+ * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (dtypes, group, alignment, V above
+ * 2^31 - 128, H above 2^31 - 16385), LMH_ERR_CUDA.  Device:
+ * LMH_DS_ROW_IDX_OUT_OF_RANGE (the row reads zeros), LMH_DS_TIMEOUT.
  */
 lmh_status lmh_project_q4(const void* hidden, lmh_dtype hidden_dtype, int64_t hidden_row_stride, int32_t num_tokens,
                           const int32_t* row_idx, int32_t rows, const lmh_q4_table* table, float logit_scale,

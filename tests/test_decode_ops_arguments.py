@@ -139,3 +139,16 @@ def test_tensors_on_the_host_are_refused(lmh):
                  lambda: lmh.lookup_q4(ids, t, out=torch.zeros(2, 64, dtype=torch.bfloat16))):
         with pytest.raises(AssertionError):
             call()
+
+
+@pytest.mark.parametrize("change", [dict(V=2 ** 31 - 127), dict(V=2 ** 31 - 1), dict(H=2 ** 31 - 128, stride=2 ** 31),
+                                    dict(H=2 ** 31 - 16384 + 128, stride=2 ** 31)])
+def test_projection_refuses_sizes_that_32_bits_cannot_round_up(change):
+    """Through the C entry; nothing is read through the stand-in pointers."""
+    from top_reduction_gb300 import _build
+    _build.build()
+    a = dict(V=10, H=128, stride=128)
+    a.update(change)
+    A, H = 1 << 20, a["H"]
+    t = L.Q4TableArg(A, H // 2, A, 0, H // 128, None, 0, a["V"], H, 128)
+    assert L.load().lmh_project_q4(A, 0, a["stride"], 1, None, 1, t, 1.0, A, 2, a["V"], None, None) == 2

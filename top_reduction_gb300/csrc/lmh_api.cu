@@ -548,6 +548,8 @@ lmh_status lmh_project_q4(const void* hidden, lmh_dtype hidden_dtype, int64_t hi
       !valid_scale(logit_scale) || (!row_idx && rows > num_tokens))
     return LMH_ERR_INVALID_ARG;
   if (hidden_dtype != LMH_BF16 && hidden_dtype != LMH_F16) return LMH_ERR_UNSUPPORTED;
+  // (the kernels round V up to whole tiles, H to whole pieces of the hidden rows, in 32 bits)
+  if (table->V > INT32_MAX - 127 || table->H > INT32_MAX - 16384) return LMH_ERR_UNSUPPORTED;
   if (out_dtype != LMH_F32 && out_dtype != hidden_dtype) return LMH_ERR_UNSUPPORTED;
   if (!aligned(hidden, 2) || !aligned(out, dtype_bytes(out_dtype))) return LMH_ERR_UNSUPPORTED;
   int sms = 0;
