@@ -44,8 +44,9 @@
  *   set bits (LMH_DS_*) in the caller's optional `dev_status` word with an
  *   atomic OR; kernels never trap.  The caller zeroes that word.
  * - Matrices are row-major; `*_stride` arguments are in elements.
- * - The first call on a device performs a one-time set-up (kernel attributes,
- *   driver entry points) under a once-flag.
+ * - The first call on a device of each family (head and reductions, draw, 4-bit
+ *   projection) performs a one-time set-up (kernel attributes, driver entry
+ *   points) under a lock.
  */
 #ifndef LMH_H
 #define LMH_H

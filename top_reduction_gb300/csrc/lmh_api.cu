@@ -19,27 +19,40 @@ namespace lmh {
 // per-device set-up
 // ---------------------------------------------------------------------------
 constexpr int kMaxDevices = 64;
+// What a call needs beside the device's properties: the attributes of its family's kernels
+// (setting them loads the kernels, which a call of another family is not to wait for).
+enum Family { kNoKernels = 0, kHeadAndReduction, kDraw, kQ4Projection, kFamilies };
 static std::mutex g_setup_mu;
-static bool g_setup_done[kMaxDevices];
+static bool g_setup_done[kMaxDevices][kFamilies];
 static int g_num_sms[kMaxDevices];
 
-static cudaError_t device_setup(int* num_sms) {
+static cudaError_t family_setup(Family f) {
+  switch (f) {
+    case kHeadAndReduction: {
+      cudaError_t e = logits_reduce_setup();
+      if (e == cudaSuccess) e = merge_setup();
+      if (e == cudaSuccess) e = head_setup();
+      return e;
+    }
+    case kDraw: return sample_logits_setup();
+    case kQ4Projection: return q4_project_setup();
+    default: return cudaSuccess;
+  }
+}
+
+static cudaError_t device_setup(int* num_sms, Family f = kHeadAndReduction) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(g_setup_mu);
-  if (!g_setup_done[dev]) {
+  if (!g_setup_done[dev][f]) {
     int sms = 0;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = logits_reduce_setup();
-    if (e == cudaSuccess) e = merge_setup();
-    if (e == cudaSuccess) e = head_setup();
-    if (e == cudaSuccess) e = sample_logits_setup();
-    if (e == cudaSuccess) e = q4_project_setup();
+    if (e == cudaSuccess) e = family_setup(f);
     if (e != cudaSuccess) return e;
     g_num_sms[dev] = sms;
-    g_setup_done[dev] = true;
+    g_setup_done[dev][f] = true;
   }
   *num_sms = g_num_sms[dev];
   return cudaSuccess;
@@ -504,7 +517,7 @@ lmh_status lmh_sample_from_logits(const void* logits, lmh_dtype dtype, int32_t r
   if (f.allowed_mask && f.mask_words < (V + 31) / 32) return LMH_ERR_INVALID_ARG;
   if (V > LMH_SAMPLE_V_MAX || !aligned(logits, dtype == LMH_F32 ? 4 : 2)) return LMH_ERR_UNSUPPORTED;
   int sms = 0;
-  if (device_setup(&sms) != cudaSuccess) return LMH_ERR_CUDA;
+  if (device_setup(&sms, kDraw) != cudaSuccess) return LMH_ERR_CUDA;
   Traced tr(kTraceSample, stream);
   return from_cuda(launch_sample_logits(logits, dtype, rows, V, row_stride, f, uniforms, sampled_ids, sampled_logprob,
                                         dev_status, sms, stream));
@@ -532,7 +545,7 @@ lmh_status lmh_quantize_q4(const void* W, int64_t w_row_stride, const lmh_q4_tab
   if (!W || w_row_stride < table->H) return LMH_ERR_INVALID_ARG;
   if (!aligned(W, 2)) return LMH_ERR_UNSUPPORTED;
   int sms = 0;
-  if (device_setup(&sms) != cudaSuccess) return LMH_ERR_CUDA;
+  if (device_setup(&sms, kNoKernels) != cudaSuccess) return LMH_ERR_CUDA;
   Traced tr(kTraceQuantizeQ4, stream);
   return from_cuda(launch_quantize_q4(W, w_row_stride, *table, stream));
 }
@@ -553,7 +566,7 @@ lmh_status lmh_project_q4(const void* hidden, lmh_dtype hidden_dtype, int64_t hi
   if (out_dtype != LMH_F32 && out_dtype != hidden_dtype) return LMH_ERR_UNSUPPORTED;
   if (!aligned(hidden, 2) || !aligned(out, dtype_bytes(out_dtype))) return LMH_ERR_UNSUPPORTED;
   int sms = 0;
-  if (device_setup(&sms) != cudaSuccess) return LMH_ERR_CUDA;
+  if (device_setup(&sms, kQ4Projection) != cudaSuccess) return LMH_ERR_CUDA;
   Traced tr(kTraceProjectQ4, stream);
   return from_cuda(launch_project_q4(hidden, hidden_dtype, hidden_row_stride, num_tokens, row_idx, rows, *table,
                                      logit_scale, out, out_dtype, out_row_stride, dev_status, sms, stream));
@@ -568,7 +581,7 @@ lmh_status lmh_lookup_q4(const int32_t* ids, int32_t n, const lmh_q4_table* tabl
   if (out_dtype != LMH_BF16 && out_dtype != LMH_F16 && out_dtype != LMH_F32) return LMH_ERR_INVALID_ARG;
   if (!aligned(out, dtype_bytes(out_dtype))) return LMH_ERR_UNSUPPORTED;
   int sms = 0;
-  if (device_setup(&sms) != cudaSuccess) return LMH_ERR_CUDA;
+  if (device_setup(&sms, kNoKernels) != cudaSuccess) return LMH_ERR_CUDA;
   Traced tr(kTraceLookupQ4, stream);
   return from_cuda(launch_lookup_q4(ids, n, *table, scale, out, out_dtype, out_row_stride, dev_status, sms, stream));
 }
