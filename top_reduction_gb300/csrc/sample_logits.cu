@@ -843,8 +843,9 @@ __device__ __forceinline__ u64 RowSampler<T>::warp_mass(const Kept& k) {
 
 // Narrows k->z_cut, k->id_cut to the shortest prefix of the order whose count (or
 // mass) reaches target >= 1.  A target above the total of the tokens with a weight
-// leaves k alone.  By mass: `total` is the row's, of which the tokens above listed_t
-// (there or thereabouts: it is the sample that leaves them out) have listed_mass.
+// leaves k alone.  By mass: `total` is that of the tokens that *k keeps so far (the sample
+// is of these alone), of which the ones above listed_t (there or thereabouts: it is the
+// sample that leaves them out) have listed_mass.
 template <typename T>
 __device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 target, u64 total, float listed_t,
                                                          u64 listed_mass, Kept* k) {
@@ -870,9 +871,10 @@ __device__ __forceinline__ void RowSampler<T>::threshold(bool by_mass, u64 targe
     const int step = attempt == 0 ? kSampleStep : 1;
 #pragma unroll 1
     for (int j = lane_ * step; j < n_ * kN; j += 32 * step) {
-      const float t = t_of(element(j));
+      const float z = element(j), t = t_of(z);
       const int b = static_cast<int>(place(t));
-      if (b < kBins && (attempt > 0 || t <= listed_t)) count_into(sh.hist[0], b, by_mass, t);
+      if (b < kBins && (attempt > 0 || ((t <= listed_t) & is_kept(z, id0_ + j, *k))))
+        count_into(sh.hist[0], b, by_mass, t);
     }
     cluster_sync();
     const u64 bin_sum = gather_bin(sh.hist[0][0], by_mass ? sh.hist[0][1] : nullptr);
