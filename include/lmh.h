@@ -557,7 +557,11 @@ lmh_status lmh_quantize_q4(const void* W, int64_t w_row_stride, const lmh_q4_tab
  * rounded to 2^-39 of it.  A row with an infinity or NaN gives infinities and NaN.
  * For batches of few rows (decode): the rows are taken in passes, each of which
  * reads the table once, of up to 32 rows where H is at most 2816 (with zero points
- * 2560), 16 up to 5120, 8 above.
+ * 2560), 16 up to 5120, 8 above.  Where a table is at hand in bf16 too,
+ * lmh_project_logprobs takes less time from 33 rows on (2560 x 151936: 141 us for
+ * 64 rows with the logits written, 186 here), less or about as much from 17 on with
+ * zero points (32 rows: 137, 150 here) or longer rows (32 rows of 4096 x 128256: 168,
+ * 162 here).
  *
  *   hidden            device [num_tokens x H] of hidden_dtype (LMH_BF16 or
  *                     LMH_F16), row stride hidden_row_stride (>= H), aligned to

@@ -3,7 +3,7 @@
 //
 // Nothing here computes results: every step of the path runs in the kernels
 // of select_rows.cu, head_gemm.cu, logits_reduce.cu, merge_partials.cu,
-// sample_logits.cu, q4_table.cu and q4_project.cu.
+// sample_logits.cu, q4_table.cu, q4_project.cuh and q4_project_wide.cuh.
 #include <atomic>
 #include <cmath>
 #include <cstring>

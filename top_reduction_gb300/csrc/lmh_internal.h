@@ -180,7 +180,7 @@ cudaError_t launch_sample_logits(const void* logits, lmh_dtype dtype, int rows, 
                                  const lmh_filters& f, const float* uniforms, int32_t* ids, float* logprobs,
                                  uint32_t* dev_status, int num_sms, cudaStream_t stream);
 
-// ---- 4-bit tables (q4_table.cu, q4_project.cu) ----
+// ---- 4-bit tables (q4_table.cu, q4_project_*.cu) ----
 
 cudaError_t q4_project_setup();
 cudaError_t launch_quantize_q4(const void* W, int64_t w_stride, const lmh_q4_table& t, cudaStream_t stream);

@@ -13,7 +13,7 @@
 // Measured with cold L2 (2560 x 151936, group 64): 53 us for 1 row, of which the table's
 // 207 MB at the copy rate are 30.5, 70 us for 16 rows (80 with zero points), 150 for 32 with
 // zero points; 4096 x 128256, group 128 with zero points, 16 rows: 92 us (41 at the copy
-// rate).  For one row the issue slots are busy 57% and the ALU 43%: what bounds it beside
+// rate), 32 rows in two reads 172 (162 without zero points).  For one row the issue slots are busy 57% and the ALU 43%: what bounds it beside
 // the reads is the unpacking.  For 16 and 32 rows it is the latency that the 12 or 8 warps
 // whose sums fit in registers cannot cover, and loads that stay in flight only as far as
 // the few stages go that the hidden rows leave.

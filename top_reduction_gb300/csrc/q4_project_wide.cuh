@@ -21,12 +21,13 @@
 //   logits of its hidden rows.
 //
 // Unpacking and the hidden rows' form are those of project_q4_kernel, whose two entries
-// of a pair have one constant here: the zero point is 8.  (Other zero points would enter
-// with a group's sum, (8 - zero) times the sum of x: where the entries are close to their
-// zero point the two cancel, and the error is more than the products' own.)
+// of a pair have one constant here: the zero point is 8.  (Tables with zero points run on
+// project_q4_kernel.  An unpacking thread owns one table row, so it could subtract the row's
+// own zero points as that kernel does; such a form has not been built.)
 //
 // Measured with cold L2: 98 us for 32 rows of 2560 x 151936, group 64 (226 MB in and out: 33
-// us at the copy rate), where mma.sync took 129; 94 for 17 rows, 59 for 24 of 1024, group 32.
+// us at the copy rate), where mma.sync took 129; 94 for 17 rows, 59 for 24 of 1024, group 32;
+// 174 for 33 rows, 186 for 64 and 709 for 256, which read and unpack the table once per 32.
 // The unpacking and the sums' warps hold the issue slots 53% busy, the tensor pipe is 11%
 // busy: what is left is the stages' hand-over between the roles, four times per 128 entries,
 // with a ring of three stages beside the hidden rows.

@@ -43,7 +43,13 @@
 // loading 6 us, the list that does not do 12, the bracket 7, the parts 8, their list 5, the
 // draw 6), 27 for 64 rows of 128256 bf16 with min-p and a mask, 147 for 256 rows of 248320
 // bf16 (127 MB; 2048 CTAs, two to an SM).  HBM is not the bound in any of them: 13% of its
-// time for the largest.  Half the CTAs per row there, with twice the logits each, were
+// time for the largest.  (The 32 rows take 33 to 43 us in a row of calls, by how many of them
+// need a threshold.)  Top-k beyond a list and top-p after it are two searches: 51 us for one
+// flat row of 151936 f32 with k 1000, 68 for 32 of them, 408 for 256 in bf16.
+// The lists' bins lie over z as it is, so that no row's maximum is needed first.  A row whose
+// logits are all above 64 or below -64, or most of them within a bin, overflows its list and
+// takes the threshold's way after it: 113 us for one row of 128256 f32 with k 50 and p 0.95
+// where 18 are usual, 164 for 32 of 151936 where 20 are.  Half the CTAs per row there, with twice the logits each, were
 // slower (205 us where an earlier state of this kernel took 166).
 // The next kernel is not let in early, although none of this library's reads ids ahead of its
 // wait any more: that would let draws in a row overlap, and has not been measured in this form.
