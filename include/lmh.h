@@ -21,6 +21,12 @@
  * input rows of token ids), lmh_project_q4 (the logits of the body's rows) and
  * lmh_sample_from_logits (the next ids, with temperature, top-k, top-p, min-p).
  *
+ * For a step of beam search, or of requests with adapters of their own:
+ * lmh_add_adapters (low-rank adapters of many requests beside a shared projection),
+ * lmh_beam_select and lmh_beam_select_lists (each group's best continuations, from
+ * logits or from the top-k lists of lmh_project_logprobs) and lmh_reorder_rows (the
+ * beams' states follow their parents).
+ *
  * The O(k+1) result of a row is: lse (fp32 log-sum-exp over the vocabulary),
  * the selected token's logprob, and the exact top-k (ids and logprobs),
  * sorted by logit descending with exact ties ordered by ascending token id.
@@ -45,7 +51,7 @@
  *   atomic OR; kernels never trap.  The caller zeroes that word.
  * - Matrices are row-major; `*_stride` arguments are in elements.
  * - The first call on a device of each family (head and reductions, draw, 4-bit
- *   projection) performs a one-time set-up (kernel attributes, driver entry
+ *   projection, adapters, beams, states) performs a one-time set-up (kernel attributes, driver entry
  *   points) under a lock.
  */
 #ifndef LMH_H
@@ -64,6 +70,8 @@ extern "C" {
 
 /* Largest k (top-k entries per row) any entry point accepts. */
 #define LMH_K_MAX 128
+/* Largest number of beams in a group. */
+#define LMH_BEAMS_MAX 128
 /* k_max = LMH_K_FULL asks for the full-vocabulary output: topk_logprobs
  * receives [rows x V] logprobs in token-id order and topk_ids is not written
  * (openinfer issue #719, "Acceptance criteria": the -1 behaviour is the
@@ -96,7 +104,9 @@ typedef enum lmh_path { LMH_PATH_PROJECT = 0, LMH_PATH_FROM_LOGITS = 1, LMH_PATH
 #define LMH_DS_ROWS_OVERFLOW 0x4u        /* more selected rows than max_out_rows (extra rows dropped) */
 #define LMH_DS_ROW_IDX_OUT_OF_RANGE 0x8u /* a row index outside [0, num_tokens) (row reads zeros)   */
 #define LMH_DS_TIMEOUT 0x10u             /* a bounded device-side wait gave up (kernel returned)     */
-#define LMH_DS_NO_ALLOWED_TOKEN 0x20u    /* sampling: a row's mask allows no token (id -1, NaN)      */
+#define LMH_DS_NO_ALLOWED_TOKEN 0x20u    /* sampling: a row's mask allows no token (id -1, NaN); beams: a
+                                            group has no continuation                               */
+#define LMH_DS_ADAPTER_OUT_OF_RANGE 0x40u /* an adapter index outside [0, count) other than -1 (none is added) */
 
 /*
  * lmh_select_rows -- which rows of a packed batch are sampled.
@@ -598,6 +608,182 @@ lmh_status lmh_project_q4(const void* hidden, lmh_dtype hidden_dtype, int64_t hi
 lmh_status lmh_lookup_q4(const int32_t* ids, int32_t n, const lmh_q4_table* table, float scale, void* out,
                          lmh_dtype out_dtype, int64_t out_row_stride, uint32_t* dev_status, cudaStream_t stream);
 
+/*
+ * Low-rank adapters of several requests, in one array each: adapter l adds
+ * scale[l] * up[l] . (down[l] . x) to a projection of x.
+ */
+#define LMH_ADAPTERS_MAX 4096
+#define LMH_ADAPTER_RANK_MAX 128
+
+typedef struct lmh_adapters {
+  const void* down;            /* device [count x rank x H] of dtype, 16-byte aligned */
+  int64_t down_adapter_stride; /* elements, a multiple of 8 */
+  int64_t down_row_stride;     /* elements, >= H, a multiple of 8 */
+  const void* up;              /* device [count x N x rank] of dtype, 16-byte aligned */
+  int64_t up_adapter_stride;   /* elements, a multiple of 8 */
+  int64_t up_row_stride;       /* elements, >= rank, a multiple of 8 */
+  lmh_dtype dtype;             /* LMH_BF16 or LMH_F16 */
+  const float* scales;         /* device fp32 [count], or NULL (1) */
+  const int32_t* ranks;        /* device int32 [count], or NULL (rank): the ranks in use, held in
+                                  [0, rank]; what stands behind them is not used */
+  int32_t count;               /* 1..LMH_ADAPTERS_MAX */
+  int32_t rank;                /* a multiple of 8, to LMH_ADAPTER_RANK_MAX */
+  int32_t H, N;                /* H a multiple of 8 */
+} lmh_adapters;
+
+/* Workspace of lmh_add_adapters (bytes; 0 for sizes it rejects), 256-byte aligned.  The size
+ * depends on the device's SM count. */
+size_t lmh_adapters_workspace_bytes(int32_t rows, const lmh_adapters* table);
+
+/*
+ * lmh_add_adapters -- each row's adapter beside a shared projection.
+ *
+ *   out[i][n] = y[i][n] + scales[l] * sum_r up[l][n][r] * d[i][r],
+ *   d[i][r]   = sum_h down[l][r][h] * x[row_idx[i]][h],      l = adapter_idx[i]
+ *
+ * y is the shared projection's result for the rows (a layer's, or the logits of
+ * lmh_project_q4 or lmh_project_logprobs), so out is the projection with the
+ * requests' adapters.  Sums are held in fp32; d enters the second product as the sum
+ * of two numbers of dtype, within 2^-17 of its value for LMH_BF16 and 2^-21 for LMH_F16
+ * (entries of a row's d below 2^-14 of the largest: within 2^-38 of the largest).
+ * Rounded once, to out_dtype.  A row of x with an infinity or NaN gives infinities and
+ * NaN.  The rows may come in any order, each with any adapter; a weight array is read
+ * about once per 32 rows that use it, and not at all if none does.
+ *
+ *   x                 device [num_tokens x H] of the table's dtype, row stride
+ *                     x_row_stride (>= H), aligned to its elements.
+ *   row_idx           device int32 [rows] or NULL, as lmh_project_logprobs.
+ *   adapter_idx       device int32 [rows]; -1: no adapter (out is y).  Any other index
+ *                     outside [0, count) counts as -1 and sets
+ *                     LMH_DS_ADAPTER_OUT_OF_RANGE.
+ *   y                 device [rows x N] of out_dtype, row stride y_row_stride (>= N).
+ *   out               device [rows x N] of out_dtype (LMH_F32 or the table's dtype), row
+ *                     stride out_row_stride (>= N).  It may be y itself with the same
+ *                     stride (rows without an adapter are not touched then); it
+ *                     overlaps y in no other way, nor x.
+ *   workspace         >= lmh_adapters_workspace_bytes(rows, table) bytes, 256-byte
+ *                     aligned.
+ * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (dtypes, rank, count, alignment),
+ * LMH_ERR_WORKSPACE_TOO_SMALL, LMH_ERR_CUDA.  Device: LMH_DS_ADAPTER_OUT_OF_RANGE,
+ * LMH_DS_ROW_IDX_OUT_OF_RANGE (the row reads zeros).
+ */
+lmh_status lmh_add_adapters(const void* x, int64_t x_row_stride, int32_t num_tokens, const int32_t* row_idx,
+                            int32_t rows, const int32_t* adapter_idx, const lmh_adapters* table, const void* y,
+                            int64_t y_row_stride, void* out, lmh_dtype out_dtype, int64_t out_row_stride,
+                            void* workspace, size_t workspace_bytes, uint32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Beam search: rows [g * beams, (g + 1) * beams) are group g's beams, each with a score
+ * (the sum of its tokens' log-probabilities) in `scores`.
+ *
+ *   parents   the row that a continuation comes from (g * beams + beam), and
+ *   tokens    the token that it adds; both -1, with a score of -inf, in places that no
+ *             continuation is left for.
+ *   finished  a beam whose flag is set has ended: it has one continuation, itself, with
+ *             pad_id as its token and its score as it is.  Its logits are not read.
+ *   k         continuations per group, best first.  Twice the beams leave enough for a
+ *             step's ended ones to be taken out by the caller.
+ *   keep_slots  (k == beams only) the continuations do not come best first: a parent's
+ *             best one stands in the parent's own place, the others fill the places left
+ *             over, best first from the lowest.  parents[parents[r]] == parents[r] then, so
+ *             lmh_reorder_rows moves the fewest rows.
+ */
+typedef struct lmh_beams {
+  int32_t groups, beams;    /* beams 1..LMH_BEAMS_MAX */
+  int32_t k;                /* 1..LMH_K_MAX */
+  int32_t keep_slots;       /* 0 or 1 */
+  const float* scores;      /* device fp32 [groups x beams]; a beam whose score is not finite
+                               has no continuation */
+  const uint8_t* finished;  /* device u8 [groups x beams], or NULL */
+  int32_t pad_id;
+  float* out_scores;        /* device fp32 [groups x k], out; may not be `scores` */
+  int32_t* out_parents;     /* device int32 [groups x k], out */
+  int32_t* out_tokens;      /* device int32 [groups x k], out */
+} lmh_beams;
+
+/* Workspace of lmh_beam_select (bytes; 0 for sizes it rejects), 256-byte aligned. */
+size_t lmh_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t V);
+
+/*
+ * lmh_beam_select -- each group's k best continuations over its beams and the vocabulary.
+ *
+ *   score(b, v) = scores[b] + z[b][v] - lse[b],   lse[b] = log sum_v exp(z[b][v])
+ *
+ * The log-sum-exp is over all tokens; allowed_mask takes tokens out of the choice only (as
+ * in lmh_project_logprobs_sample, a token's log-probability is the model's own).  Scores are
+ * compared in 64 bits, as (scores[b] - log sum_v exp(z[b][v] - M)) + (z[b][v] - M) with M
+ * the row's largest logit; equal ones are ordered by beam, then token.  A NaN logit counts as -inf, and -inf is no
+ * continuation; a row with +inf logits has these alone, as equals.  A score that fp32
+ * cannot hold is no continuation.
+ *
+ *   logits            device [groups * beams x V] of dtype, row stride row_stride (>= V),
+ *                     aligned to sizeof(dtype); beams * V below 2^31.
+ *   allowed_mask      device u32 [groups * beams x mask_words] or NULL, as in lmh_sampling.
+ *   workspace         >= lmh_beam_workspace_bytes(groups, beams, V) bytes, 256-byte aligned.
+ * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (beams, k, misaligned logits, beams * V),
+ * LMH_ERR_WORKSPACE_TOO_SMALL, LMH_ERR_CUDA.  Device: LMH_DS_NO_ALLOWED_TOKEN (a group
+ * without a continuation), LMH_DS_TIMEOUT.
+ */
+lmh_status lmh_beam_select(const lmh_beams* beams, const void* logits, lmh_dtype dtype, int32_t V,
+                           int64_t row_stride, const uint32_t* allowed_mask, int32_t mask_words, void* workspace,
+                           size_t workspace_bytes, uint32_t* dev_status, cudaStream_t stream);
+
+/*
+ * lmh_beam_select_lists -- the same from each beam's own best tokens (the top-k lists of
+ * lmh_project_logprobs, whose logits never reach memory): lists of at least k entries give
+ * what lmh_beam_select gives, up to the rounding of the lists' logprobs.
+ *
+ *   topk_ids, topk_logprobs  device [groups * beams x n], contiguous.  Entries with an id
+ *                     below 0 or a logprob that is not finite are none.  Equal scores are
+ *                     ordered by beam, then place in the list.
+ * beams * n below 2^31.  No workspace is needed.  Errors: as lmh_beam_select.
+ */
+lmh_status lmh_beam_select_lists(const lmh_beams* beams, const int32_t* topk_ids, const float* topk_logprobs,
+                                 int32_t n, uint32_t* dev_status, cudaStream_t stream);
+
+/*
+ * A state that has one row per row of the batch: token histories, block tables, caches.
+ * Row r's bytes are n0 * n1 chunks of chunk_bytes each, chunk (i, j) at
+ *   src + r * src_row_bytes + i * src_outer_bytes[0] + j * src_outer_bytes[1]
+ * and in the same way at dst.  dst == src (with the same strides): in place.  With
+ * position_bytes > 0, a chunk is a run of positions of that size.
+ */
+typedef struct lmh_row_state {
+  const void* src;
+  void* dst;
+  int64_t src_row_bytes, dst_row_bytes;
+  int64_t src_outer_bytes[2], dst_outer_bytes[2];
+  int32_t n0, n1;
+  int64_t chunk_bytes;
+  int64_t position_bytes; /* 0: chunks are moved whole */
+} lmh_row_state;
+
+/*
+ * lmh_reorder_rows -- every state's row r becomes what row parents[r] held.
+ *
+ * Rows [g * beams, (g + 1) * beams) are a group, and a row's parent is one of its group
+ * (the out_parents of a selection with k == beams).  In place, rows that are their own
+ * parents are not touched, and any other parents are right too (rows that swap, a row that
+ * is taken and replaced).
+ *
+ *   states            host array [num_states].  Their strides are not negative; rows and
+ *                     chunks of a dst do not overlap, nor do the states each other (in
+ *                     place, dst and src are the same memory), parents or lengths.
+ *   parents           device int32 [groups * beams]; -1 (no continuation): the row itself.
+ *                     Any other row outside the group counts as -1 and sets
+ *                     LMH_DS_ROW_IDX_OUT_OF_RANGE.
+ *   lengths           device int32 [groups * beams] or NULL: positions in use of each row
+ *                     as it is in src.  Of states with positions, a row's first
+ *                     lengths[parent] are moved, and what stands behind them in dst is left
+ *                     as it was.  NULL: all are moved.
+ * No workspace is needed.  Errors: LMH_ERR_INVALID_ARG (null pointers, sizes, negative
+ * strides, in place with other strides), LMH_ERR_UNSUPPORTED (beams, more than 2^31
+ * slices), LMH_ERR_CUDA.
+ */
+lmh_status lmh_reorder_rows(const lmh_row_state* states, int32_t num_states, int32_t groups, int32_t beams,
+                            const int32_t* parents, const int32_t* lengths, uint32_t* dev_status,
+                            cudaStream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* lmh_status_string(lmh_status status);
 
@@ -615,8 +801,9 @@ int32_t lmh_version(void);
  * "head_logprobs", "merge_partials", "logits_reduce" (the streaming pass of
  * lmh_logprobs_from_logits), "logits_select" (its per-row selection),
  * "full_logprobs" (the pass that writes the k_max = LMH_K_FULL output),
- * "sample_logits", "project_q4", "lookup_q4", "quantize_q4") since the last
- * reset.
+ * "sample_logits", "project_q4", "lookup_q4", "quantize_q4", "adapter_plan",
+ * "adapter_down", "adapter_up", "beam_stream", "beam_choose", "reorder_rows") since the
+ * last reset.
  * lmh_trace_reset clears the totals.
  */
 lmh_status lmh_trace_enable(int32_t enable);

@@ -3,7 +3,8 @@
 //
 // Nothing here computes results: every step of the path runs in the kernels
 // of select_rows.cu, head_gemm.cu, logits_reduce.cu, merge_partials.cu,
-// sample_logits.cu, q4_table.cu, q4_project.cuh and q4_project_wide.cuh.
+// sample_logits.cu, q4_table.cu, q4_project.cuh, q4_project_wide.cuh, adapters.cu,
+// beam_select.cu and reorder_rows.cu.
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -21,7 +22,7 @@ namespace lmh {
 constexpr int kMaxDevices = 64;
 // What a call needs beside the device's properties: the attributes of its family's kernels
 // (setting them loads the kernels, which a call of another family is not to wait for).
-enum Family { kNoKernels = 0, kHeadAndReduction, kDraw, kQ4Projection, kFamilies };
+enum Family { kNoKernels = 0, kHeadAndReduction, kDraw, kQ4Projection, kAdapters, kBeams, kStates, kFamilies };
 static std::mutex g_setup_mu;
 static bool g_setup_done[kMaxDevices][kFamilies];
 static int g_num_sms[kMaxDevices];
@@ -36,6 +37,9 @@ static cudaError_t family_setup(Family f) {
     }
     case kDraw: return sample_logits_setup();
     case kQ4Projection: return q4_project_setup();
+    case kAdapters: return adapters_setup();
+    case kBeams: return beam_setup();
+    case kStates: return reorder_setup();
     default: return cudaSuccess;
   }
 }
@@ -92,7 +96,8 @@ Partials carve_partials(void* base, int rows, int splits, int k_max) {
 static const char* const kTraceNames[kTraceCount] = {"select_rows",    "gather_rows",   "head_logprobs",
                                                      "logits_reduce",  "merge_partials", "logits_select",
                                                      "full_logprobs", "sample_logits", "project_q4",    "lookup_q4",
-                                                     "quantize_q4"};
+                                                     "quantize_q4",    "adapter_plan",   "adapter_down",  "adapter_up",
+                                                     "beam_stream",    "beam_choose",    "reorder_rows"};
 
 struct TraceRecord {
   int kernel;
@@ -584,6 +589,149 @@ lmh_status lmh_lookup_q4(const int32_t* ids, int32_t n, const lmh_q4_table* tabl
   if (device_setup(&sms, kNoKernels) != cudaSuccess) return LMH_ERR_CUDA;
   Traced tr(kTraceLookupQ4, stream);
   return from_cuda(launch_lookup_q4(ids, n, *table, scale, out, out_dtype, out_row_stride, dev_status, sms, stream));
+}
+
+static lmh_status check_adapters(const lmh_adapters* t) {
+  if (!t || !t->down || !t->up || t->count <= 0 || t->rank <= 0 || t->H <= 0 || t->N <= 0) return LMH_ERR_INVALID_ARG;
+  if (t->down_row_stride < t->H || t->up_row_stride < t->rank || t->down_adapter_stride < 0 ||
+      t->up_adapter_stride < 0)
+    return LMH_ERR_INVALID_ARG;
+  if (t->dtype != LMH_BF16 && t->dtype != LMH_F16) return LMH_ERR_UNSUPPORTED;
+  if (t->count > LMH_ADAPTERS_MAX || t->rank > LMH_ADAPTER_RANK_MAX || t->rank % 8 != 0 || t->H % 8 != 0)
+    return LMH_ERR_UNSUPPORTED;
+  if (t->down_row_stride % 8 != 0 || t->down_adapter_stride % 8 != 0 || t->up_row_stride % 8 != 0 ||
+      t->up_adapter_stride % 8 != 0)
+    return LMH_ERR_UNSUPPORTED;
+  if (!aligned(t->down, 16) || !aligned(t->up, 16)) return LMH_ERR_UNSUPPORTED;
+  // (the kernels round H and N up to whole tiles in 32 bits)
+  if (t->H > INT32_MAX - 1024 || t->N > INT32_MAX - 65536) return LMH_ERR_UNSUPPORTED;
+  return LMH_OK;
+}
+
+size_t lmh_adapters_workspace_bytes(int32_t rows, const lmh_adapters* table) {
+  if (rows < 0 || check_adapters(table) != LMH_OK) return 0;
+  if (rows == 0) return 256;
+  int sms = 0;
+  if (device_setup(&sms, kNoKernels) != cudaSuccess) return 0;
+  return adapters_workspace_bytes(rows, table->count, table->rank, table->H, sms);
+}
+
+lmh_status lmh_add_adapters(const void* x, int64_t x_row_stride, int32_t num_tokens, const int32_t* row_idx,
+                            int32_t rows, const int32_t* adapter_idx, const lmh_adapters* table, const void* y,
+                            int64_t y_row_stride, void* out, lmh_dtype out_dtype, int64_t out_row_stride,
+                            void* workspace, size_t workspace_bytes, uint32_t* dev_status, cudaStream_t stream) {
+  const lmh_status st = check_adapters(table);
+  if (st != LMH_OK) return st;
+  if (rows == 0) return LMH_OK;
+  if (rows < 0 || num_tokens < 0 || !x || !adapter_idx || !y || !out || x_row_stride < table->H ||
+      y_row_stride < table->N || out_row_stride < table->N || (!row_idx && rows > num_tokens))
+    return LMH_ERR_INVALID_ARG;
+  if (y == out && y_row_stride != out_row_stride) return LMH_ERR_INVALID_ARG;
+  if (out_dtype != LMH_F32 && out_dtype != table->dtype) return LMH_ERR_UNSUPPORTED;
+  if (!aligned(x, 2) || !aligned(y, dtype_bytes(out_dtype)) || !aligned(out, dtype_bytes(out_dtype)))
+    return LMH_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256)) return LMH_ERR_INVALID_ARG;
+  int sms = 0;
+  if (device_setup(&sms, kAdapters) != cudaSuccess) return LMH_ERR_CUDA;
+  if (workspace_bytes < adapters_workspace_bytes(rows, table->count, table->rank, table->H, sms))
+    return LMH_ERR_WORKSPACE_TOO_SMALL;
+  return from_cuda(launch_add_adapters(x, x_row_stride, num_tokens, row_idx, rows, adapter_idx, *table, y,
+                                       y_row_stride, out, out_dtype, out_row_stride, workspace, dev_status, sms,
+                                       stream));
+}
+
+// The common check of both selections.
+static lmh_status check_beams(const lmh_beams* b) {
+  if (!b || b->groups < 0 || b->beams <= 0 || b->k <= 0) return LMH_ERR_INVALID_ARG;
+  if (b->beams > LMH_BEAMS_MAX || b->k > LMH_K_MAX) return LMH_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(b->groups) * b->beams > INT32_MAX) return LMH_ERR_UNSUPPORTED;
+  if (b->keep_slots != 0 && (b->keep_slots != 1 || b->k != b->beams)) return LMH_ERR_INVALID_ARG;
+  if (b->groups == 0) return LMH_OK;
+  if (!b->scores || !b->out_scores || !b->out_parents || !b->out_tokens || b->scores == b->out_scores)
+    return LMH_ERR_INVALID_ARG;
+  return LMH_OK;
+}
+
+static BeamCall beam_call(const lmh_beams& b, int V, uint32_t* dev_status) {
+  BeamCall c{};
+  c.groups = b.groups;
+  c.beams = b.beams;
+  c.V = V;
+  c.scores = b.scores;
+  c.finished = b.finished;
+  c.pad_id = b.pad_id;
+  c.k = b.k;
+  c.keep_slots = b.keep_slots != 0;
+  c.out_scores = b.out_scores;
+  c.out_parents = b.out_parents;
+  c.out_tokens = b.out_tokens;
+  c.dev_status = dev_status;
+  return c;
+}
+
+size_t lmh_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t V) {
+  if (groups < 0 || beams <= 0 || beams > LMH_BEAMS_MAX || V <= 0 || static_cast<int64_t>(beams) * V > INT32_MAX ||
+      static_cast<int64_t>(groups) * beams > INT32_MAX)
+    return 0;
+  if (groups == 0) return 256;
+  return beam_workspace_bytes(groups * beams, V);
+}
+
+lmh_status lmh_beam_select(const lmh_beams* beams, const void* logits, lmh_dtype dtype, int32_t V,
+                           int64_t row_stride, const uint32_t* allowed_mask, int32_t mask_words, void* workspace,
+                           size_t workspace_bytes, uint32_t* dev_status, cudaStream_t stream) {
+  const lmh_status st = check_beams(beams);
+  if (st != LMH_OK) return st;
+  if (V <= 0 || row_stride < V) return LMH_ERR_INVALID_ARG;
+  if (dtype != LMH_BF16 && dtype != LMH_F16 && dtype != LMH_F32) return LMH_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(beams->beams) * V > INT32_MAX) return LMH_ERR_UNSUPPORTED;
+  if (beams->groups == 0) return LMH_OK;
+  if (!logits || (allowed_mask && mask_words < (V + 31) / 32)) return LMH_ERR_INVALID_ARG;
+  if (!aligned(logits, dtype_bytes(dtype))) return LMH_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256)) return LMH_ERR_INVALID_ARG;
+  if (workspace_bytes < beam_workspace_bytes(beams->groups * beams->beams, V)) return LMH_ERR_WORKSPACE_TOO_SMALL;
+  int sms = 0;
+  if (device_setup(&sms, kBeams) != cudaSuccess) return LMH_ERR_CUDA;
+  return from_cuda(launch_beam_select(beam_call(*beams, V, dev_status), logits, dtype, row_stride, allowed_mask,
+                                      mask_words, workspace, sms, stream));
+}
+
+lmh_status lmh_beam_select_lists(const lmh_beams* beams, const int32_t* topk_ids, const float* topk_logprobs,
+                                 int32_t n, uint32_t* dev_status, cudaStream_t stream) {
+  const lmh_status st = check_beams(beams);
+  if (st != LMH_OK) return st;
+  if (n <= 0) return LMH_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(beams->beams) * n > INT32_MAX) return LMH_ERR_UNSUPPORTED;
+  if (beams->groups == 0) return LMH_OK;
+  if (!topk_ids || !topk_logprobs) return LMH_ERR_INVALID_ARG;
+  int sms = 0;
+  if (device_setup(&sms, kBeams) != cudaSuccess) return LMH_ERR_CUDA;
+  return from_cuda(launch_beam_select_lists(beam_call(*beams, n, dev_status), topk_ids, topk_logprobs, n, stream));
+}
+
+lmh_status lmh_reorder_rows(const lmh_row_state* states, int32_t num_states, int32_t groups, int32_t beams,
+                            const int32_t* parents, const int32_t* lengths, uint32_t* dev_status,
+                            cudaStream_t stream) {
+  if (num_states < 0 || groups < 0 || beams <= 0 || (num_states > 0 && !states)) return LMH_ERR_INVALID_ARG;
+  if (beams > LMH_BEAMS_MAX || static_cast<int64_t>(groups) * beams > INT32_MAX) return LMH_ERR_UNSUPPORTED;
+  if (groups == 0 || num_states == 0) return LMH_OK;
+  if (!parents) return LMH_ERR_INVALID_ARG;
+  for (int i = 0; i < num_states; ++i) {
+    const lmh_row_state& s = states[i];
+    if (s.n0 < 0 || s.n1 < 0 || s.chunk_bytes < 0 || s.position_bytes < 0) return LMH_ERR_INVALID_ARG;
+    if (s.n0 == 0 || s.n1 == 0 || s.chunk_bytes == 0) continue;
+    if (!s.src || !s.dst || s.src_row_bytes < 0 || s.dst_row_bytes < 0) return LMH_ERR_INVALID_ARG;
+    for (int j = 0; j < 2; ++j)
+      if (s.src_outer_bytes[j] < 0 || s.dst_outer_bytes[j] < 0) return LMH_ERR_INVALID_ARG;
+    if (s.src == s.dst && (s.src_row_bytes != s.dst_row_bytes || s.src_outer_bytes[0] != s.dst_outer_bytes[0] ||
+                           s.src_outer_bytes[1] != s.dst_outer_bytes[1]))
+      return LMH_ERR_INVALID_ARG;
+    // slices of a chunk are at least 512 bytes, and are counted in 32 bits
+    if (s.chunk_bytes / 512 >= INT32_MAX || static_cast<int64_t>(s.n0) * s.n1 > INT32_MAX) return LMH_ERR_UNSUPPORTED;
+  }
+  int sms = 0;
+  if (device_setup(&sms, kStates) != cudaSuccess) return LMH_ERR_CUDA;
+  return from_cuda(launch_reorder_rows(states, num_states, groups, beams, parents, lengths, dev_status, sms, stream));
 }
 
 lmh_status lmh_debug_set_wait_limit(uint64_t limit_ns) {

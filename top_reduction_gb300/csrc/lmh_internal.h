@@ -192,6 +192,48 @@ cudaError_t launch_project_q4(const void* hidden, lmh_dtype hidden_dtype, int64_
                               lmh_dtype out_dtype, int64_t out_stride, uint32_t* dev_status, int num_sms,
                               cudaStream_t stream);
 
+// ---- low-rank adapters (adapters.cu) ----
+
+cudaError_t adapters_setup();
+size_t adapters_workspace_bytes(int rows, int count, int rank, int H, int num_sms);
+cudaError_t launch_add_adapters(const void* x, int64_t x_stride, int num_tokens, const int32_t* row_idx, int rows,
+                                const int32_t* adapter_idx, const lmh_adapters& t, const void* y, int64_t y_stride,
+                                void* out, lmh_dtype out_dtype, int64_t out_stride, void* workspace,
+                                uint32_t* dev_status, int num_sms, cudaStream_t stream);
+
+// ---- beams (beam_select.cu) ----
+
+constexpr int kBeamsMaxRows = LMH_BEAMS_MAX;
+
+// What both selections take.
+struct BeamCall {
+  int groups, beams, V;
+  const float* scores;
+  const uint8_t* finished;
+  int pad_id;
+  int k;
+  bool keep_slots;
+  float* out_scores;
+  int32_t* out_parents;
+  int32_t* out_tokens;
+  uint32_t* dev_status;
+};
+
+cudaError_t beam_setup();
+size_t beam_workspace_bytes(int rows, int V);
+cudaError_t launch_beam_select(const BeamCall& c, const void* logits, lmh_dtype dtype, int64_t row_stride,
+                               const uint32_t* mask, int mask_words, void* workspace, int num_sms,
+                               cudaStream_t stream);
+cudaError_t launch_beam_select_lists(const BeamCall& c, const int32_t* ids, const float* logprobs, int n,
+                                     cudaStream_t stream);
+
+// ---- states of rows (reorder_rows.cu) ----
+
+cudaError_t reorder_setup();
+cudaError_t launch_reorder_rows(const lmh_row_state* states, int num_states, int groups, int beams,
+                                const int32_t* parents, const int32_t* lengths, uint32_t* dev_status, int num_sms,
+                                cudaStream_t stream);
+
 // Launch `kernel` on `stream`; with pdl = true it carries the programmatic
 // stream serialization attribute, so it may start while its predecessor in the
 // stream finishes (the kernel calls pdl_wait() before reading that
@@ -225,6 +267,12 @@ enum TraceKernel {
   kTraceProjectQ4,
   kTraceLookupQ4,
   kTraceQuantizeQ4,
+  kTraceAdapterPlan,
+  kTraceAdapterDown,
+  kTraceAdapterUp,
+  kTraceBeamStream,
+  kTraceBeamChoose,
+  kTraceReorder,
   kTraceCount
 };
 void trace_begin(TraceKernel k, cudaStream_t s);

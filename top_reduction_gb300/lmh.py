@@ -27,6 +27,9 @@ DS_ROWS_OVERFLOW = 0x4
 DS_ROW_IDX_OUT_OF_RANGE = 0x8
 DS_TIMEOUT = 0x10
 DS_NO_ALLOWED_TOKEN = 0x20
+DS_ADAPTER_OUT_OF_RANGE = 0x40
+BEAMS_MAX = 128  # beams of a group
+ADAPTERS_MAX, ADAPTER_RANK_MAX = 4096, 128
 
 
 class Sampling(ctypes.Structure):
@@ -50,13 +53,39 @@ class Q4TableArg(ctypes.Structure):
                 ("group", ctypes.c_int32)]
 
 
+class AdaptersArg(ctypes.Structure):
+    """struct lmh_adapters (include/lmh.h)."""
+    _fields_ = [("down", ctypes.c_void_p), ("down_adapter_stride", ctypes.c_int64), ("down_row_stride", ctypes.c_int64),
+                ("up", ctypes.c_void_p), ("up_adapter_stride", ctypes.c_int64), ("up_row_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("scales", ctypes.c_void_p), ("ranks", ctypes.c_void_p),
+                ("count", ctypes.c_int32), ("rank", ctypes.c_int32), ("H", ctypes.c_int32), ("N", ctypes.c_int32)]
+
+
+class BeamsArg(ctypes.Structure):
+    """struct lmh_beams (include/lmh.h)."""
+    _fields_ = [("groups", ctypes.c_int32), ("beams", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("keep_slots", ctypes.c_int32), ("scores", ctypes.c_void_p), ("finished", ctypes.c_void_p),
+                ("pad_id", ctypes.c_int32), ("out_scores", ctypes.c_void_p), ("out_parents", ctypes.c_void_p),
+                ("out_tokens", ctypes.c_void_p)]
+
+
+class RowStateArg(ctypes.Structure):
+    """struct lmh_row_state (include/lmh.h)."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("src_row_bytes", ctypes.c_int64),
+                ("dst_row_bytes", ctypes.c_int64), ("src_outer_bytes", ctypes.c_int64 * 2),
+                ("dst_outer_bytes", ctypes.c_int64 * 2), ("n0", ctypes.c_int32), ("n1", ctypes.c_int32),
+                ("chunk_bytes", ctypes.c_int64), ("position_bytes", ctypes.c_int64)]
+
+
 EXPORTS = ("lmh_select_rows", "lmh_count_selected_rows", "lmh_workspace_bytes",
            "lmh_project_logprobs", "lmh_project_logprobs_scaled", "lmh_project_logprobs_sample",
            "lmh_probe_selective",
            "lmh_logprobs_from_logits", "lmh_status_string",
            "lmh_version", "lmh_trace_enable", "lmh_trace_read", "lmh_trace_reset", "lmh_debug_set_wait_limit",
            "lmh_record_bytes", "lmh_project_partials", "lmh_merge_workspace_bytes", "lmh_merge_records",
-           "lmh_sample_from_logits", "lmh_quantize_q4", "lmh_project_q4", "lmh_lookup_q4")
+           "lmh_sample_from_logits", "lmh_quantize_q4", "lmh_project_q4", "lmh_lookup_q4",
+           "lmh_adapters_workspace_bytes", "lmh_add_adapters", "lmh_beam_workspace_bytes", "lmh_beam_select",
+           "lmh_beam_select_lists", "lmh_reorder_rows")
 
 _lib = None
 
@@ -127,6 +156,19 @@ def load():
     lib.lmh_project_q4.restype = ctypes.c_int
     lib.lmh_lookup_q4.argtypes = [P, i32, T, ctypes.c_float, P, ctypes.c_int, i64, P, P]
     lib.lmh_lookup_q4.restype = ctypes.c_int
+    A, B = ctypes.POINTER(AdaptersArg), ctypes.POINTER(BeamsArg)
+    lib.lmh_adapters_workspace_bytes.argtypes = [i32, A]
+    lib.lmh_adapters_workspace_bytes.restype = u64
+    lib.lmh_add_adapters.argtypes = [P, i64, i32, P, i32, P, A, P, i64, P, ctypes.c_int, i64, P, u64, P, P]
+    lib.lmh_add_adapters.restype = ctypes.c_int
+    lib.lmh_beam_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.lmh_beam_workspace_bytes.restype = u64
+    lib.lmh_beam_select.argtypes = [B, P, ctypes.c_int, i32, i64, P, i32, P, u64, P, P]
+    lib.lmh_beam_select.restype = ctypes.c_int
+    lib.lmh_beam_select_lists.argtypes = [B, P, P, i32, P, P]
+    lib.lmh_beam_select_lists.restype = ctypes.c_int
+    lib.lmh_reorder_rows.argtypes = [ctypes.POINTER(RowStateArg), i32, i32, i32, P, P, P, P]
+    lib.lmh_reorder_rows.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -557,11 +599,344 @@ def lookup_q4(ids, table, scale=1.0, out_dtype=torch.bfloat16, out=None, dev_sta
 
 
 # ---------------------------------------------------------------------------
+# beams and per-request adapters: adapters, selection, states that follow
+# ---------------------------------------------------------------------------
+
+class AdapterTable:
+    """Low-rank adapters in one array each (struct lmh_adapters): adapter l adds
+    scales[l] * up[l] @ (down[l] @ x) to a projection of x.
+
+    down: bf16 or f16 [count, rank, H]; up: the same type [count, N, rank]; scales: fp32 [count] or None
+    (1); ranks: int32 [count] or None (rank), the ranks in use: what stands behind them is not used.
+    Adapters and rows may be strided; the object keeps the tensors alive.
+    """
+
+    def __init__(self, down, up, scales=None, ranks=None):
+        assert down.is_cuda and down.device == up.device and down.dim() == 3 and up.dim() == 3
+        if down.dtype != up.dtype or down.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("down and up must both be bfloat16 or float16")
+        L, R, H = down.shape
+        N = up.shape[1]
+        if tuple(up.shape) != (L, N, R):
+            raise ValueError("down must be [count, rank, H] and up [count, N, rank]")
+        if (down.stride(2) != 1 and H > 1) or (up.stride(2) != 1 and R > 1):
+            raise ValueError("the last dimension of down and up must be contiguous")
+        dev = down.device
+        self.scales = _per_row(scales, torch.float32, L, dev, "scales")
+        self.ranks = _per_row(ranks, torch.int32, L, dev, "ranks")
+        self.down, self.up, self.device, self.dtype = down, up, dev, down.dtype
+        self.count, self.rank, self.H, self.N = L, R, H, N
+
+        def strides(t):  # (a dimension of one entry may have any stride)
+            row = t.stride(1) if t.shape[1] > 1 else t.shape[2]
+            return (t.stride(0) if L > 1 else 0), row
+        self._arg = AdaptersArg(down.data_ptr(), *strides(down), up.data_ptr(), *strides(up), _DTYPES[down.dtype],
+                                _ptr(self.scales), _ptr(self.ranks), L, R, H, N)
+        self._bytes = {}
+
+    def workspace_bytes(self, rows):
+        """Bytes of workspace that add_adapters needs for that many rows."""
+        n = self._bytes.get(rows)
+        if n is None:
+            n = int(load().lmh_adapters_workspace_bytes(rows, self._arg))
+            if n == 0:
+                raise LMHError(ERR_UNSUPPORTED, "lmh_adapters_workspace_bytes")
+            self._bytes[rows] = n
+        return n
+
+
+def _pitch(t, rows, width):
+    """The row stride of a [rows, width] tensor whose rows are contiguous."""
+    pitch, step = t.stride()
+    if step != 1 and width > 1:
+        raise ValueError("rows must be contiguous")
+    return pitch if rows > 1 else width
+
+
+def add_adapters(x, table, adapter_idx, y, row_idx=None, out=None, workspace=None, dev_status=None, stream=None):
+    """y [rows, N] and each row's adapter of x [T, H]: y[i] + scale * up @ (down @ x[row_idx[i]])
+    (lmh_add_adapters).
+
+    table: an AdapterTable; adapter_idx: int32 [rows], -1 for none; row_idx: int32 [rows] device tensor or
+    None; y: fp32 or the table's type (rows of x and y may be strided); out: like y, or y itself (in
+    place); workspace: table.workspace_bytes(rows) bytes, 256-byte aligned; stream: the call is made on
+    it, conversions and allocations included.
+    """
+    dev = x.device
+    if stream is not None:
+        with _on_stream(stream, dev):
+            return add_adapters(x, table, adapter_idx, y, row_idx, out, workspace, dev_status)
+    if _other_device(dev):
+        with torch.cuda.device(dev):
+            return add_adapters(x, table, adapter_idx, y, row_idx, out, workspace, dev_status)
+    rows, N = y.shape
+    T, H = x.shape
+    if dev != table.device or y.device != dev:
+        raise ValueError("x, the table and y must be on one device")
+    if H != table.H or N != table.N or x.dtype != table.dtype:
+        raise ValueError("x must be %s [T, %d] and y [rows, %d]" % (str(table.dtype)[6:], table.H, table.N))
+    idx = _per_row(adapter_idx, torch.int32, rows, dev, "adapter_idx")
+    if row_idx is not None and not (row_idx.dtype == torch.int32 and row_idx.device == dev and
+                                    row_idx.is_contiguous() and row_idx.numel() >= rows):
+        raise ValueError("row_idx must be a contiguous int32 tensor on %s with %d entries" % (dev, rows))
+    y_pitch = _pitch(y, rows, N)
+    if out is None:
+        out = torch.empty((rows, N), dtype=y.dtype, device=dev)
+        out_pitch = N
+    else:
+        if out.device != dev or out.dtype != y.dtype or out.shape != y.shape:
+            raise ValueError("out must be like y")
+        out_pitch = _pitch(out, rows, N)
+    if rows == 0:
+        return out
+    need = table.workspace_bytes(rows)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < need:
+        raise ValueError("workspace must be contiguous on %s with %d bytes" % (dev, need))
+    st = _lib.lmh_add_adapters(
+        x.data_ptr(), _pitch(x, T, H), T, _ptr(row_idx), rows, idx.data_ptr(), table._arg, y.data_ptr(), y_pitch,
+        out.data_ptr(), _DTYPES[y.dtype], out_pitch, workspace.data_ptr(), need, _status_word(dev_status, dev),
+        _raw_stream(dev))
+    if st != OK:
+        raise LMHError(st, "lmh_add_adapters")
+    return out
+
+
+def _beams_arg(scores, beams, k, finished, pad_id, keep_slots, out, rows, dev):
+    """(the argument of both selections, their results, tensors to keep until the call is made)"""
+    if beams <= 0 or rows % beams:
+        raise ValueError("the rows must be whole groups of %d beams" % beams)
+    groups = rows // beams
+    scores = _per_row(scores, torch.float32, rows, dev, "scores")
+    if scores is None:
+        raise ValueError("scores is required")
+    if finished is not None:
+        if isinstance(finished, torch.Tensor) and finished.dtype == torch.bool:
+            finished = finished.view(torch.uint8)
+        finished = _per_row(finished, torch.uint8, rows, dev, "finished")
+    if out is None:
+        whole = torch.empty((2, groups, k), dtype=torch.int32, device=dev)
+        out = {"scores": torch.empty((groups, k), dtype=torch.float32, device=dev), "parents": whole[0],
+               "tokens": whole[1]}
+    n = groups * k
+    arg = BeamsArg(groups, beams, k, 1 if keep_slots else 0, scores.data_ptr(), _ptr(finished), pad_id,
+                   _written(out["scores"], _FLOATS, n, dev, "scores"),
+                   _written(out["parents"], _WORDS, n, dev, "parents"),
+                   _written(out["tokens"], _WORDS, n, dev, "tokens"))
+    return arg, out, (scores, finished)
+
+
+def beam_workspace_bytes(rows, beams, V):
+    """Bytes of workspace that beam_select needs for logits [rows, V] of groups of `beams` rows."""
+    n = int(load().lmh_beam_workspace_bytes(rows // beams, beams, V)) if beams > 0 else 0
+    if n == 0:
+        raise LMHError(ERR_UNSUPPORTED, "lmh_beam_workspace_bytes")
+    return n
+
+
+def beam_select(logits, scores, beams, k=None, finished=None, pad_id=0, mask=None, keep_slots=False, workspace=None,
+                dev_status=None, out=None, stream=None):
+    """The k best continuations (k: beams by default) of every group of `beams` rows, over the beams and
+    the vocabulary of logits [rows, V] (bf16, f16 or f32; rows may be strided): scores[b] + log-softmax
+    (lmh_beam_select).
+
+    scores: fp32 [rows], the beams' sums of log-probabilities; finished: uint8 or bool [rows] or None,
+    ended beams go on as they are with pad_id; mask: int32/uint32 [rows, words] allowed-token bits or
+    None; keep_slots: survivors stay in their places (k == beams); workspace: beam_workspace_bytes
+    bytes, 256-byte aligned; stream: the call is made on it, conversions and allocations included.
+    Returns a dict with scores (fp32), parents (int32, rows of the batch) and tokens (int32), each
+    [groups, k]; -inf, -1 and -1 where no continuation is left.  out: such a dict, filled.
+    """
+    dev = logits.device
+    if stream is not None:
+        with _on_stream(stream, dev):
+            return beam_select(logits, scores, beams, k, finished, pad_id, mask, keep_slots, workspace, dev_status, out)
+    if _other_device(dev):
+        with torch.cuda.device(dev):
+            return beam_select(logits, scores, beams, k, finished, pad_id, mask, keep_slots, workspace, dev_status, out)
+    rows, V = logits.shape
+    assert logits.is_cuda
+    pitch = _pitch(logits, rows, V)
+    words = 0
+    if mask is not None:
+        mask = torch.as_tensor(mask, device=dev).contiguous()
+        if mask.dtype not in _WORDS or mask.dim() != 2 or mask.shape[0] != rows:
+            raise ValueError("mask must be int32 or uint32 [%d, words]" % rows)
+        words = mask.shape[1]
+    arg, out, kept = _beams_arg(scores, beams, beams if k is None else k, finished, pad_id, keep_slots, out, rows, dev)
+    need = beam_workspace_bytes(rows, beams, V)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < need:
+        raise ValueError("workspace must be contiguous on %s with %d bytes" % (dev, need))
+    st = _lib.lmh_beam_select(arg, logits.data_ptr(), _DTYPES[logits.dtype], V, pitch, _ptr(mask), words,
+                              workspace.data_ptr(), need, _status_word(dev_status, dev), _raw_stream(dev))
+    if st != OK:
+        raise LMHError(st, "lmh_beam_select")
+    return out
+
+
+def beam_select_lists(topk_ids, topk_logprobs, scores, beams, k=None, finished=None, pad_id=0, keep_slots=False,
+                      dev_status=None, out=None, stream=None):
+    """beam_select from each beam's own best tokens: topk_ids (int32) and topk_logprobs (fp32) [rows, n],
+    as project_logprobs and logprobs_from_logits return them (lmh_beam_select_lists).  Lists of at least
+    k entries hold every continuation that can be chosen."""
+    dev = topk_ids.device
+    if stream is not None:
+        with _on_stream(stream, dev):
+            return beam_select_lists(topk_ids, topk_logprobs, scores, beams, k, finished, pad_id, keep_slots,
+                                     dev_status, out)
+    if _other_device(dev):
+        with torch.cuda.device(dev):
+            return beam_select_lists(topk_ids, topk_logprobs, scores, beams, k, finished, pad_id, keep_slots,
+                                     dev_status, out)
+    rows, n = topk_ids.shape
+    assert topk_ids.is_cuda
+    if topk_ids.dtype != torch.int32 or topk_logprobs.dtype != torch.float32 or topk_logprobs.shape != (rows, n) or \
+            topk_logprobs.device != dev or not topk_ids.is_contiguous() or not topk_logprobs.is_contiguous():
+        raise ValueError("topk_ids must be contiguous int32, topk_logprobs contiguous float32 of the same shape")
+    arg, out, kept = _beams_arg(scores, beams, beams if k is None else k, finished, pad_id, keep_slots, out, rows, dev)
+    st = (_lib or load()).lmh_beam_select_lists(arg, topk_ids.data_ptr(), topk_logprobs.data_ptr(), n,
+                                                _status_word(dev_status, dev), _raw_stream(dev))
+    if st != OK:
+        raise LMHError(st, "lmh_beam_select_lists")
+    return out
+
+
+def _row_state(src, dst, dim, length_dim):
+    """(struct lmh_row_state, rows) of a tensor whose dimension `dim` is the rows of a batch."""
+    nd = src.dim()
+    if not -nd <= dim < nd:
+        raise ValueError("no dimension %d in a tensor of %d" % (dim, nd))
+    dim %= nd
+    if dst.shape != src.shape or dst.dtype != src.dtype or dst.device != src.device:
+        raise ValueError("a state's output must have its shape, type and device")
+    if src.numel() == 0:
+        return RowStateArg(), src.shape[dim]
+    es, shape, a, b = src.element_size(), src.shape, src.stride(), dst.stride()
+    # the chunk: the last dimensions, as far as both are contiguous (with positions: from them on)
+    chunk, at = 1, nd
+    first = dim + 1
+    if length_dim is not None:
+        length_dim %= nd
+        if length_dim <= dim:
+            raise ValueError("the positions' dimension must come after the rows'")
+        first = length_dim
+    while at > first and (shape[at - 1] == 1 or (a[at - 1] == chunk and b[at - 1] == chunk)):
+        at -= 1
+        chunk *= shape[at]
+    position = 0
+    if length_dim is not None:
+        if at > length_dim:
+            raise ValueError("a row's positions must be contiguous")
+        position = chunk // max(shape[length_dim], 1) * es
+    outer = []  # [size, stride, stride] of what is left, neighbours taken together where both strides allow it
+    for d in range(at):
+        if d == dim or shape[d] == 1:
+            continue
+        if outer and outer[-1][1] == a[d] * shape[d] and outer[-1][2] == b[d] * shape[d]:
+            outer[-1] = [outer[-1][0] * shape[d], a[d], b[d]]
+        else:
+            outer.append([shape[d], a[d], b[d]])
+    if len(outer) > 2:
+        raise ValueError("a state may have two runs of strided dimensions beside its rows, not %d" % len(outer))
+    outer = [[1, 0, 0]] * (2 - len(outer)) + outer
+    if shape[dim] > 1 and b[dim] == 0 or any(n > 1 and t == 0 for n, _, t in outer):
+        raise ValueError("a state's rows must not share memory")
+    two = ctypes.c_int64 * 2
+    return RowStateArg(src.data_ptr(), dst.data_ptr(), a[dim] * es, b[dim] * es, two(*(o[1] * es for o in outer)),
+                       two(*(o[2] * es for o in outer)), outer[0][0], outer[1][0], chunk * es, position), shape[dim]
+
+
+class RowStates:
+    """States that follow the rows of a batch (struct lmh_row_state), made once and used every step.
+
+    tensors: any types and shapes; dims: the dimension of each that is the rows (an int for all, or one
+    each); length_dims: the dimension of each that holds positions, or None where it has none (after the
+    rows' dimension, contiguous from there on); outs: tensors of the same shapes for the moved rows, or
+    None (in place).  The object keeps the tensors alive.
+    """
+
+    def __init__(self, tensors, dims=0, length_dims=None, outs=None):
+        tensors = list(tensors)
+        n = len(tensors)
+        if not n:
+            raise ValueError("no states")
+        dims = [dims] * n if isinstance(dims, int) else list(dims)
+        length_dims = [length_dims] * n if length_dims is None or isinstance(length_dims, int) else list(length_dims)
+        outs = tensors if outs is None else list(outs)
+        if len(dims) != n or len(length_dims) != n or len(outs) != n:
+            raise ValueError("dims, length_dims and outs must have one entry for each of the %d states" % n)
+        dev = tensors[0].device
+        self._arg = (RowStateArg * n)()
+        self.rows = None
+        for i, (src, dst, dim, along) in enumerate(zip(tensors, outs, dims, length_dims)):
+            if src.device != dev:
+                raise ValueError("the states must be on one device")
+            self._arg[i], rows = _row_state(src, dst, dim, along)
+            if self.rows not in (None, rows):
+                raise ValueError("the states have %d and %d rows" % (self.rows, rows))
+            self.rows = rows
+        written = [t.data_ptr() for t in outs if t.numel()]
+        apart = [t.data_ptr() for t, u in zip(tensors, outs) if t.numel() and (
+            t.data_ptr() != u.data_ptr() or t.stride() != u.stride())]
+        if len(set(written)) < len(written) or set(written) & set(apart):
+            raise ValueError("the same memory is written twice, or written and read by two states")
+        self.tensors, self.outs, self.device, self._n = tensors, outs, dev, n
+        self._ranges = [_range(t) for t in outs if t.numel()]
+
+
+def _range(t):
+    """The first byte of a tensor's memory, and the one behind its last."""
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def reorder_rows(states, parents, beams, lengths=None, dev_status=None, stream=None):
+    """Every state's row r becomes what row parents[r] held, within groups of `beams` rows
+    (lmh_reorder_rows).
+
+    states: a RowStates (or a list of tensors [rows, ...], moved in place); parents: int32 [rows] or
+    [groups, beams], as beam_select returns them with k == beams, -1 for the row itself; lengths: int32
+    [rows] or None, the positions in use of every row as it is before: of states with positions a row's
+    first lengths[parent] are moved.  stream: the call is made on it, conversions included.
+    Returns the list of the states' outputs.
+    """
+    if not isinstance(states, RowStates):
+        states = RowStates(states)
+    dev, rows = states.device, states.rows
+    if stream is not None:
+        with _on_stream(stream, dev):
+            return reorder_rows(states, parents, beams, lengths, dev_status)
+    if _other_device(dev):
+        with torch.cuda.device(dev):
+            return reorder_rows(states, parents, beams, lengths, dev_status)
+    if beams <= 0 or rows % beams:
+        raise ValueError("the rows must be whole groups of %d beams" % beams)
+    parents = _per_row(parents, torch.int32, rows, dev, "parents")
+    lengths = _per_row(lengths, torch.int32, rows, dev, "lengths")
+    for t in (parents, lengths):
+        if t is not None:
+            lo = t.data_ptr()
+            if any(lo < e and b < lo + 4 * rows for b, e in states._ranges):
+                raise ValueError("parents and lengths may not lie in a state that is written")
+    st = (_lib or load()).lmh_reorder_rows(states._arg, states._n, rows // beams, beams, _ptr(parents), _ptr(lengths),
+                                           _status_word(dev_status, dev), _raw_stream(dev))
+    if st != OK:
+        raise LMHError(st, "lmh_reorder_rows")
+    return states.outs
+
+
+# ---------------------------------------------------------------------------
 # kernel trace
 # ---------------------------------------------------------------------------
 
 TRACE_KERNELS = ("select_rows", "gather_rows", "head_logprobs", "logits_reduce", "merge_partials",
-                 "logits_select", "full_logprobs", "sample_logits", "project_q4", "lookup_q4", "quantize_q4")
+                 "logits_select", "full_logprobs", "sample_logits", "project_q4", "lookup_q4", "quantize_q4",
+                 "adapter_plan", "adapter_down", "adapter_up", "beam_stream", "beam_choose", "reorder_rows")
 
 
 def trace_enable(on=True):
