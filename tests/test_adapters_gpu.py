@@ -27,8 +27,13 @@ def _formula(c):
     """(out in 64 bits before its rounding, how far it may be off).
 
     Every fp32 sum of n terms is within n 2^-23 of its terms' magnitudes (twice fp32's half step, for sums
-    that are cut and not rounded), d's two 16-bit parts are within 2^-17 of it (2^-38 of the row's largest
-    for the smallest f16 parts), its product with the scale within 2^-24, and y is added with one rounding."""
+    that are cut and not rounded).  d is rounded to its type, half a step being 2^-8 of it for bf16 and 2^-11
+    for f16; for fp32 outputs what that left is too, so that 2^-16 and 2^-22 remain (2^-38 of the row's largest
+    for the smallest f16 parts).  Its product
+    with the scale is within 2^-24, and y is added with one rounding."""
+    step = {BF16: 2.0 ** -8, F16: 2.0 ** -11}[c["x"].dtype]
+    if c["y"].dtype == F32:
+        step *= step
     y, x = c["y"].double(), c["x"].double()
     idx, L = c["idx"].long(), c["down"].shape[0]
     out, off = y.clone(), torch.zeros_like(y)
@@ -42,9 +47,9 @@ def _formula(c):
         xr = x[rows if c["row_idx"] is None else c["row_idx"].long()[rows]]
         down, up = c["down"][l, :r].double(), c["up"][l, :, :r].double()
         d = xr @ down.t()
-        e = xr.abs() @ down.abs().t() * (H + 8) * 2.0 ** -23 + d.abs() * (2.0 ** -17 + 2.0 ** -23)
+        e = xr.abs() @ down.abs().t() * (H + 8) * 2.0 ** -23 + d.abs() * (step + 2.0 ** -23)
         if c["x"].dtype == F16 and r:
-            e += d.abs().amax(1, keepdim=True) * 2.0 ** -38
+            e += d.abs().amax(1, keepdim=True) * 2.0 ** -38  # (f16's smallest step is 2^-24, of 2^14)
         out[rows] += s * d @ up.t()
         off[rows] = s * (e @ up.abs().t() + d.abs() @ up.abs().t() * (2 * R + 8) * 2.0 ** -23)
     return out, off

@@ -138,12 +138,18 @@ static cudaError_t launch_adapters(const AdapterArgs& a, bool bf16, lmh_dtype ou
   e = bf16 ? launch_down_bf16(a, grid, stream) : launch_down_f16(a, grid, stream);
   trace_end(kTraceAdapterDown, stream);
   if (e != cudaSuccess) return e;
-  const int64_t max_steps = max_tiles * ((a.N + kADStep - 1) / kADStep);
   trace_begin(kTraceAdapterUp, stream);
-  e = bf16 ? launch_up_bf16(a, out_dtype, vec, max_steps, num_sms, stream)
-           : launch_up_f16(a, out_dtype, vec, max_steps, num_sms, stream);
+  e = bf16 ? launch_up_bf16(a, out_dtype, vec, max_tiles, num_sms, stream)
+           : launch_up_f16(a, out_dtype, vec, max_tiles, num_sms, stream);
   trace_end(kTraceAdapterUp, stream);
   return e;
+}
+
+// Whether rows of y or out can be read and written a lane's neighbours at a time (16 bytes; 8 of 16-bit outputs at
+// ranks above 32).
+static bool adapter_rows_align(const void* p, int64_t stride, int N, lmh_dtype dtype, int rank) {
+  const int n = 4, bytes = dtype == LMH_F32 ? 16 : 2 * n;
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride % n == 0 && N % n == 0;
 }
 
 cudaError_t launch_add_adapters(const void* x, int64_t x_stride, int num_tokens, const int32_t* row_idx, int rows,
@@ -175,9 +181,8 @@ cudaError_t launch_add_adapters(const void* x, int64_t x_stride, int num_tokens,
   a.out = static_cast<char*>(out);
   a.out_stride = out_stride;
   a.in_place = y == out && y_stride == out_stride;
-  const size_t four = out_dtype == LMH_F32 ? 16 : 8;
-  const bool vec = reinterpret_cast<uintptr_t>(y) % four == 0 && reinterpret_cast<uintptr_t>(out) % four == 0 &&
-                   y_stride % 4 == 0 && out_stride % 4 == 0 && t.N % 4 == 0;
+  const bool vec = adapter_rows_align(y, y_stride, t.N, out_dtype, t.rank) &&
+                   adapter_rows_align(out, out_stride, t.N, out_dtype, t.rank);
   a.splits = adapter_splits(rows, t.count, t.H, num_sms);
   char* p = static_cast<char*>(workspace);
   a.tile_count = reinterpret_cast<int32_t*>(p);

@@ -12,8 +12,10 @@
 // from memory to the MMA's registers without a stop in shared memory.  The order of the entries along the
 // inner dimension is free as long as A and B agree, so a lane takes 16 contiguous bytes of a weight row.
 //
-// d enters the second product as two 16-bit parts, high and low: 16 bits (bf16) or 22 (f16) of its fp32
-// value, so that its rounding stays near that of the fp32 sums.
+// d enters the second product in 16 bits: for fp32 outputs as two parts, high and low (16 bits of its value for
+// bf16, 22 for f16), so that its rounding stays near that of the fp32 sums; for 16-bit outputs as one, which rounds
+// the added part as its own type would be rounded.  (The second part doubles the MMAs and the operand's reads from
+// shared memory, which bound the product for packed prompts.)
 #pragma once
 
 #include <type_traits>
@@ -29,10 +31,10 @@ namespace lmh {
 constexpr int kADTile = 64;       // rows of a tile
 constexpr int kADCols = kADTile / 8;
 constexpr int kADPlanThreads = 1024;
-constexpr int kADThreads = 256;   // both products
+constexpr int kADThreads = 256;   // first product
 constexpr int kADWarps = kADThreads / 32;
-constexpr int kADStep = 32;       // outputs n a warp takes at a time
-constexpr int kADOwnPlan = kADThreads;  // rows to which every CTA finds its tiles by itself
+constexpr int kADStep = 32;       // outputs of the second product that a warp takes at a time
+constexpr int kADOwnPlan = 256;   // rows to which every CTA finds its tiles by itself
 
 struct AdapterTile {
   int adapter;  // -1: rows without one
@@ -85,15 +87,54 @@ __device__ __forceinline__ void mma16<__half>(float (&d)[4], const uint32_t (&a)
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// d = a * b
+template <typename T>
+__device__ __forceinline__ void mma16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16_first<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                           uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+template <>
+__device__ __forceinline__ void mma16_first<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// Four 8 x 8 matrices of 16-bit entries, lane 8i + r giving row r of matrix i (16 bytes): an A operand.
+__device__ __forceinline__ void load_matrices(uint32_t (&m)[4], uint32_t smem_row) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(m[0]), "=r"(m[1]), "=r"(m[2]), "=r"(m[3])
+               : "r"(smem_row)
+               : "memory");
+}
+
 template <typename T>
 struct Half16;  // conversions of a 16-bit type
 template <>
 struct Half16<__nv_bfloat16> {
+  __device__ __forceinline__ static float2 pair(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ static uint32_t pack(float x, float y) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
   __device__ __forceinline__ static uint16_t bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
   __device__ __forceinline__ static float value(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 };
 template <>
 struct Half16<__half> {
+  __device__ __forceinline__ static float2 pair(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+  __device__ __forceinline__ static uint32_t pack(float x, float y) {
+    const __half2 p = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
   __device__ __forceinline__ static uint16_t bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
   __device__ __forceinline__ static float value(uint16_t b) { return __half2float(__ushort_as_half(b)); }
 };
@@ -104,12 +145,25 @@ struct Half16<__half> {
 // Weights, x and y come through rings in shared memory in which every lane copies (cp.async) what it will
 // itself read, in the order of its registers: no barrier, no bank conflict, and as many bytes in flight as the
 // ring holds, which registers do not (measured: DESIGN).
+// (The form that fills up with zeros was measured slower: 17 million wavefronts of shared memory in place of 6.)
 template <int BYTES>
-__device__ __forceinline__ void lane_copy(void* smem_dst, const void* src) {
+__device__ __forceinline__ void lane_copy(uint32_t smem_dst, const void* src) {
   if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(src) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "n"(BYTES) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_dst), "l"(src), "n"(BYTES) : "memory");
+}
+// The same where `go` holds, without a branch.
+template <int BYTES>
+__device__ __forceinline__ void lane_copy_if(bool go, uint32_t smem_dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(
+                     smem_dst), "l"(src), "r"(static_cast<int>(go))
+                 : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@p cp.async.ca.shared.global [%0], [%1], %3;\n\t}" ::"r"(
+                     smem_dst), "l"(src), "r"(static_cast<int>(go)), "n"(BYTES)
+                 : "memory");
 }
 __device__ __forceinline__ void lane_copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the last N groups of this lane's copies have arrived.
@@ -119,13 +173,13 @@ __device__ __forceinline__ void lane_copies_wait() { asm volatile("cp.async.wait
 // ---------------------------------------------------------------------------
 // tiles
 // ---------------------------------------------------------------------------
-// The tiles of a call as a CTA of kADThreads threads sees them.  With at most kADOwnPlan rows thread i
+// The tiles of a call as a CTA of at least kADOwnPlan threads sees them.  With at most kADOwnPlan rows thread i
 // takes row i: its place among the rows of the same adapter gives its tile and its place in it, and a tile's
 // number is its first row's among the rows that are first in a tile.  Otherwise the plan kernel's results.
 struct TileSmem {
   alignas(16) int32_t adapter_of[kADOwnPlan];
   int32_t rows[kADTile];  // of the current tile
-  int32_t adapter, part, count, tiles;
+  int32_t adapter, part, count;
 };
 
 struct TileFinder {
@@ -144,8 +198,7 @@ struct TileFinder {
         mine = -1;
       }
     }
-    sm.adapter_of[i] = mine;
-    if (i == 0) sm.tiles = 0;
+    if (i < kADOwnPlan) sm.adapter_of[i] = mine;
     __syncthreads();
     if (i < a.rows) {
       int n = 0;
@@ -162,11 +215,11 @@ struct TileFinder {
     const unsigned firsts = __ballot_sync(0xffffffffu, first);
     __syncthreads();
     // the warps' counts, in the place of the indices that nobody reads any more
-    if ((i & 31) == 0) sm.adapter_of[i >> 5] = __popc(firsts);
+    if (i < kADOwnPlan && (i & 31) == 0) sm.adapter_of[i >> 5] = __popc(firsts);
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < kADWarps; ++w) {
+    for (int w = 0; w < kADOwnPlan / 32; ++w) {
       const int c = sm.adapter_of[w];
       before += w < (i >> 5) ? c : 0;
       all += c;
@@ -233,11 +286,11 @@ __device__ __forceinline__ void down_share(const AdapterArgs& a, const T* down, 
     if (kb < hi && h < a.H) {
 #pragma unroll
       for (int rt = 0; rt < 2 * RT; ++rt)
-        if (rt * 8 + g < rank) lane_copy<16>(e + rt * 32, down + (rt * 8 + g) * a.down_row + h);
+        if (rt * 8 + g < rank) lane_copy<16>(smem_u32(e + rt * 32), down + (rt * 8 + g) * a.down_row + h);
       if (a.x_vec)
 #pragma unroll
         for (int c = 0; c < C; ++c)
-          if (have[c]) lane_copy<16>(e + (2 * RT + c) * 32, xp[c] + kb * 32);
+          if (have[c]) lane_copy<16>(smem_u32(e + (2 * RT + c) * 32), xp[c] + kb * 32);
     }
     lane_copies_end();
   };
@@ -347,69 +400,94 @@ __global__ void __launch_bounds__(kADThreads) adapter_down_kernel(const AdapterA
 // ---------------------------------------------------------------------------
 // second product, added to y
 // ---------------------------------------------------------------------------
-// Four outputs of one row, as a lane holds them.  VEC: four neighbours, read and written at once; else outputs
-// n, n + 8, n + 16 and n + 24, neighbouring lanes holding neighbours.
+// The four outputs of one row that a lane holds of a step of 32: output(g, e), e = 0..3.  VEC: neighbours, read and
+// written at once (16 bytes, or 8 of 16-bit outputs); else every eighth, neighbouring lanes holding neighbours.
+// FULL: all of them are the row's; else those below `left` (counted from the lane's first).
 template <typename Y, bool VEC>
 struct Outputs {
   static constexpr int ES = static_cast<int>(sizeof(Y));
   static constexpr bool kRing = VEC || ES == 4;  // (copies are of four bytes at least)
-  // into the ring's place (16 bytes of ES 4, 8 of ES 2, a lane): out of the row's `left` outputs from n on
-  __device__ __forceinline__ static void copy(unsigned char* to, const char* row, int left) {
+  static constexpr int BYTES = 4 * ES;           // of a lane and row
+  __device__ __forceinline__ static int output(int g, int e) { return VEC ? 4 * g + e : g + 8 * e; }
+  // A lane's place for its share of a row of its own: those of a row are neighbours, as in memory (whole sectors), and
+  // the four rows of a copy do not meet in a bank when a quarter of a warp reads.
+  __device__ __forceinline__ static int place(int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    return t * (8 * BYTES) + (((g >> 1) ^ t) * 2 + (g & 1)) * BYTES;
+  }
+  template <bool FULL>
+  __device__ __forceinline__ static void copy(uint32_t to, const char* row, bool have, int left) {
     if constexpr (VEC) {
-      lane_copy<4 * ES>(to, row);
+      lane_copy_if<4 * ES>(have && (FULL || left > 0), to, row);
     } else if constexpr (ES == 4) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (8 * q < left) lane_copy<4>(to + 4 * q, row + 32 * q);
+      for (int e = 0; e < 4; ++e) lane_copy_if<4>(have && (FULL || 8 * e < left), to + e * 4, row + 32 * e);
     }
   }
-  __device__ __forceinline__ static void add_and_store(const unsigned char* in, const char* y_row, char* row, int left,
-                                                       const float (&d)[4]) {
-    if constexpr (VEC && ES == 4) {
+  // d[e] times `by` is added to output e.
+  template <bool FULL>
+  __device__ __forceinline__ static void add_and_store(const unsigned char* in, const char* y_row, char* row, bool have,
+                                                       int left, const float (&d)[4], float by) {
+    if constexpr (ES == 4) {
       const float4 v = *reinterpret_cast<const float4*>(in);
-      *reinterpret_cast<float4*>(row) = make_float4(v.x + d[0], v.y + d[1], v.z + d[2], v.w + d[3]);
-    } else if constexpr (VEC) {
-      using C = Half16<Y>;
-      const uint2 v = *reinterpret_cast<const uint2*>(in);
-      uint2 w;
-      w.x = C::bits(C::value(v.x & 0xFFFFu) + d[0]) | static_cast<uint32_t>(C::bits(C::value(v.x >> 16) + d[1])) << 16;
-      w.y = C::bits(C::value(v.y & 0xFFFFu) + d[2]) | static_cast<uint32_t>(C::bits(C::value(v.y >> 16) + d[3])) << 16;
-      *reinterpret_cast<uint2*>(row) = w;
-    } else if constexpr (ES == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(in);
-      const float f[4] = {v.x, v.y, v.z, v.w};
+      const float4 r = make_float4(fmaf(d[0], by, v.x), fmaf(d[1], by, v.y), fmaf(d[2], by, v.z), fmaf(d[3], by, v.w));
+      if constexpr (VEC) {
+        if (have && (FULL || left > 0)) *reinterpret_cast<float4*>(row) = r;
+      } else {
+        const float f[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (8 * q < left) reinterpret_cast<float*>(row)[8 * q] = f[q] + d[q];
+        for (int e = 0; e < 4; ++e)
+          if (have && (FULL || 8 * e < left)) reinterpret_cast<float*>(row)[8 * e] = f[e];
+      }
     } else {
       using C = Half16<Y>;
-      uint16_t v[4] = {};
+      if constexpr (VEC) {
+        const uint2 v = *reinterpret_cast<const uint2*>(in);
+        const float2 a = C::pair(v.x), b = C::pair(v.y);
+        const uint2 w = make_uint2(C::pack(fmaf(d[0], by, a.x), fmaf(d[1], by, a.y)),
+                                   C::pack(fmaf(d[2], by, b.x), fmaf(d[3], by, b.y)));
+        if (have && (FULL || left > 0)) *reinterpret_cast<uint2*>(row) = w;
+      } else {
+        uint16_t v[4] = {};
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (8 * q < left) v[q] = reinterpret_cast<const uint16_t*>(y_row)[8 * q];
+        for (int e = 0; e < 4; ++e)
+          if (have && (FULL || 8 * e < left)) v[e] = reinterpret_cast<const uint16_t*>(y_row)[8 * e];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (8 * q < left) reinterpret_cast<uint16_t*>(row)[8 * q] = C::bits(C::value(v[q]) + d[q]);
+        for (int e = 0; e < 4; ++e)
+          if (have && (FULL || 8 * e < left)) reinterpret_cast<uint16_t*>(row)[8 * e] = C::bits(fmaf(d[e], by, C::value(v[e])));
+      }
     }
   }
 };
 
-// d in MMA order: the high parts (b0, b1) and the low parts (b0, b1) of a lane
-template <int KS>
+// d in MMA order, a lane's registers of a step: the 16-bit values (b0, b1), and with LO behind them what their
+// rounding left (b0, b1).
+template <bool LO>
+struct Operand;
+template <>
+struct Operand<true> {
+  using Regs = uint4;
+};
+template <>
+struct Operand<false> {
+  using Regs = uint2;
+};
+
+template <int KS, bool LO>
 struct UpSmem {
-  uint4 frag[KS][kADCols][32];
+  typename Operand<LO>::Regs frag[KS][kADCols][32];
   float unscale[kADTile];  // f16: the power of two that a row's d was divided by
   int64_t y[kADTile], out[kADTile];  // the rows' first bytes
 };
 
 // All threads: a tile's d, scaled, into sm.
-template <typename T, int KS>
-__device__ void up_operand(const AdapterArgs& a, const TileSmem& ts, UpSmem<KS>& sm, int rank) {
+template <typename T, int KS, bool LO>
+__device__ void up_operand(const AdapterArgs& a, const TileSmem& ts, UpSmem<KS, LO>& sm, int rank) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int count = ts.count, cols = (count + 7) / 8;
   const float scale = ts.adapter < 0 ? 0.0f : a.scales ? a.scales[ts.adapter] : 1.0f;
   constexpr int PER = (KS * 16 + 31) / 32;  // entries a lane; a warp takes a row at a time
-  for (int i = warp; i < cols * 8; i += kADWarps) {
+  for (int i = warp; i < cols * 8; i += blockDim.x / 32) {
     float v[PER];
     float most = 0.0f;
 #pragma unroll
@@ -423,217 +501,282 @@ __device__ void up_operand(const AdapterArgs& a, const TileSmem& ts, UpSmem<KS>&
       }
       most = fmaxf(most, fabsf(v[u]));
     }
-    float by = 1.0f, back = 1.0f;
+    float by = 1.0f;
     if constexpr (std::is_same<T, __half>::value) {
       // f16: the row's largest value goes into [2^13, 2^14), which is exact
+      float back = 1.0f;
       most = warp_max(most);
       if (most > 0.0f && most < INFINITY) {
         const int e = min(max(ilogbf(most), -112), 127);
         by = ldexpf(1.0f, 13 - e);
         back = ldexpf(1.0f, e - 13);
       }
+      if (lane == 0) sm.unscale[i] = back;
     }
-    if (lane == 0) sm.unscale[i] = back;
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
       const int r = u * 32 + lane;
       if (r >= KS * 16) break;
       const float f = v[u] * by;
       const uint16_t high = Half16<T>::bits(f);
-      const float hv = Half16<T>::value(high);
-      const uint16_t low = Half16<T>::bits(fabsf(hv) < INFINITY ? f - hv : 0.0f);
-      // where entry r stands: step, lane's t, register
-      int ks, tt, reg;
-      if (KS == 1) {
-        ks = 0, tt = r >> 2, reg = (r >> 1) & 1;
-      } else {
-        const int e = r & 31;
-        ks = (r >> 5) * 2 + ((e >> 2) & 1), tt = e >> 3, reg = (e >> 1) & 1;
-      }
-      uint16_t* p = reinterpret_cast<uint16_t*>(&sm.frag[ks][i >> 3][(i & 7) * 4 + tt]);
+      const int reg = (r >> 3) & 1;  // of the step r / 16, in the lane of r's pair
+      uint16_t* p = reinterpret_cast<uint16_t*>(&sm.frag[r >> 4][i >> 3][(i & 7) * 4 + ((r & 7) >> 1)]);
       p[reg * 2 + (r & 1)] = high;
-      p[4 + reg * 2 + (r & 1)] = low;
+      if constexpr (LO) {
+        const float hv = Half16<T>::value(high);
+        p[4 + reg * 2 + (r & 1)] = Half16<T>::bits(fabsf(hv) < INFINITY ? f - hv : 0.0f);
+      }
     }
   }
 }
 
-// 16-bit entries from `n` on made 0 (entries past an adapter's rank may hold anything)
-__device__ __forceinline__ void first_entries(uint2& w, int n) {
-  w.x &= n >= 2 ? ~0u : n == 1 ? 0xFFFFu : 0u;
-  w.y &= n >= 4 ? ~0u : n == 3 ? 0xFFFFu : 0u;
-}
-__device__ __forceinline__ void first_entries(uint4& w, int n) {
-  uint2 a = make_uint2(w.x, w.y), b = make_uint2(w.z, w.w);
-  first_entries(a, n);
-  first_entries(b, n - 4);
-  w = make_uint4(a.x, a.y, b.x, b.y);
-}
-
-// A warp's weights of 32 outputs: four rows of up a lane (q), as two MMAs' operands (q = 0, 1 and 2, 3).
-// KS 1: ranks to 16, a lane takes 8 bytes of a weight row; else 16 bytes of every 32 entries.
-template <typename T, int KS>
-struct UpWeights {
-  static constexpr int KB = KS == 1 ? 1 : KS / 2;
-  static constexpr int E = KS == 1 ? 4 : 8;  // entries of a weight row that a lane takes of a block
-  using Word = typename std::conditional<KS == 1, uint2, uint4>::type;
-  Word w[KB][4];
-
-  // The lane's words of rows `row`, row + step, ... (those below N) into the ring's place.
-  __device__ __forceinline__ static void copy(unsigned char* to, const T* up, int64_t up_row, int row, int step, int N,
-                                              int rank, int lane) {
-    const int t = lane & 3;
-    Word* e = reinterpret_cast<Word*>(to) + lane;
-    const T* p = up + row * up_row + t * E;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (row + q * step < N) {
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-          if (kb * 32 + t * E < rank) lane_copy<static_cast<int>(sizeof(Word))>(e + (kb * 4 + q) * 32, p + kb * 32);
-      }
-      p += step * up_row;
-    }
-  }
-  // Entries behind the rank become 0; rows behind N hold whatever they do: their results are not kept.
-  __device__ __forceinline__ void read(const unsigned char* from, int rank, int lane) {
-    const Word* e = reinterpret_cast<const Word*>(from) + lane;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      const int left = rank - kb * 32 - (lane & 3) * E;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        w[kb][q] = e[(kb * 4 + q) * 32];
-        if (left < E) first_entries(w[kb][q], left);
-      }
-    }
-  }
-  // acc[j] += rows (2j, 2j + 1) times column tile c of d
-  __device__ __forceinline__ void multiply(const UpSmem<KS>& sm, int c, int lane, float (&acc)[2][4]) const {
-    if constexpr (KS == 1) {
-      const uint4 b = sm.frag[0][c][lane];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t f[4] = {w[0][2 * j].x, w[0][2 * j + 1].x, w[0][2 * j].y, w[0][2 * j + 1].y};
-        mma16<T>(acc[j], f, b.x, b.y);
-        mma16<T>(acc[j], f, b.z, b.w);
-      }
-    } else {
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        const uint4 b0 = sm.frag[2 * kb][c][lane], b1 = sm.frag[2 * kb + 1][c][lane];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4 u = w[kb][2 * j], v = w[kb][2 * j + 1];
-          const uint32_t f0[4] = {u.x, v.x, u.y, v.y}, f1[4] = {u.z, v.z, u.w, v.w};
-          mma16<T>(acc[j], f0, b0.x, b0.y);
-          mma16<T>(acc[j], f0, b0.z, b0.w);
-          mma16<T>(acc[j], f1, b1.x, b1.y);
-          mma16<T>(acc[j], f1, b1.z, b1.w);
-        }
-      }
-    }
+// A warp's weights of a step: two MMAs' A operands, of 16 outputs each.  They come in 16-byte pieces of a row, CH to a
+// row, neighbouring lanes copying neighbouring pieces.  The two pieces of a 32-byte sector stay together: copies of
+// one sector to two places are two reads from L2 (measured: 2x the sectors, 110 us in place of 92 for 64 rows of 48
+// adapters of rank 32).  A row stands at 32 KS times its number, its sectors' places within 128 bytes exclusive-ored
+// with two bits of the number, so that a matrix's eight rows (ldmatrix) meet in no more than two of a bank.
+template <bool VEC, int KS>
+struct UpPlaces {
+  static constexpr int CH = 2 * KS;      // pieces of a row
+  static constexpr int ROWS = 32 / CH;   // rows that the lanes copy at a time
+  static constexpr int COPIES = kADStep / ROWS;
+  __device__ __forceinline__ static int at(int row, int c) {
+    const int x = VEC ? row >> 2 : KS == 1 ? 0 : KS == 2 ? (row >> 1) & 1 : row;
+    return (row * (32 * KS) + c * 16) ^ ((x & 3) << 5);
   }
 };
 
-// A warp's ring: entries of the weights of 32 outputs and of y for C tiles of 8 rows.
+// A warp's ring: entries of the weights of a step and of y for C tiles of 8 rows.  A CTA has an SM for itself, with as
+// many warps as its registers allow without spilling, each with a ring of at least two of the larger entries.
+constexpr int kADUpCols = 2;                                                         // C of tiles of more than 8 rows
 constexpr int up_entry(int ks, int es, int c) { return ks * 1024 + c * es * 256; }
-constexpr int up_warp_bytes(int ks, int es) {
-  const int two = 2 * up_entry(ks, es, 4), most = 13 * 1024;  // two entries of the larger kind at least
-  return two > most ? two : most;
-}
+constexpr int kADUpStatic = 2900;  // (what else a CTA holds beside d)
+constexpr int up_ring_bytes(int ks, int es) { return 227 * 1024 - ks * kADCols * 32 * 4 * es - kADUpStatic; }
+constexpr int up_warps(int ks) { return ks <= 4 ? 16 : 8; }
+constexpr int up_warp_bytes(int ks, int es) { return up_ring_bytes(ks, es) / up_warps(ks) / 512 * 512; }
 constexpr int up_depth(int ks, int es, int c) {
   const int n = up_warp_bytes(ks, es) / up_entry(ks, es, c);
   return n < 8 ? n : 8;
 }
-constexpr int up_ctas(int ks, int es) { return up_warp_bytes(ks, es) <= 13 * 1024 ? 2 : 1; }  // per SM
 
-// A warp's part of a tile's outputs [n_begin, n_end): every kADWarps-th step of 32 from its first on.  C: column
-// tiles of an entry; a tile of more rows has `halves` entries a step, of which the first brings the weights.
+// A warp's part of a tile's outputs [.., n_end): every step that is the warp's.  C: column tiles of an entry; a tile of
+// more rows has several entries a step, of which the first brings the weights.
 // start(): the copies that fill the ring; run(): the rest, once d stands in sm.
 template <typename T, typename Y, int KS, bool VEC, int C>
 struct UpShare {
-  static constexpr int ES = static_cast<int>(sizeof(Y)), D = up_depth(KS, ES, C), ENTRY = up_entry(KS, ES, C);
+  static constexpr bool LO = sizeof(Y) == 4;
+  static constexpr int ES = static_cast<int>(sizeof(Y)), J = 2, STEP = kADStep;
+  using O = Outputs<Y, VEC>;
+  using P = UpPlaces<VEC, KS>;
+  static constexpr int D = up_depth(KS, ES, C), ENTRY = up_entry(KS, ES, C);
+  static constexpr int STRIDE = up_warps(KS) * STEP;  // outputs from a step to the warp's next
+  static constexpr int W_BYTES = J * KS * 512, ROW_BYTES = 32 * O::BYTES;
+  static_assert(D >= 2, "a ring of two entries at least");
   const AdapterArgs& a;
-  const UpSmem<KS>& sm;
-  const T* up;
-  unsigned char* ring;
-  int rank, count, n_first, n_end, halves;
+  const UpSmem<KS, LO>& sm;
+  int rank, count, n_end, t, parts;  // parts: entries a step
+  unsigned char* ring_y;       // the lane's place for y in the first entry
+  uint32_t ring;               // the first entry
+  bool in_rank;                // the lane's pieces of the weight rows are
+  // the next entry to be copied
+  const char* wp;              // the lane's first piece
+  int64_t pitch, step;         // bytes from a piece to the lane's next, and to the warp's next step's
+  const char* yp0;             // C 1: the lane's two rows of y, and of out, at its first output
+  const char* yp1;
+  char* op0;
+  char* op1;
+  int in_n0, in_part, in_at;   // the step's first output, the entry's number in it, its offset in the ring
+  int lane_n;                  // the lane's first output, from the step's
 
-  __device__ __forceinline__ int output(int step) const {  // the lane's first output of a step
-    const int g = (threadIdx.x & 31) >> 2;
-    return n_first + step * (kADWarps * kADStep) + (VEC ? 4 * g : g);
+  __device__ __forceinline__ UpShare(const AdapterArgs& args, const UpSmem<KS, LO>& s, const T* up,
+                                     unsigned char* warp_ring, int rank_, int count_, int n_first, int n_end_)
+      : a(args), sm(s), rank(rank_), count(count_), n_end(n_end_) {
+    const int lane = threadIdx.x & 31;
+    t = lane & 3;
+    parts = C == 1 ? 1 : (count + 8 * C - 1) / (8 * C);
+    ring = smem_u32(warp_ring);
+    ring_y = warp_ring + W_BYTES + O::place(lane);
+    in_n0 = n_first;
+    lane_n = O::output(lane >> 2, 0);
+    in_at = in_part = 0;
+    in_rank = (lane % P::CH) * 8 < rank;
+    wp = reinterpret_cast<const char*>(up + (n_first + lane / P::CH) * a.up_row + (lane % P::CH) * 8);
+    pitch = 2 * P::ROWS * a.up_row;
+    step = 2 * STRIDE * a.up_row;
+    if constexpr (C == 1) {
+      const int64_t off = static_cast<int64_t>(n_first + lane_n) * ES;
+      const int i0 = min(2 * t, count - 1), i1 = min(2 * t + 1, count - 1);
+      yp0 = a.y + sm.y[i0] + off, yp1 = a.y + sm.y[i1] + off;
+      op0 = a.out + sm.out[i0] + off, op1 = a.out + sm.out[i1] + off;
+    }
   }
-  __device__ __forceinline__ void issue(int j) const {
-    const int lane = threadIdx.x & 31, t = lane & 3;
-    const int step = halves == 1 ? j : j >> 1, half = halves == 1 ? 0 : j & 1;
-    const int n = output(step);
-    unsigned char* e = ring + (j % D) * ENTRY;
-    if (n_first + step * (kADWarps * kADStep) < n_end) {
-      if (half == 0) UpWeights<T, KS>::copy(e, up, a.up_row, n, VEC ? 1 : 8, a.N, rank, lane);
-      if (Outputs<Y, VEC>::kRing && n < n_end) {
+  template <bool FULL>
+  __device__ __forceinline__ void copy_entry() {
+    const int lane = threadIdx.x & 31;
+    if ((C == 1 || in_part == 0) && rank > 0) {
+      const char* p = wp;
 #pragma unroll
-        for (int c = 0; c < 2 * C; ++c) {
-          const int i = half * 32 + (c >> 1) * 8 + 2 * t + (c & 1);
-          if (i < count)
-            Outputs<Y, VEC>::copy(e + KS * 1024 + (c * 32 + lane) * (4 * ES), a.y + sm.y[i] + static_cast<int64_t>(n) * ES, n_end - n);
-        }
+      for (int i = 0; i < P::COPIES; ++i) {
+        const int row = lane / P::CH + i * P::ROWS;
+        const uint32_t to = ring + in_at + P::at(row, lane % P::CH);
+        lane_copy_if<16>(in_rank && (FULL || in_n0 + row < n_end), to, p);
+        p += pitch;
       }
+    }
+    if constexpr (O::kRing) {
+      const int left = n_end - in_n0 - lane_n;
+      const uint32_t to = smem_u32(ring_y) + in_at;
+      if constexpr (C == 1) {
+        O::template copy<FULL>(to, yp0, 2 * t < count, left);
+        O::template copy<FULL>(to + ROW_BYTES, yp1, 2 * t + 1 < count, left);
+      } else {
+        const char* y = a.y + static_cast<int64_t>(in_n0 + lane_n) * ES;
+        const int row = in_part * (8 * C) + 2 * t;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)  // (rows behind the last have offsets of it)
+            O::template copy<FULL>(to + (2 * c + u) * ROW_BYTES, y + sm.y[row + c * 8 + u], row + c * 8 + u < count, left);
+      }
+    }
+  }
+  __device__ __forceinline__ void issue() {
+    if (in_n0 < n_end) {
+      if (in_n0 + STEP <= n_end) copy_entry<true>();
+      else copy_entry<false>();
+      if (C == 1 || ++in_part == parts) {
+        in_part = 0;
+        in_n0 += STRIDE;
+        wp += step;
+        if constexpr (C == 1 && O::kRing) yp0 += STRIDE * ES, yp1 += STRIDE * ES;
+      }
+      in_at = in_at == (D - 1) * ENTRY ? 0 : in_at + ENTRY;
     }
     lane_copies_end();
   }
-  __device__ __forceinline__ void start() const {
+  __device__ __forceinline__ void start() {
 #pragma unroll 1
-    for (int j = 0; j < D - 1; ++j) issue(j);
+    for (int j = 0; j < D - 1; ++j) issue();
   }
-  __device__ __forceinline__ void run() const {
-    const int lane = threadIdx.x & 31, t = lane & 3;
-    UpWeights<T, KS> w;
-#pragma unroll 1
-    for (int j = 0;; ++j) {
-      const int step = halves == 1 ? j : j >> 1, half = halves == 1 ? 0 : j & 1;
-      if (n_first + step * (kADWarps * kADStep) >= n_end) break;
-      issue(j + D - 1);
-      lane_copies_wait<D - 1>();
-      const unsigned char* e = ring + (j % D) * ENTRY;
-      const int n = output(step);
-      if (half == 0) w.read(e, rank, lane);
+  // The weights of the entry, as far as the rank goes.
+  __device__ __forceinline__ void read_weights(uint32_t entry, uint32_t (&w)[KS][J][4]) const {
+    const int lane = threadIdx.x & 31;
+    // a rank that ends inside a step's 16 entries: the words of its two pieces that count
+    const int rest = rank % 16 - 2 * t;
+    const uint32_t keep0 = rank % 16 == 0 || rest >= 2 ? ~0u : rest == 1 ? 0xFFFFu : 0u;
+    const uint32_t keep1 = rank % 16 == 0 || rest >= 10 ? ~0u : rest == 9 ? 0xFFFFu : 0u;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      if (ks * 16 >= rank) break;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        // matrices of the tile: a lane group's outputs 2 j and 2 j + 1 (e) in piece 2 ks, the same in piece 2 ks + 1
+        const int e = 2 * j + ((lane >> 3) & 1);
+        load_matrices(w[ks][j], entry + P::at(O::output(lane & 7, e), 2 * ks + (lane >> 4)));
+      }
+      if (ks * 16 + 16 > rank) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) w[ks][j][0] &= keep0, w[ks][j][1] &= keep0, w[ks][j][2] &= keep1, w[ks][j][3] &= keep1;
+      }
+    }
+  }
+  // acc[c][j] = the step's outputs 16 j .. times column tile c of the entry's part of d.
+  __device__ __forceinline__ void multiply(const uint32_t (&w)[KS][J][4], int part,
+                                           const typename Operand<LO>::Regs (&kept)[KS], float (&acc)[C][J][4]) const {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      if (ks * 16 >= rank) break;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int c0 = half * 4 + c;
-        if (c0 * 8 >= count) break;
-        float acc[2][4] = {};
-        w.multiply(sm, c0, lane, acc);
+        const auto b = C == 1 ? kept[ks] : sm.frag[ks][part * C + c][threadIdx.x & 31];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int i = c0 * 8 + 2 * t + u;
-          if (i >= count || n >= n_end) continue;
-          const float back = sm.unscale[i];
-          const float dv[4] = {acc[0][u] * back, acc[0][2 + u] * back, acc[1][u] * back, acc[1][2 + u] * back};
-          Outputs<Y, VEC>::add_and_store(e + KS * 1024 + ((2 * c + u) * 32 + lane) * (4 * ES),
-                                         a.y + sm.y[i] + static_cast<int64_t>(n) * ES,
-                                         a.out + sm.out[i] + static_cast<int64_t>(n) * ES, n_end - n, dv);
+        for (int j = 0; j < J; ++j) {
+          if (ks == 0) mma16_first<T>(acc[c][j], w[ks][j], b.x, b.y);
+          else mma16<T>(acc[c][j], w[ks][j], b.x, b.y);
+        }
+        if constexpr (LO) {
+#pragma unroll
+          for (int j = 0; j < J; ++j) mma16<T>(acc[c][j], w[ks][j], b.z, b.w);
         }
       }
     }
+  }
+  // A column tile's results: rows i and i + 1 of the tile.
+  template <bool FULL>
+  __device__ __forceinline__ void finish(const float (&acc)[J][4], int i, const unsigned char* in, int n) {
+    const int64_t off = static_cast<int64_t>(n) * ES;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float dv[2 * J];
+#pragma unroll
+      for (int e = 0; e < 2 * J; ++e) dv[e] = acc[e >> 1][(e & 1) * 2 + u];
+      const float back = std::is_same<T, __half>::value ? sm.unscale[i + u] : 1.0f;
+      const char* y = C == 1 ? (u ? yp1 : yp0) : a.y + off + sm.y[i + u];
+      char* out = C == 1 ? (u ? op1 : op0) : a.out + off + sm.out[i + u];
+      O::template add_and_store<FULL>(in + u * ROW_BYTES, y, out, i + u < count, n_end - n, dv, back);
+    }
+  }
+  __device__ __forceinline__ void run(int n0) {
+    const int lane = threadIdx.x & 31;
+    int at = 0, part = 0;
+    typename Operand<LO>::Regs kept[KS];
+    if constexpr (C == 1) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) kept[ks] = sm.frag[ks][0][lane];
+    }
+    uint32_t w[KS][J][4];
+    while (n0 < n_end) {
+      __syncwarp();  // the entry that is copied over has been read by all lanes
+      issue();
+      lane_copies_wait<D - 1>();
+      __syncwarp();  // the weights are read by other lanes than copied them
+      if (C == 1 || part == 0) read_weights(ring + at, w);
+      float acc[C][J][4];
+      multiply(w, part, kept, acc);
+      if (rank == 0) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[c][j][e] = 0.0f;
+      }
+      const bool full = n0 + STEP <= n_end;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const unsigned char* in = ring_y + at + 2 * c * ROW_BYTES;
+        const int i = (part * C + c) * 8 + 2 * t;
+        if (full) finish<true>(acc[c], i, in, n0 + lane_n);
+        else finish<false>(acc[c], i, in, n0 + lane_n);
+      }
+      if (C == 1 || ++part == parts) {
+        part = 0;
+        n0 += STRIDE;
+        if constexpr (C == 1) {
+          op0 += STRIDE * ES, op1 += STRIDE * ES;
+          if constexpr (!O::kRing) yp0 += STRIDE * ES, yp1 += STRIDE * ES;
+        }
+      }
+      at = at == (D - 1) * ENTRY ? 0 : at + ENTRY;
+    }
     lane_copies_wait<0>();
+    __syncwarp();
   }
 };
 
-// A warp takes 32 outputs at a time as two MMAs of 16 weight rows.  VEC: rows n0 + 4g and n0 + 4g + 1 are row g
-// and g + 8 of the first, n0 + 4g + 2 and + 3 of the second, so that a lane's results for a batch row are four
-// neighbours.  Else n0 + g + 8q: neighbouring lanes hold neighbours.
-// The work is (tile, step of 32 outputs); every CTA takes a contiguous share, so that it seldom changes tiles.
+// The work is (tile, step of outputs); every CTA takes a contiguous share, so that it seldom changes tiles.
 template <typename T, typename Y, int KS, bool VEC>
-__global__ void __launch_bounds__(kADThreads, up_ctas(KS, sizeof(Y))) adapter_up_kernel(const AdapterArgs a) {
-  extern __shared__ __align__(16) unsigned char up_ring[];
-  __shared__ UpSmem<KS> sm;
+__global__ void __launch_bounds__(32 * up_warps(KS), 1) adapter_up_kernel(const AdapterArgs a) {
+  extern __shared__ __align__(128) unsigned char up_ring[];
+  __shared__ UpSmem<KS, sizeof(Y) == 4> sm;
   __shared__ TileSmem ts;
+  constexpr int STEP = kADStep;
   const int tid = threadIdx.x, warp = tid >> 5;
   // the kernel before this one is the first product, which has itself waited for all before it: only d has to
   // wait for its end, and what the plan kernel wrote has been waited for
   TileFinder finder;
   const int n_tiles = finder.start(a, ts);
-  const int64_t steps = (a.N + kADStep - 1) / kADStep;
+  const int64_t steps = (a.N + STEP - 1) / STEP;
   const int64_t all = steps * n_tiles;
   int64_t at = all * blockIdx.x / gridDim.x;
   const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
@@ -644,24 +787,25 @@ __global__ void __launch_bounds__(kADThreads, up_ctas(KS, sizeof(Y))) adapter_up
     at += s1 - s0;
     finder.take(a, ts, ti);
     const int count = ts.count, rank = adapter_rank(a, ts.adapter);
-    if (tid < count) {
-      sm.y[tid] = ts.rows[tid] * a.y_stride * static_cast<int64_t>(sizeof(Y));
-      sm.out[tid] = ts.rows[tid] * a.out_stride * static_cast<int64_t>(sizeof(Y));
+    if (tid < kADTile) {
+      const int row = ts.rows[min(tid, count - 1)];
+      sm.y[tid] = row * a.y_stride * static_cast<int64_t>(sizeof(Y));
+      sm.out[tid] = row * a.out_stride * static_cast<int64_t>(sizeof(Y));
     }
     __syncthreads();
     const T* up = reinterpret_cast<const T*>(a.up) + static_cast<int64_t>(max(ts.adapter, 0)) * a.up_adapter;
     unsigned char* ring = up_ring + warp * up_warp_bytes(KS, sizeof(Y));
-    const int n_first = (s0 + warp) * kADStep, n_end = min(a.N, s1 * kADStep);
-    auto share = [&](const auto& part) {
+    const int n_first = (s0 + warp) * STEP, n_end = min(a.N, s1 * STEP);
+    auto share = [&](auto&& part) {
       part.start();
       if (!waited) pdl_wait();
       waited = true;
-      up_operand<T, KS>(a, ts, sm, rank);
+      up_operand<T, KS, sizeof(Y) == 4>(a, ts, sm, rank);
       __syncthreads();
-      part.run();
+      part.run(n_first);
     };
-    if (count <= 8) share(UpShare<T, Y, KS, VEC, 1>{a, sm, up, ring, rank, count, n_first, n_end, 1});
-    else share(UpShare<T, Y, KS, VEC, 4>{a, sm, up, ring, rank, count, n_first, n_end, count <= 32 ? 1 : 2});
+    if (count <= 8) share(UpShare<T, Y, KS, VEC, 1>(a, sm, up, ring, rank, count, n_first, n_end));
+    else share(UpShare<T, Y, KS, VEC, kADUpCols>(a, sm, up, ring, rank, count, n_first, n_end));
   }
   // a CTA without work waits too: this grid is not to end before the one that makes d
   if (!waited) pdl_wait();
@@ -679,7 +823,7 @@ cudaError_t down_setup() {
 template <typename T, typename Y, int KS, bool VEC>
 cudaError_t up_setup() {
   return cudaFuncSetAttribute(adapter_up_kernel<T, Y, KS, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kADWarps * up_warp_bytes(KS, sizeof(Y)));
+                              up_warps(KS) * up_warp_bytes(KS, sizeof(Y)));
 }
 
 template <typename T, typename Y, bool VEC>
@@ -714,30 +858,31 @@ cudaError_t launch_down(const AdapterArgs& a, int grid, cudaStream_t stream) {
 }
 
 template <typename T, typename Y, int KS, bool VEC>
-cudaError_t launch_up_ks(const AdapterArgs& a, int64_t max_steps, int num_sms, cudaStream_t stream) {
-  const int64_t most = static_cast<int64_t>(num_sms) * up_ctas(KS, sizeof(Y));  // one wave
-  const int64_t few = (max_steps + kADWarps - 1) / kADWarps;
+cudaError_t launch_up_ks(const AdapterArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
+  constexpr int STEP = kADStep;
+  const int64_t max_steps = max_tiles * ((a.N + STEP - 1) / STEP);
+  const int64_t most = num_sms;  // one wave
+  const int64_t few = (max_steps + up_warps(KS) - 1) / up_warps(KS);
   return launch_kernel(adapter_up_kernel<T, Y, KS, VEC>, dim3(static_cast<unsigned>(few < most ? few : most)),
-                       dim3(kADThreads), static_cast<size_t>(kADWarps * up_warp_bytes(KS, sizeof(Y))), stream, true, a);
+                       dim3(32 * up_warps(KS)), static_cast<size_t>(up_warps(KS) * up_warp_bytes(KS, sizeof(Y))), stream, true, a);
 }
 
 template <typename T, typename Y, bool VEC>
-cudaError_t launch_up_of(const AdapterArgs& a, int64_t max_steps, int num_sms, cudaStream_t stream) {
-  if (a.R <= 16) return launch_up_ks<T, Y, 1, VEC>(a, max_steps, num_sms, stream);
-  if (a.R <= 32) return launch_up_ks<T, Y, 2, VEC>(a, max_steps, num_sms, stream);
-  if (a.R <= 64) return launch_up_ks<T, Y, 4, VEC>(a, max_steps, num_sms, stream);
-  return launch_up_ks<T, Y, 8, VEC>(a, max_steps, num_sms, stream);
+cudaError_t launch_up_of(const AdapterArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
+  if (a.R <= 16) return launch_up_ks<T, Y, 1, VEC>(a, max_tiles, num_sms, stream);
+  if (a.R <= 32) return launch_up_ks<T, Y, 2, VEC>(a, max_tiles, num_sms, stream);
+  if (a.R <= 64) return launch_up_ks<T, Y, 4, VEC>(a, max_tiles, num_sms, stream);
+  return launch_up_ks<T, Y, 8, VEC>(a, max_tiles, num_sms, stream);
 }
 
-// max_steps: (tiles) x (steps of 32 outputs), at most
 template <typename T>
-cudaError_t launch_up(const AdapterArgs& a, lmh_dtype out_dtype, bool vec, int64_t max_steps, int num_sms,
+cudaError_t launch_up(const AdapterArgs& a, lmh_dtype out_dtype, bool vec, int64_t max_tiles, int num_sms,
                       cudaStream_t stream) {
   if (out_dtype == LMH_F32)
-    return vec ? launch_up_of<T, float, true>(a, max_steps, num_sms, stream)
-               : launch_up_of<T, float, false>(a, max_steps, num_sms, stream);
-  return vec ? launch_up_of<T, T, true>(a, max_steps, num_sms, stream)
-             : launch_up_of<T, T, false>(a, max_steps, num_sms, stream);
+    return vec ? launch_up_of<T, float, true>(a, max_tiles, num_sms, stream)
+               : launch_up_of<T, float, false>(a, max_tiles, num_sms, stream);
+  return vec ? launch_up_of<T, T, true>(a, max_tiles, num_sms, stream)
+             : launch_up_of<T, T, false>(a, max_tiles, num_sms, stream);
 }
 
 // The two types' kernels (adapters_bf16.cu, adapters_f16.cu).
@@ -745,9 +890,9 @@ cudaError_t adapters_setup_bf16();
 cudaError_t adapters_setup_f16();
 cudaError_t launch_down_bf16(const AdapterArgs& a, int grid, cudaStream_t stream);
 cudaError_t launch_down_f16(const AdapterArgs& a, int grid, cudaStream_t stream);
-cudaError_t launch_up_bf16(const AdapterArgs& a, lmh_dtype out_dtype, bool vec, int64_t max_steps, int num_sms,
+cudaError_t launch_up_bf16(const AdapterArgs& a, lmh_dtype out_dtype, bool vec, int64_t max_tiles, int num_sms,
                            cudaStream_t stream);
-cudaError_t launch_up_f16(const AdapterArgs& a, lmh_dtype out_dtype, bool vec, int64_t max_steps, int num_sms,
+cudaError_t launch_up_f16(const AdapterArgs& a, lmh_dtype out_dtype, bool vec, int64_t max_tiles, int num_sms,
                           cudaStream_t stream);
 
 }  // namespace lmh
