@@ -220,7 +220,10 @@ def test_strides_alignment_and_streams(lmh):
         st.wait_stream(torch.cuda.current_stream())
         got = lmh.beam_select(wide[:, at:at + 4099], s, 4, k=8, stream=st)
         st.synchronize()
-        assert all(torch.equal(got[n], want[n]) for n in want)
+        # (a row's terms are summed in another order where it begins elsewhere: scores agree to twice the tolerance)
+        assert torch.equal(got["parents"], want["parents"]) and torch.equal(got["tokens"], want["tokens"])
+        a, b = (o["scores"].double().cpu() for o in (got, want))
+        assert ((a - b).abs() <= 2 * _tol(4099, b)).all()
 
 
 @pytest.mark.parametrize("groups,beams,n,k", [(1, 1, 1, 1), (3, 4, 20, 8), (2, 8, 5, 16), (2, 128, 128, 128), (4, 3, 7, 3)])

@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(kADPlanThreads) adapter_plan_kernel(const Adap
   bool bad = false;
   auto slot = [&](int i) {  // -1 behind the last row
     if (i >= a.rows) return -1;
-    const int l = a.adapter_idx[i];
+    const int l = __ldcg(a.adapter_idx + i);
     if (l >= 0 && l < L) return l;
     bad |= l != -1;
     return L;

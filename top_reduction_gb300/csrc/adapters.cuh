@@ -187,12 +187,13 @@ struct TileFinder {
   int place = 0;   // among the rows with the same
   int number = -1;  // of the tile that this thread's row is first in
 
-  // All threads; the indices may be read.  Returns the number of tiles.
+  // All threads; the indices may be read.  (Through L2: this grid may start before the kernel that writes them ends,
+  // and an L1 line could be of before.)  Returns the number of tiles.
   __device__ int start(const AdapterArgs& a, TileSmem& sm) {
     if (a.rows > kADOwnPlan) return __ldcg(a.tile_count);
     const int i = threadIdx.x;
     if (i < a.rows) {
-      mine = a.adapter_idx[i];
+      mine = __ldcg(a.adapter_idx + i);
       if (mine < 0 || mine >= a.count) {
         if (mine != -1) set_status(a.dev_status, LMH_DS_ADAPTER_OUT_OF_RANGE);
         mine = -1;
@@ -249,7 +250,7 @@ struct TileFinder {
 };
 
 __device__ __forceinline__ int adapter_rank(const AdapterArgs& a, int adapter) {
-  return adapter < 0 ? 0 : a.ranks ? min(max(a.ranks[adapter], 0), a.R) : a.R;
+  return adapter < 0 ? 0 : a.ranks ? min(max(__ldcg(a.ranks + adapter), 0), a.R) : a.R;
 }
 
 // ---------------------------------------------------------------------------
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kADThreads) adapter_down_kernel(const AdapterA
     if (tid < kADTile) {
       int tk = -1;
       if (tid < count) {
-        tk = a.row_idx ? a.row_idx[ts.rows[tid]] : ts.rows[tid];
+        tk = a.row_idx ? __ldcg(a.row_idx + ts.rows[tid]) : ts.rows[tid];
         if (tk < 0 || tk >= a.num_tokens) {
           tk = -1;  // reads zeros
           set_status(a.dev_status, LMH_DS_ROW_IDX_OUT_OF_RANGE);
@@ -485,7 +486,7 @@ template <typename T, int KS, bool LO>
 __device__ void up_operand(const AdapterArgs& a, const TileSmem& ts, UpSmem<KS, LO>& sm, int rank) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int count = ts.count, cols = (count + 7) / 8;
-  const float scale = ts.adapter < 0 ? 0.0f : a.scales ? a.scales[ts.adapter] : 1.0f;
+  const float scale = ts.adapter < 0 ? 0.0f : a.scales ? __ldcg(a.scales + ts.adapter) : 1.0f;
   constexpr int PER = (KS * 16 + 31) / 32;  // entries a lane; a warp takes a row at a time
   for (int i = warp; i < cols * 8; i += blockDim.x / 32) {
     float v[PER];

@@ -5,27 +5,44 @@
 //
 // and of every group's beams x V scores the k largest, ties by beam, then token.  Scores are
 // compared in 64 bits: two beams' scores differ by what their log-sum-exps differ by, which
-// 32 bits would round to a step of the score (5e-7 at 8).
+// 32 bits would round to a step of the score (5e-7 at 8).  As whole numbers of the same order:
+// this GPU's rate of 64-bit floating operations is low (two a clock and SM).
+//
+//   * beam_stream_kernel reads every logit once (persistent CTAs, bulk copies into a ring, a
+//     thread 128 bytes): the largest allowed logit of every block of 64 and of every span of
+//     32 threads, and the span's (max, sum of exponentials) go to the workspace.
+//   * beam_choose_kernel, one CTA a group: the rows' lse from the spans' pairs; a bound t that at
+//     least k spans reach, the blocks of the spans that reach it, a tighter bound from those, the
+//     logits of the blocks that reach that, and their exact order.
 #include "device_common.cuh"
 #include "lmh_internal.h"
 #include "logits_vec.cuh"
 
 namespace lmh {
 
-constexpr int kBSThreads = 256;                       // stream kernel
-constexpr int kBSBlocksPerWarp = 8;                   // 64-blocks a warp takes of a chunk
-constexpr int kBSBlocks = kBSBlocksPerWarp * kBSThreads / 32;  // 64-blocks of a chunk
-constexpr int kBGThreads = 512;                       // choice kernel: one CTA a group
+// stream kernel
+constexpr int kBSConsumerWarps = 4;
+constexpr int kBSConsumers = kBSConsumerWarps * 32;
+constexpr int kBSThreads = kBSConsumers + 32;        // + one producer warp
+constexpr int kBSChunkBytes = kBSConsumers * 128;    // 128 bytes of a row a consumer
+constexpr int kBSStageBytes = kBSChunkBytes + 128;   // (a chunk that begins off a 16-byte boundary takes 16 more)
+constexpr int kBSStages = 3;
+constexpr int kBSCtasPerSm = 4;
+constexpr int kBSSmem = kBSStages * kBSStageBytes + kBSStages * 32 + 2 * kBSStages * 8 + 16;
+// choice
+constexpr int kBGThreads = 512;                       // one CTA a group
 constexpr int kBGWarps = kBGThreads / 32;
+constexpr int kBGHeld = 4;                            // spans or blocks a thread holds between its two looks at them
 constexpr int kBGCand = 1024;                         // candidates held in shared memory
-constexpr int kBGKept = 1024;                         // kept blocks listed
-constexpr int kBeamsMax = LMH_K_MAX;
+constexpr int kBGKept = 512;                          // spans, blocks listed
+constexpr int kBLThreads = 256;                       // from lists
 
 struct BeamArgs {
   const char* logits;
   int64_t row_stride;  // elements
   int rows, beams, V, nblk;
-  int slots;  // (m, s) pairs a row
+  int chunks;  // of a row
+  int spans;   // of a row
   const float* cum;
   const uint8_t* finished;
   int pad_id;
@@ -36,121 +53,320 @@ struct BeamArgs {
   float* out_scores;
   int32_t* out_parents;
   int32_t* out_tokens;
-  float2* part_ms;
-  float* bmax;
+  float2* part_ms;  // [rows][spans]
+  float* smax;      // [rows][spans], with a mask: the largest allowed logit (without: part_ms.x)
+  float* bmax;      // [rows][nblk]
   uint32_t* dev_status;
+  uint64_t wait_ns;
   // lists
   const int32_t* ids;
   const float* lps;
   int n;
 };
 
+// Inputs are read through L2: this grid may start before the kernel that writes them ends, and an L1 line could be
+// of before.
 __device__ __forceinline__ bool mask_allows(const uint32_t* words, int v) {
-  return words == nullptr || ((__ldg(words + (v >> 5)) >> (v & 31)) & 1u);
+  return (__ldcg(words + (v >> 5)) >> (v & 31)) & 1u;
+}
+template <typename T>
+__device__ __forceinline__ float logit_at(const char* base, int64_t i) {
+  if constexpr (sizeof(T) == 4) {
+    return __ldcg(reinterpret_cast<const float*>(base) + i);
+  } else {
+    const uint16_t b = __ldcg(reinterpret_cast<const uint16_t*>(base) + i);
+    return Vec16<T>::at(&b, 0);
+  }
 }
 
 // ---------------------------------------------------------------------------
-// stream kernel: one chunk of kBSBlocks 64-blocks of one row a CTA
+// stream kernel
 // ---------------------------------------------------------------------------
-// Every thread holds its logits in registers: the block maxima (over allowed tokens) go to the
-// workspace, the chunk's (m, s) over all tokens to one slot.  x - m is taken before the product with
-// log2(e): the rounding of m * log2(e) would be common to a row's terms, and shift its lse.
+// A chunk is 128 bytes of a row for each consumer.  Rows need not begin on 16-byte boundaries: the copy begins
+// on the one before (inside the same 16 bytes of memory), `skip` elements ahead, and a consumer looks at nine
+// vectors in place of eight, the first `skip` elements of its first and the others of its last left out.
+struct BeamStage {
+  int row;   // < 0: no more chunks
+  int lb;    // first block of the chunk in the row
+  int ne;    // logits in the chunk
+  int skip;  // elements of the stage before the first logit
+};
+
+// 16 bytes of logits as they count: element e is kept where bit e of `keep` is set, else -inf.
 template <typename T>
-__global__ void __launch_bounds__(kBSThreads) beam_stream_kernel(const BeamArgs a) {
+__device__ __forceinline__ uint4 keep_elements(uint4 w, uint32_t keep) {
+  if constexpr (sizeof(T) == 4) {
+    w.x = keep & 1u ? w.x : Vec16<T>::kNegInfWord;
+    w.y = keep & 2u ? w.y : Vec16<T>::kNegInfWord;
+    w.z = keep & 4u ? w.z : Vec16<T>::kNegInfWord;
+    w.w = keep & 8u ? w.w : Vec16<T>::kNegInfWord;
+  } else {
+    uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t m = ((keep >> (2 * i)) & 1u ? 0xFFFFu : 0u) | ((keep >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u);
+      u[i] = (u[i] & m) | (Vec16<T>::kNegInfWord & ~m);
+    }
+  }
+  return w;
+}
+
+// The sum of exp(x - m) over a vector, in two lanes: 2^(x L - ML) with ML = m L rounded; the caller makes up for
+// that rounding, which all terms share (it would shift the row's lse).
+template <typename T>
+__device__ __forceinline__ void add_exps(const uint4& w, float2 L2, float2 nml2, float2 (&acc)[2]) {
+  constexpr int EPV = Vec16<T>::N;
+  float2 p[EPV / 2];
+  Vec16<T>::pairs(w, p);
+#pragma unroll
+  for (int q = 0; q < EPV / 2; ++q) {
+    const float2 y = __ffma2_rn(p[q], L2, nml2);
+    acc[q & 1] = __fadd2_rn(acc[q & 1], make_float2(ex2_approx(y.x), ex2_approx(y.y)));
+  }
+}
+
+template <typename T, bool MASK>
+__global__ void __launch_bounds__(kBSThreads, kBSCtasPerSm) beam_stream_kernel(const BeamArgs a) {
   using VT = Vec16<T>;
-  __shared__ float red[32];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int row = blockIdx.x, chunk = blockIdx.y;
-  if (a.finished && a.finished[row]) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const T* src = reinterpret_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.row_stride;
-  const uint32_t* mrow = a.mask ? a.mask + static_cast<int64_t>(row) * a.mask_words : nullptr;
-  const int b0 = chunk * kBSBlocks + warp;  // this warp's blocks: b0, b0 + 8, ...
-  float x[2 * kBSBlocksPerWarp];
-  float tm = -INFINITY;
+  constexpr int ES = static_cast<int>(sizeof(T));
+  constexpr int EPV = VT::N;               // elements of a vector
+  constexpr int EPT = 128 / ES;            // of a consumer
+  constexpr int TPB = kBlock / EPT;        // consumers of a block of 64 (1, or 2 for fp32)
+  constexpr int CH = kBSConsumers / TPB;   // blocks of a chunk
+  constexpr int S = kBSStages;
+  extern __shared__ __align__(128) unsigned char smem[];
+  BeamStage* desc = reinterpret_cast<BeamStage*>(smem + S * kBSStageBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * kBSStageBytes + S * 32);
+  uint64_t* empty = full + S;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + S);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kBSConsumerWarps);
+    }
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  __syncthreads();
+  pdl_launch_dependents();  // the choice may be scheduled; it waits for this grid's results
+
+  if (warp == kBSConsumerWarps) {  // producer
+    if (lane != 0) return;
+    const int64_t total = static_cast<int64_t>(a.rows) * a.chunks;
+    const uint64_t policy = l2_evict_first_policy();
+    int64_t c = blockIdx.x;  // this CTA's chunks: every gridDim.x-th
+    auto issue = [&](int s) {
+      BeamStage& d = desc[s];
+      if (c >= total) {
+        d.row = -1;
+        mbar_arrive(&full[s]);
+        return false;
+      }
+      const int row = static_cast<int>(c / a.chunks);
+      const int lb = static_cast<int>(c - static_cast<int64_t>(row) * a.chunks) * CH;
+      const int ne = min(CH * kBlock, a.V - lb * kBlock);
+      const char* src = a.logits + (static_cast<int64_t>(row) * a.row_stride + static_cast<int64_t>(lb) * kBlock) * ES;
+      const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) & 15u);
+      d.row = row;
+      d.lb = lb;
+      d.ne = ne;
+      d.skip = static_cast<int>(off) / ES;
+      const uint32_t bytes = (off + static_cast<uint32_t>(ne * ES) + 15u) & ~15u;
+      mbar_arrive_expect_tx(&full[s], bytes);
+      bulk_load_hint(smem + s * kBSStageBytes, src - off, bytes, &full[s], policy);
+      c += gridDim.x;
+      return true;
+    };
+    // The first S chunks go out before the grid-dependency wait (they read logits only; see lmh.h), the others
+    // behind it, without the rows of ended beams.
+    uint32_t issued = 0;
+    bool ended = false;
+    for (; issued < static_cast<uint32_t>(S) && !ended; ++issued) ended = !issue(static_cast<int>(issued));
+    pdl_wait();
+    for (; !ended; ++issued) {
+      const int s = static_cast<int>(issued % S);
+      if (!wait_or_abort(&empty[s], ((issued / S) & 1u) ^ 1u, abort_flag, a.dev_status, a.wait_ns)) break;
+      if (a.finished)
+        while (c < total && __ldcg(a.finished + c / a.chunks)) c += gridDim.x;
+      ended = !issue(s);
+    }
+    // copies still in flight (after an abort) land before the CTA exits
+    const uint32_t first = issued > static_cast<uint32_t>(S) ? issued - S : 0u;
+    for (uint32_t i = first; i < issued; ++i) mbar_wait(&full[i % S], (i / S) & 1u);
+    return;
+  }
+
+  const int rot = tid & 7;  // vector order turned by lane: no bank conflict
+  const uint64_t keep_policy = l2_evict_last_policy();
+  const float L = kLog2e;
+  pdl_wait();  // the workspace may be written
+  for (uint32_t i = 0;; ++i) {
+    const int s = static_cast<int>(i % S);
+    const bool ok = wait_or_abort(&full[s], (i / S) & 1u, abort_flag, a.dev_status, a.wait_ns);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    const BeamStage d = desc[s];
+    if (d.row < 0) break;
+    const int ne_t = min(max(d.ne - tid * EPT, 0), EPT);  // this thread's logits
+    uint64_t allowed = ~0ull;
+    if constexpr (MASK) {  // (asked for before the stage is read)
+      const uint32_t* m = a.mask + static_cast<int64_t>(d.row) * a.mask_words;
+      const int word = (d.lb * kBlock + tid * EPT) / 32;
+      allowed = 0;
+      if (ne_t > 0) allowed = __ldcg(m + word);
+      if (EPT == 64 && ne_t > 32) allowed |= static_cast<uint64_t>(__ldcg(m + word + 1)) << 32;
+    }
+    const unsigned char* mine = smem + s * kBSStageBytes + tid * 128;
+    uint4 w[8], w8 = make_uint4(VT::kNegInfWord, VT::kNegInfWord, VT::kNegInfWord, VT::kNegInfWord);
 #pragma unroll
-  for (int i = 0; i < kBSBlocksPerWarp; ++i) {
-    const int b = b0 + i * (kBSThreads / 32);
+    for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint4*>(mine + ((j + rot) & 7) * 16);
+    if (d.skip) w8 = *reinterpret_cast<const uint4*>(mine + 128);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+    if (d.skip || ne_t < EPT) {  // element x of vector v is logit v * EPV + x - skip of the thread
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int v = b * kBlock + h * 32 + lane;
-      float t = v < a.V ? VT::at(src, v) : -INFINITY;
-      t = t == t ? t : -INFINITY;  // NaN counts as -inf
-      x[2 * i + h] = t;
-      tm = fmaxf(tm, t);
+      for (int j = 0; j < 8; ++j) {
+        const int first = ((j + rot) & 7) * EPV - d.skip;
+        uint32_t keep = 0;
+#pragma unroll
+        for (int x = 0; x < EPV; ++x) keep |= (first + x >= 0 && first + x < ne_t ? 1u : 0u) << x;
+        w[j] = keep_elements<T>(w[j], keep);
+      }
+      uint32_t keep = 0;
+#pragma unroll
+      for (int x = 0; x < EPV; ++x) keep |= (x < d.skip && EPT - d.skip + x < ne_t ? 1u : 0u) << x;
+      w8 = keep_elements<T>(w8, keep);
+    }
+    float tail = -INFINITY;  // of the ninth vector
+    if (d.skip) {
+      float x[EPV];
+      VT::unpack(w8, x);
+#pragma unroll
+      for (int e = 0; e < EPV; ++e) tail = fmaxf(tail, x[e]);
+    }
+    float vm = fmaxf(VT::max8(w), tail);  // (NaN is dropped)
+    vm = vm == vm ? vm : -INFINITY;
+    float bm = vm;
+    if constexpr (MASK) {
+      bm = -INFINITY;
+      if (allowed) {
+        uint4 k[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int first = ((j + rot) & 7) * EPV - d.skip;
+          k[j] = keep_elements<T>(w[j], static_cast<uint32_t>(first >= 0 ? allowed >> first : allowed << -first));
+        }
+        bm = VT::max8(k);
+        if (d.skip) {
+          float x[EPV];
+          VT::unpack(keep_elements<T>(w8, static_cast<uint32_t>(allowed >> (EPT - d.skip))), x);
+#pragma unroll
+          for (int e = 0; e < EPV; ++e) bm = fmaxf(bm, x[e]);
+        }
+        bm = bm == bm ? bm : -INFINITY;
+      }
+    }
+    const float smx = MASK ? warp_max(bm) : 0.0f;
+    const float M = warp_max(vm);
+    if (TPB == 2) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
+    const int b = d.lb + tid / TPB;
+    if (tid % TPB == 0 && b < a.nblk) st_keep(a.bmax + static_cast<int64_t>(d.row) * a.nblk + b, bm, keep_policy);
+    float ts = 0.0f;  // sum of exp(x - vm) over this thread's logits
+    if (vm > -INFINITY) {
+      const float ml = vm * L;
+      const float2 L2 = make_float2(L, L), nml2 = make_float2(-ml, -ml);
+      float2 acc0[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      float2 acc1[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        add_exps<T>(w[j], L2, nml2, acc0);
+        add_exps<T>(w[j + 1], L2, nml2, acc1);
+      }
+      if (d.skip) add_exps<T>(w8, L2, nml2, acc0);
+      const float2 r = __fadd2_rn(__fadd2_rn(acc0[0], acc0[1]), __fadd2_rn(acc1[0], acc1[1]));
+      ts = r.x + r.y;
+      ts = fmaf(ts, fmaf(vm, L, -ml) * -0.6931471805599453f, ts);  // * 2^-(vm L - ml)
+      if (!(ts < INFINITY)) {  // +inf or NaN among the logits: one by one
+        ts = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 9; ++j) {
+          float x[EPV];
+          VT::unpack(j < 8 ? w[j & 7] : w8, x);
+#pragma unroll
+          for (int e = 0; e < EPV; ++e) {
+            if (vm == INFINITY) ts += x[e] == INFINITY ? 1.0f : 0.0f;
+            else ts += x[e] == x[e] ? ex2_approx((x[e] - vm) * L) : 0.0f;
+          }
+        }
+      }
+    }
+    // the span's pair
+    const float sc = warp_sum(vm == -INFINITY ? 0.0f : vm == M ? ts : M == INFINITY ? 0.0f : ts * ex2_approx((vm - M) * L));
+    const int span = d.lb / (CH / kBSConsumerWarps) + warp;
+    if (lane == 0 && span < a.spans) {
+      const int64_t at = static_cast<int64_t>(d.row) * a.spans + span;
+      a.part_ms[at] = make_float2(M, sc);
+      if constexpr (MASK) a.smax[at] = smx;
     }
   }
-#pragma unroll
-  for (int i = 0; i < kBSBlocksPerWarp; ++i) {
-    const int b = b0 + i * (kBSThreads / 32);
-    float m = -INFINITY;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int v = b * kBlock + h * 32 + lane;
-      if (v < a.V && mask_allows(mrow, v)) m = fmaxf(m, x[2 * i + h]);
-    }
-    m = warp_max(m);
-    if (lane == 0 && b < a.nblk) a.bmax[static_cast<int64_t>(row) * a.nblk + b] = m;
-  }
-  const float M = block_max(tm, red);
-  float s = 0.0f;
-  if (M == INFINITY) {
-#pragma unroll
-    for (int i = 0; i < 2 * kBSBlocksPerWarp; ++i) s += x[i] == INFINITY ? 1.0f : 0.0f;
-  } else if (M > -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < 2 * kBSBlocksPerWarp; ++i) s += ex2_approx((x[i] - M) * kLog2e);
-  }
-  s = block_sum(s, red);
-  if (threadIdx.x == 0) a.part_ms[static_cast<int64_t>(row) * a.slots + chunk] = make_float2(M, s);
 }
 
 // ---------------------------------------------------------------------------
 // choice of a group
 // ---------------------------------------------------------------------------
-struct Cand {
-  double score;
-  uint32_t at;  // beam * V + token (lists: beam * n + place)
-};
-
-// (score, at) goes before (score2, at2)
-__device__ __forceinline__ bool before(double s, uint32_t at, double s2, uint32_t at2) {
-  return s > s2 || (s == s2 && at < at2);
+// A score as a whole number of the same order (scores are above -inf and not NaN; 0 is none).
+__device__ __forceinline__ uint64_t score_key(double s) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(s + 0.0));  // (-0 becomes +0)
+  return (u >> 63) ? ~u : u | (1ull << 63);
+}
+__device__ __forceinline__ float key_score(uint64_t k) {
+  return static_cast<float>(__longlong_as_double(static_cast<long long>((k >> 63) ? k & ~(1ull << 63) : ~k)));
+}
+// (key, at) goes before (key2, at2); at: beam * V + token (lists: beam * n + place)
+__device__ __forceinline__ bool before(uint64_t k, uint32_t at, uint64_t k2, uint32_t at2) {
+  return k > k2 || (k == k2 && at < at2);
 }
 
 enum RowState : uint8_t { kRowNone = 0, kRowNormal = 1, kRowPlusInf = 2, kRowEnded = 3 };
 
 template <int NT>
 struct ChoiceSmem {
-  double score[kBGCand];
+  uint64_t key[kBGCand];
   uint32_t at[kBGCand];
-  double res_score[kBeamsMax];
-  uint32_t res_at[kBeamsMax];
-  double off[kBeamsMax];   // cum - log sum exp(z - M) of the group's rows
-  float offf[kBeamsMax];
-  float top_z[kBeamsMax];  // M, their largest logit
-  uint8_t state[kBeamsMax];
-  int first[kBeamsMax];    // keep_slots: the place of a candidate, or -1
-  double wscore[NT / 32];
+  uint64_t res_key[kBeamsMaxRows];
+  uint32_t res_at[kBeamsMaxRows];
+  double off[kBeamsMaxRows];   // cum - log sum exp(z - M) of the group's rows
+  float offf[kBeamsMaxRows];
+  float top_z[kBeamsMaxRows];  // M, their largest logit
+  uint8_t state[kBeamsMaxRows];
+  int first[kBeamsMaxRows];    // keep_slots: the candidate in a place, or -1
+  int slot[kBeamsMaxRows];     // keep_slots: a candidate's place
+  uint64_t wkey[NT / 32];
   uint32_t wat[NT / 32];
-  uint32_t count, kept;
+  uint32_t count, spans, blocks;
   float top[NT / 32 * 64];
   float bound;
   float off_max;
+  uint32_t kept_spans[kBGKept];
   uint32_t kept_blocks[kBGKept];
 };
 
-// Orders sm.score/at[0 .. cnt) into sm.res_*[0 .. min(cnt, k)): every thread counts those before its own.
+// Orders sm.key/at[0 .. cnt) into sm.res_*[0 .. min(cnt, k)): G threads a candidate count those before it.
 template <int NT>
 __device__ void rank_candidates(ChoiceSmem<NT>& sm, int cnt, int k) {
-  for (int i = threadIdx.x; i < cnt; i += NT) {
-    const double s = sm.score[i];
-    const uint32_t at = sm.at[i];
+  int G = 1;  // a power of two, to 32, with G * cnt <= NT where that can be
+  while (G < 32 && 2 * G * cnt <= NT) G *= 2;
+  const int sub = threadIdx.x % G;
+  for (int base = 0; base < cnt; base += NT / G) {
+    const int i = base + static_cast<int>(threadIdx.x) / G;
+    const uint64_t key = i < cnt ? sm.key[i] : 0;
+    const uint32_t at = i < cnt ? sm.at[i] : 0;
     int rank = 0;
-    for (int j = 0; j < cnt; ++j) rank += before(sm.score[j], sm.at[j], s, at);
-    if (rank < k) {
-      sm.res_score[rank] = s;
+    if (i < cnt)
+      for (int j = sub; j < cnt; j += G) rank += before(sm.key[j], sm.at[j], key, at);
+    for (int o = G / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (i < cnt && sub == 0 && rank < k) {
+      sm.res_key[rank] = key;
       sm.res_at[rank] = at;
     }
   }
@@ -171,10 +387,10 @@ __device__ void write_results(const BeamArgs& a, ChoiceSmem<NT>& sm, int group, 
       first = true;
       const int b = beam_of(r);
       for (int j = 0; j < r; ++j) first &= beam_of(j) != b;
-      if (first) sm.first[b] = r;  // slot b is taken by candidate r
+      if (first) sm.first[b] = r;
     }
     __syncthreads();
-    if (r < k && !first) {  // the turn-th candidate that is no first child takes the turn-th free slot
+    if (r < k && !first) {  // the turn-th candidate that is no first child takes the turn-th free place
       int turn = 0;
       for (int j = 0; j < r; ++j) {
         const int b = beam_of(j);
@@ -183,16 +399,16 @@ __device__ void write_results(const BeamArgs& a, ChoiceSmem<NT>& sm, int group, 
       int slot = 0;
       for (int t = 0; slot < k; ++slot)
         if (sm.first[slot] < 0 && t++ == turn) break;
-      sm.kept_blocks[r] = static_cast<uint32_t>(slot);
+      sm.slot[r] = slot;
     } else if (r < k) {
-      sm.kept_blocks[r] = static_cast<uint32_t>(beam_of(r));
+      sm.slot[r] = beam_of(r);
     }
     __syncthreads();
   }
   for (int r = threadIdx.x; r < k; r += NT) {
-    const int64_t to = base + (a.keep_slots ? static_cast<int>(sm.kept_blocks[r]) : r);
+    const int64_t to = base + (a.keep_slots ? sm.slot[r] : r);
     const int b = beam_of(r);
-    a.out_scores[to] = b < 0 ? -INFINITY : static_cast<float>(sm.res_score[r]);
+    a.out_scores[to] = b < 0 ? -INFINITY : key_score(sm.res_key[r]);
     a.out_parents[to] = b < 0 ? -1 : group * a.beams + b;
     a.out_tokens[to] = b < 0 ? -1 : (sm.state[b] == kRowEnded ? a.pad_id : token(sm.res_at[r], b));
   }
@@ -200,38 +416,36 @@ __device__ void write_results(const BeamArgs& a, ChoiceSmem<NT>& sm, int group, 
 }
 
 // The k best by repeatedly taking the best that is left: exact for any number of ties, used where the
-// candidates do not fit.  `scan(s, at, last_s, last_at)` puts the thread's best item behind (last_s, last_at)
-// into (s, at), s = -inf for none.  Returns the number found.
+// candidates do not fit.  `scan(key, at, last_key, last_at)` puts the thread's best item behind (last_key, last_at)
+// into (key, at), key = 0 for none.  Returns the number found.
 template <int NT, typename Scan>
 __device__ int take_in_turn(ChoiceSmem<NT>& sm, int k, Scan scan) {
-  double last_s = INFINITY;
-  uint32_t last_at = 0;
-  double s = -INFINITY;
-  uint32_t at = 0xFFFFFFFFu;
+  uint64_t last = ~0ull, key = 0;
+  uint32_t last_at = 0, at = 0xFFFFFFFFu;
   bool stale = true;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int r = 0;
   for (; r < k; ++r) {
-    if (stale) scan(s, at, last_s, last_at);
-    double bs = s;
+    if (stale) scan(key, at, last, last_at);
+    uint64_t bk = key;
     uint32_t bat = at;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const double os = __shfl_xor_sync(0xffffffffu, bs, o);
+      const uint64_t ok = __shfl_xor_sync(0xffffffffu, bk, o);
       const uint32_t oat = __shfl_xor_sync(0xffffffffu, bat, o);
-      if (before(os, oat, bs, bat)) bs = os, bat = oat;
+      if (before(ok, oat, bk, bat)) bk = ok, bat = oat;
     }
     __syncthreads();
-    if (lane == 0) sm.wscore[warp] = bs, sm.wat[warp] = bat;
+    if (lane == 0) sm.wkey[warp] = bk, sm.wat[warp] = bat;
     __syncthreads();
-    bs = sm.wscore[0], bat = sm.wat[0];
+    bk = sm.wkey[0], bat = sm.wat[0];
 #pragma unroll
     for (int w = 1; w < NT / 32; ++w)
-      if (before(sm.wscore[w], sm.wat[w], bs, bat)) bs = sm.wscore[w], bat = sm.wat[w];
-    if (!(static_cast<float>(bs) > -INFINITY)) break;
-    if (threadIdx.x == 0) sm.res_score[r] = bs, sm.res_at[r] = bat;
-    last_s = bs, last_at = bat;
-    stale = s == bs && at == bat;  // (the pair is one thread's alone)
+      if (before(sm.wkey[w], sm.wat[w], bk, bat)) bk = sm.wkey[w], bat = sm.wat[w];
+    if (bk == 0) break;
+    if (threadIdx.x == 0) sm.res_key[r] = bk, sm.res_at[r] = bat;
+    last = bk, last_at = bat;
+    stale = key == bk && at == bat;  // (the pair is one thread's alone)
   }
   __syncthreads();
   return r;
@@ -245,36 +459,82 @@ __device__ __forceinline__ F below_top(uint8_t state, float z, float M) {
   return static_cast<F>(z) - static_cast<F>(M);
 }
 
+// a + b and what its rounding left
+__device__ __forceinline__ void two_sum(float& s, float& c, float b) {
+  const float t = s + b, z = t - s;
+  c += (s - (t - z)) + (b - z);
+  s = t;
+}
+
+// sm.bound = a value that at least k of the threads' values reach, or -inf if they are fewer: of every warp the q
+// largest of its threads' two largest (16 warps: 16 q >= k), of those the k-th.  Two barriers.
+template <int NT>
+__device__ void bound_of(ChoiceSmem<NT>& sm, float m1, float m2, int k) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int q = min(64, max(2, (k + 3) / 4));
+  uint32_t k1 = f32_ord(m1), k2 = f32_ord(m2);
+  for (int r = 0; r < q; ++r) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, k1);
+    const unsigned holders = __ballot_sync(0xffffffffu, k1 == m);
+    if (lane == __ffs(holders) - 1) {
+      sm.top[warp * q + r] = m ? ord_f32(m) : -INFINITY;
+      k1 = k2;
+      k2 = 0;
+    }
+  }
+  __syncthreads();
+  const int nv = NT / 32 * q;
+  for (int i = threadIdx.x; i < nv; i += NT) {
+    const float v = sm.top[i];
+    int rank = 0;
+    for (int j = 0; j < nv; ++j) rank += sm.top[j] > v || (sm.top[j] == v && j < i);
+    if (rank == k - 1) sm.bound = v;
+  }
+  __syncthreads();
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kBGThreads) beam_choose_kernel(const BeamArgs a) {
-  using VT = Vec16<T>;
   constexpr int NT = kBGThreads;
+  constexpr int SB = 32 / (kBlock / (128 / static_cast<int>(sizeof(T))));  // blocks of a span
   extern __shared__ __align__(16) unsigned char smem_raw[];
   ChoiceSmem<NT>& sm = *reinterpret_cast<ChoiceSmem<NT>*>(smem_raw);
   const int group = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int B = a.beams, nblk = a.nblk;
+  const int B = a.beams, nblk = a.nblk, P = a.spans;
   const int row0 = group * B;
   pdl_wait();
-  if (tid == 0) sm.count = 0, sm.kept = 0, sm.off_max = 0.0f;
+  if (tid == 0) sm.count = 0, sm.spans = 0, sm.blocks = 0, sm.off_max = 0.0f;
 
-  // ---- the rows' cum - lse ----
+  // ---- the rows' cum - log sum exp(z - M) ----
+  // 32 bits but for the last sum: the terms are good to 2^-23, the sum carries what its roundings leave, and
+  // log S = e ln 2 + log f with f next to 1, whose 32-bit logarithm is off by 2^-25.
   for (int b = warp; b < B; b += kBGWarps) {
     const int row = row0 + b;
-    const float cum = a.cum[row];
-    const bool ended = a.finished && a.finished[row];
-    const float2* ms = a.part_ms + static_cast<int64_t>(row) * a.slots;
-    float M = -INFINITY;
-    double S = 0.0;
+    const float cum = __ldcg(a.cum + row);
+    const bool ended = a.finished && __ldcg(a.finished + row);
+    const float2* ms = a.part_ms + static_cast<int64_t>(row) * P;
+    float M = -INFINITY, S = 0.0f, c = 0.0f;
     if (!ended) {
-      for (int j = lane; j < a.slots; j += 32) M = fmaxf(M, __ldcg(ms + j).x);
-      M = warp_max(M);
-      for (int j = lane; j < a.slots; j += 32) {
-        const float2 p = __ldcg(ms + j);
-        if (p.x == M) S += p.y;
-        else if (p.x > -INFINITY && M < INFINITY) S += static_cast<double>(p.y) * exp2(static_cast<double>(p.x - M) * 1.4426950408889634);
-      }
+      float2 p[4];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+      for (int u = 0; u < 4; ++u) p[u] = u * 32 + lane < P ? __ldcg(ms + u * 32 + lane) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) M = fmaxf(M, p[u].x);
+      for (int j = 128 + lane; j < P; j += 32) M = fmaxf(M, __ldcg(ms + j).x);
+      M = warp_max(M);
+      auto add = [&](float2 q) {
+        if (q.x == M) two_sum(S, c, q.x > -INFINITY ? q.y : 0.0f);
+        else if (q.x > -INFINITY && M < INFINITY) two_sum(S, c, q.y * exp2f((q.x - M) * kLog2e));
+      };
+#pragma unroll
+      for (int u = 0; u < 4; ++u) add(p[u]);
+      for (int j = 128 + lane; j < P; j += 32) add(__ldcg(ms + j));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float s2 = __shfl_xor_sync(0xffffffffu, S, o), c2 = __shfl_xor_sync(0xffffffffu, c, o);
+        two_sum(S, c, s2);
+        c += c2;
+      }
     }
     if (lane == 0) {
       const bool fin = cum > -INFINITY && cum < INFINITY;  // (false for NaN)
@@ -285,7 +545,10 @@ __global__ void __launch_bounds__(kBGThreads) beam_choose_kernel(const BeamArgs 
         off = cum;
       } else if (fin && M > -INFINITY) {
         st = M == INFINITY ? kRowPlusInf : kRowNormal;
-        off = static_cast<double>(cum) - log(S);
+        int e;
+        float f = frexpf(S, &e);
+        if (f < 0.70710678f) f *= 2.0f, --e;
+        off = static_cast<double>(cum) - (e * 0.69314718055994530942 + static_cast<double>(logf(f) + c / S));
       }
       sm.state[b] = st;
       sm.off[b] = off;
@@ -297,116 +560,128 @@ __global__ void __launch_bounds__(kBGThreads) beam_choose_kernel(const BeamArgs 
   if (tid < B) {
     if (sm.state[tid] == kRowEnded) {
       const uint32_t i = atomicAdd(&sm.count, 1u);
-      sm.score[i] = sm.off[tid];
+      sm.key[i] = score_key(sm.off[tid]);
       sm.at[i] = static_cast<uint32_t>(tid) * static_cast<uint32_t>(a.V);
     }
     atomicMax(reinterpret_cast<int*>(&sm.off_max), __float_as_int(fabsf(sm.offf[tid])));
   }
-
-  // ---- a bound that at least k blocks reach ----
-  const float* bm = a.bmax + static_cast<int64_t>(row0) * nblk;
-  const int nb = B * nblk;
-  auto block_score = [&](int i) -> float {  // in fp32
-    const int b = i / nblk;
+  auto score32 = [&](int b, float z) -> float {
     const uint8_t st = sm.state[b];
-    return st == kRowNormal || st == kRowPlusInf ? below_top<float>(st, __ldcg(bm + i), sm.top_z[b]) + sm.offf[b]
-                                                 : -INFINITY;
+    return st == kRowNormal || st == kRowPlusInf ? below_top<float>(st, z, sm.top_z[b]) + sm.offf[b] : -INFINITY;
   };
-  float m1 = -INFINITY, m2 = -INFINITY;
-  for (int i = tid; i < nb; i += NT) {
-    const float v = block_score(i);
-    m2 = fmaxf(m2, fminf(m1, v));
-    m1 = fmaxf(m1, v);
-  }
-  const int q = min(64, max(2, (a.k + 3) / 4));  // values of a warp that are looked at: 16 q >= k
-  {
-    uint32_t k1 = f32_ord(m1), k2 = f32_ord(m2);
-    for (int r = 0; r < q; ++r) {
-      const uint32_t m = __reduce_max_sync(0xffffffffu, k1);
-      const unsigned holders = __ballot_sync(0xffffffffu, k1 == m);
-      if (lane == __ffs(holders) - 1) {
-        sm.top[warp * q + r] = m ? ord_f32(m) : -INFINITY;
-        k1 = k2;
-        k2 = 0;
+  // The k-th best score is at least `bound` but for fp32's rounding of it and of the sums compared with it (2^-24 of
+  // each term): 2^-21 covers both.
+  auto floor_of = [&](float bound) {
+    return bound > -INFINITY ? bound - ldexpf(fabsf(bound) + sm.off_max, -21) : bound;
+  };
+  // Items 0 .. n - 1 with value(i): the items that reach a bound that k of them reach go to list[0 .. *count), that
+  // bound is returned.  A thread holds its first values between its two looks.
+  auto filter = [&](int n, auto value, uint32_t* list, uint32_t* count) -> float {
+    float m1 = -INFINITY, m2 = -INFINITY, held[kBGHeld];
+    auto top2 = [&](float v) {
+      m2 = fmaxf(m2, fminf(m1, v));
+      m1 = fmaxf(m1, v);
+    };
+#pragma unroll
+    for (int u = 0; u < kBGHeld; ++u) held[u] = u * NT + tid < n ? value(u * NT + tid) : -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kBGHeld; ++u) top2(held[u]);
+    for (int i = kBGHeld * NT + tid; i < n; i += NT) top2(value(i));
+    bound_of(sm, m1, m2, a.k);
+    const float t = floor_of(sm.bound);
+    auto keep = [&](int i, float v) {
+      if (v >= t && v > -INFINITY) {
+        const uint32_t p = atomicAdd(count, 1u);
+        if (p < kBGKept) list[p] = static_cast<uint32_t>(i);
       }
-    }
-  }
-  __syncthreads();
-  const int nv = kBGWarps * q;
-  for (int i = tid; i < nv; i += NT) {
-    const float v = sm.top[i];
-    int rank = 0;
-    for (int j = 0; j < nv; ++j) rank += sm.top[j] > v || (sm.top[j] == v && j < i);
-    if (rank == a.k - 1) sm.bound = v;
-  }
-  __syncthreads();
-  // The k-th best score is at least `bound` but for fp32's rounding of bound and of the sums compared
-  // with it (2^-24 of each term): 2^-21 covers both.
-  float t = sm.bound;
-  if (t > -INFINITY) t -= ldexpf(fabsf(t) + sm.off_max, -21);
-
-  // ---- the blocks that reach it ----
-  for (int i = tid; i < nb; i += NT) {
-    const float v = block_score(i);
-    if (v >= t && v > -INFINITY) {
-      const uint32_t p = atomicAdd(&sm.kept, 1u);
-      if (p < kBGKept) sm.kept_blocks[p] = static_cast<uint32_t>(i);
-    }
-  }
-  __syncthreads();
-  const int nkept = static_cast<int>(sm.kept);
+    };
+#pragma unroll
+    for (int u = 0; u < kBGHeld; ++u) keep(u * NT + tid, held[u]);
+    for (int i = kBGHeld * NT + tid; i < n; i += NT) keep(i, value(i));
+    __syncthreads();
+    return t;
+  };
+  const float* bm = a.bmax + static_cast<int64_t>(row0) * nblk;
+  const int64_t span0 = static_cast<int64_t>(row0) * P;
+  auto span_max = [&](int i) { return a.mask ? __ldcg(a.smax + span0 + i) : __ldcg(&a.part_ms[span0 + i].x); };
+  filter(B * P, [&](int i) { return score32(i / P, span_max(i)); }, sm.kept_spans, &sm.spans);
+  const int n_spans = static_cast<int>(sm.spans);
+  bool fits = n_spans <= kBGKept;
+  int cnt = 0;
   auto logit = [&](int b, int v) -> float {  // -inf for a token that is not allowed
     const int row = row0 + b;
     if (a.mask && !mask_allows(a.mask + static_cast<int64_t>(row) * a.mask_words, v)) return -INFINITY;
-    const float z = VT::at(a.logits, static_cast<int64_t>(row) * a.row_stride + v);
+    const float z = logit_at<T>(a.logits, static_cast<int64_t>(row) * a.row_stride + v);
     return z == z ? z : -INFINITY;
   };
-  auto score_of = [&](int b, float z) -> double {
-    return sm.off[b] + below_top<double>(sm.state[b], z, sm.top_z[b]);
+  auto key_of = [&](int b, float z) -> uint64_t {  // 0: no continuation
+    const double s = sm.off[b] + below_top<double>(sm.state[b], z, sm.top_z[b]);
+    return static_cast<float>(s) > -INFINITY ? score_key(s) : 0;
   };
-  if (nkept <= kBGKept) {
-    for (int j = tid; j < nkept * kBlock; j += NT) {
-      const int i = static_cast<int>(sm.kept_blocks[j / kBlock]);
-      const int b = i / nblk, v = (i - b * nblk) * kBlock + j % kBlock;
+  if (fits) {
+    // item i: block i % SB of kept span i / SB; its number is row * nblk + block
+    auto block_at = [&](int i, int& b, int& blk) {
+      const int span = static_cast<int>(sm.kept_spans[i / SB]);
+      b = span / P;
+      blk = (span - b * P) * SB + i % SB;
+    };
+    const float t = filter(
+        n_spans * SB,
+        [&](int i) {
+          int b, blk;
+          block_at(i, b, blk);
+          return blk < nblk ? score32(b, __ldcg(bm + static_cast<int64_t>(b) * nblk + blk)) : -INFINITY;
+        },
+        sm.kept_blocks, &sm.blocks);
+    const int n_blocks = static_cast<int>(sm.blocks);
+    fits = n_blocks <= kBGKept;
+    for (int j = tid; fits && j < n_blocks * kBlock; j += NT) {
+      int b, blk;
+      block_at(static_cast<int>(sm.kept_blocks[j / kBlock]), b, blk);
+      const int v = blk * kBlock + j % kBlock;
       if (v >= a.V) continue;
       const float z = logit(b, v);
-      const float f = below_top<float>(sm.state[b], z, sm.top_z[b]) + sm.offf[b];
+      const float f = score32(b, z);
       if (!(f >= t) || !(f > -INFINITY)) continue;
+      const uint64_t key = key_of(b, z);
+      if (key == 0) continue;
       const uint32_t p = atomicAdd(&sm.count, 1u);
       if (p < kBGCand) {
-        sm.score[p] = score_of(b, z);
+        sm.key[p] = key;
         sm.at[p] = static_cast<uint32_t>(b) * static_cast<uint32_t>(a.V) + static_cast<uint32_t>(v);
       }
     }
+    __syncthreads();
+    cnt = static_cast<int>(sm.count);
+    fits = fits && cnt <= kBGCand;
   }
-  __syncthreads();
-  int cnt = static_cast<int>(sm.count);
-  if (nkept <= kBGKept && cnt <= kBGCand) {
+  if (fits) {
     rank_candidates(sm, cnt, a.k);
     cnt = min(cnt, a.k);
     __syncthreads();
   } else {
     // a thread's blocks are a contiguous share, looked through again only after its best is taken
-    const int per = (nb + NT - 1) / NT;
+    const int nb = B * nblk, per = (nb + NT - 1) / NT;
     const int lo = min(nb, tid * per), hi = min(nb, lo + per);
-    cnt = take_in_turn(sm, a.k, [&](double& s, uint32_t& at, double last_s, uint32_t last_at) {
-      s = -INFINITY;
+    cnt = take_in_turn(sm, a.k, [&](uint64_t& key, uint32_t& at, uint64_t last, uint32_t last_at) {
+      key = 0;
       at = 0xFFFFFFFFu;
       for (int i = lo; i < hi; ++i) {
         const int b = i / nblk, blk = i - b * nblk;
         const uint8_t st = sm.state[b];
+        const uint32_t e0 = static_cast<uint32_t>(b) * static_cast<uint32_t>(a.V);
         if (st == kRowNone) continue;
         if (st == kRowEnded) {
-          const uint32_t e = static_cast<uint32_t>(b) * static_cast<uint32_t>(a.V);
-          if (blk == 0 && before(last_s, last_at, sm.off[b], e) && before(sm.off[b], e, s, at)) s = sm.off[b], at = e;
+          const uint64_t c = score_key(sm.off[b]);
+          if (blk == 0 && before(last, last_at, c, e0) && before(c, e0, key, at)) key = c, at = e0;
           continue;
         }
         // (an equal score further on comes after the one that is held)
-        const double most = score_of(b, __ldcg(bm + i));
-        for (int v = blk * kBlock; most > s && v < min(a.V, (blk + 1) * kBlock); ++v) {
-          const double c = score_of(b, logit(b, v));
-          const uint32_t e = static_cast<uint32_t>(b) * static_cast<uint32_t>(a.V) + static_cast<uint32_t>(v);
-          if (static_cast<float>(c) > -INFINITY && before(last_s, last_at, c, e) && c > s) s = c, at = e;
+        const uint64_t most = key_of(b, __ldcg(bm + i));
+        for (int v = blk * kBlock; most > key && v < min(a.V, (blk + 1) * kBlock); ++v) {
+          const uint64_t c = key_of(b, logit(b, v));
+          const uint32_t e = e0 + static_cast<uint32_t>(v);
+          if (c > key && before(last, last_at, c, e)) key = c, at = e;
         }
       }
     });
@@ -418,8 +693,6 @@ __global__ void __launch_bounds__(kBGThreads) beam_choose_kernel(const BeamArgs 
 // ---------------------------------------------------------------------------
 // from top-k lists
 // ---------------------------------------------------------------------------
-constexpr int kBLThreads = 256;
-
 __global__ void __launch_bounds__(kBLThreads) beam_lists_kernel(const BeamArgs a) {
   constexpr int NT = kBLThreads;
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -427,32 +700,33 @@ __global__ void __launch_bounds__(kBLThreads) beam_lists_kernel(const BeamArgs a
   const int group = blockIdx.x, tid = threadIdx.x;
   const int B = a.beams, n = a.n, row0 = group * B;
   pdl_wait();
+  const int64_t e0 = static_cast<int64_t>(row0) * n;
+  const int total = B * n;
+  // the first entries are on their way while the rows' scores arrive
+  const int id0 = tid < total ? __ldcg(a.ids + e0 + tid) : -1;
+  const float lp0 = tid < total ? __ldcg(a.lps + e0 + tid) : 0.0f;
   if (tid == 0) sm.count = 0;
   if (tid < B) {
-    const float cum = a.cum[row0 + tid];
+    const float cum = __ldcg(a.cum + row0 + tid);
     const bool fin = cum > -INFINITY && cum < INFINITY;
-    sm.state[tid] = !fin ? kRowNone : (a.finished && a.finished[row0 + tid]) ? kRowEnded : kRowNormal;
+    sm.state[tid] = !fin ? kRowNone : (a.finished && __ldcg(a.finished + row0 + tid)) ? kRowEnded : kRowNormal;
     sm.off[tid] = cum;
   }
   __syncthreads();
-  const int64_t e0 = static_cast<int64_t>(row0) * n;
-  const int total = B * n;
-  // the score of entry i of the group's lists; -inf for none
-  auto entry = [&](int i) -> double {
+  // the key of entry i of the group's lists; 0 for none
+  auto entry = [&](int i, int id, float lp) -> uint64_t {
     const int b = i / n;
     const uint8_t st = sm.state[b];
-    if (st == kRowEnded) return i == b * n ? sm.off[b] : -INFINITY;
-    if (st == kRowNone || a.ids[e0 + i] < 0) return -INFINITY;
-    const float lp = a.lps[e0 + i];
-    if (!(lp > -INFINITY && lp < INFINITY)) return -INFINITY;
+    if (st == kRowEnded) return i == b * n ? score_key(sm.off[b]) : 0;
+    if (st == kRowNone || id < 0 || !(lp > -INFINITY && lp < INFINITY)) return 0;
     const double s = sm.off[b] + static_cast<double>(lp);
-    return static_cast<float>(s) > -INFINITY ? s : -INFINITY;
+    return static_cast<float>(s) > -INFINITY ? score_key(s) : 0;
   };
   for (int i = tid; i < total; i += NT) {
-    const double s = entry(i);
-    if (s > -INFINITY) {
+    const uint64_t key = i == tid ? entry(i, id0, lp0) : entry(i, __ldcg(a.ids + e0 + i), __ldcg(a.lps + e0 + i));
+    if (key) {
       const uint32_t p = atomicAdd(&sm.count, 1u);
-      if (p < kBGCand) sm.score[p] = s, sm.at[p] = static_cast<uint32_t>(i);
+      if (p < kBGCand) sm.key[p] = key, sm.at[p] = static_cast<uint32_t>(i);
     }
   }
   __syncthreads();
@@ -462,17 +736,17 @@ __global__ void __launch_bounds__(kBLThreads) beam_lists_kernel(const BeamArgs a
     cnt = min(cnt, a.k);
     __syncthreads();
   } else {
-    cnt = take_in_turn(sm, a.k, [&](double& s, uint32_t& at, double last_s, uint32_t last_at) {
-      s = -INFINITY;
+    cnt = take_in_turn(sm, a.k, [&](uint64_t& key, uint32_t& at, uint64_t last, uint32_t last_at) {
+      key = 0;
       at = 0xFFFFFFFFu;
       for (int i = tid; i < total; i += NT) {
-        const double c = entry(i);
+        const uint64_t c = entry(i, __ldcg(a.ids + e0 + i), __ldcg(a.lps + e0 + i));
         const uint32_t e = static_cast<uint32_t>(i);
-        if (c > -INFINITY && before(last_s, last_at, c, e) && before(c, e, s, at)) s = c, at = e;
+        if (c && before(last, last_at, c, e) && before(c, e, key, at)) key = c, at = e;
       }
     });
   }
-  write_results(a, sm, group, cnt, n, [&](uint32_t at, int) { return a.ids[e0 + at]; });
+  write_results(a, sm, group, cnt, n, [&](uint32_t at, int) { return __ldcg(a.ids + e0 + at); });
 }
 
 // ---------------------------------------------------------------------------
@@ -480,18 +754,28 @@ __global__ void __launch_bounds__(kBLThreads) beam_lists_kernel(const BeamArgs a
 // ---------------------------------------------------------------------------
 static size_t align_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-static int beam_slots(int V) { return ((V + kBlock - 1) / kBlock + kBSBlocks - 1) / kBSBlocks; }
+// Spans of a row: of 32 threads' 128 bytes; the workspace is sized for fp32's, the shortest.
+static int beam_spans(int V, int es) { return static_cast<int>((static_cast<int64_t>(V) * es + 4095) / 4096); }
 
 size_t beam_workspace_bytes(int rows, int V) {
   const size_t nblk = (static_cast<size_t>(V) + kBlock - 1) / kBlock;
-  return align_up(static_cast<size_t>(rows) * static_cast<size_t>(beam_slots(V)) * 8) +
-         align_up(static_cast<size_t>(rows) * nblk * 4);
+  const size_t spans = static_cast<size_t>(rows) * static_cast<size_t>(beam_spans(V, 4));
+  return align_up(spans * 8) + align_up(spans * 4) + align_up(static_cast<size_t>(rows) * nblk * 4);
 }
 
 template <typename T>
 static cudaError_t beam_setup_one() {
-  return cudaFuncSetAttribute(beam_choose_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              sizeof(ChoiceSmem<kBGThreads>));
+  cudaError_t e = cudaFuncSetAttribute(beam_choose_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       sizeof(ChoiceSmem<kBGThreads>));
+  for (auto* f : {beam_stream_kernel<T, false>, beam_stream_kernel<T, true>}) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kBSSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  }
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(beam_choose_kernel<T>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  return e;
 }
 
 cudaError_t beam_setup() {
@@ -515,13 +799,20 @@ static BeamArgs beam_args(const BeamCall& c) {
   a.out_parents = c.out_parents;
   a.out_tokens = c.out_tokens;
   a.dev_status = c.dev_status;
+  a.wait_ns = wait_limit_ns();
   return a;
 }
 
 template <typename T>
-static cudaError_t launch_beams(const BeamArgs& a, int groups, cudaStream_t stream) {
+static cudaError_t launch_beams(BeamArgs a, int groups, int num_sms, cudaStream_t stream) {
+  constexpr int64_t per_chunk = kBSChunkBytes / static_cast<int>(sizeof(T));
+  a.chunks = static_cast<int>((a.V + per_chunk - 1) / per_chunk);
+  a.spans = beam_spans(a.V, sizeof(T));
+  const int64_t chunks = static_cast<int64_t>(a.rows) * a.chunks, most = static_cast<int64_t>(num_sms) * kBSCtasPerSm;
+  const dim3 grid(static_cast<unsigned>(chunks < most ? chunks : most));
   trace_begin(kTraceBeamStream, stream);
-  cudaError_t e = launch_kernel(beam_stream_kernel<T>, dim3(a.rows, a.slots), dim3(kBSThreads), 0, stream, true, a);
+  cudaError_t e = launch_kernel(a.mask ? beam_stream_kernel<T, true> : beam_stream_kernel<T, false>, grid, dim3(kBSThreads),
+                                static_cast<size_t>(kBSSmem), stream, true, a);
   trace_end(kTraceBeamStream, stream);
   if (e != cudaSuccess) return e;
   trace_begin(kTraceBeamChoose, stream);
@@ -537,16 +828,19 @@ cudaError_t launch_beam_select(const BeamCall& c, const void* logits, lmh_dtype 
   a.logits = static_cast<const char*>(logits);
   a.row_stride = row_stride;
   a.nblk = (c.V + kBlock - 1) / kBlock;
-  a.slots = beam_slots(c.V);
   a.mask = mask;
   a.mask_words = mask_words;
-  a.part_ms = static_cast<float2*>(workspace);
-  a.bmax = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                    align_up(static_cast<size_t>(a.rows) * static_cast<size_t>(a.slots) * 8));
+  const size_t spans = static_cast<size_t>(a.rows) * static_cast<size_t>(beam_spans(c.V, 4));
+  char* p = static_cast<char*>(workspace);
+  a.part_ms = reinterpret_cast<float2*>(p);
+  p += align_up(spans * 8);
+  a.smax = reinterpret_cast<float*>(p);
+  p += align_up(spans * 4);
+  a.bmax = reinterpret_cast<float*>(p);
   switch (dtype) {
-    case LMH_BF16: return launch_beams<__nv_bfloat16>(a, c.groups, stream);
-    case LMH_F16: return launch_beams<__half>(a, c.groups, stream);
-    default: return launch_beams<float>(a, c.groups, stream);
+    case LMH_BF16: return launch_beams<__nv_bfloat16>(a, c.groups, num_sms, stream);
+    case LMH_F16: return launch_beams<__half>(a, c.groups, num_sms, stream);
+    default: return launch_beams<float>(a, c.groups, num_sms, stream);
   }
 }
 

@@ -49,11 +49,11 @@ __global__ void __launch_bounds__(kRRThreads) reorder_rows_kernel(const __grid_c
     const int row0 = group * B;
     __syncthreads();
     if (tid < B) {
-      const int p = a.parents[row0 + tid];
+      const int p = __ldcg(a.parents + row0 + tid);  // (through L2: the kernel before may have just written them)
       const bool ok = p >= row0 && p < row0 + B;
       if (!ok && p != -1) set_status(a.dev_status, LMH_DS_ROW_IDX_OUT_OF_RANGE);
       parent[tid] = static_cast<int16_t>(ok ? p - row0 : tid);
-      length[tid] = a.lengths ? a.lengths[row0 + tid] : 0x7FFFFFFF;
+      length[tid] = a.lengths ? __ldcg(a.lengths + row0 + tid) : 0x7FFFFFFF;
     }
     __syncthreads();
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
