@@ -70,6 +70,36 @@ def test_in_place_and_out_of_place(lmh, groups, beams, kind):
         assert int(st.item()) == 0
 
 
+@pytest.mark.parametrize("kind", ["swap", "one", "any", "some"])
+@pytest.mark.parametrize("groups,beams", [(1, 1), (3, 4), (5, 3), (1, 33), (1, 128), (40, 2)])
+def test_large_states(lmh, groups, beams, kind):
+    """States that move by bulk copies: positions of 4 and 48 bytes, chunks of odd multiples of 16 bytes, lengths that
+    end inside a slice, before the first position and behind the last."""
+    rows = groups * beams
+    p = _parents(groups, beams, rows + 1, kind)
+    g = torch.Generator("cuda").manual_seed(2)
+    T = (24 << 20) // (4 * rows) // 4 * 4
+    lengths = torch.randint(-2, T + T // 4, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    t = (24 << 20) // (48 * 12 * rows) + 1
+    shorter = torch.clamp(lengths * t // T, max=t + 1)
+    for tensors, dims, along, lens in (
+            ([torch.randint(-99, 99, (rows, T), generator=g, device="cuda", dtype=torch.int32)], [0], [1], lengths),
+            ([torch.randint(-99, 99, (2, 2, rows, 3, t, 24), generator=g, device="cuda", dtype=torch.int16),
+              torch.randint(-99, 99, (3, rows, 4 * t, 8), generator=g, device="cuda", dtype=torch.int16)[:, :, 1:]],
+             [2, 1], [4, None], shorter)):
+        for use in (None, lens):
+            first = [x.clone() for x in tensors]
+            outs = [torch.full_like(x, 7) for x in first]
+            want = [_want(x, o, d, a, p, use) for x, o, d, a in zip(first, outs, dims, along)]
+            st = torch.zeros(1, dtype=torch.int32, device="cuda")
+            got = lmh.reorder_rows(lmh.RowStates(tensors, dims, along, outs), p, beams, lengths=use, dev_status=st)
+            assert all(torch.equal(o, w) for o, w in zip(got, want))
+            want = [_want(x, x, d, a, p, use) for x, d, a in zip(first, dims, along)]
+            lmh.reorder_rows(lmh.RowStates(tensors, dims, along), p, beams, lengths=use, dev_status=st)
+            assert all(torch.equal(x, w) for x, w in zip(tensors, want))
+            assert int(st.item()) == 0
+
+
 def test_neighbours_are_left_alone(lmh):
     """Views in larger tensors: what lies between the rows and behind the positions stays."""
     whole = torch.arange(2 * 8 * 64, dtype=torch.int32, device="cuda").view(2, 8, 64)

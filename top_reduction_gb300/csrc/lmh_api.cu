@@ -716,6 +716,7 @@ lmh_status lmh_reorder_rows(const lmh_row_state* states, int32_t num_states, int
   if (beams > LMH_BEAMS_MAX || static_cast<int64_t>(groups) * beams > INT32_MAX) return LMH_ERR_UNSUPPORTED;
   if (groups == 0 || num_states == 0) return LMH_OK;
   if (!parents) return LMH_ERR_INVALID_ARG;
+  int64_t slices = 0;
   for (int i = 0; i < num_states; ++i) {
     const lmh_row_state& s = states[i];
     if (s.n0 < 0 || s.n1 < 0 || s.chunk_bytes < 0 || s.position_bytes < 0) return LMH_ERR_INVALID_ARG;
@@ -726,8 +727,10 @@ lmh_status lmh_reorder_rows(const lmh_row_state* states, int32_t num_states, int
     if (s.src == s.dst && (s.src_row_bytes != s.dst_row_bytes || s.src_outer_bytes[0] != s.dst_outer_bytes[0] ||
                            s.src_outer_bytes[1] != s.dst_outer_bytes[1]))
       return LMH_ERR_INVALID_ARG;
-    // slices of a chunk are at least 512 bytes, and are counted in 32 bits
-    if (s.chunk_bytes / 512 >= INT32_MAX || static_cast<int64_t>(s.n0) * s.n1 > INT32_MAX) return LMH_ERR_UNSUPPORTED;
+    // slices of a chunk are at least 256 bytes, and are counted in 32 bits
+    if (s.chunk_bytes / 256 >= INT32_MAX || static_cast<int64_t>(s.n0) * s.n1 > INT32_MAX) return LMH_ERR_UNSUPPORTED;
+    slices += static_cast<int64_t>(s.n0) * s.n1 * (s.chunk_bytes / 256 + 1);
+    if (slices > INT32_MAX) return LMH_ERR_UNSUPPORTED;
   }
   int sms = 0;
   if (device_setup(&sms, kStates) != cudaSuccess) return LMH_ERR_CUDA;
