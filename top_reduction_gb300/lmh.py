@@ -645,6 +645,30 @@ class AdapterTable:
         return n
 
 
+_SCRATCH = {}
+_SCRATCH_MOST = 64 << 20
+
+
+def _scratch(nbytes, device, stream):
+    """A workspace for a call on the raw `stream`: one for each stream, whose calls follow one another, kept from
+    call to call (an allocation costs a few microseconds).  While a stream is captured, and for large calls,
+    one of its own: a graph may be replayed beside anything."""
+    if nbytes > _SCRATCH_MOST or torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    key = device.index, stream
+    t = _SCRATCH.get(key)
+    if t is None or t.numel() < nbytes:
+        t = _SCRATCH[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    return t
+
+
+def _own_workspace(t, nbytes, device):
+    """The address of a caller's workspace."""
+    if t.device != device or not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+        raise ValueError("workspace must be contiguous on %s with %d bytes" % (device, nbytes))
+    return t.data_ptr()
+
+
 def _pitch(t, rows, width):
     """The row stride of a [rows, width] tensor whose rows are contiguous."""
     pitch, step = t.stride()
@@ -690,15 +714,11 @@ def add_adapters(x, table, adapter_idx, y, row_idx=None, out=None, workspace=Non
     if rows == 0:
         return out
     need = table.workspace_bytes(rows)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous() or \
-            workspace.numel() * workspace.element_size() < need:
-        raise ValueError("workspace must be contiguous on %s with %d bytes" % (dev, need))
+    raw = _raw_stream(dev)
+    ws = _scratch(need, dev, raw).data_ptr() if workspace is None else _own_workspace(workspace, need, dev)
     st = _lib.lmh_add_adapters(
         x.data_ptr(), _pitch(x, T, H), T, _ptr(row_idx), rows, idx.data_ptr(), table._arg, y.data_ptr(), y_pitch,
-        out.data_ptr(), _DTYPES[y.dtype], out_pitch, workspace.data_ptr(), need, _status_word(dev_status, dev),
-        _raw_stream(dev))
+        out.data_ptr(), _DTYPES[y.dtype], out_pitch, ws, need, _status_word(dev_status, dev), raw)
     if st != OK:
         raise LMHError(st, "lmh_add_adapters")
     return out
@@ -716,15 +736,16 @@ def _beams_arg(scores, beams, k, finished, pad_id, keep_slots, out, rows, dev):
         if isinstance(finished, torch.Tensor) and finished.dtype == torch.bool:
             finished = finished.view(torch.uint8)
         finished = _per_row(finished, torch.uint8, rows, dev, "finished")
-    if out is None:
-        whole = torch.empty((2, groups, k), dtype=torch.int32, device=dev)
-        out = {"scores": torch.empty((groups, k), dtype=torch.float32, device=dev), "parents": whole[0],
-               "tokens": whole[1]}
     n = groups * k
-    arg = BeamsArg(groups, beams, k, 1 if keep_slots else 0, scores.data_ptr(), _ptr(finished), pad_id,
-                   _written(out["scores"], _FLOATS, n, dev, "scores"),
-                   _written(out["parents"], _WORDS, n, dev, "parents"),
-                   _written(out["tokens"], _WORDS, n, dev, "tokens"))
+    if out is None:  # (three allocations: views of one take longer)
+        out = {"scores": torch.empty((groups, k), dtype=torch.float32, device=dev),
+               "parents": torch.empty((groups, k), dtype=torch.int32, device=dev),
+               "tokens": torch.empty((groups, k), dtype=torch.int32, device=dev)}
+        to = out["scores"].data_ptr(), out["parents"].data_ptr(), out["tokens"].data_ptr()
+    else:
+        to = (_written(out["scores"], _FLOATS, n, dev, "scores"), _written(out["parents"], _WORDS, n, dev, "parents"),
+              _written(out["tokens"], _WORDS, n, dev, "tokens"))
+    arg = BeamsArg(groups, beams, k, 1 if keep_slots else 0, scores.data_ptr(), _ptr(finished), pad_id, *to)
     return arg, out, (scores, finished)
 
 
@@ -761,19 +782,17 @@ def beam_select(logits, scores, beams, k=None, finished=None, pad_id=0, mask=Non
     pitch = _pitch(logits, rows, V)
     words = 0
     if mask is not None:
-        mask = torch.as_tensor(mask, device=dev).contiguous()
+        if not (isinstance(mask, torch.Tensor) and mask.device == dev and mask.is_contiguous()):
+            mask = torch.as_tensor(mask, device=dev).contiguous()
         if mask.dtype not in _WORDS or mask.dim() != 2 or mask.shape[0] != rows:
             raise ValueError("mask must be int32 or uint32 [%d, words]" % rows)
         words = mask.shape[1]
     arg, out, kept = _beams_arg(scores, beams, beams if k is None else k, finished, pad_id, keep_slots, out, rows, dev)
     need = beam_workspace_bytes(rows, beams, V)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous() or \
-            workspace.numel() * workspace.element_size() < need:
-        raise ValueError("workspace must be contiguous on %s with %d bytes" % (dev, need))
-    st = _lib.lmh_beam_select(arg, logits.data_ptr(), _DTYPES[logits.dtype], V, pitch, _ptr(mask), words,
-                              workspace.data_ptr(), need, _status_word(dev_status, dev), _raw_stream(dev))
+    raw = _raw_stream(dev)
+    ws = _scratch(need, dev, raw).data_ptr() if workspace is None else _own_workspace(workspace, need, dev)
+    st = _lib.lmh_beam_select(arg, logits.data_ptr(), _DTYPES[logits.dtype], V, pitch, _ptr(mask), words, ws, need,
+                              _status_word(dev_status, dev), raw)
     if st != OK:
         raise LMHError(st, "lmh_beam_select")
     return out
