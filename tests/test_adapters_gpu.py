@@ -76,6 +76,7 @@ def _run(lmh, c, **kw):
 
 @pytest.mark.parametrize("dtype,y_dtype", [(BF16, F32), (BF16, BF16), (F16, F32), (F16, F16)])
 @pytest.mark.parametrize("rows,H,N,R,L", [
+    (300, 64, 520, 8, 70), (513, 128, 1001, 16, 3), (400, 72, 264, 32, 2), (290, 256, 777, 64, 5), (257, 128, 512, 128, 4),
     (1, 8, 1, 8, 1), (1, 2560, 2560, 16, 4), (5, 128, 4096, 8, 3), (7, 1000, 33, 24, 2), (33, 512, 5003, 16, 8),
     (64, 4096, 1001, 32, 48), (70, 264, 640, 64, 1), (100, 1024, 515, 128, 3), (257, 136, 300, 40, 100)])
 def test_against_the_formula(lmh, rows, H, N, R, L, dtype, y_dtype):
@@ -83,7 +84,8 @@ def test_against_the_formula(lmh, rows, H, N, R, L, dtype, y_dtype):
     _check(c, _run(lmh, c))
 
 
-@pytest.mark.parametrize("rows,H,N,R,L", [(9, 256, 700, 16, 4), (40, 512, 333, 64, 12), (200, 128, 96, 128, 6)])
+@pytest.mark.parametrize("rows,H,N,R,L", [(9, 256, 700, 16, 4), (40, 512, 333, 64, 12), (200, 128, 96, 128, 6),
+                                          (333, 96, 400, 64, 9), (600, 64, 260, 16, 5), (260, 64, 264, 128, 5)])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_ranks_and_what_stands_behind_them(lmh, rows, H, N, R, L, dtype):
     c = _case(rows, H, N, R, L, dtype, seed=3, ranks=True, tokens=2 * rows)
@@ -96,7 +98,7 @@ def test_ranks_and_what_stands_behind_them(lmh, rows, H, N, R, L, dtype):
     _check(c, _run(lmh, c))
 
 
-@pytest.mark.parametrize("rows", [1, 31, 32, 33, 64, 500])
+@pytest.mark.parametrize("rows", [1, 8, 9, 31, 32, 33, 64, 65, 256, 257, 500, 17000])
 def test_one_adapter_many_rows(lmh, rows):
     c = _case(rows, 320, 770, 16, 2, seed=rows, none=False)
     c["idx"].fill_(1)
@@ -104,10 +106,14 @@ def test_one_adapter_many_rows(lmh, rows):
     _check(c, _run(lmh, c))
 
 
-def test_no_row_has_an_adapter(lmh):
-    c = _case(50, 128, 100, 8, 2)
+@pytest.mark.parametrize("rows", [50, 700])
+def test_no_row_has_an_adapter(lmh, rows):
+    c = _case(rows, 128, 100, 8, 2)
     c["idx"].fill_(-1)
     assert torch.equal(_run(lmh, c), c["y"])
+    y = c["y"].clone()
+    _run(lmh, dict(c, y=y), out=y)
+    assert torch.equal(y, c["y"])
 
 
 def test_long_packed_prompts(lmh):
@@ -129,11 +135,12 @@ def test_whole_numbers_are_exact(lmh):
         assert torch.equal(_run(lmh, c).double(), _formula(c)[0])
 
 
-def test_strides_alignment_and_in_place(lmh):
-    c = _case(21, 264, 99, 24, 5, seed=4)
-    big_x = torch.zeros(21, 271, dtype=BF16, device="cuda")
+@pytest.mark.parametrize("rows", [21, 290])
+def test_strides_alignment_and_in_place(lmh, rows):
+    c = _case(rows, 264, 99, 24, 5, seed=4)
+    big_x = torch.zeros(rows, 271, dtype=BF16, device="cuda")
     big_x[:, 3:267] = c["x"]
-    big_y = torch.zeros(21, 103, device="cuda")
+    big_y = torch.zeros(rows, 103, device="cuda")
     big_y[:, 2:101] = c["y"]
     down = torch.zeros(5, 30, 280, dtype=BF16, device="cuda")[:, 2:26, 8:272]
     up = torch.zeros(7, 99, 40, dtype=BF16, device="cuda")[1:6, :, 8:32]
@@ -141,7 +148,7 @@ def test_strides_alignment_and_in_place(lmh):
     want = _run(lmh, c)
     s = dict(c, x=big_x[:, 3:267], down=down, up=up, y=big_y[:, 2:101])
     assert torch.equal(_run(lmh, s), want)
-    out = torch.full((21, 110), 7.0, device="cuda")
+    out = torch.full((rows, 110), 7.0, device="cuda")
     assert torch.equal(_run(lmh, s, out=out[:, 5:104]), want)
     assert (out[:, :5] == 7).all() and (out[:, 104:] == 7).all()
     assert _run(lmh, s, out=s["y"]) is s["y"]
@@ -195,10 +202,11 @@ def test_large_small_and_infinite_values(lmh, dtype):
     assert torch.equal(got[others], plain[others])
 
 
-def test_a_rows_result_does_not_depend_on_its_batch(lmh):
-    c = _case(80, 512, 300, 32, 7, seed=6)
+@pytest.mark.parametrize("rows", [80, 400])
+def test_a_rows_result_does_not_depend_on_its_place(lmh, rows):
+    c = _case(rows, 512, 300, 32, 7, seed=6)
     whole = _run(lmh, c)
-    perm = torch.randperm(80, generator=torch.Generator().manual_seed(0)).cuda()
+    perm = torch.randperm(rows, generator=torch.Generator().manual_seed(0)).cuda()
     again = _run(lmh, dict(c, x=c["x"][perm], idx=c["idx"][perm], y=c["y"][perm]))
     assert torch.equal(again, whole[perm])
 

@@ -23,18 +23,31 @@ __global__ void __launch_bounds__(kADPlanThreads) adapter_plan_kernel(const Adap
   if (tid < 2) carry[tid] = 0;
   __syncthreads();
   bool bad = false;
-  auto slot = [&](int i) {  // -1 behind the last row
-    if (i >= a.rows) return -1;
-    const int l = __ldcg(a.adapter_idx + i);
-    if (l >= 0 && l < L) return l;
-    bad |= l != -1;
-    return L;
+  constexpr int HELD = 16;  // rows a thread looks up at once
+  // f(row, slot) for every row, a warp's lanes together; slot -1 behind the last
+  auto for_rows = [&](auto f) {
+    for (int base = 0; base < a.rows; base += HELD * kADPlanThreads) {
+      int l[HELD];
+#pragma unroll
+      for (int u = 0; u < HELD; ++u) {
+        const int i = base + u * kADPlanThreads + tid;
+        l[u] = i < a.rows ? __ldcg(a.adapter_idx + i) : -2;
+      }
+#pragma unroll
+      for (int u = 0; u < HELD; ++u) {
+        if (base + u * kADPlanThreads >= a.rows) break;
+        const bool in = l[u] >= 0 && l[u] < L;
+        bad |= !in && l[u] != -1 && l[u] != -2;
+        const int i = base + u * kADPlanThreads + tid;
+        bad |= l[u] == -2 && i < a.rows;
+        f(i, i >= a.rows ? -1 : in ? l[u] : L);
+      }
+    }
   };
-  for (int base = 0; base < a.rows; base += kADPlanThreads) {
-    const int l = slot(base + tid);
+  for_rows([&](int, int l) {
     const unsigned same = __match_any_sync(0xffffffffu, l);
     if (l >= 0 && lane == __ffs(same) - 1) atomicAdd(&next[l], __popc(same));
-  }
+  });
   __syncthreads();
   // exclusive sums of rows and of tiles over the adapters
   for (int base = 0; base <= L; base += kADPlanThreads) {
@@ -76,15 +89,14 @@ __global__ void __launch_bounds__(kADPlanThreads) adapter_plan_kernel(const Adap
     a.tiles[t] = AdapterTile{lo < L ? lo : -1, at, min(kADTile, end - at), 0};
   }
   __syncthreads();
-  for (int base = 0; base < a.rows; base += kADPlanThreads) {
-    const int l = slot(base + tid);
+  for_rows([&](int i, int l) {
     const unsigned same = __match_any_sync(0xffffffffu, l);
     const int leader = __ffs(same) - 1;
     int at = 0;
     if (l >= 0 && lane == leader) at = atomicAdd(&next[l], __popc(same));
     at = __shfl_sync(0xffffffffu, at, leader);
-    if (l >= 0) a.order[at + __popc(same & ((1u << lane) - 1))] = base + tid;
-  }
+    if (l >= 0) a.order[at + __popc(same & ((1u << lane) - 1))] = i;
+  });
   if (bad) set_status(a.dev_status, LMH_DS_ADAPTER_OUT_OF_RANGE);
 }
 
@@ -145,10 +157,10 @@ static cudaError_t launch_adapters(const AdapterArgs& a, bool bf16, lmh_dtype ou
   return e;
 }
 
-// Whether rows of y or out can be read and written a lane's neighbours at a time (16 bytes; 8 of 16-bit outputs at
-// ranks above 32).
-static bool adapter_rows_align(const void* p, int64_t stride, int N, lmh_dtype dtype, int rank) {
-  const int n = 4, bytes = dtype == LMH_F32 ? 16 : 2 * n;
+// Whether rows of y or out can be read and written a lane's neighbours at a time (16 bytes, or four 16-bit outputs in
+// calls of few rows).
+static bool adapter_rows_align(const void* p, int64_t stride, int N, lmh_dtype dtype, int rows) {
+  const int n = dtype != LMH_F32 && rows > kADOwnPlan ? 8 : 4, bytes = n * (dtype == LMH_F32 ? 4 : 2);
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride % n == 0 && N % n == 0;
 }
 
@@ -181,8 +193,8 @@ cudaError_t launch_add_adapters(const void* x, int64_t x_stride, int num_tokens,
   a.out = static_cast<char*>(out);
   a.out_stride = out_stride;
   a.in_place = y == out && y_stride == out_stride;
-  const bool vec = adapter_rows_align(y, y_stride, t.N, out_dtype, t.rank) &&
-                   adapter_rows_align(out, out_stride, t.N, out_dtype, t.rank);
+  const bool vec = adapter_rows_align(y, y_stride, t.N, out_dtype, rows) &&
+                   adapter_rows_align(out, out_stride, t.N, out_dtype, rows);
   a.splits = adapter_splits(rows, t.count, t.H, num_sms);
   char* p = static_cast<char*>(workspace);
   a.tile_count = reinterpret_cast<int32_t*>(p);

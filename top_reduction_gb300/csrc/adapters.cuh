@@ -813,6 +813,300 @@ __global__ void __launch_bounds__(32 * up_warps(KS), 1) adapter_up_kernel(const 
 }
 
 // ---------------------------------------------------------------------------
+// second product, calls of many rows
+// ---------------------------------------------------------------------------
+// Here the batch's rows are the MMA's A operand (16 a warp, held in registers for a whole tile) and 8 rows of the
+// weights the B operand.  A lane's part of d and its two rows of y and out stay the same from step to step, which
+// leaves about a fifth of the instructions of the kernel above per output (packed prompts, 16384 rows of rank 64 x
+// 4096: 108 us there).  The weights come in stages of kADWideStage outputs that the whole CTA copies and reads;
+// warps share a stage by rows (one for every 16 of the tile's) and by outputs.  A block is 32 outputs; column c of
+// its tile j stands for output 8 (c / 2) + 2 j + c % 2, so that a lane has eight neighbours of a row.
+constexpr int kADWideThreads = 256;
+constexpr int kADWideWarps = kADWideThreads / 32;
+constexpr int kADWideStage = 256;  // outputs
+constexpr int kADWideStages = 3;
+constexpr int wide_stage_bytes(int ks) { return kADWideStage * 32 * ks; }
+// 64-row tiles, 8 warps: a warp takes up to four blocks of a stage
+constexpr int kADWideBlocks = 4;
+
+// Eight neighbouring outputs of a row.
+template <typename Y, bool VEC>
+struct Eight {
+  static constexpr int ES = static_cast<int>(sizeof(Y));
+  static constexpr int WORDS = VEC ? ES * 2 : 1;  // (not VEC: read where they are used)
+  uint32_t w[WORDS];
+  // Outputs n .. n + 7 of the row at `row`; pieces that are not below `end` are read from its start.
+  __device__ __forceinline__ void load(const char* row, int n, int end) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int p = 0; p < ES / 2; ++p) {
+        const int at = n + p * (16 / ES);
+        const uint4 v = *reinterpret_cast<const uint4*>(row + static_cast<int64_t>(at < end ? at : 0) * ES);
+        w[4 * p] = v.x, w[4 * p + 1] = v.y, w[4 * p + 2] = v.z, w[4 * p + 3] = v.w;
+      }
+    }
+  }
+  // outputs e = 2 j, 2 j + 1: acc[j][0], acc[j][1] times `by`, added
+  __device__ __forceinline__ void add_and_store(const char* y_row, char* row, int left, const float (&d)[8], float by) const {
+    if constexpr (VEC && ES == 4) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        if (left > 4 * p)
+          *reinterpret_cast<float4*>(row + 16 * p) =
+              make_float4(fmaf(d[4 * p], by, __uint_as_float(w[4 * p])), fmaf(d[4 * p + 1], by, __uint_as_float(w[4 * p + 1])),
+                          fmaf(d[4 * p + 2], by, __uint_as_float(w[4 * p + 2])), fmaf(d[4 * p + 3], by, __uint_as_float(w[4 * p + 3])));
+    } else if constexpr (VEC) {
+      using C = Half16<Y>;
+      uint32_t r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = C::pair(w[i]);
+        r[i] = C::pack(fmaf(d[2 * i], by, v.x), fmaf(d[2 * i + 1], by, v.y));
+      }
+      if (left > 0) *reinterpret_cast<uint4*>(row) = make_uint4(r[0], r[1], r[2], r[3]);
+    } else if constexpr (ES == 4) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = e < left ? reinterpret_cast<const float*>(y_row)[e] : 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) reinterpret_cast<float*>(row)[e] = fmaf(d[e], by, v[e]);
+    } else {
+      using C = Half16<Y>;
+      uint16_t v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = e < left ? reinterpret_cast<const uint16_t*>(y_row)[e] : 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) reinterpret_cast<uint16_t*>(row)[e] = C::bits(fmaf(d[e], by, C::value(v[e])));
+    }
+  }
+};
+
+constexpr int wide_ctas(int ks, int es) { return ks <= 4 && es == 2 ? 2 : 1; }
+
+template <typename T, typename Y, int KS, bool VEC>
+__global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y))) adapter_wide_kernel(const AdapterArgs a) {
+  extern __shared__ __align__(128) unsigned char wide_ring[];
+  __shared__ TileSmem ts;
+  constexpr bool LO = sizeof(Y) == 4;
+  constexpr int ES = static_cast<int>(sizeof(Y)), CH = 2 * KS, S = kADWideStages;
+  constexpr int ROWS = kADWideThreads / CH;  // weight rows that the CTA copies at a time
+  using E8 = Eight<Y, VEC>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  // (as in the kernel above: all but d was complete before this kernel started)
+  TileFinder finder;
+  const int n_tiles = finder.start(a, ts);
+  const int64_t stages = (a.N + kADWideStage - 1) / kADWideStage;
+  const int64_t all = stages * n_tiles;
+  int64_t at = all * blockIdx.x / gridDim.x;
+  const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
+  // where a weight row's piece stands in a stage: whole sectors, and the eight rows of a matrix two to a bank
+  auto place = [](int row, int c) { return (row * (32 * KS) + c * 16) ^ (((row >> 3) & 3) << 5); };
+  bool waited = false;
+  while (at < end) {
+    const int ti = static_cast<int>(at / stages);
+    const int s0 = static_cast<int>(at - ti * stages), s1 = static_cast<int>(min(stages, s0 + (end - at)));
+    at += s1 - s0;
+    finder.take(a, ts, ti);
+    const int count = ts.count, rank = adapter_rank(a, ts.adapter);
+    const int rg = count <= 16 ? 1 : count <= 32 ? 2 : 4, ng = kADWideWarps / rg;  // warps by rows and by outputs
+    const int row0 = (warp % rg) * 16 + g;
+    const int blocks = 8 / ng, first_block = warp / rg * blocks;  // of a stage, the warp's: neighbours
+    const bool have[2] = {row0 < count, row0 + 8 < count};
+    const int row[2] = {ts.rows[have[0] ? row0 : 0], ts.rows[have[1] ? row0 + 8 : 0]};
+    const char* y[2];
+    char* out[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      y[u] = a.y + (row[u] * a.y_stride + 8 * t) * ES;
+      out[u] = a.out + (row[u] * a.out_stride + 8 * t) * ES;
+    }
+    const T* up = reinterpret_cast<const T*>(a.up) + static_cast<int64_t>(max(ts.adapter, 0)) * a.up_adapter;
+    auto issue = [&](int st) {
+      if (st < s1 && rank > 0) {
+        const int n0 = st * kADWideStage;
+        const uint32_t to = smem_u32(wide_ring) + (st - s0) % S * wide_stage_bytes(KS);
+        const int c = tid % CH;
+        const T* p = up + (n0 + tid / CH) * a.up_row + c * 8;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int r = tid / CH + i * ROWS;
+          lane_copy_if<16>(c * 8 < rank && n0 + r < a.N, to + place(r, c), p);
+          p += ROWS * a.up_row;
+        }
+      }
+      lane_copies_end();
+    };
+    for (int i = 0; i < S - 1; ++i) issue(s0 + i);
+    if (!waited) pdl_wait();
+    waited = true;
+
+    // ---- the lane's part of d: rows row0 and row0 + 8, entries 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of every 16 ----
+    const float scale = ts.adapter < 0 ? 0.0f : a.scales ? __ldcg(a.scales + ts.adapter) : 1.0f;
+    uint32_t hi[KS][4], lo[LO ? KS : 1][4];
+    float back[2] = {1.0f, 1.0f};
+    {
+      float v[2][KS][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float most = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = ks * 16 + h * 8 + 2 * t;
+            float2 s = make_float2(0.0f, 0.0f);
+            if (have[u] && r < rank) {  // (r is even, a.R a multiple of 8)
+              const float* d = a.d + static_cast<int64_t>(row[u]) * a.R + r;
+              for (int i = 0; i < a.splits; ++i) {
+                const float2 p = __ldcg(reinterpret_cast<const float2*>(d + static_cast<int64_t>(i) * a.rows * a.R));
+                s.x += p.x, s.y += p.y;
+              }
+            }
+            v[u][ks][2 * h] = s.x * scale;
+            v[u][ks][2 * h + 1] = r + 1 < rank ? s.y * scale : 0.0f;
+            most = fmaxf(most, fmaxf(fabsf(v[u][ks][2 * h]), fabsf(v[u][ks][2 * h + 1])));
+          }
+        if constexpr (std::is_same<T, __half>::value) {
+          // f16: the row's largest value goes into [2^13, 2^14), which is exact
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+          if (most > 0.0f && most < INFINITY) {
+            const int e = min(max(ilogbf(most), -112), 127);
+            back[u] = ldexpf(1.0f, e - 13);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) v[u][ks][q] *= ldexpf(1.0f, 13 - e);
+          }
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {  // registers (row, k), (row + 8, k), (row, k + 8), (row + 8, k + 8)
+          const float x0 = v[q & 1][ks][(q >> 1) * 2], x1 = v[q & 1][ks][(q >> 1) * 2 + 1];
+          hi[ks][q] = Half16<T>::pack(x0, x1);
+          if constexpr (LO) {
+            const float2 b = Half16<T>::pair(hi[ks][q]);
+            lo[ks][q] = Half16<T>::pack(fabsf(b.x) < INFINITY ? x0 - b.x : 0.0f, fabsf(b.y) < INFINITY ? x1 - b.y : 0.0f);
+          }
+        }
+    }
+    // a rank that ends inside a step's 16 entries: the words of its two pieces that count
+    const int rest = rank % 16 - 2 * t;
+    const uint32_t keep0 = rank % 16 == 0 || rest >= 2 ? ~0u : rest == 1 ? 0xFFFFu : 0u;
+    const uint32_t keep1 = rank % 16 == 0 || rest >= 10 ? ~0u : rest == 9 ? 0xFFFFu : 0u;
+
+    const int last = rank % 16 != 0 ? rank / 16 : -1;  // the step of 16 entries that is cut
+
+    // lane 8 i + c gives the row of matrix i that column c stands for; its place in a stage's first block (tile j: 64 KS
+    // bytes further on, block b: 1024 KS; KS 1: matrices of two tiles' two pieces, else of a tile's four of 32 entries)
+    const int mc = lane & 7, mi = lane >> 3, mrow = 8 * (mc >> 1) + (mc & 1);
+    uint32_t from[KS == 1 ? 1 : KS / 2];
+    if constexpr (KS == 1) {
+      from[0] = place(mrow + 2 * (mi >> 1), mi & 1);
+    } else {
+#pragma unroll
+      for (int kp = 0; kp < KS / 2; ++kp) from[kp] = place(mrow, 4 * kp + mi);
+    }
+
+    // y of a stage; a block's is replaced by the next stage's as soon as it is used.  No branch and no condition, so
+    // that nothing waits for it before its use: rows that are not there have the first one's address, outputs behind
+    // the row's end and stages behind the last the row's start.
+    E8 v[kADWideBlocks][2];
+    auto load_block = [&](int st, int b) {
+      const int n = st * kADWideStage + (first_block + b) * 32;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) v[b][u].load(y[u] - 8 * t * ES, n + 8 * t, st < s1 ? a.N : 0);
+    };
+    // FULL: the stage's outputs are all the row's.  ALL: the rank is the whole of the KS steps.
+    auto work = [&](int st, auto full_const, auto all_const) {
+      constexpr bool FULL = decltype(full_const)::value, ALL = decltype(all_const)::value;
+      const uint32_t stage = smem_u32(wide_ring) + (st - s0) % S * wide_stage_bytes(KS);
+#pragma unroll
+      for (int b = 0; b < kADWideBlocks; ++b) {
+        if (b >= blocks) break;
+        const int block = first_block + b, n = st * kADWideStage + block * 32;
+        const uint32_t bs = stage + block * (1024 * KS);
+        float acc[4][4];
+        if constexpr (!ALL) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+        }
+        auto multiply = [&](int j, int ks, uint32_t b0, uint32_t b1) {
+          if (ALL && ks == 0) mma16_first<T>(acc[j], hi[0], b0, b1);
+          else mma16<T>(acc[j], hi[ks], b0, b1);
+          if constexpr (LO) mma16<T>(acc[j], lo[ks], b0, b1);
+        };
+        if constexpr (KS == 1) {
+          if (ALL || rank > 0) {
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              uint32_t w[4];
+              load_matrices(w, bs + from[0] + j * 64);
+              if constexpr (!ALL) w[0] &= keep0, w[1] &= keep1, w[2] &= keep0, w[3] &= keep1;
+              multiply(j, 0, w[0], w[1]);
+              multiply(j + 1, 0, w[2], w[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int kp = 0; kp < KS / 2; ++kp) {
+            if (!ALL && kp * 32 >= rank) break;
+            const bool both = ALL || kp * 32 + 16 < rank;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+              load_matrices(w, bs + from[kp] + j * (64 * KS));
+              if (!ALL && last == 2 * kp) w[0] &= keep0, w[1] &= keep1;
+              multiply(j, 2 * kp, w[0], w[1]);
+              if (both) {
+                if (!ALL && last == 2 * kp + 1) w[2] &= keep0, w[3] &= keep1;
+                multiply(j, 2 * kp + 1, w[2], w[3]);
+              }
+            }
+          }
+        }
+        const int left = FULL ? 8 : a.N - n - 8 * t;
+        const int64_t off = static_cast<int64_t>(n) * ES;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float dv[8] = {acc[0][2 * u], acc[0][2 * u + 1], acc[1][2 * u], acc[1][2 * u + 1],
+                               acc[2][2 * u], acc[2][2 * u + 1], acc[3][2 * u], acc[3][2 * u + 1]};
+          if (have[u]) v[b][u].add_and_store(y[u] + off, out[u] + off, left, dv, back[u]);
+        }
+        if constexpr (FULL) load_block(st + 1, b);
+      }
+    };
+    auto begin = [&](int st) {
+      lane_copies_wait<S - 2>();
+      __syncthreads();  // the stage is there, and the one before it has been read
+      issue(st + S - 1);
+    };
+#pragma unroll
+    for (int b = 0; b < kADWideBlocks; ++b)
+      if (b < blocks) load_block(s0, b);
+    const int whole = min(s1, a.N / kADWideStage);
+#pragma unroll 1
+    for (int st = s0; st < whole; ++st) {
+      begin(st);
+      if (rank == 16 * KS) work(st, std::true_type{}, std::true_type{});
+      else work(st, std::true_type{}, std::false_type{});
+    }
+    if (whole < s1) {  // the row's last stage is a part of one
+      begin(s1 - 1);
+      work(s1 - 1, std::false_type{}, std::false_type{});
+    }
+    lane_copies_wait<0>();
+  }
+  if (!waited) pdl_wait();
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 template <typename T, int RT>
@@ -827,9 +1121,19 @@ cudaError_t up_setup() {
                               up_warps(KS) * up_warp_bytes(KS, sizeof(Y)));
 }
 
+template <typename T, typename Y, int KS, bool VEC>
+cudaError_t wide_setup() {
+  return cudaFuncSetAttribute(adapter_wide_kernel<T, Y, KS, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kADWideStages * wide_stage_bytes(KS));
+}
+
 template <typename T, typename Y, bool VEC>
 cudaError_t up_setup_of() {
-  cudaError_t e = up_setup<T, Y, 1, VEC>();
+  cudaError_t e = wide_setup<T, Y, 1, VEC>();
+  if (e == cudaSuccess) e = wide_setup<T, Y, 2, VEC>();
+  if (e == cudaSuccess) e = wide_setup<T, Y, 4, VEC>();
+  if (e == cudaSuccess) e = wide_setup<T, Y, 8, VEC>();
+  if (e == cudaSuccess) e = up_setup<T, Y, 1, VEC>();
   if (e == cudaSuccess) e = up_setup<T, Y, 2, VEC>();
   if (e == cudaSuccess) e = up_setup<T, Y, 4, VEC>();
   if (e == cudaSuccess) e = up_setup<T, Y, 8, VEC>();
@@ -860,6 +1164,12 @@ cudaError_t launch_down(const AdapterArgs& a, int grid, cudaStream_t stream) {
 
 template <typename T, typename Y, int KS, bool VEC>
 cudaError_t launch_up_ks(const AdapterArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
+  if (a.rows > kADOwnPlan) {
+    const int64_t most = static_cast<int64_t>(num_sms) * wide_ctas(KS, sizeof(Y));
+    const int64_t stages = max_tiles * ((a.N + kADWideStage - 1) / kADWideStage);
+    return launch_kernel(adapter_wide_kernel<T, Y, KS, VEC>, dim3(static_cast<unsigned>(stages < most ? stages : most)),
+                         dim3(kADWideThreads), static_cast<size_t>(kADWideStages * wide_stage_bytes(KS)), stream, true, a);
+  }
   constexpr int STEP = kADStep;
   const int64_t max_steps = max_tiles * ((a.N + STEP - 1) / STEP);
   const int64_t most = num_sms;  // one wave
