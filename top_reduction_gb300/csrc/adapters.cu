@@ -44,8 +44,12 @@ __global__ void __launch_bounds__(kADPlanThreads) adapter_plan_kernel(const Adap
       }
     }
   };
+  // The lanes with the same slot.  Packed prompts hand a warp rows of one adapter, which is seen at once.
+  auto same_slot = [&](int l) {
+    return __all_sync(0xffffffffu, l == __shfl_sync(0xffffffffu, l, 0)) ? 0xffffffffu : __match_any_sync(0xffffffffu, l);
+  };
   for_rows([&](int, int l) {
-    const unsigned same = __match_any_sync(0xffffffffu, l);
+    const unsigned same = same_slot(l);
     if (l >= 0 && lane == __ffs(same) - 1) atomicAdd(&next[l], __popc(same));
   });
   __syncthreads();
@@ -90,7 +94,7 @@ __global__ void __launch_bounds__(kADPlanThreads) adapter_plan_kernel(const Adap
   }
   __syncthreads();
   for_rows([&](int i, int l) {
-    const unsigned same = __match_any_sync(0xffffffffu, l);
+    const unsigned same = same_slot(l);
     const int leader = __ffs(same) - 1;
     int at = 0;
     if (l >= 0 && lane == leader) at = atomicAdd(&next[l], __popc(same));
@@ -108,6 +112,7 @@ static size_t align_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255);
 // Shares of H of the first product: enough CTAs for the GPU when the tiles are few, each with
 // work for its warps.
 static int adapter_splits(int rows, int count, int H, int num_sms) {
+  if (rows > kADOwnPlan) return 1;
   const int blocks = (H + 31) / 32;
   const int64_t tiles = static_cast<int64_t>((rows + kADTile - 1) / kADTile) + (rows < count ? rows : count);
   int64_t s = num_sms / (tiles > 0 ? tiles : 1);

@@ -399,6 +399,146 @@ __global__ void __launch_bounds__(kADThreads) adapter_down_kernel(const AdapterA
 }
 
 // ---------------------------------------------------------------------------
+// first product, calls of many rows
+// ---------------------------------------------------------------------------
+// The batch's rows are the MMA's A operand, 16 a warp, and 8 adapter rows the B operand: the tile's four row groups
+// share the weights, which come in stages of 128 entries of H that the whole CTA copies; two warps share a row group
+// by entries of H.  As above a lane takes 16 contiguous bytes of a row for two steps of 16, so the operands need no
+// transposition: a lane's registers of x are its own loads, a stage ahead.
+constexpr int kADDownStage = 128;  // entries of H: four blocks of 32
+constexpr int kADDownStages = 3;
+constexpr int down_wide_stage_bytes(int rt) { return rt * 16 * kADDownStage * 2; }
+constexpr int down_wide_smem(int rt) {
+  const int ring = kADDownStages * down_wide_stage_bytes(rt), sums = 4 * 16 * (rt * 16 + 4) * 4;
+  return ring > sums ? ring : sums;
+}
+
+template <typename T, int RT>
+__global__ void __launch_bounds__(kADThreads, RT <= 4 ? 2 : 1) adapter_down_wide_kernel(const AdapterArgs a) {
+  extern __shared__ __align__(128) unsigned char dw_ring[];  // [stages][block of 32][adapter row][64 bytes]
+  __shared__ TileSmem ts;
+  constexpr int S = kADDownStages, NT = 2 * RT;  // NT: tiles of 8 adapter rows
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int rgroup = warp & 3, half = warp >> 2;  // half: blocks 2 half, 2 half + 1 of a stage
+  pdl_wait();
+  pdl_launch_dependents();
+  TileFinder finder;
+  const int n_tiles = finder.start(a, ts);
+  const int stages = (a.H + kADDownStage - 1) / kADDownStage;
+  for (int ti = blockIdx.x; ti < n_tiles; ti += gridDim.x) {
+    finder.take(a, ts, ti);
+    if (ts.adapter < 0) continue;  // (uniform)
+    const int count = ts.count, rank = adapter_rank(a, ts.adapter);
+    const T* down = reinterpret_cast<const T*>(a.down) + static_cast<int64_t>(ts.adapter) * a.down_adapter;
+    auto issue = [&](int st) {
+      if (st < stages) {
+        // pieces of 16 bytes: 16 of an adapter row's 128 entries
+        const int c = tid % 16, h = st * kADDownStage + c * 8;
+        const uint32_t to = smem_u32(dw_ring) + st % S * down_wide_stage_bytes(RT) + (c / 4) * (RT * 16 * 64) + (c % 4) * 16;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const int r = tid / 16 + i * 16;
+          lane_copy_if<16>(r < rank && h < a.H, to + r * 64, down + r * a.down_row + h);
+        }
+      }
+      lane_copies_end();
+    };
+    for (int i = 0; i < S - 1; ++i) issue(i);
+    const char* x[2];
+    bool have[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = rgroup * 16 + u * 8 + g;
+      int tk = -1;
+      if (i < count) {
+        tk = a.row_idx ? __ldcg(a.row_idx + ts.rows[i]) : ts.rows[i];
+        if (tk < 0 || tk >= a.num_tokens) {
+          tk = -1;  // reads zeros
+          set_status(a.dev_status, LMH_DS_ROW_IDX_OUT_OF_RANGE);
+        }
+      }
+      have[u] = tk >= 0;
+      x[u] = a.x + (static_cast<int64_t>(max(tk, 0)) * a.x_stride + t * 8) * 2;
+    }
+    uint4 xv[2][2];  // [block][row], of the stage to come
+    auto load_x = [&](int st) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int h = st * kADDownStage + (half * 2 + b) * 32;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          xv[b][u] = make_uint4(0, 0, 0, 0);
+          if (!have[u] || h + t * 8 >= a.H) continue;
+          const char* p = x[u] + static_cast<int64_t>(h) * 2;
+          if (a.x_vec) {
+            xv[b][u] = __ldcg(reinterpret_cast<const uint4*>(p));
+          } else {
+            const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
+            xv[b][u] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+          }
+        }
+      }
+    };
+    float acc[NT][4] = {};
+    load_x(0);
+    const bool work = rgroup * 16 < count;
+    for (int st = 0; st < stages; ++st) {
+      uint4 xc[2][2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) xc[b][u] = xv[b][u];
+      load_x(st + 1);  // (behind H: zeros)
+      lane_copies_wait<S - 2>();
+      __syncthreads();  // the stage is there, and the one before it has been read
+      issue(st + S - 1);
+      if (!work) continue;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int block = half * 2 + b;
+        const bool in = st * kADDownStage + block * 32 + t * 8 < a.H;
+        const unsigned char* w = dw_ring + st % S * down_wide_stage_bytes(RT) + block * (RT * 16 * 64) + g * 64 + t * 16;
+        const uint32_t a0[4] = {xc[b][0].x, xc[b][1].x, xc[b][0].y, xc[b][1].y};
+        const uint32_t a1[4] = {xc[b][0].z, xc[b][1].z, xc[b][0].w, xc[b][1].w};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (n * 8 >= rank) break;
+          uint4 v = *reinterpret_cast<const uint4*>(w + n * (8 * 64));
+          if (!in || n * 8 + g >= rank) v = make_uint4(0, 0, 0, 0);  // (not copied)
+          mma16<T>(acc[n], a0, v.x, v.y);
+          mma16<T>(acc[n], a1, v.z, v.w);
+        }
+      }
+    }
+    lane_copies_wait<0>();
+    __syncthreads();  // the ring is done with
+    // the halves' sums meet in shared memory: [row group][16 rows][RT * 16, and 4 so that rows differ in bank]
+    constexpr int PITCH = RT * 16 + 4;
+    float* sums = reinterpret_cast<float*>(dw_ring) + rgroup * (16 * PITCH);
+    if (half == 1)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          *reinterpret_cast<float2*>(sums + (g + 8 * u) * PITCH + n * 8 + 2 * t) = make_float2(acc[n][2 * u], acc[n][2 * u + 1]);
+    __syncthreads();
+    if (half == 0)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = rgroup * 16 + u * 8 + g;
+        if (i >= count) continue;
+        float* d = a.d + static_cast<int64_t>(ts.rows[i]) * a.R;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (n * 8 >= a.R) break;
+          const float2 s = *reinterpret_cast<const float2*>(sums + (g + 8 * u) * PITCH + n * 8 + 2 * t);
+          *reinterpret_cast<float2*>(d + n * 8 + 2 * t) = make_float2(acc[n][2 * u] + s.x, acc[n][2 * u + 1] + s.y);
+        }
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // second product, added to y
 // ---------------------------------------------------------------------------
 // The four outputs of one row that a lane holds of a step of 32: output(g, e), e = 0..3.  VEC: neighbours, read and
@@ -1111,6 +1251,9 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y))) adap
 // ---------------------------------------------------------------------------
 template <typename T, int RT>
 cudaError_t down_setup() {
+  const cudaError_t e = cudaFuncSetAttribute(adapter_down_wide_kernel<T, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             down_wide_smem(RT));
+  if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(adapter_down_kernel<T, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               adapter_down_smem(RT));
 }
@@ -1153,13 +1296,21 @@ cudaError_t adapters_setup_one() {
   return e;
 }
 
+template <typename T, int RT>
+cudaError_t launch_down_rt(const AdapterArgs& a, int grid, cudaStream_t stream) {
+  if (a.rows > kADOwnPlan)
+    return launch_kernel(adapter_down_wide_kernel<T, RT>, dim3(grid), dim3(kADThreads),
+                         static_cast<size_t>(down_wide_smem(RT)), stream, true, a);
+  return launch_kernel(adapter_down_kernel<T, RT>, dim3(grid, a.splits), dim3(kADThreads),
+                       static_cast<size_t>(adapter_down_smem(RT)), stream, true, a);
+}
+
 template <typename T>
 cudaError_t launch_down(const AdapterArgs& a, int grid, cudaStream_t stream) {
-  const dim3 g(grid, a.splits), b(kADThreads);
-  if (a.R <= 16) return launch_kernel(adapter_down_kernel<T, 1>, g, b, static_cast<size_t>(adapter_down_smem(1)), stream, true, a);
-  if (a.R <= 32) return launch_kernel(adapter_down_kernel<T, 2>, g, b, static_cast<size_t>(adapter_down_smem(2)), stream, true, a);
-  if (a.R <= 64) return launch_kernel(adapter_down_kernel<T, 4>, g, b, static_cast<size_t>(adapter_down_smem(4)), stream, true, a);
-  return launch_kernel(adapter_down_kernel<T, 8>, g, b, static_cast<size_t>(adapter_down_smem(8)), stream, true, a);
+  if (a.R <= 16) return launch_down_rt<T, 1>(a, grid, stream);
+  if (a.R <= 32) return launch_down_rt<T, 2>(a, grid, stream);
+  if (a.R <= 64) return launch_down_rt<T, 4>(a, grid, stream);
+  return launch_down_rt<T, 8>(a, grid, stream);
 }
 
 template <typename T, typename Y, int KS, bool VEC>
