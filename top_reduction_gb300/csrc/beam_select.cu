@@ -11,7 +11,8 @@
 //   * beam_stream_kernel reads every logit once (persistent CTAs, bulk copies into a ring, a
 //     thread 128 bytes): the largest allowed logit of every block of 64 and of every span of
 //     32 threads, and the span's (max, sum of exponentials) go to the workspace.
-//   * beam_choose_kernel, one CTA a group: the rows' lse from the spans' pairs; a bound t that at
+//   * beam_choose_kernel, one CTA a group (its code runs once, so it is kept short: what is used more than once is
+//     called, not inlined; with everything inlined it took 2.6 us more): the rows' lse from the spans' pairs; a bound t that at
 //     least k spans reach, the blocks of the spans that reach it, a tighter bound from those, the
 //     logits of the blocks that reach that, and their exact order.
 #include "device_common.cuh"
@@ -32,7 +33,7 @@ constexpr int kBSSmem = kBSStages * kBSStageBytes + kBSStages * 32 + 2 * kBSStag
 // choice
 constexpr int kBGThreads = 512;                       // one CTA a group
 constexpr int kBGWarps = kBGThreads / 32;
-constexpr int kBGHeld = 4;                            // spans or blocks a thread holds between its two looks at them
+constexpr int kBGHeld = 2;                            // spans or blocks a thread holds between its two looks at them
 constexpr int kBGCand = 1024;                         // candidates held in shared memory
 constexpr int kBGKept = 512;                          // spans, blocks listed
 constexpr int kBLThreads = 256;                       // from lists
@@ -333,8 +334,11 @@ template <int NT>
 struct ChoiceSmem {
   uint64_t key[kBGCand];
   uint32_t at[kBGCand];
+  float z[kBGCand];        // the candidate's logit, until its key is made
+  uint8_t beam[kBGCand];
   uint64_t res_key[kBeamsMaxRows];
   uint32_t res_at[kBeamsMaxRows];
+  uint8_t res_beam[kBeamsMaxRows];
   double off[kBeamsMaxRows];   // cum - log sum exp(z - M) of the group's rows
   float offf[kBeamsMaxRows];
   float top_z[kBeamsMaxRows];  // M, their largest logit
@@ -343,41 +347,42 @@ struct ChoiceSmem {
   int slot[kBeamsMaxRows];     // keep_slots: a candidate's place
   uint64_t wkey[NT / 32];
   uint32_t wat[NT / 32];
-  uint32_t count, spans, blocks;
-  float top[NT / 32 * 64];
-  float bound;
+  uint32_t count, spans, blocks, real;
+  alignas(16) uint32_t top[NT / 32 * 64];
+  uint32_t bound;
   float off_max;
   uint32_t kept_spans[kBGKept];
   uint32_t kept_blocks[kBGKept];
 };
 
-// Orders sm.key/at[0 .. cnt) into sm.res_*[0 .. min(cnt, k)): G threads a candidate count those before it.
+// Orders sm.key/at[0 .. cnt) into sm.res_*[0 .. min(cnt, k)): eight threads a candidate count those before it.
 template <int NT>
-__device__ void rank_candidates(ChoiceSmem<NT>& sm, int cnt, int k) {
-  int G = 1;  // a power of two, to 32, with G * cnt <= NT where that can be
-  while (G < 32 && 2 * G * cnt <= NT) G *= 2;
-  const int sub = threadIdx.x % G;
-  for (int base = 0; base < cnt; base += NT / G) {
-    const int i = base + static_cast<int>(threadIdx.x) / G;
+__device__ __noinline__ void rank_candidates(ChoiceSmem<NT>& sm, int cnt, int k) {
+  const int sub = threadIdx.x % 8;
+  for (int base = 0; base < cnt; base += NT / 8) {
+    const int i = base + static_cast<int>(threadIdx.x) / 8;
     const uint64_t key = i < cnt ? sm.key[i] : 0;
     const uint32_t at = i < cnt ? sm.at[i] : 0;
     int rank = 0;
-    if (i < cnt)
-      for (int j = sub; j < cnt; j += G) rank += before(sm.key[j], sm.at[j], key, at);
-    for (int o = G / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+#pragma unroll 1
+    for (int j = sub; j < cnt; j += 8) rank += before(sm.key[j], sm.at[j], key, at);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 4);
     if (i < cnt && sub == 0 && rank < k) {
       sm.res_key[rank] = key;
       sm.res_at[rank] = at;
+      sm.res_beam[rank] = sm.beam[i];
     }
   }
 }
 
 // Writes the group's k results (the first `cnt` of sm.res_* are real).  `token(at, beam)` gives a token.
 template <int NT, typename Token>
-__device__ void write_results(const BeamArgs& a, ChoiceSmem<NT>& sm, int group, int cnt, int per_beam, Token token) {
+__device__ __forceinline__ void write_results(const BeamArgs& a, ChoiceSmem<NT>& sm, int group, int cnt, Token token) {
   const int k = a.k;
   const int64_t base = static_cast<int64_t>(group) * k;
-  auto beam_of = [&](int r) { return r < cnt ? static_cast<int>(sm.res_at[r] / static_cast<uint32_t>(per_beam)) : -1; };
+  auto beam_of = [&](int r) { return r < cnt ? static_cast<int>(sm.res_beam[r]) : -1; };
   if (a.keep_slots) {  // k == beams <= NT
     const int r = threadIdx.x;
     if (r < k) sm.first[r] = -1;
@@ -419,7 +424,7 @@ __device__ void write_results(const BeamArgs& a, ChoiceSmem<NT>& sm, int group, 
 // candidates do not fit.  `scan(key, at, last_key, last_at)` puts the thread's best item behind (last_key, last_at)
 // into (key, at), key = 0 for none.  Returns the number found.
 template <int NT, typename Scan>
-__device__ int take_in_turn(ChoiceSmem<NT>& sm, int k, Scan scan) {
+__device__ __noinline__ int take_in_turn(ChoiceSmem<NT>& sm, int k, uint32_t per_beam, Scan scan) {
   uint64_t last = ~0ull, key = 0;
   uint32_t last_at = 0, at = 0xFFFFFFFFu;
   bool stale = true;
@@ -443,7 +448,7 @@ __device__ int take_in_turn(ChoiceSmem<NT>& sm, int k, Scan scan) {
     for (int w = 1; w < NT / 32; ++w)
       if (before(sm.wkey[w], sm.wat[w], bk, bat)) bk = sm.wkey[w], bat = sm.wat[w];
     if (bk == 0) break;
-    if (threadIdx.x == 0) sm.res_key[r] = bk, sm.res_at[r] = bat;
+    if (threadIdx.x == 0) sm.res_key[r] = bk, sm.res_at[r] = bat, sm.res_beam[r] = static_cast<uint8_t>(bat / per_beam);
     last = bk, last_at = bat;
     stale = key == bk && at == bat;  // (the pair is one thread's alone)
   }
@@ -466,31 +471,70 @@ __device__ __forceinline__ void two_sum(float& s, float& c, float b) {
   s = t;
 }
 
-// sm.bound = a value that at least k of the threads' values reach, or -inf if they are fewer: of every warp the q
-// largest of its threads' two largest (16 warps: 16 q >= k), of those the k-th.  Two barriers.
+// sm.bound = a value that at least k of the threads' values reach, or 0 if they are fewer (values: order-preserving
+// whole numbers, 0 for none): of every warp the q largest of its threads' two largest (q warps >= k), of those the
+// k-th, which every thread counts for a value.  Two barriers.
 template <int NT>
-__device__ void bound_of(ChoiceSmem<NT>& sm, float m1, float m2, int k) {
+__device__ __noinline__ void bound_of(ChoiceSmem<NT>& sm, uint32_t k1, uint32_t k2, int k) {
+  constexpr int W = NT / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int q = min(64, max(2, (k + 3) / 4));
-  uint32_t k1 = f32_ord(m1), k2 = f32_ord(m2);
+  const int q = min(64, max(2, (4 * k + W - 1) / W));
   for (int r = 0; r < q; ++r) {
     const uint32_t m = __reduce_max_sync(0xffffffffu, k1);
     const unsigned holders = __ballot_sync(0xffffffffu, k1 == m);
     if (lane == __ffs(holders) - 1) {
-      sm.top[warp * q + r] = m ? ord_f32(m) : -INFINITY;
+      sm.top[warp * q + r] = m;
       k1 = k2;
       k2 = 0;
     }
   }
   __syncthreads();
-  const int nv = NT / 32 * q;
+  const int nv = W * q;  // a multiple of 4
   for (int i = threadIdx.x; i < nv; i += NT) {
-    const float v = sm.top[i];
+    const uint32_t v = sm.top[i];
     int rank = 0;
-    for (int j = 0; j < nv; ++j) rank += sm.top[j] > v || (sm.top[j] == v && j < i);
+    for (int j = 0; j < nv; j += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(&sm.top[j]);
+      rank += (o.x > v || (o.x == v && j < i)) + (o.y > v || (o.y == v && j + 1 < i)) +
+              (o.z > v || (o.z == v && j + 2 < i)) + (o.w > v || (o.w == v && j + 3 < i));
+    }
     if (rank == k - 1) sm.bound = v;
   }
   __syncthreads();
+}
+
+// Leaves, of the candidates sm.key/at[0 .. cnt), those that a bound on the upper halves of their keys lets through:
+// hardly more than k.  Returns how many.
+template <int NT>
+__device__ __noinline__ int thin_candidates(ChoiceSmem<NT>& sm, int cnt, int k) {
+  constexpr int MOST = kBGCand / NT;
+  uint64_t key[MOST];
+  uint32_t at[MOST], k1 = 0, k2 = 0;
+  uint8_t beam[MOST];
+#pragma unroll
+  for (int u = 0; u < MOST; ++u) {
+    const int i = u * NT + static_cast<int>(threadIdx.x);
+    key[u] = i < cnt ? sm.key[i] : 0;
+    at[u] = i < cnt ? sm.at[i] : 0;
+    beam[u] = i < cnt ? sm.beam[i] : 0;
+    const uint32_t h = static_cast<uint32_t>(key[u] >> 32);
+    k2 = max(k2, min(k1, h));
+    k1 = max(k1, h);
+  }
+  bound_of(sm, k1, k2, k);
+  const uint32_t t = sm.bound;
+  if (threadIdx.x == 0) sm.count = 0;
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < MOST; ++u)
+    if (key[u] != 0 && static_cast<uint32_t>(key[u] >> 32) >= t) {
+      const uint32_t p = atomicAdd(&sm.count, 1u);
+      sm.key[p] = key[u];
+      sm.at[p] = at[u];
+      sm.beam[p] = beam[u];
+    }
+  __syncthreads();
+  return static_cast<int>(sm.count);
 }
 
 template <typename T>
@@ -503,7 +547,7 @@ __global__ void __launch_bounds__(kBGThreads) beam_choose_kernel(const BeamArgs 
   const int B = a.beams, nblk = a.nblk, P = a.spans;
   const int row0 = group * B;
   pdl_wait();
-  if (tid == 0) sm.count = 0, sm.spans = 0, sm.blocks = 0, sm.off_max = 0.0f;
+  if (tid == 0) sm.count = 0, sm.spans = 0, sm.blocks = 0, sm.real = 0, sm.off_max = 0.0f;
 
   // ---- the rows' cum - log sum exp(z - M) ----
   // 32 bits but for the last sum: the terms are good to 2^-23, the sum carries what its roundings leave, and
@@ -560,7 +604,8 @@ __global__ void __launch_bounds__(kBGThreads) beam_choose_kernel(const BeamArgs 
   if (tid < B) {
     if (sm.state[tid] == kRowEnded) {
       const uint32_t i = atomicAdd(&sm.count, 1u);
-      sm.key[i] = score_key(sm.off[tid]);
+      sm.z[i] = 0.0f;
+      sm.beam[i] = static_cast<uint8_t>(tid);
       sm.at[i] = static_cast<uint32_t>(tid) * static_cast<uint32_t>(a.V);
     }
     atomicMax(reinterpret_cast<int*>(&sm.off_max), __float_as_int(fabsf(sm.offf[tid])));
@@ -569,26 +614,54 @@ __global__ void __launch_bounds__(kBGThreads) beam_choose_kernel(const BeamArgs 
     const uint8_t st = sm.state[b];
     return st == kRowNormal || st == kRowPlusInf ? below_top<float>(st, z, sm.top_z[b]) + sm.offf[b] : -INFINITY;
   };
-  // The k-th best score is at least `bound` but for fp32's rounding of it and of the sums compared with it (2^-24 of
-  // each term): 2^-21 covers both.
-  auto floor_of = [&](float bound) {
-    return bound > -INFINITY ? bound - ldexpf(fabsf(bound) + sm.off_max, -21) : bound;
+  auto key_of = [&](int b, float z) -> uint64_t {  // 0: no continuation
+    const uint8_t st = sm.state[b];
+    const double s = st == kRowEnded ? sm.off[b] : sm.off[b] + below_top<double>(st, z, sm.top_z[b]);
+    return static_cast<float>(s) > -INFINITY ? score_key(s) : 0;
   };
-  // Items 0 .. n - 1 with value(i): the items that reach a bound that k of them reach go to list[0 .. *count), that
-  // bound is returned.  A thread holds its first values between its two looks.
-  auto filter = [&](int n, auto value, uint32_t* list, uint32_t* count) -> float {
+  const float* bm = a.bmax + static_cast<int64_t>(row0) * nblk;
+  const int64_t span0 = static_cast<int64_t>(row0) * P;
+  // Twice the same: items 0 .. n - 1, first the group's spans, then the blocks of the kept spans (item i: block i % SB
+  // of kept span i / SB), of which those that reach a bound that k of them reach are listed.  A thread holds its first
+  // values between its two looks.  The k-th best score is at least the bound but for fp32's rounding of it and of the
+  // sums compared with it (2^-24 of each term): 2^-21 covers both.
+  float t = -INFINITY;
+  bool fits = true;
+  int n_blocks = 0;
+#pragma unroll 1
+  for (int level = 0; level < 2 && fits; ++level) {
+    const int n = level == 0 ? B * P : static_cast<int>(sm.spans) * SB;
+    auto value = [&](int i) -> float {
+      int span = i, blk = 0;
+      if (level) {
+        span = static_cast<int>(sm.kept_spans[i / SB]);
+        blk = i % SB;
+      }
+      const int b = span / P;
+      const float* p = a.mask ? a.smax + span0 + span : &a.part_ms[span0 + span].x;
+      if (level) {
+        blk += (span - b * P) * SB;
+        if (blk >= nblk) return -INFINITY;
+        p = bm + static_cast<int64_t>(b) * nblk + blk;
+      }
+      return score32(b, __ldcg(p));
+    };
     float m1 = -INFINITY, m2 = -INFINITY, held[kBGHeld];
+#pragma unroll
+    for (int u = 0; u < kBGHeld; ++u) held[u] = u * NT + tid < n ? value(u * NT + tid) : -INFINITY;
     auto top2 = [&](float v) {
       m2 = fmaxf(m2, fminf(m1, v));
       m1 = fmaxf(m1, v);
     };
 #pragma unroll
-    for (int u = 0; u < kBGHeld; ++u) held[u] = u * NT + tid < n ? value(u * NT + tid) : -INFINITY;
-#pragma unroll
     for (int u = 0; u < kBGHeld; ++u) top2(held[u]);
+#pragma unroll 1
     for (int i = kBGHeld * NT + tid; i < n; i += NT) top2(value(i));
-    bound_of(sm, m1, m2, a.k);
-    const float t = floor_of(sm.bound);
+    bound_of(sm, m1 > -INFINITY ? f32_ord(m1) : 0u, m2 > -INFINITY ? f32_ord(m2) : 0u, a.k);
+    t = sm.bound ? ord_f32(sm.bound) : -INFINITY;
+    if (t > -INFINITY) t -= (fabsf(t) + sm.off_max) * 4.76837158203125e-7f;  // 2^-21
+    uint32_t* list = level ? sm.kept_blocks : sm.kept_spans;
+    uint32_t* count = level ? &sm.blocks : &sm.spans;
     auto keep = [&](int i, float v) {
       if (v >= t && v > -INFINITY) {
         const uint32_t p = atomicAdd(count, 1u);
@@ -597,73 +670,58 @@ __global__ void __launch_bounds__(kBGThreads) beam_choose_kernel(const BeamArgs 
     };
 #pragma unroll
     for (int u = 0; u < kBGHeld; ++u) keep(u * NT + tid, held[u]);
+#pragma unroll 1
     for (int i = kBGHeld * NT + tid; i < n; i += NT) keep(i, value(i));
     __syncthreads();
-    return t;
-  };
-  const float* bm = a.bmax + static_cast<int64_t>(row0) * nblk;
-  const int64_t span0 = static_cast<int64_t>(row0) * P;
-  auto span_max = [&](int i) { return a.mask ? __ldcg(a.smax + span0 + i) : __ldcg(&a.part_ms[span0 + i].x); };
-  filter(B * P, [&](int i) { return score32(i / P, span_max(i)); }, sm.kept_spans, &sm.spans);
-  const int n_spans = static_cast<int>(sm.spans);
-  bool fits = n_spans <= kBGKept;
-  int cnt = 0;
+    n_blocks = static_cast<int>(*count);
+    fits = n_blocks <= kBGKept;
+  }
   auto logit = [&](int b, int v) -> float {  // -inf for a token that is not allowed
     const int row = row0 + b;
     if (a.mask && !mask_allows(a.mask + static_cast<int64_t>(row) * a.mask_words, v)) return -INFINITY;
     const float z = logit_at<T>(a.logits, static_cast<int64_t>(row) * a.row_stride + v);
     return z == z ? z : -INFINITY;
   };
-  auto key_of = [&](int b, float z) -> uint64_t {  // 0: no continuation
-    const double s = sm.off[b] + below_top<double>(sm.state[b], z, sm.top_z[b]);
-    return static_cast<float>(s) > -INFINITY ? score_key(s) : 0;
-  };
+  int cnt = 0;
   if (fits) {
-    // item i: block i % SB of kept span i / SB; its number is row * nblk + block
-    auto block_at = [&](int i, int& b, int& blk) {
-      const int span = static_cast<int>(sm.kept_spans[i / SB]);
-      b = span / P;
-      blk = (span - b * P) * SB + i % SB;
-    };
-    const float t = filter(
-        n_spans * SB,
-        [&](int i) {
-          int b, blk;
-          block_at(i, b, blk);
-          return blk < nblk ? score32(b, __ldcg(bm + static_cast<int64_t>(b) * nblk + blk)) : -INFINITY;
-        },
-        sm.kept_blocks, &sm.blocks);
-    const int n_blocks = static_cast<int>(sm.blocks);
-    fits = n_blocks <= kBGKept;
-    for (int j = tid; fits && j < n_blocks * kBlock; j += NT) {
-      int b, blk;
-      block_at(static_cast<int>(sm.kept_blocks[j / kBlock]), b, blk);
-      const int v = blk * kBlock + j % kBlock;
+#pragma unroll 1
+    for (int j = tid; j < n_blocks * kBlock; j += NT) {
+      const int i = static_cast<int>(sm.kept_blocks[j / kBlock]);
+      const int span = static_cast<int>(sm.kept_spans[i / SB]), b = span / P;
+      const int v = ((span - b * P) * SB + i % SB) * kBlock + j % kBlock;
       if (v >= a.V) continue;
       const float z = logit(b, v);
       const float f = score32(b, z);
       if (!(f >= t) || !(f > -INFINITY)) continue;
-      const uint64_t key = key_of(b, z);
-      if (key == 0) continue;
       const uint32_t p = atomicAdd(&sm.count, 1u);
       if (p < kBGCand) {
-        sm.key[p] = key;
+        sm.z[p] = z;
+        sm.beam[p] = static_cast<uint8_t>(b);
         sm.at[p] = static_cast<uint32_t>(b) * static_cast<uint32_t>(a.V) + static_cast<uint32_t>(v);
       }
     }
     __syncthreads();
     cnt = static_cast<int>(sm.count);
-    fits = fits && cnt <= kBGCand;
+    fits = cnt <= kBGCand;
   }
   if (fits) {
+    // (64 bits only here, in few warps)
+    for (int i = tid; i < cnt; i += NT) {
+      const uint64_t key = key_of(sm.beam[i], sm.z[i]);
+      sm.key[i] = key;
+      if (key) atomicAdd(&sm.real, 1u);
+    }
+    __syncthreads();
+    const int real = static_cast<int>(sm.real);
+    if (cnt > 128 && cnt > a.k) cnt = thin_candidates(sm, cnt, a.k);
     rank_candidates(sm, cnt, a.k);
-    cnt = min(cnt, a.k);
+    cnt = min(real, a.k);
     __syncthreads();
   } else {
     // a thread's blocks are a contiguous share, looked through again only after its best is taken
     const int nb = B * nblk, per = (nb + NT - 1) / NT;
     const int lo = min(nb, tid * per), hi = min(nb, lo + per);
-    cnt = take_in_turn(sm, a.k, [&](uint64_t& key, uint32_t& at, uint64_t last, uint32_t last_at) {
+    cnt = take_in_turn(sm, a.k, static_cast<uint32_t>(a.V), [&](uint64_t& key, uint32_t& at, uint64_t last, uint32_t last_at) {
       key = 0;
       at = 0xFFFFFFFFu;
       for (int i = lo; i < hi; ++i) {
@@ -686,7 +744,7 @@ __global__ void __launch_bounds__(kBGThreads) beam_choose_kernel(const BeamArgs 
       }
     });
   }
-  write_results(a, sm, group, cnt, a.V,
+  write_results(a, sm, group, cnt,
                 [&](uint32_t at, int b) { return static_cast<int32_t>(at - static_cast<uint32_t>(b) * static_cast<uint32_t>(a.V)); });
 }
 
@@ -722,21 +780,34 @@ __global__ void __launch_bounds__(kBLThreads) beam_lists_kernel(const BeamArgs a
     const double s = sm.off[b] + static_cast<double>(lp);
     return static_cast<float>(s) > -INFINITY ? score_key(s) : 0;
   };
+  auto key_at = [&](int i) { return i == tid ? entry(i, id0, lp0) : entry(i, __ldcg(a.ids + e0 + i), __ldcg(a.lps + e0 + i)); };
+  uint32_t least = 0;  // of a key's upper half
+  if (total > kBGCand) {  // more than the list holds: those that a bound lets through
+    uint32_t k1 = 0, k2 = 0;
+    for (int i = tid; i < total; i += NT) {
+      const uint32_t h = static_cast<uint32_t>(key_at(i) >> 32);
+      k2 = max(k2, min(k1, h));
+      k1 = max(k1, h);
+    }
+    bound_of(sm, k1, k2, a.k);
+    least = sm.bound;
+  }
   for (int i = tid; i < total; i += NT) {
-    const uint64_t key = i == tid ? entry(i, id0, lp0) : entry(i, __ldcg(a.ids + e0 + i), __ldcg(a.lps + e0 + i));
-    if (key) {
+    const uint64_t key = key_at(i);
+    if (key && static_cast<uint32_t>(key >> 32) >= least) {
       const uint32_t p = atomicAdd(&sm.count, 1u);
-      if (p < kBGCand) sm.key[p] = key, sm.at[p] = static_cast<uint32_t>(i);
+      if (p < kBGCand) sm.key[p] = key, sm.at[p] = static_cast<uint32_t>(i), sm.beam[p] = static_cast<uint8_t>(i / n);
     }
   }
   __syncthreads();
   int cnt = static_cast<int>(sm.count);
   if (cnt <= kBGCand) {
+    if (cnt > 128 && cnt > a.k) cnt = thin_candidates(sm, cnt, a.k);
     rank_candidates(sm, cnt, a.k);
     cnt = min(cnt, a.k);
     __syncthreads();
   } else {
-    cnt = take_in_turn(sm, a.k, [&](uint64_t& key, uint32_t& at, uint64_t last, uint32_t last_at) {
+    cnt = take_in_turn(sm, a.k, static_cast<uint32_t>(n), [&](uint64_t& key, uint32_t& at, uint64_t last, uint32_t last_at) {
       key = 0;
       at = 0xFFFFFFFFu;
       for (int i = tid; i < total; i += NT) {
@@ -746,7 +817,7 @@ __global__ void __launch_bounds__(kBLThreads) beam_lists_kernel(const BeamArgs a
       }
     });
   }
-  write_results(a, sm, group, cnt, n, [&](uint32_t at, int) { return __ldcg(a.ids + e0 + at); });
+  write_results(a, sm, group, cnt, [&](uint32_t at, int) { return __ldcg(a.ids + e0 + at); });
 }
 
 // ---------------------------------------------------------------------------
