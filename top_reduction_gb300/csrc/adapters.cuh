@@ -547,13 +547,15 @@ __global__ void __launch_bounds__(kADThreads, RT <= 4 ? 2 : 1) adapter_down_wide
 template <typename Y, bool VEC>
 struct Outputs {
   static constexpr int ES = static_cast<int>(sizeof(Y));
-  static constexpr bool kRing = VEC || ES == 4;  // (copies are of four bytes at least)
-  static constexpr int BYTES = 4 * ES;           // of a lane and row
+  static constexpr int BYTES = 4 * ES;               // of a lane and row
+  static constexpr int ROWS4 = ES == 4 ? 512 : 320;  // bytes in the ring of the four rows that the lanes copy at once
   __device__ __forceinline__ static int output(int g, int e) { return VEC ? 4 * g + e : g + 8 * e; }
   // A lane's place for its share of a row of its own: those of a row are neighbours, as in memory (whole sectors), and
   // the four rows of a copy do not meet in a bank when a quarter of a warp reads.
+  // (16-bit outputs that do not align: a row's 32 take 16 or 17 words of four bytes, the least that a copy moves.)
   __device__ __forceinline__ static int place(int lane) {
     const int g = lane >> 2, t = lane & 3;
+    if constexpr (!VEC && ES == 2) return t * 80;
     return t * (8 * BYTES) + (((g >> 1) ^ t) * 2 + (g & 1)) * BYTES;
   }
   template <bool FULL>
@@ -563,6 +565,15 @@ struct Outputs {
     } else if constexpr (ES == 4) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) lane_copy_if<4>(have && (FULL || 8 * e < left), to + e * 4, row + 32 * e);
+    } else {  // words g, g + 8 and (lane group 0) 16 of those that hold the row's outputs of the step
+      const int g = (static_cast<int>(threadIdx.x) & 31) >> 2;
+      const uintptr_t first = reinterpret_cast<uintptr_t>(row) - 2 * g;
+      const int skip = static_cast<int>(first >> 1) & 1;
+      const char* p = reinterpret_cast<const char*>(first - 2 * skip) + 4 * g;
+#pragma unroll
+      for (int w = 0; w < 3; ++w)
+        lane_copy_if<4>(have && (w < 2 || (g == 0 && skip)) && (FULL || 2 * (g + 8 * w) - skip < left + g), to + 4 * (g + 8 * w),
+                        p + 32 * w);
     }
   }
   // d[e] times `by` is added to output e.
@@ -589,13 +600,14 @@ struct Outputs {
                                    C::pack(fmaf(d[2], by, b.x), fmaf(d[3], by, b.y)));
         if (have && (FULL || left > 0)) *reinterpret_cast<uint2*>(row) = w;
       } else {
-        uint16_t v[4] = {};
+        const int g = (static_cast<int>(threadIdx.x) & 31) >> 2;
+        const int skip = static_cast<int>((reinterpret_cast<uintptr_t>(y_row) >> 1) - g) & 1;
+        const uint16_t* v = reinterpret_cast<const uint16_t*>(in) + skip + g;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (have && (FULL || 8 * e < left)) v[e] = reinterpret_cast<const uint16_t*>(y_row)[8 * e];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (have && (FULL || 8 * e < left)) reinterpret_cast<uint16_t*>(row)[8 * e] = C::bits(fmaf(d[e], by, C::value(v[e])));
+        for (int e = 0; e < 4; ++e) {
+          const uint16_t r = C::bits(fmaf(d[e], by, C::value(v[8 * e])));
+          if (have && (FULL || 8 * e < left)) reinterpret_cast<uint16_t*>(row)[8 * e] = r;
+        }
       }
     }
   }
@@ -690,7 +702,7 @@ struct UpPlaces {
 // A warp's ring: entries of the weights of a step and of y for C tiles of 8 rows.  A CTA has an SM for itself, with as
 // many warps as its registers allow without spilling, each with a ring of at least two of the larger entries.
 constexpr int kADUpCols = 2;                                                         // C of tiles of more than 8 rows
-constexpr int up_entry(int ks, int es, int c) { return ks * 1024 + c * es * 256; }
+constexpr int up_entry(int ks, int es, int c) { return ks * 1024 + c * (es == 4 ? 1024 : 640); }
 constexpr int kADUpStatic = 2900;  // (what else a CTA holds beside d)
 constexpr int up_ring_bytes(int ks, int es) { return 227 * 1024 - ks * kADCols * 32 * 4 * es - kADUpStatic; }
 constexpr int up_warps(int ks) { return ks <= 4 ? 16 : 8; }
@@ -711,7 +723,7 @@ struct UpShare {
   using P = UpPlaces<VEC, KS>;
   static constexpr int D = up_depth(KS, ES, C), ENTRY = up_entry(KS, ES, C);
   static constexpr int STRIDE = up_warps(KS) * STEP;  // outputs from a step to the warp's next
-  static constexpr int W_BYTES = J * KS * 512, ROW_BYTES = 32 * O::BYTES;
+  static constexpr int W_BYTES = J * KS * 512, ROW_BYTES = O::ROWS4;
   static_assert(D >= 2, "a ring of two entries at least");
   const AdapterArgs& a;
   const UpSmem<KS, LO>& sm;
@@ -764,21 +776,19 @@ struct UpShare {
         p += pitch;
       }
     }
-    if constexpr (O::kRing) {
-      const int left = n_end - in_n0 - lane_n;
-      const uint32_t to = smem_u32(ring_y) + in_at;
-      if constexpr (C == 1) {
-        O::template copy<FULL>(to, yp0, 2 * t < count, left);
-        O::template copy<FULL>(to + ROW_BYTES, yp1, 2 * t + 1 < count, left);
-      } else {
-        const char* y = a.y + static_cast<int64_t>(in_n0 + lane_n) * ES;
-        const int row = in_part * (8 * C) + 2 * t;
+    const int left = n_end - in_n0 - lane_n;
+    const uint32_t to = smem_u32(ring_y) + in_at;
+    if constexpr (C == 1) {
+      O::template copy<FULL>(to, yp0, 2 * t < count, left);
+      O::template copy<FULL>(to + ROW_BYTES, yp1, 2 * t + 1 < count, left);
+    } else {
+      const char* y = a.y + static_cast<int64_t>(in_n0 + lane_n) * ES;
+      const int row = in_part * (8 * C) + 2 * t;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+      for (int c = 0; c < C; ++c)
 #pragma unroll
-          for (int u = 0; u < 2; ++u)  // (rows behind the last have offsets of it)
-            O::template copy<FULL>(to + (2 * c + u) * ROW_BYTES, y + sm.y[row + c * 8 + u], row + c * 8 + u < count, left);
-      }
+        for (int u = 0; u < 2; ++u)  // (rows behind the last have offsets of it)
+          O::template copy<FULL>(to + (2 * c + u) * ROW_BYTES, y + sm.y[row + c * 8 + u], row + c * 8 + u < count, left);
     }
   }
   __device__ __forceinline__ void issue() {
@@ -789,7 +799,7 @@ struct UpShare {
         in_part = 0;
         in_n0 += STRIDE;
         wp += step;
-        if constexpr (C == 1 && O::kRing) yp0 += STRIDE * ES, yp1 += STRIDE * ES;
+        if constexpr (C == 1) yp0 += STRIDE * ES, yp1 += STRIDE * ES;
       }
       in_at = in_at == (D - 1) * ENTRY ? 0 : in_at + ENTRY;
     }
@@ -895,7 +905,6 @@ struct UpShare {
         n0 += STRIDE;
         if constexpr (C == 1) {
           op0 += STRIDE * ES, op1 += STRIDE * ES;
-          if constexpr (!O::kRing) yp0 += STRIDE * ES, yp1 += STRIDE * ES;
         }
       }
       at = at == (D - 1) * ENTRY ? 0 : at + ENTRY;
@@ -969,33 +978,30 @@ constexpr int wide_stage_bytes(int ks) { return kADWideStage * 32 * ks; }
 // 64-row tiles, 8 warps: a warp takes up to four blocks of a stage
 constexpr int kADWideBlocks = 4;
 
-// Eight neighbouring outputs of a row.
-template <typename Y, bool VEC>
+// Eight neighbouring outputs of a row, read and written 16 bytes at a time.
+template <typename Y>
 struct Eight {
   static constexpr int ES = static_cast<int>(sizeof(Y));
-  static constexpr int WORDS = VEC ? ES * 2 : 1;  // (not VEC: read where they are used)
-  uint32_t w[WORDS];
+  uint32_t w[2 * ES];
   // Outputs n .. n + 7 of the row at `row`; pieces that are not below `end` are read from its start.
   __device__ __forceinline__ void load(const char* row, int n, int end) {
-    if constexpr (VEC) {
 #pragma unroll
-      for (int p = 0; p < ES / 2; ++p) {
-        const int at = n + p * (16 / ES);
-        const uint4 v = *reinterpret_cast<const uint4*>(row + static_cast<int64_t>(at < end ? at : 0) * ES);
-        w[4 * p] = v.x, w[4 * p + 1] = v.y, w[4 * p + 2] = v.z, w[4 * p + 3] = v.w;
-      }
+    for (int p = 0; p < ES / 2; ++p) {
+      const int at = n + p * (16 / ES);
+      const uint4 v = *reinterpret_cast<const uint4*>(row + static_cast<int64_t>(at < end ? at : 0) * ES);
+      w[4 * p] = v.x, w[4 * p + 1] = v.y, w[4 * p + 2] = v.z, w[4 * p + 3] = v.w;
     }
   }
-  // outputs e = 2 j, 2 j + 1: acc[j][0], acc[j][1] times `by`, added
-  __device__ __forceinline__ void add_and_store(const char* y_row, char* row, int left, const float (&d)[8], float by) const {
-    if constexpr (VEC && ES == 4) {
+  // d[e] times `by` is added to output e, and those below `left` are written.
+  __device__ __forceinline__ void add_and_store(char* row, int left, const float (&d)[8], float by) const {
+    if constexpr (ES == 4) {
 #pragma unroll
       for (int p = 0; p < 2; ++p)
         if (left > 4 * p)
           *reinterpret_cast<float4*>(row + 16 * p) =
               make_float4(fmaf(d[4 * p], by, __uint_as_float(w[4 * p])), fmaf(d[4 * p + 1], by, __uint_as_float(w[4 * p + 1])),
                           fmaf(d[4 * p + 2], by, __uint_as_float(w[4 * p + 2])), fmaf(d[4 * p + 3], by, __uint_as_float(w[4 * p + 3])));
-    } else if constexpr (VEC) {
+    } else {
       using C = Half16<Y>;
       uint32_t r[4];
 #pragma unroll
@@ -1004,35 +1010,54 @@ struct Eight {
         r[i] = C::pack(fmaf(d[2 * i], by, v.x), fmaf(d[2 * i + 1], by, v.y));
       }
       if (left > 0) *reinterpret_cast<uint4*>(row) = make_uint4(r[0], r[1], r[2], r[3]);
-    } else if constexpr (ES == 4) {
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = e < left ? reinterpret_cast<const float*>(y_row)[e] : 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < left) reinterpret_cast<float*>(row)[e] = fmaf(d[e], by, v[e]);
-    } else {
-      using C = Half16<Y>;
-      uint16_t v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = e < left ? reinterpret_cast<const uint16_t*>(y_row)[e] : 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < left) reinterpret_cast<uint16_t*>(row)[e] = C::bits(fmaf(d[e], by, C::value(v[e])));
     }
   }
 };
 
-constexpr int wide_ctas(int ks, int es) { return ks <= 4 && es == 2 ? 2 : 1; }
+// Rows that do not align for that: a block's 16 rows x 32 outputs cross shared memory, and a lane reads and writes
+// one output of each row, neighbouring lanes neighbours.
+template <typename Y>
+struct Sixteen {
+  static constexpr int ES = static_cast<int>(sizeof(Y));
+  uint32_t w[16];  // the lane's output of every row
+  // Output n of the rows at base + off[i] (that of the row's start, if n is not below `end`).
+  __device__ __forceinline__ void load(const char* base, const int64_t* off, int n, int end) {
+    const int64_t at = static_cast<int64_t>(n < end ? n : 0) * ES;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const char* p = base + off[i] + at;
+      if constexpr (ES == 4) w[i] = *reinterpret_cast<const uint32_t*>(p);
+      else w[i] = *reinterpret_cast<const uint16_t*>(p);
+    }
+  }
+  // delta[i * pitch] is added to the output of row i, of `rows` rows.
+  __device__ __forceinline__ void add_and_store(char* base, const int64_t* off, int n, bool in, int rows, const float* delta,
+                                                int pitch) const {
+    const int64_t at = static_cast<int64_t>(n) * ES;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float d = delta[i * pitch];
+      if (i >= rows || !in) continue;
+      char* p = base + off[i] + at;
+      if constexpr (ES == 4) *reinterpret_cast<float*>(p) = __uint_as_float(w[i]) + d;
+      else *reinterpret_cast<uint16_t*>(p) = Half16<Y>::bits(Half16<Y>::value(static_cast<uint16_t>(w[i])) + d);
+    }
+  }
+};
+
+constexpr int wide_ctas(int ks, int es, bool vec) { return ks <= 4 && es == 2 && vec ? 2 : 1; }
 
 template <typename T, typename Y, int KS, bool VEC>
-__global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y))) adapter_wide_kernel(const AdapterArgs a) {
+__global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y), VEC)) adapter_wide_kernel(const AdapterArgs a) {
   extern __shared__ __align__(128) unsigned char wide_ring[];
   __shared__ TileSmem ts;
   constexpr bool LO = sizeof(Y) == 4;
   constexpr int ES = static_cast<int>(sizeof(Y)), CH = 2 * KS, S = kADWideStages;
   constexpr int ROWS = kADWideThreads / CH;  // weight rows that the CTA copies at a time
-  using E8 = Eight<Y, VEC>;
+  using Held = typename std::conditional<VEC, Eight<Y>[2], Sixteen<Y>>::type;  // y of a lane and block
+  constexpr int PITCH = 36;
+  __shared__ float cross[VEC ? 1 : kADWideWarps][VEC ? 1 : 16 * PITCH];
+  __shared__ int64_t offs[VEC ? 1 : 4][2][VEC ? 1 : 16];  // [16 rows of the tile][y, out]: the rows' first bytes
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   // (as in the kernel above: all but d was complete before this kernel started)
   TileFinder finder;
@@ -1155,11 +1180,24 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y))) adap
     // y of a stage; a block's is replaced by the next stage's as soon as it is used.  No branch and no condition, so
     // that nothing waits for it before its use: rows that are not there have the first one's address, outputs behind
     // the row's end and stages behind the last the row's start.
-    E8 v[kADWideBlocks][2];
+    Held v[kADWideBlocks];
+    const int rset = warp % rg, rows_here = count - rset * 16;
+    if constexpr (!VEC) {
+      if (tid < kADTile) {
+        const int64_t r = ts.rows[min(tid, count - 1)];
+        offs[tid / 16][0][tid % 16] = r * a.y_stride * ES;
+        offs[tid / 16][1][tid % 16] = r * a.out_stride * ES;
+      }
+      __syncthreads();
+    }
     auto load_block = [&](int st, int b) {
-      const int n = st * kADWideStage + (first_block + b) * 32;
+      const int n = st * kADWideStage + (first_block + b) * 32, end = st < s1 ? a.N : 0;
+      if constexpr (VEC) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) v[b][u].load(y[u] - 8 * t * ES, n + 8 * t, st < s1 ? a.N : 0);
+        for (int u = 0; u < 2; ++u) v[b][u].load(y[u] - 8 * t * ES, n + 8 * t, end);
+      } else {
+        v[b].load(a.y, offs[rset][0], n + lane, end);
+      }
     };
     // FULL: the stage's outputs are all the row's.  ALL: the rank is the whole of the KS steps.
     auto work = [&](int st, auto full_const, auto all_const) {
@@ -1211,13 +1249,26 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y))) adap
             }
           }
         }
-        const int left = FULL ? 8 : a.N - n - 8 * t;
-        const int64_t off = static_cast<int64_t>(n) * ES;
+        if constexpr (VEC) {
+          const int left = FULL ? 8 : a.N - n - 8 * t;
+          const int64_t off = static_cast<int64_t>(n) * ES;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float dv[8] = {acc[0][2 * u], acc[0][2 * u + 1], acc[1][2 * u], acc[1][2 * u + 1],
-                               acc[2][2 * u], acc[2][2 * u + 1], acc[3][2 * u], acc[3][2 * u + 1]};
-          if (have[u]) v[b][u].add_and_store(y[u] + off, out[u] + off, left, dv, back[u]);
+          for (int u = 0; u < 2; ++u) {
+            const float dv[8] = {acc[0][2 * u], acc[0][2 * u + 1], acc[1][2 * u], acc[1][2 * u + 1],
+                                 acc[2][2 * u], acc[2][2 * u + 1], acc[3][2 * u], acc[3][2 * u + 1]};
+            if (have[u]) v[b][u].add_and_store(out[u] + off, left, dv, back[u]);
+          }
+        } else {
+          float* mine = cross[warp];
+          __syncwarp();  // the block before has been read
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float2*>(mine + (g + 8 * u) * PITCH + 8 * t + 2 * j) =
+                  make_float2(acc[j][2 * u] * back[u], acc[j][2 * u + 1] * back[u]);
+          __syncwarp();
+          v[b].add_and_store(a.out, offs[rset][1], n + lane, FULL || n + lane < a.N, rows_here, mine + lane, PITCH);
         }
         if constexpr (FULL) load_block(st + 1, b);
       }
@@ -1316,7 +1367,7 @@ cudaError_t launch_down(const AdapterArgs& a, int grid, cudaStream_t stream) {
 template <typename T, typename Y, int KS, bool VEC>
 cudaError_t launch_up_ks(const AdapterArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
   if (a.rows > kADOwnPlan) {
-    const int64_t most = static_cast<int64_t>(num_sms) * wide_ctas(KS, sizeof(Y));
+    const int64_t most = static_cast<int64_t>(num_sms) * wide_ctas(KS, sizeof(Y), VEC);
     const int64_t stages = max_tiles * ((a.N + kADWideStage - 1) / kADWideStage);
     return launch_kernel(adapter_wide_kernel<T, Y, KS, VEC>, dim3(static_cast<unsigned>(stages < most ? stages : most)),
                          dim3(kADWideThreads), static_cast<size_t>(kADWideStages * wide_stage_bytes(KS)), stream, true, a);
