@@ -967,16 +967,16 @@ __global__ void __launch_bounds__(32 * up_warps(KS), 1) adapter_up_kernel(const 
 // Here the batch's rows are the MMA's A operand (16 a warp, held in registers for a whole tile) and 8 rows of the
 // weights the B operand.  A lane's part of d and its two rows of y and out stay the same from step to step, which
 // leaves about a fifth of the instructions of the kernel above per output (packed prompts, 16384 rows of rank 64 x
-// 4096: 108 us there).  The weights come in stages of kADWideStage outputs that the whole CTA copies and reads;
+// 4096: 108 us there).  The weights come in stages of wide_stage() outputs that the whole CTA copies and reads;
 // warps share a stage by rows (one for every 16 of the tile's) and by outputs.  A block is 32 outputs; column c of
 // its tile j stands for output 8 (c / 2) + 2 j + c % 2, so that a lane has eight neighbours of a row.
 constexpr int kADWideThreads = 256;
 constexpr int kADWideWarps = kADWideThreads / 32;
-constexpr int kADWideStage = 256;  // outputs
 constexpr int kADWideStages = 3;
-constexpr int wide_stage_bytes(int ks) { return kADWideStage * 32 * ks; }
-// 64-row tiles, 8 warps: a warp takes up to four blocks of a stage
-constexpr int kADWideBlocks = 4;
+// Outputs of a stage: of 64-row tiles a warp takes four blocks, or the two that leave registers for a second CTA on the
+// SM where y takes twice of them (fp32, 1257 rows of rank 64 x 23728: 109 us with four).
+constexpr int wide_stage(int es, bool vec) { return es == 2 && vec ? 256 : 128; }
+constexpr int wide_stage_bytes(int ks, int es, bool vec) { return wide_stage(es, vec) * 32 * ks; }
 
 // Eight neighbouring outputs of a row, read and written 16 bytes at a time.
 template <typename Y>
@@ -1045,14 +1045,15 @@ struct Sixteen {
   }
 };
 
-constexpr int wide_ctas(int ks, int es, bool vec) { return ks <= 4 && es == 2 && vec ? 2 : 1; }
+constexpr int wide_ctas(int ks) { return ks <= 4 ? 2 : 1; }
 
 template <typename T, typename Y, int KS, bool VEC>
-__global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y), VEC)) adapter_wide_kernel(const AdapterArgs a) {
+__global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_kernel(const AdapterArgs a) {
   extern __shared__ __align__(128) unsigned char wide_ring[];
   __shared__ TileSmem ts;
   constexpr bool LO = sizeof(Y) == 4;
   constexpr int ES = static_cast<int>(sizeof(Y)), CH = 2 * KS, S = kADWideStages;
+  constexpr int STAGE = wide_stage(ES, VEC), STAGE_BYTES = wide_stage_bytes(KS, ES, VEC), MOST = STAGE / 64;  // MOST: blocks a warp
   constexpr int ROWS = kADWideThreads / CH;  // weight rows that the CTA copies at a time
   using Held = typename std::conditional<VEC, Eight<Y>[2], Sixteen<Y>>::type;  // y of a lane and block
   constexpr int PITCH = 36;
@@ -1062,7 +1063,7 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y), VEC))
   // (as in the kernel above: all but d was complete before this kernel started)
   TileFinder finder;
   const int n_tiles = finder.start(a, ts);
-  const int64_t stages = (a.N + kADWideStage - 1) / kADWideStage;
+  const int64_t stages = (a.N + STAGE - 1) / STAGE;
   const int64_t all = stages * n_tiles;
   int64_t at = all * blockIdx.x / gridDim.x;
   const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
@@ -1077,7 +1078,8 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y), VEC))
     const int count = ts.count, rank = adapter_rank(a, ts.adapter);
     const int rg = count <= 16 ? 1 : count <= 32 ? 2 : 4, ng = kADWideWarps / rg;  // warps by rows and by outputs
     const int row0 = (warp % rg) * 16 + g;
-    const int blocks = 8 / ng, first_block = warp / rg * blocks;  // of a stage, the warp's: neighbours
+    const int blocks = max(1, STAGE / 32 / ng), first_block = warp / rg * blocks;  // of a stage, the warp's: neighbours
+    const bool idle = first_block * 32 >= STAGE;  // (fewer blocks than warps)
     const bool have[2] = {row0 < count, row0 + 8 < count};
     const int row[2] = {ts.rows[have[0] ? row0 : 0], ts.rows[have[1] ? row0 + 8 : 0]};
     const char* y[2];
@@ -1090,12 +1092,12 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y), VEC))
     const T* up = reinterpret_cast<const T*>(a.up) + static_cast<int64_t>(max(ts.adapter, 0)) * a.up_adapter;
     auto issue = [&](int st) {
       if (st < s1 && rank > 0) {
-        const int n0 = st * kADWideStage;
-        const uint32_t to = smem_u32(wide_ring) + (st - s0) % S * wide_stage_bytes(KS);
+        const int n0 = st * STAGE;
+        const uint32_t to = smem_u32(wide_ring) + (st - s0) % S * STAGE_BYTES;
         const int c = tid % CH;
         const T* p = up + (n0 + tid / CH) * a.up_row + c * 8;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
+        for (int i = 0; i < STAGE / ROWS; ++i) {
           const int r = tid / CH + i * ROWS;
           lane_copy_if<16>(c * 8 < rank && n0 + r < a.N, to + place(r, c), p);
           p += ROWS * a.up_row;
@@ -1180,7 +1182,7 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y), VEC))
     // y of a stage; a block's is replaced by the next stage's as soon as it is used.  No branch and no condition, so
     // that nothing waits for it before its use: rows that are not there have the first one's address, outputs behind
     // the row's end and stages behind the last the row's start.
-    Held v[kADWideBlocks];
+    Held v[MOST];
     const int rset = warp % rg, rows_here = count - rset * 16;
     if constexpr (!VEC) {
       if (tid < kADTile) {
@@ -1191,7 +1193,7 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y), VEC))
       __syncthreads();
     }
     auto load_block = [&](int st, int b) {
-      const int n = st * kADWideStage + (first_block + b) * 32, end = st < s1 ? a.N : 0;
+      const int n = st * STAGE + (first_block + b) * 32, end = st < s1 ? a.N : 0;
       if constexpr (VEC) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) v[b][u].load(y[u] - 8 * t * ES, n + 8 * t, end);
@@ -1202,11 +1204,11 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y), VEC))
     // FULL: the stage's outputs are all the row's.  ALL: the rank is the whole of the KS steps.
     auto work = [&](int st, auto full_const, auto all_const) {
       constexpr bool FULL = decltype(full_const)::value, ALL = decltype(all_const)::value;
-      const uint32_t stage = smem_u32(wide_ring) + (st - s0) % S * wide_stage_bytes(KS);
+      const uint32_t stage = smem_u32(wide_ring) + (st - s0) % S * STAGE_BYTES;
 #pragma unroll
-      for (int b = 0; b < kADWideBlocks; ++b) {
-        if (b >= blocks) break;
-        const int block = first_block + b, n = st * kADWideStage + block * 32;
+      for (int b = 0; b < MOST; ++b) {
+        if (b >= blocks || idle) break;
+        const int block = first_block + b, n = st * STAGE + block * 32;
         const uint32_t bs = stage + block * (1024 * KS);
         float acc[4][4];
         if constexpr (!ALL) {
@@ -1279,9 +1281,9 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS, sizeof(Y), VEC))
       issue(st + S - 1);
     };
 #pragma unroll
-    for (int b = 0; b < kADWideBlocks; ++b)
+    for (int b = 0; b < MOST; ++b)
       if (b < blocks) load_block(s0, b);
-    const int whole = min(s1, a.N / kADWideStage);
+    const int whole = min(s1, a.N / STAGE);
 #pragma unroll 1
     for (int st = s0; st < whole; ++st) {
       begin(st);
@@ -1318,7 +1320,7 @@ cudaError_t up_setup() {
 template <typename T, typename Y, int KS, bool VEC>
 cudaError_t wide_setup() {
   return cudaFuncSetAttribute(adapter_wide_kernel<T, Y, KS, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kADWideStages * wide_stage_bytes(KS));
+                              kADWideStages * wide_stage_bytes(KS, sizeof(Y), VEC));
 }
 
 template <typename T, typename Y, bool VEC>
@@ -1367,10 +1369,11 @@ cudaError_t launch_down(const AdapterArgs& a, int grid, cudaStream_t stream) {
 template <typename T, typename Y, int KS, bool VEC>
 cudaError_t launch_up_ks(const AdapterArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
   if (a.rows > kADOwnPlan) {
-    const int64_t most = static_cast<int64_t>(num_sms) * wide_ctas(KS, sizeof(Y), VEC);
-    const int64_t stages = max_tiles * ((a.N + kADWideStage - 1) / kADWideStage);
+    const int64_t most = static_cast<int64_t>(num_sms) * wide_ctas(KS);
+    constexpr int STAGE = wide_stage(sizeof(Y), VEC);
+    const int64_t stages = max_tiles * ((a.N + STAGE - 1) / STAGE);
     return launch_kernel(adapter_wide_kernel<T, Y, KS, VEC>, dim3(static_cast<unsigned>(stages < most ? stages : most)),
-                         dim3(kADWideThreads), static_cast<size_t>(kADWideStages * wide_stage_bytes(KS)), stream, true, a);
+                         dim3(kADWideThreads), static_cast<size_t>(kADWideStages * wide_stage_bytes(KS, sizeof(Y), VEC)), stream, true, a);
   }
   constexpr int STEP = kADStep;
   const int64_t max_steps = max_tiles * ((a.N + STEP - 1) / STEP);
