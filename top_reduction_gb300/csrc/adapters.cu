@@ -112,11 +112,11 @@ static size_t align_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255);
 // Shares of H of the first product: enough CTAs for the GPU when the tiles are few, each with
 // work for its warps.
 static int adapter_splits(int rows, int count, int H, int num_sms) {
-  if (rows > kADOwnPlan) return 1;
   const int blocks = (H + 31) / 32;
   const int64_t tiles = static_cast<int64_t>((rows + kADTile - 1) / kADTile) + (rows < count ? rows : count);
   int64_t s = num_sms / (tiles > 0 ? tiles : 1);
-  const int most = blocks / (2 * kADWarps);  // two blocks of 32 a warp at least
+  // two blocks of 32 a warp at least; calls of many rows: four stages a CTA
+  const int most = rows > kADOwnPlan ? (H + kADDownStage - 1) / kADDownStage / 4 : blocks / (2 * kADWarps);
   if (s > most) s = most;
   if (s > 8) s = 8;
   return s < 1 ? 1 : static_cast<int>(s);

@@ -424,14 +424,17 @@ __global__ void __launch_bounds__(kADThreads, RT <= 4 ? 2 : 1) adapter_down_wide
   pdl_launch_dependents();
   TileFinder finder;
   const int n_tiles = finder.start(a, ts);
-  const int stages = (a.H + kADDownStage - 1) / kADDownStage;
+  // this CTA's share of H (few tiles: several shares), in stages
+  const int all = (a.H + kADDownStage - 1) / kADDownStage;
+  const int lo = static_cast<int>(static_cast<int64_t>(all) * blockIdx.y / a.splits);
+  const int hi = static_cast<int>(static_cast<int64_t>(all) * (blockIdx.y + 1) / a.splits);
   for (int ti = blockIdx.x; ti < n_tiles; ti += gridDim.x) {
     finder.take(a, ts, ti);
     if (ts.adapter < 0) continue;  // (uniform)
     const int count = ts.count, rank = adapter_rank(a, ts.adapter);
     const T* down = reinterpret_cast<const T*>(a.down) + static_cast<int64_t>(ts.adapter) * a.down_adapter;
     auto issue = [&](int st) {
-      if (st < stages) {
+      if (st < hi) {
         // pieces of 16 bytes: 16 of an adapter row's 128 entries
         const int c = tid % 16, h = st * kADDownStage + c * 8;
         const uint32_t to = smem_u32(dw_ring) + st % S * down_wide_stage_bytes(RT) + (c / 4) * (RT * 16 * 64) + (c % 4) * 16;
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(kADThreads, RT <= 4 ? 2 : 1) adapter_down_wide
       }
       lane_copies_end();
     };
-    for (int i = 0; i < S - 1; ++i) issue(i);
+    for (int i = 0; i < S - 1; ++i) issue(lo + i);
     const char* x[2];
     bool have[2];
 #pragma unroll
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(kADThreads, RT <= 4 ? 2 : 1) adapter_down_wide
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           xv[b][u] = make_uint4(0, 0, 0, 0);
-          if (!have[u] || h + t * 8 >= a.H) continue;
+          if (!have[u] || st >= hi || h + t * 8 >= a.H) continue;
           const char* p = x[u] + static_cast<int64_t>(h) * 2;
           if (a.x_vec) {
             xv[b][u] = __ldcg(reinterpret_cast<const uint4*>(p));
@@ -480,15 +483,15 @@ __global__ void __launch_bounds__(kADThreads, RT <= 4 ? 2 : 1) adapter_down_wide
       }
     };
     float acc[NT][4] = {};
-    load_x(0);
+    load_x(lo);
     const bool work = rgroup * 16 < count;
-    for (int st = 0; st < stages; ++st) {
+    for (int st = lo; st < hi; ++st) {
       uint4 xc[2][2];
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int u = 0; u < 2; ++u) xc[b][u] = xv[b][u];
-      load_x(st + 1);  // (behind H: zeros)
+      load_x(st + 1);  // (behind the share: zeros)
       lane_copies_wait<S - 2>();
       __syncthreads();  // the stage is there, and the one before it has been read
       issue(st + S - 1);
@@ -527,7 +530,7 @@ __global__ void __launch_bounds__(kADThreads, RT <= 4 ? 2 : 1) adapter_down_wide
       for (int u = 0; u < 2; ++u) {
         const int i = rgroup * 16 + u * 8 + g;
         if (i >= count) continue;
-        float* d = a.d + static_cast<int64_t>(ts.rows[i]) * a.R;
+        float* d = a.d + (static_cast<int64_t>(blockIdx.y) * a.rows + ts.rows[i]) * a.R;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if (n * 8 >= a.R) break;
@@ -1352,7 +1355,7 @@ cudaError_t adapters_setup_one() {
 template <typename T, int RT>
 cudaError_t launch_down_rt(const AdapterArgs& a, int grid, cudaStream_t stream) {
   if (a.rows > kADOwnPlan)
-    return launch_kernel(adapter_down_wide_kernel<T, RT>, dim3(grid), dim3(kADThreads),
+    return launch_kernel(adapter_down_wide_kernel<T, RT>, dim3(grid, a.splits), dim3(kADThreads),
                          static_cast<size_t>(down_wide_smem(RT)), stream, true, a);
   return launch_kernel(adapter_down_kernel<T, RT>, dim3(grid, a.splits), dim3(kADThreads),
                        static_cast<size_t>(adapter_down_smem(RT)), stream, true, a);
