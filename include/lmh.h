@@ -646,9 +646,10 @@ size_t lmh_adapters_workspace_bytes(int32_t rows, const lmh_adapters* table);
  * requests' adapters.  Sums are held in fp32.  d enters the second product rounded to
  * dtype, and for fp32 outputs as the sum of two numbers of dtype: within 2^-16 of its value
  * for LMH_BF16 and 2^-22 for LMH_F16 (f16 parts of a row's d below 2^-28 of its largest:
- * within 2^-38 of the largest).  Rounded once, to out_dtype.  A row of x with an infinity or NaN gives infinities and
- * NaN.  The rows may come in any order, each with any adapter; a weight array is read
- * about once per 32 rows that use it, and not at all if none does.
+ * within 2^-38 of the largest).  Rounded once, to out_dtype.  A row of x with an infinity
+ * or NaN gives infinities and NaN.  The rows may come in any order, each with any adapter;
+ * an adapter's weights are read about once per 64 rows that use it, and not at all if none
+ * does.
  *
  *   x                 device [num_tokens x H] of the table's dtype, row stride
  *                     x_row_stride (>= H), aligned to its elements.
@@ -663,8 +664,8 @@ size_t lmh_adapters_workspace_bytes(int32_t rows, const lmh_adapters* table);
  *                     overlaps y in no other way, nor x.
  *   workspace         >= lmh_adapters_workspace_bytes(rows, table) bytes, 256-byte
  *                     aligned.
- * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (dtypes, rank, count, alignment),
- * LMH_ERR_WORKSPACE_TOO_SMALL, LMH_ERR_CUDA.  Device: LMH_DS_ADAPTER_OUT_OF_RANGE,
+ * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (dtypes, rank, count, alignment, sizes
+ * near 2^31), LMH_ERR_WORKSPACE_TOO_SMALL, LMH_ERR_CUDA.  Device: LMH_DS_ADAPTER_OUT_OF_RANGE,
  * LMH_DS_ROW_IDX_OUT_OF_RANGE (the row reads zeros).
  */
 lmh_status lmh_add_adapters(const void* x, int64_t x_row_stride, int32_t num_tokens, const int32_t* row_idx,
@@ -717,7 +718,7 @@ size_t lmh_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t V);
  * cannot hold is no continuation.
  *
  *   logits            device [groups * beams x V] of dtype, row stride row_stride (>= V),
- *                     aligned to sizeof(dtype); beams * V below 2^31.
+ *                     aligned to sizeof(dtype); beams * V to 2^31 - 2^16 - 1.
  *   allowed_mask      device u32 [groups * beams x mask_words] or NULL, as in lmh_sampling.
  *   workspace         >= lmh_beam_workspace_bytes(groups, beams, V) bytes, 256-byte aligned.
  * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (beams, k, misaligned logits, beams * V),
@@ -736,7 +737,7 @@ lmh_status lmh_beam_select(const lmh_beams* beams, const void* logits, lmh_dtype
  *   topk_ids, topk_logprobs  device [groups * beams x n], contiguous.  Entries with an id
  *                     below 0 or a logprob that is not finite are none.  Equal scores are
  *                     ordered by beam, then place in the list.
- * beams * n below 2^31.  No workspace is needed.  Errors: as lmh_beam_select.
+ * beams * n to 2^31 - 2^16 - 1.  No workspace is needed.  Errors: as lmh_beam_select.
  */
 lmh_status lmh_beam_select_lists(const lmh_beams* beams, const int32_t* topk_ids, const float* topk_logprobs,
                                  int32_t n, uint32_t* dev_status, cudaStream_t stream);
@@ -777,8 +778,9 @@ typedef struct lmh_row_state {
  *                     lengths[parent] are moved, and what stands behind them in dst is left
  *                     as it was.  NULL: all are moved.
  * No workspace is needed.  Errors: LMH_ERR_INVALID_ARG (null pointers, sizes, negative
- * strides, in place with other strides), LMH_ERR_UNSUPPORTED (beams, more than 2^31
- * slices), LMH_ERR_CUDA.
+ * strides, in place with other strides), LMH_ERR_UNSUPPORTED (beams, positions of
+ * 2^31 bytes or more, states of some 2^39 bytes a row), LMH_ERR_CUDA.  Device:
+ * LMH_DS_ROW_IDX_OUT_OF_RANGE, LMH_DS_TIMEOUT (rows may be partly moved then, in place too).
  */
 lmh_status lmh_reorder_rows(const lmh_row_state* states, int32_t num_states, int32_t groups, int32_t beams,
                             const int32_t* parents, const int32_t* lengths, uint32_t* dev_status,

@@ -247,3 +247,41 @@ def test_parents_in_a_state_are_refused(mod, monkeypatch):
         mod.reorder_rows([t], torch.zeros(8, dtype=torch.int32), 4, lengths=t.view(-1)[24:])
     with pytest.raises(ValueError, match="whole groups"):
         mod.reorder_rows([t], torch.zeros(8, dtype=torch.int32), 3)
+
+
+# ---------------------------------------------------------------------------
+# the largest sizes, and workspaces that are kept
+# ---------------------------------------------------------------------------
+
+def test_sizes_that_32_bits_cannot_go_through_are_refused(mod):
+    most = 2147483647 - 65536
+    lib = mod.load()
+    t = adapters(mod, N=1)
+    assert lib.lmh_adapters_workspace_bytes(most + 1, t) == 0
+    assert add(mod, t, rows=most + 1, tokens=2147483647) == UNSUPPORTED
+    for V in (most + 1, 2147483647):
+        b = beams(mod, beams=1, k=1)
+        assert lib.lmh_beam_workspace_bytes(2, 1, V) == 0
+        assert select(mod, b, V=V, stride=V) == UNSUPPORTED
+        assert lib.lmh_beam_select_lists(b, A, A, V, None, None) == UNSUPPORTED
+    assert lib.lmh_beam_workspace_bytes(2, 1, most) > 0
+    # a length times a position's bytes stays below 2^62
+    assert lib.lmh_reorder_rows(state(mod, chunk_bytes=1 << 33, position_bytes=1 << 31, src_row_bytes=1 << 33,
+                                      dst_row_bytes=1 << 33), 1, 2, 4, A, A, None, None) == UNSUPPORTED
+
+
+def test_kept_workspaces_are_a_threads_own(mod, monkeypatch):
+    """Two host threads that call on one stream: their kernels may come in turn, so their workspaces differ."""
+    import threading
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False)
+    monkeypatch.setattr(mod, "_SCRATCH", threading.local())
+    dev, got = torch.device("cpu"), []
+    mine = mod._scratch(1000, dev, 7)
+    assert mod._scratch(900, dev, 7) is mine and mod._scratch(900, dev, 8) is not mine
+    other = threading.Thread(target=lambda: got.append(mod._scratch(1000, dev, 7)))
+    other.start()
+    other.join()
+    assert got[0].data_ptr() != mine.data_ptr()
+    assert mod._scratch(mine.numel() + 1, dev, 7).numel() > mine.numel()
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: True)
+    assert mod._scratch(1000, dev, 7).data_ptr() not in (mine.data_ptr(), got[0].data_ptr())

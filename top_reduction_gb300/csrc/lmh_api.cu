@@ -20,6 +20,8 @@ namespace lmh {
 // per-device set-up
 // ---------------------------------------------------------------------------
 constexpr int kMaxDevices = 64;
+// The largest count of what adapter and beam kernels go through in 32 bits, a CTA's step of it (16384 at most) at a time.
+constexpr int32_t kMostItems = INT32_MAX - 65536;
 // What a call needs beside the device's properties: the attributes of its family's kernels
 // (setting them loads the kernels, which a call of another family is not to wait for).
 enum Family { kNoKernels = 0, kHeadAndReduction, kDraw, kQ4Projection, kAdapters, kBeams, kStates, kFamilies };
@@ -604,12 +606,12 @@ static lmh_status check_adapters(const lmh_adapters* t) {
     return LMH_ERR_UNSUPPORTED;
   if (!aligned(t->down, 16) || !aligned(t->up, 16)) return LMH_ERR_UNSUPPORTED;
   // (the kernels round H and N up to whole tiles in 32 bits)
-  if (t->H > INT32_MAX - 1024 || t->N > INT32_MAX - 65536) return LMH_ERR_UNSUPPORTED;
+  if (t->H > INT32_MAX - 1024 || t->N > kMostItems) return LMH_ERR_UNSUPPORTED;
   return LMH_OK;
 }
 
 size_t lmh_adapters_workspace_bytes(int32_t rows, const lmh_adapters* table) {
-  if (rows < 0 || check_adapters(table) != LMH_OK) return 0;
+  if (rows < 0 || rows > kMostItems || check_adapters(table) != LMH_OK) return 0;
   if (rows == 0) return 256;
   int sms = 0;
   if (device_setup(&sms, kNoKernels) != cudaSuccess) return 0;
@@ -628,6 +630,7 @@ lmh_status lmh_add_adapters(const void* x, int64_t x_row_stride, int32_t num_tok
     return LMH_ERR_INVALID_ARG;
   if (y == out && y_row_stride != out_row_stride) return LMH_ERR_INVALID_ARG;
   if (out_dtype != LMH_F32 && out_dtype != table->dtype) return LMH_ERR_UNSUPPORTED;
+  if (rows > kMostItems) return LMH_ERR_UNSUPPORTED;
   if (!aligned(x, 2) || !aligned(y, dtype_bytes(out_dtype)) || !aligned(out, dtype_bytes(out_dtype)))
     return LMH_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256)) return LMH_ERR_INVALID_ARG;
@@ -670,7 +673,7 @@ static BeamCall beam_call(const lmh_beams& b, int V, uint32_t* dev_status) {
 }
 
 size_t lmh_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t V) {
-  if (groups < 0 || beams <= 0 || beams > LMH_BEAMS_MAX || V <= 0 || static_cast<int64_t>(beams) * V > INT32_MAX ||
+  if (groups < 0 || beams <= 0 || beams > LMH_BEAMS_MAX || V <= 0 || static_cast<int64_t>(beams) * V > kMostItems ||
       static_cast<int64_t>(groups) * beams > INT32_MAX)
     return 0;
   if (groups == 0) return 256;
@@ -684,7 +687,7 @@ lmh_status lmh_beam_select(const lmh_beams* beams, const void* logits, lmh_dtype
   if (st != LMH_OK) return st;
   if (V <= 0 || row_stride < V) return LMH_ERR_INVALID_ARG;
   if (dtype != LMH_BF16 && dtype != LMH_F16 && dtype != LMH_F32) return LMH_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(beams->beams) * V > INT32_MAX) return LMH_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(beams->beams) * V > kMostItems) return LMH_ERR_UNSUPPORTED;
   if (beams->groups == 0) return LMH_OK;
   if (!logits || (allowed_mask && mask_words < (V + 31) / 32)) return LMH_ERR_INVALID_ARG;
   if (!aligned(logits, dtype_bytes(dtype))) return LMH_ERR_UNSUPPORTED;
@@ -701,7 +704,7 @@ lmh_status lmh_beam_select_lists(const lmh_beams* beams, const int32_t* topk_ids
   const lmh_status st = check_beams(beams);
   if (st != LMH_OK) return st;
   if (n <= 0) return LMH_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(beams->beams) * n > INT32_MAX) return LMH_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(beams->beams) * n > kMostItems) return LMH_ERR_UNSUPPORTED;
   if (beams->groups == 0) return LMH_OK;
   if (!topk_ids || !topk_logprobs) return LMH_ERR_INVALID_ARG;
   int sms = 0;
@@ -727,8 +730,9 @@ lmh_status lmh_reorder_rows(const lmh_row_state* states, int32_t num_states, int
     if (s.src == s.dst && (s.src_row_bytes != s.dst_row_bytes || s.src_outer_bytes[0] != s.dst_outer_bytes[0] ||
                            s.src_outer_bytes[1] != s.dst_outer_bytes[1]))
       return LMH_ERR_INVALID_ARG;
-    // slices of a chunk are at least 256 bytes, and are counted in 32 bits
-    if (s.chunk_bytes / 256 >= INT32_MAX || static_cast<int64_t>(s.n0) * s.n1 > INT32_MAX) return LMH_ERR_UNSUPPORTED;
+    // slices of a chunk are at least 256 bytes, and are counted in 32 bits; a row's bytes in use, in 64, are a length
+    // times a position
+    if (s.position_bytes > INT32_MAX || s.chunk_bytes / 256 >= INT32_MAX || static_cast<int64_t>(s.n0) * s.n1 > INT32_MAX) return LMH_ERR_UNSUPPORTED;
     slices += static_cast<int64_t>(s.n0) * s.n1 * (s.chunk_bytes / 256 + 1);
     if (slices > INT32_MAX) return LMH_ERR_UNSUPPORTED;
   }

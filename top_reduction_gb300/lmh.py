@@ -8,6 +8,7 @@ or no CUDA device is present, the calls raise.
 """
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -645,20 +646,22 @@ class AdapterTable:
         return n
 
 
-_SCRATCH = {}
+_SCRATCH = threading.local()
 _SCRATCH_MOST = 64 << 20
 
 
 def _scratch(nbytes, device, stream):
-    """A workspace for a call on the raw `stream`: one for each stream, whose calls follow one another, kept from
-    call to call (an allocation costs a few microseconds).  While a stream is captured, and for large calls,
-    one of its own: a graph may be replayed beside anything."""
+    """A workspace for a call on the raw `stream`, kept from call to call (an allocation costs a few microseconds): one
+    for each host thread and stream.  A thread's calls on a stream follow one another; two threads' kernels may come
+    in turn, one's second product behind the other's first.  While a stream is captured, and for large calls, one of
+    its own: a graph may be replayed beside anything."""
     if nbytes > _SCRATCH_MOST or torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    kept = _SCRATCH.__dict__
     key = device.index, stream
-    t = _SCRATCH.get(key)
+    t = kept.get(key)
     if t is None or t.numel() < nbytes:
-        t = _SCRATCH[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        t = kept[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
     return t
 
 
