@@ -690,7 +690,8 @@ __device__ void up_operand(const AdapterArgs& a, const TileSmem& ts, UpSmem<KS, 
 // row, neighbouring lanes copying neighbouring pieces.  The two pieces of a 32-byte sector stay together: copies of
 // one sector to two places are two reads from L2 (measured: 2x the sectors, 110 us in place of 92 for 64 rows of 48
 // adapters of rank 32).  A row stands at 32 KS times its number, its sectors' places within 128 bytes exclusive-ored
-// with two bits of the number, so that a matrix's eight rows (ldmatrix) meet in no more than two of a bank.
+// with two bits of the number and the halves' places in a sector with a third, so that no two of a matrix's eight rows
+// (ldmatrix) meet in a bank (64 rows of 48 adapters: 79 us with two to a bank, 77 so).
 template <bool VEC, int KS>
 struct UpPlaces {
   static constexpr int CH = 2 * KS;      // pieces of a row
@@ -698,7 +699,7 @@ struct UpPlaces {
   static constexpr int COPIES = kADStep / ROWS;
   __device__ __forceinline__ static int at(int row, int c) {
     const int x = VEC ? row >> 2 : KS == 1 ? 0 : KS == 2 ? (row >> 1) & 1 : row;
-    return (row * (32 * KS) + c * 16) ^ ((x & 3) << 5);
+    return (row * (32 * KS) + c * 16) ^ ((x & 3) << 5) ^ ((row >> (VEC ? 4 : 2) & 1) << 4);
   }
 };
 
@@ -1070,8 +1071,9 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_ke
   const int64_t all = stages * n_tiles;
   int64_t at = all * blockIdx.x / gridDim.x;
   const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
-  // where a weight row's piece stands in a stage: whole sectors, and the eight rows of a matrix two to a bank
-  auto place = [](int row, int c) { return (row * (32 * KS) + c * 16) ^ (((row >> 3) & 3) << 5); };
+  // where a weight row's piece stands in a stage: sectors stay whole, and no two of a matrix's eight rows meet in a
+  // bank (packed prompts: 109 us with two to a bank, 102 so)
+  auto place = [](int row, int c) { return (row * (32 * KS) + c * 16) ^ (((row >> 3) & 3) << 5) ^ ((row & 1) << 4); };
   bool waited = false;
   while (at < end) {
     const int ti = static_cast<int>(at / stages);
@@ -1109,6 +1111,32 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_ke
       lane_copies_end();
     };
     for (int i = 0; i < S - 1; ++i) issue(s0 + i);
+
+    // y of a stage; a block's is replaced by the next stage's as soon as it is used.  No branch and no condition, so
+    // that nothing waits for it before its use: rows that are not there have the first one's address, outputs behind
+    // the row's end and stages behind the last the row's start.
+    Held v[MOST];
+    const int rset = warp % rg, rows_here = count - rset * 16;
+    if constexpr (!VEC) {
+      if (tid < kADTile) {
+        const int64_t r = ts.rows[min(tid, count - 1)];
+        offs[tid / 16][0][tid % 16] = r * a.y_stride * ES;
+        offs[tid / 16][1][tid % 16] = r * a.out_stride * ES;
+      }
+      __syncthreads();
+    }
+    auto load_block = [&](int st, int b) {
+      const int n = st * STAGE + (first_block + b) * 32, end = st < s1 ? a.N : 0;
+      if constexpr (VEC) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) v[b][u].load(y[u] - 8 * t * ES, n + 8 * t, end);
+      } else {
+        v[b].load(a.y, offs[rset][0], n + lane, end);
+      }
+    };
+#pragma unroll
+    for (int b = 0; b < MOST; ++b)
+      if (b < blocks) load_block(s0, b);
     if (!waited) pdl_wait();
     waited = true;
 
@@ -1117,6 +1145,26 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_ke
     uint32_t hi[KS][4], lo[LO ? KS : 1][4];
     float back[2] = {1.0f, 1.0f};
     {
+      // (every load of a share of H is out before the first is used; what is not there is read from the row's start;
+      // one after the other: 102 us for packed prompts, 97 so)
+      float2 p[2][KS][2] = {};
+      for (int i = 0; i < a.splits; ++i) {
+        const float* d = a.d + static_cast<int64_t>(i) * a.rows * a.R + 2 * t;
+        float2 q[2][KS][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 2 * KS; ++e)  // (R is a multiple of 8)
+            q[u][e >> 1][e & 1] =
+                __ldcg(reinterpret_cast<const float2*>(d + static_cast<int64_t>(row[u]) * a.R + (e * 8 < a.R ? e * 8 : 0)));
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 2 * KS; ++e) {
+            p[u][e >> 1][e & 1].x += q[u][e >> 1][e & 1].x;
+            p[u][e >> 1][e & 1].y += q[u][e >> 1][e & 1].y;
+          }
+      }
       float v[2][KS][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -1126,16 +1174,8 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_ke
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int r = ks * 16 + h * 8 + 2 * t;
-            float2 s = make_float2(0.0f, 0.0f);
-            if (have[u] && r < rank) {  // (r is even, a.R a multiple of 8)
-              const float* d = a.d + static_cast<int64_t>(row[u]) * a.R + r;
-              for (int i = 0; i < a.splits; ++i) {
-                const float2 p = __ldcg(reinterpret_cast<const float2*>(d + static_cast<int64_t>(i) * a.rows * a.R));
-                s.x += p.x, s.y += p.y;
-              }
-            }
-            v[u][ks][2 * h] = s.x * scale;
-            v[u][ks][2 * h + 1] = r + 1 < rank ? s.y * scale : 0.0f;
+            v[u][ks][2 * h] = have[u] && r < rank ? p[u][ks][h].x * scale : 0.0f;
+            v[u][ks][2 * h + 1] = have[u] && r + 1 < rank ? p[u][ks][h].y * scale : 0.0f;
             most = fmaxf(most, fmaxf(fabsf(v[u][ks][2 * h]), fabsf(v[u][ks][2 * h + 1])));
           }
         if constexpr (std::is_same<T, __half>::value) {
@@ -1182,28 +1222,6 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_ke
       for (int kp = 0; kp < KS / 2; ++kp) from[kp] = place(mrow, 4 * kp + mi);
     }
 
-    // y of a stage; a block's is replaced by the next stage's as soon as it is used.  No branch and no condition, so
-    // that nothing waits for it before its use: rows that are not there have the first one's address, outputs behind
-    // the row's end and stages behind the last the row's start.
-    Held v[MOST];
-    const int rset = warp % rg, rows_here = count - rset * 16;
-    if constexpr (!VEC) {
-      if (tid < kADTile) {
-        const int64_t r = ts.rows[min(tid, count - 1)];
-        offs[tid / 16][0][tid % 16] = r * a.y_stride * ES;
-        offs[tid / 16][1][tid % 16] = r * a.out_stride * ES;
-      }
-      __syncthreads();
-    }
-    auto load_block = [&](int st, int b) {
-      const int n = st * STAGE + (first_block + b) * 32, end = st < s1 ? a.N : 0;
-      if constexpr (VEC) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) v[b][u].load(y[u] - 8 * t * ES, n + 8 * t, end);
-      } else {
-        v[b].load(a.y, offs[rset][0], n + lane, end);
-      }
-    };
     // FULL: the stage's outputs are all the row's.  ALL: the rank is the whole of the KS steps.
     auto work = [&](int st, auto full_const, auto all_const) {
       constexpr bool FULL = decltype(full_const)::value, ALL = decltype(all_const)::value;
@@ -1283,9 +1301,6 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_ke
       __syncthreads();  // the stage is there, and the one before it has been read
       issue(st + S - 1);
     };
-#pragma unroll
-    for (int b = 0; b < MOST; ++b)
-      if (b < blocks) load_block(s0, b);
     const int whole = min(s1, a.N / STAGE);
 #pragma unroll 1
     for (int st = s0; st < whole; ++st) {
