@@ -971,16 +971,17 @@ __global__ void __launch_bounds__(32 * up_warps(KS), 1) adapter_up_kernel(const 
 // Here the batch's rows are the MMA's A operand (16 a warp, held in registers for a whole tile) and 8 rows of the
 // weights the B operand.  A lane's part of d and its two rows of y and out stay the same from step to step, which
 // leaves about a fifth of the instructions of the kernel above per output (packed prompts, 16384 rows of rank 64 x
-// 4096: 108 us there).  The weights come in stages of wide_stage() outputs that the whole CTA copies and reads;
+// 4096: 108 us there).  The weights come in stages of kADWideStage outputs that the whole CTA copies and reads;
 // warps share a stage by rows (one for every 16 of the tile's) and by outputs.  A block is 32 outputs; column c of
 // its tile j stands for output 8 (c / 2) + 2 j + c % 2, so that a lane has eight neighbours of a row.
 constexpr int kADWideThreads = 256;
 constexpr int kADWideWarps = kADWideThreads / 32;
 constexpr int kADWideStages = 3;
-// Outputs of a stage: of 64-row tiles a warp takes four blocks, or the two that leave registers for a second CTA on the
-// SM where y takes twice of them (fp32, 1257 rows of rank 64 x 23728: 109 us with four).
-constexpr int wide_stage(int es, bool vec) { return es == 2 && vec ? 256 : 128; }
-constexpr int wide_stage_bytes(int ks, int es, bool vec) { return wide_stage(es, vec) * 32 * ks; }
+// Outputs of a stage: of 64-row tiles a warp takes two blocks.  (Four, and a ring twice as large: 75 us for packed
+// prompts' second product where this takes 60, and 109 for 1257 fp32 rows of rank 64 x 23728 where this takes 98.
+// What is in flight queues then: even the copies' issue waited 1500 cycles a stage.)
+constexpr int kADWideStage = 128;
+constexpr int wide_stage_bytes(int ks) { return kADWideStage * 32 * ks; }
 
 // Eight neighbouring outputs of a row, read and written 16 bytes at a time.
 template <typename Y>
@@ -1057,7 +1058,7 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_ke
   __shared__ TileSmem ts;
   constexpr bool LO = sizeof(Y) == 4;
   constexpr int ES = static_cast<int>(sizeof(Y)), CH = 2 * KS, S = kADWideStages;
-  constexpr int STAGE = wide_stage(ES, VEC), STAGE_BYTES = wide_stage_bytes(KS, ES, VEC), MOST = STAGE / 64;  // MOST: blocks a warp
+  constexpr int STAGE = kADWideStage, STAGE_BYTES = wide_stage_bytes(KS), MOST = STAGE / 64;  // MOST: blocks a warp
   constexpr int ROWS = kADWideThreads / CH;  // weight rows that the CTA copies at a time
   using Held = typename std::conditional<VEC, Eight<Y>[2], Sixteen<Y>>::type;  // y of a lane and block
   constexpr int PITCH = 36;
@@ -1338,7 +1339,7 @@ cudaError_t up_setup() {
 template <typename T, typename Y, int KS, bool VEC>
 cudaError_t wide_setup() {
   return cudaFuncSetAttribute(adapter_wide_kernel<T, Y, KS, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kADWideStages * wide_stage_bytes(KS, sizeof(Y), VEC));
+                              kADWideStages * wide_stage_bytes(KS));
 }
 
 template <typename T, typename Y, bool VEC>
@@ -1388,10 +1389,10 @@ template <typename T, typename Y, int KS, bool VEC>
 cudaError_t launch_up_ks(const AdapterArgs& a, int64_t max_tiles, int num_sms, cudaStream_t stream) {
   if (a.rows > kADOwnPlan) {
     const int64_t most = static_cast<int64_t>(num_sms) * wide_ctas(KS);
-    constexpr int STAGE = wide_stage(sizeof(Y), VEC);
+    constexpr int STAGE = kADWideStage;
     const int64_t stages = max_tiles * ((a.N + STAGE - 1) / STAGE);
     return launch_kernel(adapter_wide_kernel<T, Y, KS, VEC>, dim3(static_cast<unsigned>(stages < most ? stages : most)),
-                         dim3(kADWideThreads), static_cast<size_t>(kADWideStages * wide_stage_bytes(KS, sizeof(Y), VEC)), stream, true, a);
+                         dim3(kADWideThreads), static_cast<size_t>(kADWideStages * wide_stage_bytes(KS)), stream, true, a);
   }
   constexpr int STEP = kADStep;
   const int64_t max_steps = max_tiles * ((a.N + STEP - 1) / STEP);
