@@ -255,3 +255,17 @@ def test_binding_refusals(lmh, change, what):
         a[k] = made[v]()
     with pytest.raises(ValueError, match=what):
         lmh.add_adapters(**a)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("rows,H,N,R,L", [(300, 64, 4, 8, 3), (257, 128, 516, 16, 4), (700, 72, 1004, 32, 2),
+                                          (290, 256, 780, 64, 5), (513, 96, 260, 128, 3)])
+def test_16_bit_rows_that_align_to_8_bytes(lmh, rows, H, N, R, L, dtype):
+    c = _case(rows, H, N, R, L, dtype, dtype, seed=N, ranks=True)
+    want = _run(lmh, c)
+    _check(c, want)
+    wide = torch.full((rows, N + 8), 7.0, dtype=dtype, device="cuda")
+    wide[:, 4:N + 4] = c["y"]
+    _run(lmh, dict(c, y=wide[:, 4:N + 4]), out=wide[:, 4:N + 4])  # in place, 8 bytes into a row
+    assert torch.equal(wide[:, 4:N + 4], want)
+    assert (wide[:, :4] == 7).all() and (wide[:, N + 4:] == 7).all()

@@ -162,10 +162,9 @@ static cudaError_t launch_adapters(const AdapterArgs& a, bool bf16, lmh_dtype ou
   return e;
 }
 
-// Whether rows of y or out can be read and written a lane's neighbours at a time (16 bytes, or four 16-bit outputs in
-// calls of few rows).
-static bool adapter_rows_align(const void* p, int64_t stride, int N, lmh_dtype dtype, int rows) {
-  const int n = dtype != LMH_F32 && rows > kADOwnPlan ? 8 : 4, bytes = n * (dtype == LMH_F32 ? 4 : 2);
+// Whether rows of y or out can be read and written n neighbours at a time.
+static bool adapter_rows_align(const void* p, int64_t stride, int N, lmh_dtype dtype, int n) {
+  const int bytes = n * (dtype == LMH_F32 ? 4 : 2);
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride % n == 0 && N % n == 0;
 }
 
@@ -198,8 +197,11 @@ cudaError_t launch_add_adapters(const void* x, int64_t x_stride, int num_tokens,
   a.out = static_cast<char*>(out);
   a.out_stride = out_stride;
   a.in_place = y == out && y_stride == out_stride;
-  const bool vec = adapter_rows_align(y, y_stride, t.N, out_dtype, rows) &&
-                   adapter_rows_align(out, out_stride, t.N, out_dtype, rows);
+  auto align = [&](int n) {
+    return adapter_rows_align(y, y_stride, t.N, out_dtype, n) && adapter_rows_align(out, out_stride, t.N, out_dtype, n);
+  };
+  const bool vec = align(4);
+  a.piece = out_dtype == LMH_F32 || align(8) ? 16 : 8;
   a.splits = adapter_splits(rows, t.count, t.H, num_sms);
   char* p = static_cast<char*>(workspace);
   a.tile_count = reinterpret_cast<int32_t*>(p);

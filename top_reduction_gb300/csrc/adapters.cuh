@@ -63,6 +63,7 @@ struct AdapterArgs {
   char* out;
   int64_t out_stride;
   bool in_place;
+  int piece;  // calls of many rows: bytes that rows of y and out can be read and written at a time (8, 16)
   // workspace
   int32_t* tile_count;  // written by the plan kernel, as are tiles and order
   AdapterTile* tiles;
@@ -983,18 +984,25 @@ constexpr int kADWideStages = 3;
 constexpr int kADWideStage = 128;
 constexpr int wide_stage_bytes(int ks) { return kADWideStage * 32 * ks; }
 
-// Eight neighbouring outputs of a row, read and written 16 bytes at a time.
-template <typename Y>
+// Eight neighbouring outputs of a row, read and written in pieces of PIECE bytes: 16, or 8 where 16-bit rows align for
+// no more (N a multiple of 4: 1591 rows of rank 16 x 42180 bf16 take 84 us so, 141 as unaligned rows).
+template <typename Y, int PIECE>
 struct Eight {
-  static constexpr int ES = static_cast<int>(sizeof(Y));
+  static constexpr int ES = static_cast<int>(sizeof(Y)), PN = PIECE / ES;  // PN: outputs of a piece
   uint32_t w[2 * ES];
   // Outputs n .. n + 7 of the row at `row`; pieces that are not below `end` are read from its start.
   __device__ __forceinline__ void load(const char* row, int n, int end) {
 #pragma unroll
-    for (int p = 0; p < ES / 2; ++p) {
-      const int at = n + p * (16 / ES);
-      const uint4 v = *reinterpret_cast<const uint4*>(row + static_cast<int64_t>(at < end ? at : 0) * ES);
-      w[4 * p] = v.x, w[4 * p + 1] = v.y, w[4 * p + 2] = v.z, w[4 * p + 3] = v.w;
+    for (int p = 0; p < 8 / PN; ++p) {
+      const int at = n + p * PN;
+      const char* from = row + static_cast<int64_t>(at < end ? at : 0) * ES;
+      if constexpr (PIECE == 16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(from);
+        w[4 * p] = v.x, w[4 * p + 1] = v.y, w[4 * p + 2] = v.z, w[4 * p + 3] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(from);
+        w[2 * p] = v.x, w[2 * p + 1] = v.y;
+      }
     }
   }
   // d[e] times `by` is added to output e, and those below `left` are written.
@@ -1014,7 +1022,12 @@ struct Eight {
         const float2 v = C::pair(w[i]);
         r[i] = C::pack(fmaf(d[2 * i], by, v.x), fmaf(d[2 * i + 1], by, v.y));
       }
-      if (left > 0) *reinterpret_cast<uint4*>(row) = make_uint4(r[0], r[1], r[2], r[3]);
+      if constexpr (PIECE == 16) {
+        if (left > 0) *reinterpret_cast<uint4*>(row) = make_uint4(r[0], r[1], r[2], r[3]);
+      } else {
+        if (left > 0) *reinterpret_cast<uint2*>(row) = make_uint2(r[0], r[1]);
+        if (left > 4) *reinterpret_cast<uint2*>(row + 8) = make_uint2(r[2], r[3]);
+      }
     }
   }
 };
@@ -1052,15 +1065,16 @@ struct Sixteen {
 
 constexpr int wide_ctas(int ks) { return ks <= 4 ? 2 : 1; }
 
-template <typename T, typename Y, int KS, bool VEC>
+// PIECE: bytes of a row that are read and written at once, 0: its elements.
+template <typename T, typename Y, int KS, int PIECE>
 __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_kernel(const AdapterArgs a) {
   extern __shared__ __align__(128) unsigned char wide_ring[];
   __shared__ TileSmem ts;
-  constexpr bool LO = sizeof(Y) == 4;
+  constexpr bool LO = sizeof(Y) == 4, VEC = PIECE != 0;
   constexpr int ES = static_cast<int>(sizeof(Y)), CH = 2 * KS, S = kADWideStages;
   constexpr int STAGE = kADWideStage, STAGE_BYTES = wide_stage_bytes(KS), MOST = STAGE / 64;  // MOST: blocks a warp
   constexpr int ROWS = kADWideThreads / CH;  // weight rows that the CTA copies at a time
-  using Held = typename std::conditional<VEC, Eight<Y>[2], Sixteen<Y>>::type;  // y of a lane and block
+  using Held = typename std::conditional<VEC, Eight<Y, VEC ? PIECE : 16>[2], Sixteen<Y>>::type;  // y of a lane and block
   constexpr int PITCH = 36;
   __shared__ float cross[VEC ? 1 : kADWideWarps][VEC ? 1 : 16 * PITCH];
   __shared__ int64_t offs[VEC ? 1 : 4][2][VEC ? 1 : 16];  // [16 rows of the tile][y, out]: the rows' first bytes
@@ -1336,10 +1350,17 @@ cudaError_t up_setup() {
                               up_warps(KS) * up_warp_bytes(KS, sizeof(Y)));
 }
 
+template <typename T, typename Y, int KS, int PIECE>
+cudaError_t wide_setup_piece() {
+  return cudaFuncSetAttribute(adapter_wide_kernel<T, Y, KS, PIECE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kADWideStages * wide_stage_bytes(KS));
+}
 template <typename T, typename Y, int KS, bool VEC>
 cudaError_t wide_setup() {
-  return cudaFuncSetAttribute(adapter_wide_kernel<T, Y, KS, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kADWideStages * wide_stage_bytes(KS));
+  cudaError_t e = wide_setup_piece<T, Y, KS, VEC ? 16 : 0>();
+  if constexpr (VEC && sizeof(Y) == 2)
+    if (e == cudaSuccess) e = wide_setup_piece<T, Y, KS, 8>();
+  return e;
 }
 
 template <typename T, typename Y, bool VEC>
@@ -1391,8 +1412,12 @@ cudaError_t launch_up_ks(const AdapterArgs& a, int64_t max_tiles, int num_sms, c
     const int64_t most = static_cast<int64_t>(num_sms) * wide_ctas(KS);
     constexpr int STAGE = kADWideStage;
     const int64_t stages = max_tiles * ((a.N + STAGE - 1) / STAGE);
-    return launch_kernel(adapter_wide_kernel<T, Y, KS, VEC>, dim3(static_cast<unsigned>(stages < most ? stages : most)),
-                         dim3(kADWideThreads), static_cast<size_t>(kADWideStages * wide_stage_bytes(KS)), stream, true, a);
+    const dim3 grid(static_cast<unsigned>(stages < most ? stages : most));
+    constexpr size_t smem = kADWideStages * wide_stage_bytes(KS);
+    if constexpr (VEC && sizeof(Y) == 2)
+      if (a.piece == 8)
+        return launch_kernel(adapter_wide_kernel<T, Y, KS, 8>, grid, dim3(kADWideThreads), smem, stream, true, a);
+    return launch_kernel(adapter_wide_kernel<T, Y, KS, VEC ? 16 : 0>, grid, dim3(kADWideThreads), smem, stream, true, a);
   }
   constexpr int STEP = kADStep;
   const int64_t max_steps = max_tiles * ((a.N + STEP - 1) / STEP);
