@@ -3,19 +3,24 @@
 //
 //   out[i][n] = y[i][n] + scale_l * sum_r up[l][n][r] * d[i][r],   d[i][r] = sum_h down[l][r][h] * x[i][h]
 //
-// with l = adapter_idx[i].  The rows are cut into tiles of up to kADTile rows of one adapter.  One kernel
-// makes d of every tile, the next the second product, added to y.  Up to kADOwnPlan rows every CTA works out
-// the tiles from the indices by itself; above, a kernel before the two sorts the rows by adapter.
+// with l = adapter_idx[i].  The rows are cut into tiles of up to kADTile rows of one adapter.  One kernel makes d of
+// every tile, the next the second product, added to y.
 //
-// Both products run on mma.sync m16n8k16 with 16 rows of the weights as the A operand and 8 rows of the
-// batch as the B operand: a batch of one row costs the same weight reads as one of eight, and weights go
-// from memory to the MMA's registers without a stop in shared memory.  The order of the entries along the
-// inner dimension is free as long as A and B agree, so a lane takes 16 contiguous bytes of a weight row.
+// To kADOwnPlan rows every CTA works out the tiles from the indices by itself.  Both products run on mma.sync
+// m16n8k16 with 16 rows of the weights as the A operand and 8 rows of the batch as the B operand: a tile of one row
+// costs the same weight reads as one of eight, and the weights' bytes bound calls of few rows (64 rows of 48 adapters
+// of ranks to 32, f16, x 128256: the second product reads 411 MB from DRAM in 77 us, 0.8 of the copy rate; the ranks in
+// use are half of it, but DRAM hands out 64 bytes at a time, a whole row of rank 32).  Above, a kernel before the
+// two sorts the rows by adapter; the batch's rows are the A operand, 16 a warp, and a CTA shares the weights: rows'
+// bytes bound these calls (packed prompts, 16384 rows of rank 64, 1024 -> 4096: 83 us for 304 MB, 0.54 of the copy rate).
+//
+// The order of the entries along the inner dimension is free as long as A and B agree, so in the first product a lane
+// takes 16 contiguous bytes of a weight row and of x.
 //
 // d enters the second product in 16 bits: for fp32 outputs as two parts, high and low (16 bits of its value for
 // bf16, 22 for f16), so that its rounding stays near that of the fp32 sums; for 16-bit outputs as one, which rounds
 // the added part as its own type would be rounded.  (The second part doubles the MMAs and the operand's reads from
-// shared memory, which bound the product for packed prompts.)
+// shared memory.)
 #pragma once
 
 #include <type_traits>
@@ -145,7 +150,7 @@ struct Half16<__half> {
 // ---------------------------------------------------------------------------
 // Weights, x and y come through rings in shared memory in which every lane copies (cp.async) what it will
 // itself read, in the order of its registers: no barrier, no bank conflict, and as many bytes in flight as the
-// ring holds, which registers do not (measured: DESIGN).
+// ring holds, which registers do not (33 rows of 8 adapters x 151936: 56 us with loads to registers, 21 so).
 // (The form that fills up with zeros was measured slower: 17 million wavefronts of shared memory in place of 6.)
 template <int BYTES>
 __device__ __forceinline__ void lane_copy(uint32_t smem_dst, const void* src) {
@@ -257,7 +262,8 @@ __device__ __forceinline__ int adapter_rank(const AdapterArgs& a, int adapter) {
 // ---------------------------------------------------------------------------
 // first product
 // ---------------------------------------------------------------------------
-// One CTA a (tile, share of H).  A warp takes 16 rows of a small tile (or what there is of them), 32 of a
+// One CTA a (tile, share of H).  Few rows are bound by latency here (33 rows of 2560 x rank 16: 7 us alone, of which
+// the weights' 0.7 MB take 0.1).  A warp takes 16 rows of a small tile (or what there is of them), 32 of a
 // larger one, so one or two warps share the tile by rows and the others the blocks of 32 entries of H; their
 // sums meet in shared memory in a fixed order.  RT: tiles of 16 adapter rows.
 constexpr int adapter_down_depth(int rt) { return rt == 8 ? 2 : 4; }
@@ -405,7 +411,9 @@ __global__ void __launch_bounds__(kADThreads) adapter_down_kernel(const AdapterA
 // The batch's rows are the MMA's A operand, 16 a warp, and 8 adapter rows the B operand: the tile's four row groups
 // share the weights, which come in stages of 128 entries of H that the whole CTA copies; two warps share a row group
 // by entries of H.  As above a lane takes 16 contiguous bytes of a row for two steps of 16, so the operands need no
-// transposition: a lane's registers of x are its own loads, a stage ahead.
+// transposition: a lane's registers of x are its own loads, a stage ahead.  (16384 rows of 1024 x rank 64: 22 us alone,
+// 31 MB from DRAM; a wave of 261 tiles that each wait for their own eight stages.  x two stages ahead, 2 or 5 stages
+// of weights: the same or slower.)
 constexpr int kADDownStage = 128;  // entries of H: four blocks of 32
 constexpr int kADDownStages = 3;
 constexpr int down_wide_stage_bytes(int rt) { return rt * 16 * kADDownStage * 2; }
@@ -972,9 +980,11 @@ __global__ void __launch_bounds__(32 * up_warps(KS), 1) adapter_up_kernel(const 
 // Here the batch's rows are the MMA's A operand (16 a warp, held in registers for a whole tile) and 8 rows of the
 // weights the B operand.  A lane's part of d and its two rows of y and out stay the same from step to step, which
 // leaves about a fifth of the instructions of the kernel above per output (packed prompts, 16384 rows of rank 64 x
-// 4096: 108 us there).  The weights come in stages of kADWideStage outputs that the whole CTA copies and reads;
-// warps share a stage by rows (one for every 16 of the tile's) and by outputs.  A block is 32 outputs; column c of
-// its tile j stands for output 8 (c / 2) + 2 j + c % 2, so that a lane has eight neighbours of a row.
+// 4096: 108 us there, 60 here).  268 MB of rows make a floor of 40 us; issue slots are 35% busy and DRAM 60%: what is
+// left is latency, of a tile's start and of the stages' barriers, with 16 warps an SM.
+// The weights come in stages of kADWideStage outputs that the whole CTA copies and reads; warps share a stage by rows
+// (one for every 16 of the tile's) and by outputs.  A block is 32 outputs; column c of its tile j stands for output
+// 8 (c / 2) + 2 j + c % 2, so that a lane has eight neighbours of a row.
 constexpr int kADWideThreads = 256;
 constexpr int kADWideWarps = kADWideThreads / 32;
 constexpr int kADWideStages = 3;

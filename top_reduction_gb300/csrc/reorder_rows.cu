@@ -6,8 +6,10 @@
 // take is read once.
 //
 //   * reorder_bulk_kernel, for states whose rows and chunks begin on 16-byte boundaries: one warp a CTA, bulk
-//     copies into a ring of stages and from there to the rows that take them; no byte passes a register.
-//   * reorder_rows_kernel, for the others and for calls that move little: plain loads and stores.
+//     copies into a ring of stages and from there to the rows that take them; no byte passes a register.  Bound
+//     by the bytes moved: caches of four layers (420 MB read, 420 written) take 153 us, 0.81 of the copy rate.
+//   * reorder_rows_kernel, for the others and for calls that move little: plain loads and stores.  A step's
+//     histories and block tables (256 rows, 4.9 MB read and written): 4.5 us in a graph, latency.  (With it alone the caches take 308 us.)
 #include "device_common.cuh"
 #include "lmh_internal.h"
 
@@ -134,6 +136,8 @@ __global__ void __launch_bounds__(kRRThreads) reorder_rows_kernel(const __grid_c
 // ---------------------------------------------------------------------------
 // bulk copies
 // ---------------------------------------------------------------------------
+// (caches of four layers, 153 us; 4 stages of 24 KB: 162; 3 CTAs of 4 stages of 16 KB: 157, of 3 of 24 KB: 204;
+// 1 CTA of 6 stages: 232)
 constexpr int kRBStages = 3;
 constexpr int kRBCtasPerSm = 2;
 constexpr int kRBStageBytes = 32 * 1024;
