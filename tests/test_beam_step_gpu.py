@@ -160,3 +160,93 @@ def test_first_calls_need_no_other_family(lmh):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_two_threads_on_one_stream(lmh):
+    """Two host threads' kernels may come in turn on the stream that both call on."""
+    import threading
+    main = torch.cuda.current_stream()
+    cases = []
+    for i, rows in enumerate((300, 40)):
+        ad = lmh.AdapterTable(_randn(20 + i, 4, 16, 256).to(torch.bfloat16), _randn(22 + i, 4, 520, 16).to(torch.bfloat16))
+        c = dict(x=_randn(24 + i, rows, 256).to(torch.bfloat16), table=ad, y=_randn(26 + i, rows, 520),
+                 adapter_idx=(torch.arange(rows, device="cuda") * 3 % 5 - 1).int())
+        z, s = _randn(28 + i, 12, 9001), -_randn(30 + i, 12).abs()
+        cases.append((c, z, s, lmh.add_adapters(**c), lmh.beam_select(z, s, 4)["scores"]))
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def calls(i):
+        c, z, s = cases[i][:3]
+        with torch.cuda.stream(main):
+            for _ in range(200):
+                got[i].append((lmh.add_adapters(**c), lmh.beam_select(z, s, 4)["scores"]))
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 200
+        for a, b in got[i]:
+            assert torch.equal(a, cases[i][3]) and torch.equal(b, cases[i][4])
+
+
+def test_graphs_and_eager_calls_have_workspaces_of_their_own(lmh):
+    """A graph captured without a workspace is replayed on one stream while eager calls run on another."""
+    x, y = _randn(1, 300, 256).to(torch.bfloat16), _randn(2, 300, 512)
+    ad = lmh.AdapterTable(_randn(3, 4, 16, 256).to(torch.bfloat16), _randn(4, 4, 512, 16).to(torch.bfloat16))
+    idx = (torch.arange(300, device="cuda") * 3 % 5 - 1).int()
+    z, s = _randn(5, 64, 30000), -_randn(6, 64).abs()
+    other = (torch.arange(300, device="cuda") % 4).int()
+    want = lmh.add_adapters(x, ad, idx, y), lmh.beam_select(z, s, 4)["scores"].clone()
+    want2 = lmh.add_adapters(x, ad, other, y), lmh.beam_select(z + 1, s - 1, 4)["scores"].clone()
+    z2, s2 = z + 1, s - 1
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a, b = lmh.add_adapters(x, ad, idx, y), lmh.beam_select(z, s, 4)["scores"]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        a.zero_()
+        b.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        got = [(lmh.add_adapters(x, ad, other, y), lmh.beam_select(z2, s2, 4)["scores"]) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+        assert all(torch.equal(p, want2[0]) and torch.equal(q, want2[1]) for p, q in got)
+
+
+@pytest.mark.parametrize("rows", [3, 258])
+def test_offsets_behind_32_bits(lmh, rows):
+    """Rows, adapters and outputs further apart than 2^31 elements (few of them: 258 rows share a row of x)."""
+    far = (1 << 30) + 8
+    big = torch.zeros(3 * far, dtype=torch.bfloat16, device="cuda")
+    H, N, R = 64, 520, 16
+    down, up = _randn(1, 3, R, H).to(torch.bfloat16), _randn(2, 3, N, R).to(torch.bfloat16)
+    x = _randn(3, 3, H).to(torch.bfloat16)
+    at = 0  # each in its own part of the far rows
+    views = []
+    for t in (down, up, x):
+        v = big.as_strided(t.shape, (far,) + t.stride()[1:], at)
+        v.copy_(t)
+        views.append(v)
+        at += (t[0].numel() + 63) // 64 * 64
+    row_idx = (torch.arange(rows, device="cuda") % 3).int()
+    idx = ((torch.arange(rows, device="cuda") + 1) % 3).int()
+    y = _randn(4, rows, N).to(torch.bfloat16)
+    want = lmh.add_adapters(x, lmh.AdapterTable(down, up), idx, y, row_idx=row_idx)
+    got = lmh.add_adapters(views[2], lmh.AdapterTable(views[0], views[1]), idx, y, row_idx=row_idx)
+    assert torch.equal(got, want)
+    if rows == 3:  # outputs and logits too
+        out = big.as_strided((3, N), (far, 1), at)
+        out.copy_(y)
+        lmh.add_adapters(views[2], lmh.AdapterTable(views[0], views[1]), idx, out, row_idx=row_idx, out=out)
+        assert torch.equal(out, want)
+        s = torch.zeros(3, device="cuda")
+        a, b = lmh.beam_select(out, s, 3), lmh.beam_select(want, s, 3)
+        assert all(torch.equal(a[k], b[k]) for k in a)
