@@ -725,6 +725,11 @@ constexpr int up_depth(int ks, int es, int c) {
   return n < 8 ? n : 8;
 }
 
+// A tile's start (its rows, the first copies, d) takes a CTA about as long as this many steps: 33 rows of 8 adapters x
+// 151936 take 20.5 us in a graph with equal shares, 19.0 so.  Not more than a part of a tile, as shares of small calls
+// would be all start (5 rows x 4096: 4.5 us, 4.8 with 64 steps).
+__device__ __forceinline__ int up_start(int64_t steps) { return static_cast<int>(min(static_cast<int64_t>(96), steps / 32)); }
+
 // A warp's part of a tile's outputs [.., n_end): every step that is the warp's.  C: column tiles of an entry; a tile of
 // more rows has several entries a step, of which the first brings the weights.
 // start(): the copies that fill the ring; run(): the rest, once d stands in sm.
@@ -939,15 +944,19 @@ __global__ void __launch_bounds__(32 * up_warps(KS), 1) adapter_up_kernel(const 
   // wait for its end, and what the plan kernel wrote has been waited for
   TileFinder finder;
   const int n_tiles = finder.start(a, ts);
-  const int64_t steps = (a.N + STEP - 1) / STEP;
+  // a share that goes on in a second tile is shorter by what the tile's start takes
+  const int start = up_start((a.N + STEP - 1) / STEP);
+  const int64_t steps = (a.N + STEP - 1) / STEP + start;
   const int64_t all = steps * n_tiles;
   int64_t at = all * blockIdx.x / gridDim.x;
   const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
   bool waited = false;
   while (at < end) {
     const int ti = static_cast<int>(at / steps);
-    const int s0 = static_cast<int>(at - ti * steps), s1 = static_cast<int>(min(steps, s0 + (end - at)));
-    at += s1 - s0;
+    const int from = static_cast<int>(at - ti * steps), to = static_cast<int>(min(steps, from + (end - at)));
+    at += to - from;
+    const int s0 = max(0, from - start), s1 = max(0, to - start);
+    if (s0 == s1) continue;
     finder.take(a, ts, ti);
     const int count = ts.count, rank = adapter_rank(a, ts.adapter);
     if (tid < kADTile) {
