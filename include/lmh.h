@@ -721,7 +721,7 @@ size_t lmh_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t V);
  *                     aligned to sizeof(dtype); beams * V to 2^31 - 2^16 - 1.
  *   allowed_mask      device u32 [groups * beams x mask_words] or NULL, as in lmh_sampling.
  *   workspace         >= lmh_beam_workspace_bytes(groups, beams, V) bytes, 256-byte aligned.
- * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (beams, k, misaligned logits, beams * V),
+ * Errors: LMH_ERR_INVALID_ARG, LMH_ERR_UNSUPPORTED (beams, k, misaligned logits or mask, beams * V),
  * LMH_ERR_WORKSPACE_TOO_SMALL, LMH_ERR_CUDA.  Device: LMH_DS_NO_ALLOWED_TOKEN (a group
  * without a continuation), LMH_DS_TIMEOUT.
  */

@@ -285,3 +285,7 @@ def test_kept_workspaces_are_a_threads_own(mod, monkeypatch):
     assert mod._scratch(mine.numel() + 1, dev, 7).numel() > mine.numel()
     monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: True)
     assert mod._scratch(1000, dev, 7).data_ptr() not in (mine.data_ptr(), got[0].data_ptr())
+
+
+def test_misaligned_mask_is_refused(mod):
+    assert select(mod, beams(mod), mask=A + 2, words=32) == UNSUPPORTED

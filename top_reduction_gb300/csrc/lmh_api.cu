@@ -690,7 +690,7 @@ lmh_status lmh_beam_select(const lmh_beams* beams, const void* logits, lmh_dtype
   if (static_cast<int64_t>(beams->beams) * V > kMostItems) return LMH_ERR_UNSUPPORTED;
   if (beams->groups == 0) return LMH_OK;
   if (!logits || (allowed_mask && mask_words < (V + 31) / 32)) return LMH_ERR_INVALID_ARG;
-  if (!aligned(logits, dtype_bytes(dtype))) return LMH_ERR_UNSUPPORTED;
+  if (!aligned(logits, dtype_bytes(dtype)) || !aligned(allowed_mask, 4)) return LMH_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256)) return LMH_ERR_INVALID_ARG;
   if (workspace_bytes < beam_workspace_bytes(beams->groups * beams->beams, V)) return LMH_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
