@@ -645,53 +645,74 @@ struct UpSmem {
   int64_t y[kADTile], out[kADTile];  // the rows' first bytes
 };
 
-// All threads: a tile's d, scaled, into sm.
-template <typename T, int KS, bool LO>
+// All threads: a tile's d, scaled, into sm.  A warp takes every W-th row, four at a time, all of whose loads of a share
+// of H are out before the first is used (128 rows of rank 64, 4096 -> 4096: 27 us with a row at a time, 17 so, which
+// takes 8 warps in place of 16 for rank 64).
+template <typename T, int KS, bool LO, int W>
 __device__ void up_operand(const AdapterArgs& a, const TileSmem& ts, UpSmem<KS, LO>& sm, int rank) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int count = ts.count, cols = (count + 7) / 8;
   const float scale = ts.adapter < 0 ? 0.0f : a.scales ? __ldcg(a.scales + ts.adapter) : 1.0f;
-  constexpr int PER = (KS * 16 + 31) / 32;  // entries a lane; a warp takes a row at a time
-  for (int i = warp; i < cols * 8; i += blockDim.x / 32) {
-    float v[PER];
-    float most = 0.0f;
+  constexpr int PER = (KS * 16 + 31) / 32;  // entries a lane
+  auto rows = [&](auto rows_const, int first) {  // of a warp
+    constexpr int K = decltype(rows_const)::value;
+    float v[K][PER] = {};
+    const float* d[K];
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const int r = u * 32 + lane;
-      v[u] = 0.0f;
-      if (i < count && r < rank) {
-        const float* d = a.d + static_cast<int64_t>(ts.rows[i]) * a.R + r;
-        for (int s = 0; s < a.splits; ++s) v[u] += __ldcg(d + static_cast<int64_t>(s) * a.rows * a.R);
-        v[u] *= scale;
+    for (int k = 0; k < K; ++k) d[k] = a.d + static_cast<int64_t>(ts.rows[min(first + k * W, count - 1)]) * a.R;
+    if (rank > 0 && first < count) {
+#pragma unroll (K == 1 ? 4 : 2)
+      for (int s = 0; s < a.splits; ++s) {
+        const int64_t off = static_cast<int64_t>(s) * a.rows * a.R;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int u = 0; u < PER; ++u) v[k][u] += __ldcg(d[k] + off + min(u * 32 + lane, a.R - 1));
       }
-      most = fmaxf(most, fabsf(v[u]));
-    }
-    float by = 1.0f;
-    if constexpr (std::is_same<T, __half>::value) {
-      // f16: the row's largest value goes into [2^13, 2^14), which is exact
-      float back = 1.0f;
-      most = warp_max(most);
-      if (most > 0.0f && most < INFINITY) {
-        const int e = min(max(ilogbf(most), -112), 127);
-        by = ldexpf(1.0f, 13 - e);
-        back = ldexpf(1.0f, e - 13);
-      }
-      if (lane == 0) sm.unscale[i] = back;
     }
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const int r = u * 32 + lane;
-      if (r >= KS * 16) break;
-      const float f = v[u] * by;
-      const uint16_t high = Half16<T>::bits(f);
-      const int reg = (r >> 3) & 1;  // of the step r / 16, in the lane of r's pair
-      uint16_t* p = reinterpret_cast<uint16_t*>(&sm.frag[r >> 4][i >> 3][(i & 7) * 4 + ((r & 7) >> 1)]);
-      p[reg * 2 + (r & 1)] = high;
-      if constexpr (LO) {
-        const float hv = Half16<T>::value(high);
-        p[4 + reg * 2 + (r & 1)] = Half16<T>::bits(fabsf(hv) < INFINITY ? f - hv : 0.0f);
+    for (int k = 0; k < K; ++k) {
+      const int i = first + k * W;
+      if (i >= cols * 8) break;
+      float most = 0.0f;
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        v[k][u] = i < count && u * 32 + lane < rank ? v[k][u] * scale : 0.0f;
+        most = fmaxf(most, fabsf(v[k][u]));
+      }
+      float by = 1.0f;
+      if constexpr (std::is_same<T, __half>::value) {
+        // f16: the row's largest value goes into [2^13, 2^14), which is exact
+        float back = 1.0f;
+        most = warp_max(most);
+        if (most > 0.0f && most < INFINITY) {
+          const int e = min(max(ilogbf(most), -112), 127);
+          by = ldexpf(1.0f, 13 - e);
+          back = ldexpf(1.0f, e - 13);
+        }
+        if (lane == 0) sm.unscale[i] = back;
+      }
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int r = u * 32 + lane;
+        if (r >= KS * 16) break;
+        const float f = v[k][u] * by;
+        const uint16_t high = Half16<T>::bits(f);
+        const int reg = (r >> 3) & 1;  // of the step r / 16, in the lane of r's pair
+        uint16_t* p = reinterpret_cast<uint16_t*>(&sm.frag[r >> 4][i >> 3][(i & 7) * 4 + ((r & 7) >> 1)]);
+        p[reg * 2 + (r & 1)] = high;
+        if constexpr (LO) {
+          const float hv = Half16<T>::value(high);
+          p[4 + reg * 2 + (r & 1)] = Half16<T>::bits(fabsf(hv) < INFINITY ? f - hv : 0.0f);
+        }
       }
     }
+  };
+  if (cols * 8 <= W) {
+    rows(std::integral_constant<int, 1>{}, warp);
+  } else {
+#pragma unroll 1
+    for (int first = warp; first < cols * 8; first += 4 * W) rows(std::integral_constant<int, 4>{}, first);
   }
 }
 
@@ -718,7 +739,7 @@ constexpr int kADUpCols = 2;                                                    
 constexpr int up_entry(int ks, int es, int c) { return ks * 1024 + c * (es == 4 ? 1024 : 640); }
 constexpr int kADUpStatic = 2900;  // (what else a CTA holds beside d)
 constexpr int up_ring_bytes(int ks, int es) { return 227 * 1024 - ks * kADCols * 32 * 4 * es - kADUpStatic; }
-constexpr int up_warps(int ks) { return ks <= 4 ? 16 : 8; }
+constexpr int up_warps(int ks) { return ks <= 2 ? 16 : 8; }
 constexpr int up_warp_bytes(int ks, int es) { return up_ring_bytes(ks, es) / up_warps(ks) / 512 * 512; }
 constexpr int up_depth(int ks, int es, int c) {
   const int n = up_warp_bytes(ks, es) / up_entry(ks, es, c);
@@ -972,7 +993,7 @@ __global__ void __launch_bounds__(32 * up_warps(KS), 1) adapter_up_kernel(const 
       part.start();
       if (!waited) pdl_wait();
       waited = true;
-      up_operand<T, KS, sizeof(Y) == 4>(a, ts, sm, rank);
+      up_operand<T, KS, sizeof(Y) == 4, up_warps(KS)>(a, ts, sm, rank);
       __syncthreads();
       part.run(n_first);
     };
