@@ -9,7 +9,7 @@
 // To kADOwnPlan rows every CTA works out the tiles from the indices by itself.  Both products run on mma.sync
 // m16n8k16 with 16 rows of the weights as the A operand and 8 rows of the batch as the B operand: a tile of one row
 // costs the same weight reads as one of eight, and the weights' bytes bound calls of few rows (64 rows of 48 adapters
-// of ranks to 32, f16, x 128256: the second product reads 411 MB from DRAM in 77 us, 0.8 of the copy rate; the ranks in
+// of ranks to 32, f16, x 128256: the second product reads 411 MB from DRAM in 78 us, 0.8 of the copy rate; the ranks in
 // use are half of it, but DRAM hands out 64 bytes at a time, a whole row of rank 32).  Above, a kernel before the
 // two sorts the rows by adapter; the batch's rows are the A operand, 16 a warp, and a CTA shares the weights: rows'
 // bytes bound these calls (packed prompts, 16384 rows of rank 64, 1024 -> 4096: 83 us for 304 MB, 0.54 of the copy rate).
