@@ -12,15 +12,15 @@
 // of ranks to 32, f16, x 128256: the second product reads 411 MB from DRAM in 78 us, 0.8 of the copy rate; the ranks in
 // use are half of it, but DRAM hands out 64 bytes at a time, a whole row of rank 32).  Above, a kernel before the
 // two sorts the rows by adapter; the batch's rows are the A operand, 16 a warp, and a CTA shares the weights: rows'
-// bytes bound these calls (packed prompts, 16384 rows of rank 64, 1024 -> 4096: 83 us for 304 MB, 0.54 of the copy rate).
+// bytes bound these calls (packed prompts, 16384 rows of rank 64, 1024 -> 4096: 90 us for 304 MB, 0.50 of the copy rate).
 //
 // The order of the entries along the inner dimension is free as long as A and B agree, so in the first product a lane
 // takes 16 contiguous bytes of a weight row and of x.
 //
-// d enters the second product in 16 bits: for fp32 outputs as two parts, high and low (16 bits of its value for
-// bf16, 22 for f16), so that its rounding stays near that of the fp32 sums; for 16-bit outputs as one, which rounds
-// the added part as its own type would be rounded.  (The second part doubles the MMAs and the operand's reads from
-// shared memory.)
+// d enters the second product as two 16-bit parts, high and low (16 bits of its value for bf16, 22 for f16), so that
+// its rounding stays near that of the fp32 sums.  For 16-bit outputs too, whose y may take nearly all of the added part
+// away.  (The second part doubles the MMAs and the operand's reads from shared memory: packed prompts as above take
+// 84 us with one part and 90 so, 64 rows of 48 adapters 78 and 79.)
 #pragma once
 
 #include <type_traits>
@@ -625,22 +625,10 @@ struct Outputs {
   }
 };
 
-// d in MMA order, a lane's registers of a step: the 16-bit values (b0, b1), and with LO behind them what their
-// rounding left (b0, b1).
-template <bool LO>
-struct Operand;
-template <>
-struct Operand<true> {
-  using Regs = uint4;
-};
-template <>
-struct Operand<false> {
-  using Regs = uint2;
-};
-
-template <int KS, bool LO>
+template <int KS>
 struct UpSmem {
-  typename Operand<LO>::Regs frag[KS][kADCols][32];
+  // d in MMA order, a lane's registers of a step: the 16-bit values (b0, b1) and what their rounding left (b0, b1)
+  uint4 frag[KS][kADCols][32];
   float unscale[kADTile];  // f16: the power of two that a row's d was divided by
   int64_t y[kADTile], out[kADTile];  // the rows' first bytes
 };
@@ -648,8 +636,8 @@ struct UpSmem {
 // All threads: a tile's d, scaled, into sm.  A warp takes every W-th row, four at a time, all of whose loads of a share
 // of H are out before the first is used (128 rows of rank 64, 4096 -> 4096: 27 us with a row at a time, 17 so, which
 // takes 8 warps in place of 16 for rank 64).
-template <typename T, int KS, bool LO, int W>
-__device__ void up_operand(const AdapterArgs& a, const TileSmem& ts, UpSmem<KS, LO>& sm, int rank) {
+template <typename T, int KS, int W>
+__device__ void up_operand(const AdapterArgs& a, const TileSmem& ts, UpSmem<KS>& sm, int rank) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int count = ts.count, cols = (count + 7) / 8;
   const float scale = ts.adapter < 0 ? 0.0f : a.scales ? __ldcg(a.scales + ts.adapter) : 1.0f;
@@ -701,10 +689,8 @@ __device__ void up_operand(const AdapterArgs& a, const TileSmem& ts, UpSmem<KS, 
         const int reg = (r >> 3) & 1;  // of the step r / 16, in the lane of r's pair
         uint16_t* p = reinterpret_cast<uint16_t*>(&sm.frag[r >> 4][i >> 3][(i & 7) * 4 + ((r & 7) >> 1)]);
         p[reg * 2 + (r & 1)] = high;
-        if constexpr (LO) {
-          const float hv = Half16<T>::value(high);
-          p[4 + reg * 2 + (r & 1)] = Half16<T>::bits(fabsf(hv) < INFINITY ? f - hv : 0.0f);
-        }
+        const float hv = Half16<T>::value(high);
+        p[4 + reg * 2 + (r & 1)] = Half16<T>::bits(fabsf(hv) < INFINITY ? f - hv : 0.0f);
       }
     }
   };
@@ -738,11 +724,11 @@ struct UpPlaces {
 constexpr int kADUpCols = 2;                                                         // C of tiles of more than 8 rows
 constexpr int up_entry(int ks, int es, int c) { return ks * 1024 + c * (es == 4 ? 1024 : 640); }
 constexpr int kADUpStatic = 2900;  // (what else a CTA holds beside d)
-constexpr int up_ring_bytes(int ks, int es) { return 227 * 1024 - ks * kADCols * 32 * 4 * es - kADUpStatic; }
+constexpr int up_ring_bytes(int ks) { return 227 * 1024 - ks * kADCols * 32 * 16 - kADUpStatic; }
 constexpr int up_warps(int ks) { return ks <= 2 ? 16 : 8; }
-constexpr int up_warp_bytes(int ks, int es) { return up_ring_bytes(ks, es) / up_warps(ks) / 512 * 512; }
+constexpr int up_warp_bytes(int ks) { return up_ring_bytes(ks) / up_warps(ks) / 512 * 512; }
 constexpr int up_depth(int ks, int es, int c) {
-  const int n = up_warp_bytes(ks, es) / up_entry(ks, es, c);
+  const int n = up_warp_bytes(ks) / up_entry(ks, es, c);
   return n < 8 ? n : 8;
 }
 
@@ -756,7 +742,6 @@ __device__ __forceinline__ int up_start(int64_t steps) { return static_cast<int>
 // start(): the copies that fill the ring; run(): the rest, once d stands in sm.
 template <typename T, typename Y, int KS, bool VEC, int C>
 struct UpShare {
-  static constexpr bool LO = sizeof(Y) == 4;
   static constexpr int ES = static_cast<int>(sizeof(Y)), J = 2, STEP = kADStep;
   using O = Outputs<Y, VEC>;
   using P = UpPlaces<VEC, KS>;
@@ -765,7 +750,7 @@ struct UpShare {
   static constexpr int W_BYTES = J * KS * 512, ROW_BYTES = O::ROWS4;
   static_assert(D >= 2, "a ring of two entries at least");
   const AdapterArgs& a;
-  const UpSmem<KS, LO>& sm;
+  const UpSmem<KS>& sm;
   int rank, count, n_end, t, parts;  // parts: entries a step
   unsigned char* ring_y;       // the lane's place for y in the first entry
   uint32_t ring;               // the first entry
@@ -780,7 +765,7 @@ struct UpShare {
   int in_n0, in_part, in_at;   // the step's first output, the entry's number in it, its offset in the ring
   int lane_n;                  // the lane's first output, from the step's
 
-  __device__ __forceinline__ UpShare(const AdapterArgs& args, const UpSmem<KS, LO>& s, const T* up,
+  __device__ __forceinline__ UpShare(const AdapterArgs& args, const UpSmem<KS>& s, const T* up,
                                      unsigned char* warp_ring, int rank_, int count_, int n_first, int n_end_)
       : a(args), sm(s), rank(rank_), count(count_), n_end(n_end_) {
     const int lane = threadIdx.x & 31;
@@ -872,22 +857,20 @@ struct UpShare {
   }
   // acc[c][j] = the step's outputs 16 j .. times column tile c of the entry's part of d.
   __device__ __forceinline__ void multiply(const uint32_t (&w)[KS][J][4], int part,
-                                           const typename Operand<LO>::Regs (&kept)[KS], float (&acc)[C][J][4]) const {
+                                           const uint4 (&kept)[KS], float (&acc)[C][J][4]) const {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       if (ks * 16 >= rank) break;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const auto b = C == 1 ? kept[ks] : sm.frag[ks][part * C + c][threadIdx.x & 31];
+        const uint4 b = C == 1 ? kept[ks] : sm.frag[ks][part * C + c][threadIdx.x & 31];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           if (ks == 0) mma16_first<T>(acc[c][j], w[ks][j], b.x, b.y);
           else mma16<T>(acc[c][j], w[ks][j], b.x, b.y);
         }
-        if constexpr (LO) {
 #pragma unroll
-          for (int j = 0; j < J; ++j) mma16<T>(acc[c][j], w[ks][j], b.z, b.w);
-        }
+        for (int j = 0; j < J; ++j) mma16<T>(acc[c][j], w[ks][j], b.z, b.w);
       }
     }
   }
@@ -909,7 +892,7 @@ struct UpShare {
   __device__ __forceinline__ void run(int n0) {
     const int lane = threadIdx.x & 31;
     int at = 0, part = 0;
-    typename Operand<LO>::Regs kept[KS];
+    uint4 kept[KS];
     if constexpr (C == 1) {
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) kept[ks] = sm.frag[ks][0][lane];
@@ -957,7 +940,7 @@ struct UpShare {
 template <typename T, typename Y, int KS, bool VEC>
 __global__ void __launch_bounds__(32 * up_warps(KS), 1) adapter_up_kernel(const AdapterArgs a) {
   extern __shared__ __align__(128) unsigned char up_ring[];
-  __shared__ UpSmem<KS, sizeof(Y) == 4> sm;
+  __shared__ UpSmem<KS> sm;
   __shared__ TileSmem ts;
   constexpr int STEP = kADStep;
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -987,13 +970,13 @@ __global__ void __launch_bounds__(32 * up_warps(KS), 1) adapter_up_kernel(const 
     }
     __syncthreads();
     const T* up = reinterpret_cast<const T*>(a.up) + static_cast<int64_t>(max(ts.adapter, 0)) * a.up_adapter;
-    unsigned char* ring = up_ring + warp * up_warp_bytes(KS, sizeof(Y));
+    unsigned char* ring = up_ring + warp * up_warp_bytes(KS);
     const int n_first = (s0 + warp) * STEP, n_end = min(a.N, s1 * STEP);
     auto share = [&](auto&& part) {
       part.start();
       if (!waited) pdl_wait();
       waited = true;
-      up_operand<T, KS, sizeof(Y) == 4, up_warps(KS)>(a, ts, sm, rank);
+      up_operand<T, KS, up_warps(KS)>(a, ts, sm, rank);
       __syncthreads();
       part.run(n_first);
     };
@@ -1110,7 +1093,7 @@ template <typename T, typename Y, int KS, int PIECE>
 __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_kernel(const AdapterArgs a) {
   extern __shared__ __align__(128) unsigned char wide_ring[];
   __shared__ TileSmem ts;
-  constexpr bool LO = sizeof(Y) == 4, VEC = PIECE != 0;
+  constexpr bool VEC = PIECE != 0;
   constexpr int ES = static_cast<int>(sizeof(Y)), CH = 2 * KS, S = kADWideStages;
   constexpr int STAGE = kADWideStage, STAGE_BYTES = wide_stage_bytes(KS), MOST = STAGE / 64;  // MOST: blocks a warp
   constexpr int ROWS = kADWideThreads / CH;  // weight rows that the CTA copies at a time
@@ -1197,7 +1180,7 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_ke
 
     // ---- the lane's part of d: rows row0 and row0 + 8, entries 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of every 16 ----
     const float scale = ts.adapter < 0 ? 0.0f : a.scales ? __ldcg(a.scales + ts.adapter) : 1.0f;
-    uint32_t hi[KS][4], lo[LO ? KS : 1][4];
+    uint32_t hi[KS][4], lo[KS][4];
     float back[2] = {1.0f, 1.0f};
     {
       // (every load of a share of H is out before the first is used; what is not there is read from the row's start;
@@ -1253,10 +1236,8 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_ke
         for (int q = 0; q < 4; ++q) {  // registers (row, k), (row + 8, k), (row, k + 8), (row + 8, k + 8)
           const float x0 = v[q & 1][ks][(q >> 1) * 2], x1 = v[q & 1][ks][(q >> 1) * 2 + 1];
           hi[ks][q] = Half16<T>::pack(x0, x1);
-          if constexpr (LO) {
-            const float2 b = Half16<T>::pair(hi[ks][q]);
-            lo[ks][q] = Half16<T>::pack(fabsf(b.x) < INFINITY ? x0 - b.x : 0.0f, fabsf(b.y) < INFINITY ? x1 - b.y : 0.0f);
-          }
+          const float2 b = Half16<T>::pair(hi[ks][q]);
+          lo[ks][q] = Half16<T>::pack(fabsf(b.x) < INFINITY ? x0 - b.x : 0.0f, fabsf(b.y) < INFINITY ? x1 - b.y : 0.0f);
         }
     }
     // a rank that ends inside a step's 16 entries: the words of its two pieces that count
@@ -1296,7 +1277,7 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_ke
         auto multiply = [&](int j, int ks, uint32_t b0, uint32_t b1) {
           if (ALL && ks == 0) mma16_first<T>(acc[j], hi[0], b0, b1);
           else mma16<T>(acc[j], hi[ks], b0, b1);
-          if constexpr (LO) mma16<T>(acc[j], lo[ks], b0, b1);
+          mma16<T>(acc[j], lo[ks], b0, b1);
         };
         if constexpr (KS == 1) {
           if (ALL || rank > 0) {
@@ -1387,7 +1368,7 @@ cudaError_t down_setup() {
 template <typename T, typename Y, int KS, bool VEC>
 cudaError_t up_setup() {
   return cudaFuncSetAttribute(adapter_up_kernel<T, Y, KS, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              up_warps(KS) * up_warp_bytes(KS, sizeof(Y)));
+                              up_warps(KS) * up_warp_bytes(KS));
 }
 
 template <typename T, typename Y, int KS, int PIECE>
@@ -1464,7 +1445,7 @@ cudaError_t launch_up_ks(const AdapterArgs& a, int64_t max_tiles, int num_sms, c
   const int64_t most = num_sms;  // one wave
   const int64_t few = (max_steps + up_warps(KS) - 1) / up_warps(KS);
   return launch_kernel(adapter_up_kernel<T, Y, KS, VEC>, dim3(static_cast<unsigned>(few < most ? few : most)),
-                       dim3(32 * up_warps(KS)), static_cast<size_t>(up_warps(KS) * up_warp_bytes(KS, sizeof(Y))), stream, true, a);
+                       dim3(32 * up_warps(KS)), static_cast<size_t>(up_warps(KS) * up_warp_bytes(KS)), stream, true, a);
 }
 
 template <typename T, typename Y, bool VEC>
