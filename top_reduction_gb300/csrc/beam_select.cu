@@ -19,6 +19,8 @@
 //     graph, all latency: its code runs once, and most of the time is its first reading.  So it is
 //     kept short: what is used more than once is called, not inlined (with everything inlined it
 //     took 2.6 us more).
+#include <type_traits>
+
 #include "device_common.cuh"
 #include "lmh_internal.h"
 #include "logits_vec.cuh"
@@ -116,16 +118,17 @@ __device__ __forceinline__ uint4 keep_elements(uint4 w, uint32_t keep) {
   return w;
 }
 
-// The sum of exp(x - m) over a vector, in two lanes: 2^(x L - ML) with ML = m L rounded; the caller makes up for
-// that rounding, which all terms share (it would shift the row's lse).
-template <typename T>
-__device__ __forceinline__ void add_exps(const uint4& w, float2 L2, float2 nml2, float2 (&acc)[2]) {
+// The sum of exp(x - m) over a vector, in two lanes: 2^(x L + by) with by = -(m L rounded); the caller makes up for
+// that rounding, which all terms share (it would shift the row's lse).  FAR: 2^((x + by) L) with by = -m, one operation
+// more a pair, for an m whose m L is rounded by more than can be made up for.
+template <typename T, bool FAR>
+__device__ __forceinline__ void add_exps(const uint4& w, float2 L2, float2 by, float2 (&acc)[2]) {
   constexpr int EPV = Vec16<T>::N;
   float2 p[EPV / 2];
   Vec16<T>::pairs(w, p);
 #pragma unroll
   for (int q = 0; q < EPV / 2; ++q) {
-    const float2 y = __ffma2_rn(p[q], L2, nml2);
+    const float2 y = FAR ? __fmul2_rn(__fadd2_rn(p[q], by), L2) : __ffma2_rn(p[q], L2, by);
     acc[q & 1] = __fadd2_rn(acc[q & 1], make_float2(ex2_approx(y.x), ex2_approx(y.y)));
   }
 }
@@ -278,19 +281,28 @@ __global__ void __launch_bounds__(kBSThreads, kBSCtasPerSm) beam_stream_kernel(c
     if (tid % TPB == 0 && b < a.nblk) st_keep(a.bmax + static_cast<int64_t>(d.row) * a.nblk + b, bm, keep_policy);
     float ts = 0.0f;  // sum of exp(x - vm) over this thread's logits
     if (vm > -INFINITY) {
-      const float ml = vm * L;
-      const float2 L2 = make_float2(L, L), nml2 = make_float2(-ml, -ml);
-      float2 acc0[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-      float2 acc1[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      const float ml = vm * L, shift = fmaf(vm, L, -ml);  // what the rounding of ml left
+      auto sum_of = [&](auto far_const, float by) {
+        constexpr bool FAR = decltype(far_const)::value;
+        const float2 L2 = make_float2(L, L), by2 = make_float2(by, by);
+        float2 acc0[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        float2 acc1[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        add_exps<T>(w[j], L2, nml2, acc0);
-        add_exps<T>(w[j + 1], L2, nml2, acc1);
+        for (int j = 0; j < 8; j += 2) {
+          add_exps<T, FAR>(w[j], L2, by2, acc0);
+          add_exps<T, FAR>(w[j + 1], L2, by2, acc1);
+        }
+        if (d.skip) add_exps<T, FAR>(w8, L2, by2, acc0);
+        const float2 r = __fadd2_rn(__fadd2_rn(acc0[0], acc0[1]), __fadd2_rn(acc1[0], acc1[1]));
+        return r.x + r.y;
+      };
+      // 2^-shift as 1 - shift ln 2, off by 2^-26 at the limit (|vm| to 5678 is always within it; 1e9 has a shift of 18)
+      if (fabsf(shift) <= 2.44140625e-4f) {
+        ts = sum_of(std::false_type{}, -ml);
+        ts = fmaf(ts, shift * -0.6931471805599453f, ts);
+      } else {
+        ts = sum_of(std::true_type{}, -vm);
       }
-      if (d.skip) add_exps<T>(w8, L2, nml2, acc0);
-      const float2 r = __fadd2_rn(__fadd2_rn(acc0[0], acc0[1]), __fadd2_rn(acc1[0], acc1[1]));
-      ts = r.x + r.y;
-      ts = fmaf(ts, fmaf(vm, L, -ml) * -0.6931471805599453f, ts);  // * 2^-(vm L - ml)
       if (!(ts < INFINITY)) {  // +inf or NaN among the logits: one by one
         ts = 0.0f;
 #pragma unroll
