@@ -69,3 +69,51 @@ def test_large_values_beside_infinities_and_nan(lmh, dtype):
     z[4] = -1e9
     z[4, 100:200] = INF
     _check(lmh.beam_select(z, s, 4, k=8), _candidates(z, s, 4), 4, 8)
+
+
+@pytest.mark.parametrize("far", [-1e4, -1e9, -1e30])
+@pytest.mark.parametrize("dtype,V", [(F32, 5003), (BF16, 30000), (F32, 151936), (BF16, 248320)])
+def test_a_search_that_begins(lmh, V, dtype, far):
+    """The first step of a search: rows alike, all beams but a group's first far below."""
+    z = _logits(2, V, dtype, 5)[0].repeat_interleave(4, 0).contiguous()
+    s = torch.full((8,), far, device="cuda")
+    s[0] = s[4] = 0.0
+    _check(lmh.beam_select(z, s, 4, k=8), _candidates(z, s, 4), 4, 8)
+    keep = lmh.beam_select(z, s, 4, keep_slots=True)
+    _check(keep, _candidates(z, s, 4), 4, 4, keep=True)
+
+
+def _choice_ms(lmh, z, s):
+    """The choice kernel's shortest time of ten calls."""
+    from top_reduction_gb300 import lmh as L
+    best = INF
+    L.trace_enable(True)
+    try:
+        for _ in range(10):
+            L.trace_reset()
+            lmh.beam_select(z, s, 4, k=8)
+            best = min(best, L.trace_read("beam_choose")[1])
+    finally:
+        L.trace_enable(False)
+        L.trace_reset()
+    return best
+
+
+@pytest.mark.parametrize("dtype,V", [(F32, 151936), (BF16, 248320)])
+def test_a_search_that_begins_takes_a_usual_steps_time(lmh, V, dtype):
+    """Beams far below do not widen what the choice looks through: nine blocks of ten are sorted out as in any step.
+    (Looked through one by one a group's logits take hundreds of times as long.)"""
+    z, s = _logits(4, V, dtype, 6)
+    usual = _choice_ms(lmh, z, s)
+    s[1:] = -1e9
+    assert _choice_ms(lmh, z, s) <= 3 * usual
+
+
+def test_scores_above_0(lmh):
+    """A leader far above the others, alone or with fewer tokens than are asked for."""
+    for k in (2, 8):
+        z, s = _logits(8, 3001, F32, 7)
+        s[1], s[6] = 5e4, 300.0
+        z[1, 3:] = -INF
+        z[6, 1:] = -INF
+        _check(lmh.beam_select(z, s, 4, k=k), _candidates(z, s, 4), 4, k)

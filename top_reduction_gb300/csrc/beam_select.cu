@@ -366,7 +366,7 @@ struct ChoiceSmem {
   uint32_t count, spans, blocks, real;
   alignas(16) uint32_t top[NT / 32 * 64];
   uint32_t bound;
-  float off_max;
+  float off_max;  // the largest off of a row that goes on, if above 0
   uint32_t kept_spans[kBGKept];
   uint32_t kept_blocks[kBGKept];
 };
@@ -623,8 +623,9 @@ __global__ void __launch_bounds__(kBGThreads) beam_choose_kernel(const BeamArgs 
       sm.z[i] = 0.0f;
       sm.beam[i] = static_cast<uint8_t>(tid);
       sm.at[i] = static_cast<uint32_t>(tid) * static_cast<uint32_t>(a.V);
+    } else {
+      atomicMax(reinterpret_cast<int*>(&sm.off_max), __float_as_int(fmaxf(sm.offf[tid], 0.0f)));
     }
-    atomicMax(reinterpret_cast<int*>(&sm.off_max), __float_as_int(fabsf(sm.offf[tid])));
   }
   auto score32 = [&](int b, float z) -> float {
     const uint8_t st = sm.state[b];
@@ -639,8 +640,12 @@ __global__ void __launch_bounds__(kBGThreads) beam_choose_kernel(const BeamArgs 
   const int64_t span0 = static_cast<int64_t>(row0) * P;
   // Twice the same: items 0 .. n - 1, first the group's spans, then the blocks of the kept spans (item i: block i % SB
   // of kept span i / SB), of which those that reach a bound that k of them reach are listed.  A thread holds its first
-  // values between its two looks.  The k-th best score is at least the bound but for fp32's rounding of it and of the
-  // sums compared with it (2^-24 of each term): 2^-21 covers both.
+  // values between its two looks.  The k-th best score is at least the bound t but for fp32's rounding of it and of the
+  // sums compared with it.  A sum (z - M) + off is off by 2^-24 of its terms and of itself; z - M is not above 0, so that
+  // is 2^-23 |score| for off <= 0, and 2^-23 (|score| + off) above.  Scores next to t have no other size than t, or
+  // than the largest off above 0: 2^-21 (|t| + that off) is twice what both need.  (A beam far below, as those that
+  // are not the first have when a search begins, widens nothing.  With its |off| in the margin, 4 beams of 151936 fp32
+  // logits overflowed the lists: 1490 us for this kernel, 14 so.)
   float t = -INFINITY;
   bool fits = true;
   int n_blocks = 0;
