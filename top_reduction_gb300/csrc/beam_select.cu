@@ -187,10 +187,11 @@ __global__ void __launch_bounds__(kBSThreads, kBSCtasPerSm) beam_stream_kernel(c
       return true;
     };
     // The first S chunks go out before the grid-dependency wait (they read logits only; see lmh.h), the others
-    // behind it, without the rows of ended beams.
+    // behind it.  With ended beams all go out behind it, where the flags may be read: an ended beam's logits are not.
     uint32_t issued = 0;
     bool ended = false;
-    for (; issued < static_cast<uint32_t>(S) && !ended; ++issued) ended = !issue(static_cast<int>(issued));
+    const uint32_t ahead = a.finished ? 0u : static_cast<uint32_t>(S);
+    for (; issued < ahead && !ended; ++issued) ended = !issue(static_cast<int>(issued));
     pdl_wait();
     for (; !ended; ++issued) {
       const int s = static_cast<int>(issued % S);
