@@ -902,13 +902,81 @@ class RowStates:
             if self.rows not in (None, rows):
                 raise ValueError("the states have %d and %d rows" % (self.rows, rows))
             self.rows = rows
-        written = [t.data_ptr() for t in outs if t.numel()]
-        apart = [t.data_ptr() for t, u in zip(tensors, outs) if t.numel() and (
-            t.data_ptr() != u.data_ptr() or t.stride() != u.stride())]
-        if len(set(written)) < len(written) or set(written) & set(apart):
-            raise ValueError("the same memory is written twice, or written and read by two states")
+        _check_apart(tensors, outs)
         self.tensors, self.outs, self.device, self._n = tensors, outs, dev, n
         self._ranges = [_range(t) for t in outs if t.numel()]
+
+
+def _layout(t):
+    """A tensor's bytes as ([(count, stride)], width): runs of `width` bytes at sums of multiples of the strides (none
+    of them 0), the largest first."""
+    es = t.element_size()
+    dims = sorted(((s * es, n) for n, s in zip(t.shape, t.stride()) if n > 1 and s), reverse=True)
+    width = es
+    while dims and dims[-1][0] == width:
+        width *= dims.pop()[1]
+    return [(n, s) for s, n in dims], width
+
+
+def _extent(dims, width):
+    return width + sum((n - 1) * s for n, s in dims)
+
+
+def _meet(a, b, shift, steps):
+    """Whether two layouts, the second `shift` bytes behind the first, have a byte in common.  steps: [how many looks are
+    left]; without one they count as meeting."""
+    steps[0] -= 1
+    if steps[0] < 0:
+        return True
+    if not -_extent(*b) < shift < _extent(*a):
+        return False
+    (da, wa), (db, wb) = a, b
+    if not da and not db:
+        return True
+    S = max(d[0][1] for d in (da, db) if d)
+    na, da = (da[0][0], da[1:]) if da and da[0][1] == S else (1, da)
+    nb, db = (db[0][0], db[1:]) if db and db[0][1] == S else (1, db)
+    a, b = (da, wa), (db, wb)
+    # the second's place along S less the first's: those for which the rest can meet
+    least, most = max(1 - na, -((_extent(*b) + shift - 1) // S)), min(nb - 1, (_extent(*a) - shift - 1) // S)
+    return any(_meet(a, b, shift + d * S, steps) for d in range(least, most + 1))
+
+
+_MEET_STEPS = 4096  # (nested strides take a few dozen)
+
+
+def _meets_itself(t):
+    """Whether two of a tensor's elements share memory."""
+    if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        return True
+    dims, width = _layout(t)
+    steps = [_MEET_STEPS]
+    for i, (n, S) in enumerate(dims):
+        rest = dims[i + 1:], width
+        if any(_meet(rest, rest, d * S, steps) for d in range(1, min(n - 1, (_extent(*rest) - 1) // S) + 1)):
+            return True
+    return False
+
+
+def _check_apart(tensors, outs):
+    """What is written is written once, and read by no state but one in place."""
+    spans = []
+    for t, u in zip(tensors, outs):
+        if not u.numel():
+            continue
+        if _meets_itself(u):
+            raise ValueError("a state's rows must not share memory")
+        spans.append((*_range(u), u, True))
+        if t.data_ptr() != u.data_ptr() or t.stride() != u.stride():
+            spans.append((*_range(t), t, False))
+    spans.sort(key=lambda s: s[0])
+    live = []
+    for lo, hi, t, written in spans:
+        live = [s for s in live if s[1] > lo]
+        for first, _, u, too in live:
+            if (written or too) and _meet(_layout(u), _layout(t), lo - first, [_MEET_STEPS]):
+                raise ValueError("the same memory is written twice, or written and read by two states")
+        live.append((lo, hi, t, written))
 
 
 def _range(t):
