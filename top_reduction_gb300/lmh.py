@@ -902,9 +902,8 @@ class RowStates:
             if self.rows not in (None, rows):
                 raise ValueError("the states have %d and %d rows" % (self.rows, rows))
             self.rows = rows
-        _check_apart(tensors, outs)
+        self._ranges = _check_apart(tensors, outs)
         self.tensors, self.outs, self.device, self._n = tensors, outs, dev, n
-        self._ranges = [_range(t) for t in outs if t.numel()]
 
 
 def _layout(t):
@@ -947,6 +946,8 @@ _MEET_STEPS = 4096  # (nested strides take a few dozen)
 
 def _meets_itself(t):
     """Whether two of a tensor's elements share memory."""
+    if t.is_contiguous():
+        return False
     if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
         return True
     dims, width = _layout(t)
@@ -959,28 +960,41 @@ def _meets_itself(t):
 
 
 def _check_apart(tensors, outs):
-    """What is written is written once, and read by no state but one in place."""
-    spans = []
+    """What is written is written once, and read by no state but one in place.  Returns the outputs' ranges."""
+    spans, ranges = [], []
     for t, u in zip(tensors, outs):
         if not u.numel():
             continue
         if _meets_itself(u):
             raise ValueError("a state's rows must not share memory")
-        spans.append((*_range(u), u, True))
-        if t.data_ptr() != u.data_ptr() or t.stride() != u.stride():
+        lo, hi = _range(u)
+        ranges.append((lo, hi))
+        spans.append((lo, hi, u, True))
+        if t is not u and (t.data_ptr() != lo or t.stride() != u.stride()):
             spans.append((*_range(t), t, False))
     spans.sort(key=lambda s: s[0])
-    live = []
-    for lo, hi, t, written in spans:
-        live = [s for s in live if s[1] > lo]
+    live, most = [], 0  # the spans so far that go on; where the last of them ends
+    layouts = {}
+
+    def layout(t):
+        if id(t) not in layouts:
+            layouts[id(t)] = _layout(t)
+        return layouts[id(t)]
+    for span in spans:
+        lo, hi, t, written = span
+        live = [s for s in live if s[1] > lo] if lo < most else []
         for first, _, u, too in live:
-            if (written or too) and _meet(_layout(u), _layout(t), lo - first, [_MEET_STEPS]):
+            if (written or too) and _meet(layout(u), layout(t), lo - first, [_MEET_STEPS]):
                 raise ValueError("the same memory is written twice, or written and read by two states")
-        live.append((lo, hi, t, written))
+        live.append(span)
+        most = max(most, hi)
+    return ranges
 
 
 def _range(t):
     """The first byte of a tensor's memory, and the one behind its last."""
+    if t.is_contiguous():
+        return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
     last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
     return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
 
