@@ -24,3 +24,19 @@ def test_parts_that_cancel(lmh, rows, H, N, R, L, dtype):
     off = off + (want.abs() + off) * (2.0 ** -24 + torch.finfo(dtype).eps / 2) + (2.0 ** -25 if dtype == F16 else 0)
     bad = ~((got.double() - want).abs() <= off)
     assert not bad.any(), (int(bad.sum()), float((got.double() - want).abs().max()), float(off.max()))
+
+
+@pytest.mark.parametrize("dtype,y_dtype", [(BF16, BF16), (BF16, F32), (F16, F16), (F16, F32)])
+@pytest.mark.parametrize("N", [40, 44, 33])
+@pytest.mark.parametrize("rows", [5, 20, 300])
+def test_rows_that_nothing_is_added_to(lmh, rows, N, dtype, y_dtype):
+    """A row without an adapter, or with one of rank 0, is y to the sign of its zeros."""
+    c = _case(rows, 64, N, 16, 3, dtype, y_dtype, seed=N)
+    c["ranks"] = torch.tensor([0, 16, 5], dtype=torch.int32, device="cuda")
+    c["idx"][0], c["idx"][1], c["idx"][2] = -1, 0, 1
+    c["y"][:, ::3] = -0.0
+    c["y"][:, 1::3] = 0.0
+    got = _run(lmh, c)
+    same = c["idx"] <= 0
+    bits = torch.int32 if y_dtype == F32 else torch.int16
+    assert torch.equal(got[same].view(bits), c["y"][same].view(bits))

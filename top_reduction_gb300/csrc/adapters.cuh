@@ -906,13 +906,13 @@ struct UpShare {
       if (C == 1 || part == 0) read_weights(ring + at, w);
       float acc[C][J][4];
       multiply(w, part, kept, acc);
-      if (rank == 0) {
+      if (rank == 0) {  // nothing is added: -0, which leaves a y of -0 too
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
           for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[c][j][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) acc[c][j][e] = -0.0f;
       }
       const bool full = n0 + STEP <= n_end;
 #pragma unroll
@@ -1268,11 +1268,11 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_ke
         const int block = first_block + b, n = st * STAGE + block * 32;
         const uint32_t bs = stage + block * (1024 * KS);
         float acc[4][4];
-        if constexpr (!ALL) {
+        if constexpr (!ALL) {  // (-0: where the rank is 0, y is left as it is, a -0 too)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) acc[j][e] = -0.0f;
         }
         auto multiply = [&](int j, int ks, uint32_t b0, uint32_t b1) {
           if (ALL && ks == 0) mma16_first<T>(acc[j], hi[0], b0, b1);
