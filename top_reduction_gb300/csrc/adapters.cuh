@@ -41,7 +41,7 @@ constexpr int kADWarps = kADThreads / 32;
 constexpr int kADStep = 32;       // outputs of the second product that a warp takes at a time
 constexpr int kADOwnPlan = 256;   // rows to which every CTA finds its tiles by itself
 
-struct AdapterTile {
+struct alignas(16) AdapterTile {
   int adapter;  // -1: rows without one
   int first;    // in `order`
   int count;
@@ -239,7 +239,8 @@ struct TileFinder {
   __device__ void take(const AdapterArgs& a, TileSmem& sm, int t) {
     __syncthreads();  // nobody reads the tile before
     if (a.rows > kADOwnPlan) {
-      const AdapterTile tile = a.tiles[t];
+      const int4 tile4 = __ldcg(reinterpret_cast<const int4*>(a.tiles + t));  // (through L2 as well)
+      const AdapterTile tile{tile4.x, tile4.y, tile4.z, tile4.w};
       if (threadIdx.x == 0) sm.adapter = tile.adapter, sm.count = tile.count;
       if (threadIdx.x < static_cast<unsigned>(tile.count)) sm.rows[threadIdx.x] = __ldcg(a.order + tile.first + threadIdx.x);
       __syncthreads();
