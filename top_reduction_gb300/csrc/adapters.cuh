@@ -179,13 +179,33 @@ __device__ __forceinline__ void lane_copies_wait() { asm volatile("cp.async.wait
 // ---------------------------------------------------------------------------
 // tiles
 // ---------------------------------------------------------------------------
-// The tiles of a call as a CTA of at least kADOwnPlan threads sees them.  With at most kADOwnPlan rows thread i
-// takes row i: its place among the rows of the same adapter gives its tile and its place in it, and a tile's
-// number is its first row's among the rows that are first in a tile.  Otherwise the plan kernel's results.
+// The tiles of a call as a CTA sees them.
 struct TileSmem {
-  alignas(16) int32_t adapter_of[kADOwnPlan];
   int32_t rows[kADTile];  // of the current tile
-  int32_t adapter, part, count;
+  int32_t adapter, count;
+};
+
+// Calls of many rows: the plan kernel's results.
+struct PlannedTiles {
+  // Returns the number of tiles.
+  __device__ __forceinline__ int start(const AdapterArgs& a, TileSmem&) { return __ldcg(a.tile_count); }
+  // All threads: tile `t`'s rows, adapter and count into sm (behind a barrier of its own).
+  __device__ __forceinline__ void take(const AdapterArgs& a, TileSmem& sm, int t) {
+    __syncthreads();  // nobody reads the tile before
+    const int4 tile4 = __ldcg(reinterpret_cast<const int4*>(a.tiles + t));
+    const AdapterTile tile{tile4.x, tile4.y, tile4.z, tile4.w};
+    if (threadIdx.x == 0) sm.adapter = tile.adapter, sm.count = tile.count;
+    if (threadIdx.x < static_cast<unsigned>(tile.count)) sm.rows[threadIdx.x] = __ldcg(a.order + tile.first + threadIdx.x);
+    __syncthreads();
+  }
+};
+
+// To kADOwnPlan rows: found by each CTA, of at least as many threads.  Thread i takes row i: its place among the rows
+// of the same adapter gives its tile and its place in it, and a tile's number is its first row's among the rows that
+// are first in a tile.
+struct OwnTileSmem : TileSmem {
+  alignas(16) int32_t adapter_of[kADOwnPlan];
+  int32_t part;
 };
 
 struct TileFinder {
@@ -195,8 +215,7 @@ struct TileFinder {
 
   // All threads; the indices may be read.  (Through L2: this grid may start before the kernel that writes them ends,
   // and an L1 line could be of before.)  Returns the number of tiles.
-  __device__ int start(const AdapterArgs& a, TileSmem& sm) {
-    if (a.rows > kADOwnPlan) return __ldcg(a.tile_count);
+  __device__ int start(const AdapterArgs& a, OwnTileSmem& sm) {
     const int i = threadIdx.x;
     if (i < a.rows) {
       mine = __ldcg(a.adapter_idx + i);
@@ -236,16 +255,8 @@ struct TileFinder {
   }
 
   // All threads: tile `t`'s rows, adapter and count into sm (behind a barrier of its own).
-  __device__ void take(const AdapterArgs& a, TileSmem& sm, int t) {
+  __device__ void take(const AdapterArgs& a, OwnTileSmem& sm, int t) {
     __syncthreads();  // nobody reads the tile before
-    if (a.rows > kADOwnPlan) {
-      const int4 tile4 = __ldcg(reinterpret_cast<const int4*>(a.tiles + t));  // (through L2 as well)
-      const AdapterTile tile{tile4.x, tile4.y, tile4.z, tile4.w};
-      if (threadIdx.x == 0) sm.adapter = tile.adapter, sm.count = tile.count;
-      if (threadIdx.x < static_cast<unsigned>(tile.count)) sm.rows[threadIdx.x] = __ldcg(a.order + tile.first + threadIdx.x);
-      __syncthreads();
-      return;
-    }
     if (number == t) sm.adapter = mine, sm.part = place / kADTile, sm.count = 0;
     __syncthreads();
     if (mine == sm.adapter && place / kADTile == sm.part) {  // (a thread without a row has mine = -2)
@@ -342,7 +353,7 @@ __device__ __forceinline__ void down_share(const AdapterArgs& a, const T* down, 
 template <typename T, int RT>
 __global__ void __launch_bounds__(kADThreads) adapter_down_kernel(const AdapterArgs a) {
   extern __shared__ __align__(16) unsigned char down_smem[];  // the warps' rings, then their sums [warp][rows][RT * 16]
-  __shared__ TileSmem ts;
+  __shared__ OwnTileSmem ts;
   __shared__ int32_t tok[kADTile];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   pdl_wait();
@@ -432,7 +443,7 @@ __global__ void __launch_bounds__(kADThreads, RT <= 4 ? 2 : 1) adapter_down_wide
   const int rgroup = warp & 3, half = warp >> 2;  // half: blocks 2 half, 2 half + 1 of a stage
   pdl_wait();
   pdl_launch_dependents();
-  TileFinder finder;
+  PlannedTiles finder;
   const int n_tiles = finder.start(a, ts);
   // this CTA's share of H (few tiles: several shares), in stages
   const int all = (a.H + kADDownStage - 1) / kADDownStage;
@@ -942,7 +953,7 @@ template <typename T, typename Y, int KS, bool VEC>
 __global__ void __launch_bounds__(32 * up_warps(KS), 1) adapter_up_kernel(const AdapterArgs a) {
   extern __shared__ __align__(128) unsigned char up_ring[];
   __shared__ UpSmem<KS> sm;
-  __shared__ TileSmem ts;
+  __shared__ OwnTileSmem ts;
   constexpr int STEP = kADStep;
   const int tid = threadIdx.x, warp = tid >> 5;
   // the kernel before this one is the first product, which has itself waited for all before it: only d has to
@@ -1104,7 +1115,7 @@ __global__ void __launch_bounds__(kADWideThreads, wide_ctas(KS)) adapter_wide_ke
   __shared__ int64_t offs[VEC ? 1 : 4][2][VEC ? 1 : 16];  // [16 rows of the tile][y, out]: the rows' first bytes
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   // (as in the kernel above: all but d was complete before this kernel started)
-  TileFinder finder;
+  PlannedTiles finder;
   const int n_tiles = finder.start(a, ts);
   const int64_t stages = (a.N + STAGE - 1) / STAGE;
   const int64_t all = stages * n_tiles;
