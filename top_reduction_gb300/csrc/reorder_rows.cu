@@ -278,6 +278,8 @@ __global__ void __launch_bounds__(32) reorder_bulk_kernel(const __grid_constant_
       // ---- the stage: its last stores have read it, then its loads ----
       const int sg = static_cast<int>(issued % S);
       bulk_stores_read<S - 2>();  // (a group of stores a stage: this one's were S - 1 stages ago)
+      // a run's last bytes were written and read there by threads, before copies write to the same place
+      if (a.ragged) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       ReorderStage& e = st[sg];
       if (lane == 0) e.dst = dst + h * sub, e.dst_row = s.dst_row, e.slice = sub;
