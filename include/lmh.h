@@ -645,10 +645,11 @@ size_t lmh_adapters_workspace_bytes(int32_t rows, const lmh_adapters* table);
  * lmh_project_q4 or lmh_project_logprobs), so out is the projection with the
  * requests' adapters.  Sums are held in fp32.  d enters the second product as the sum of
  * two numbers of dtype: within 2^-16 of its value for LMH_BF16 and 2^-22 for LMH_F16 (f16
- * parts of a row's d below 2^-28 of its largest: within 2^-38 of the largest).  Rounded once, to out_dtype.  A row of x with an infinity
- * or NaN gives infinities and NaN.  The rows may come in any order, each with any adapter;
- * an adapter's weights are read about once per 64 rows that use it, and not at all if none
- * does.
+ * parts of a row's d below 2^-28 of its largest: within 2^-38 of the largest).  Rounded
+ * once, to out_dtype.  A row of x with an infinity or NaN gives infinities and NaN, and so
+ * does a row of up in the output that it makes.  The rows may come in any order, each with
+ * any adapter; an adapter's weights are read about once per 64 rows that use it, and not at
+ * all if none does.
  *
  *   x                 device [num_tokens x H] of the table's dtype, row stride
  *                     x_row_stride (>= H), aligned to its elements.

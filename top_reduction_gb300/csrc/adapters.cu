@@ -8,7 +8,7 @@ namespace lmh {
 // ---------------------------------------------------------------------------
 // One CTA.  Counts per adapter (slot `count` holds the rows without one), a scan, the rows' places.  Lanes
 // with the same adapter take their places with one atomic.  The order of an adapter's rows is whatever the
-// atomics make it: no row's result depends on it.  16384 rows take 13 us, of one SM's latency and issue (0.66 of its
+// atomics make it: no row's result depends on it.  16384 rows take 13 us alone, of one SM's latency and issue (0.66 of its
 // slots); indices loaded one look ahead in place of 16 at once: 17 us.
 __global__ void __launch_bounds__(kADPlanThreads) adapter_plan_kernel(const AdapterArgs a) {
   extern __shared__ int32_t plan_smem[];

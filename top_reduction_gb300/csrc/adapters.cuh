@@ -9,7 +9,7 @@
 // To kADOwnPlan rows every CTA works out the tiles from the indices by itself.  Both products run on mma.sync
 // m16n8k16 with 16 rows of the weights as the A operand and 8 rows of the batch as the B operand: a tile of one row
 // costs the same weight reads as one of eight, and the weights' bytes bound calls of few rows (64 rows of 48 adapters
-// of ranks to 32, f16, x 128256: the second product reads 411 MB from DRAM in 78 us, 0.8 of the copy rate; the ranks in
+// of ranks to 32, f16, x 128256: the second product reads 411 MB from DRAM in 77 us, 0.82 of the copy rate; the ranks in
 // use are half of it, but DRAM hands out 64 bytes at a time, a whole row of rank 32).  Above, a kernel before the
 // two sorts the rows by adapter; the batch's rows are the A operand, 16 a warp, and a CTA shares the weights: rows'
 // bytes bound these calls (packed prompts, 16384 rows of rank 64, 1024 -> 4096: 90 us for 304 MB, 0.50 of the copy rate).
@@ -39,7 +39,11 @@ constexpr int kADPlanThreads = 1024;
 constexpr int kADThreads = 256;   // first product
 constexpr int kADWarps = kADThreads / 32;
 constexpr int kADStep = 32;       // outputs of the second product that a warp takes at a time
-constexpr int kADOwnPlan = 256;   // rows to which every CTA finds its tiles by itself
+// Rows to which every CTA finds its tiles by itself, a thread a row.  The kernels of many rows took longer below (bf16 in
+// a graph, H 4096, ranks 16 / 64 with 8 adapters): 64 rows x 4096 7.1 / 10.1 us here and 14.7 / 28.1 there, 256 rows
+// 14.0 / 18.9 and 14.6 / 27.7, 256 x 151936 fp32 71.5 and 76.9; 256 rows of H 1024 x 28672 18.7 and 16.0, the one size
+// of 28 that lost.  A packed batch of more rows has no such kernel here: its indices go beyond a CTA's threads.
+constexpr int kADOwnPlan = 256;
 
 struct alignas(16) AdapterTile {
   int adapter;  // -1: rows without one
@@ -423,7 +427,7 @@ __global__ void __launch_bounds__(kADThreads) adapter_down_kernel(const AdapterA
 // The batch's rows are the MMA's A operand, 16 a warp, and 8 adapter rows the B operand: the tile's four row groups
 // share the weights, which come in stages of 128 entries of H that the whole CTA copies; two warps share a row group
 // by entries of H.  As above a lane takes 16 contiguous bytes of a row for two steps of 16, so the operands need no
-// transposition: a lane's registers of x are its own loads, a stage ahead.  (16384 rows of 1024 x rank 64: 22 us alone,
+// transposition: a lane's registers of x are its own loads, a stage ahead.  (16384 rows of 1024 x rank 64: 21 us alone,
 // 31 MB from DRAM; a wave of 261 tiles that each wait for their own eight stages.  x two stages ahead, 2 or 5 stages
 // of weights: the same or slower.)
 constexpr int kADDownStage = 128;  // entries of H: four blocks of 32
@@ -732,7 +736,8 @@ struct UpPlaces {
 };
 
 // A warp's ring: entries of the weights of a step and of y for C tiles of 8 rows.  A CTA has an SM for itself, with as
-// many warps as its registers allow without spilling, each with a ring of at least two of the larger entries.
+// many warps as its registers allow (8 to 12 bytes spilled for ranks above 64, none below), each with a ring of at least
+// two of the larger entries.
 constexpr int kADUpCols = 2;                                                         // C of tiles of more than 8 rows
 constexpr int up_entry(int ks, int es, int c) { return ks * 1024 + c * (es == 4 ? 1024 : 640); }
 constexpr int kADUpStatic = 2900;  // (what else a CTA holds beside d)
@@ -745,7 +750,7 @@ constexpr int up_depth(int ks, int es, int c) {
 }
 
 // A tile's start (its rows, the first copies, d) takes a CTA about as long as this many steps: 33 rows of 8 adapters x
-// 151936 take 20.5 us in a graph with equal shares, 19.0 so.  Not more than a part of a tile, as shares of small calls
+// 151936 take 20.5 us in a graph with equal shares, 19.3 so.  Not more than a part of a tile, as shares of small calls
 // would be all start (5 rows x 4096: 4.5 us, 4.8 with 64 steps).
 __device__ __forceinline__ int up_start(int64_t steps) { return static_cast<int>(min(static_cast<int64_t>(96), steps / 32)); }
 
@@ -1005,16 +1010,19 @@ __global__ void __launch_bounds__(32 * up_warps(KS), 1) adapter_up_kernel(const 
 // Here the batch's rows are the MMA's A operand (16 a warp, held in registers for a whole tile) and 8 rows of the
 // weights the B operand.  A lane's part of d and its two rows of y and out stay the same from step to step, which
 // leaves about a fifth of the instructions of the kernel above per output (packed prompts, 16384 rows of rank 64 x
-// 4096: 108 us there, 60 here).  268 MB of rows make a floor of 40 us; issue slots are 35% busy and DRAM 60%: what is
-// left is latency, of a tile's start and of the stages' barriers, with 16 warps an SM.
+// 4096, with one part of d: 108 us there, 60 here; with both 66 here).  268 MB of rows make a floor of 40 us; issue
+// slots are 35% busy, the tensor pipe 44% and DRAM 54%: what is left is latency, of a tile's start and of the stages'
+// barriers, with 16 warps an SM.  For ranks of 33 to 64 some of the kernel's registers spill (up to 68 bytes; none
+// for aligned bf16 outputs).
 // The weights come in stages of kADWideStage outputs that the whole CTA copies and reads; warps share a stage by rows
 // (one for every 16 of the tile's) and by outputs.  A block is 32 outputs; column c of its tile j stands for output
 // 8 (c / 2) + 2 j + c % 2, so that a lane has eight neighbours of a row.
 constexpr int kADWideThreads = 256;
 constexpr int kADWideWarps = kADWideThreads / 32;
 constexpr int kADWideStages = 3;
-// Outputs of a stage: of 64-row tiles a warp takes two blocks.  (Four, and a ring twice as large: 75 us for packed
-// prompts' second product where this takes 60, and 109 for 1257 fp32 rows of rank 64 x 23728 where this takes 98.
+// Outputs of a stage: of 64-row tiles a warp takes two blocks.  (Four, and a ring twice as large, with one part of d for
+// 16-bit outputs: 75 us for packed prompts' second product where this took 60, and 109 for 1257 fp32 rows of rank 64 x
+// 23728 where this took 98.
 // What is in flight queues then: even the copies' issue waited 1500 cycles a stage.)
 constexpr int kADWideStage = 128;
 constexpr int wide_stage_bytes(int ks) { return kADWideStage * 32 * ks; }

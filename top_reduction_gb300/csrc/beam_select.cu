@@ -11,8 +11,9 @@
 //   * beam_stream_kernel reads every logit once (persistent CTAs, bulk copies into a ring, a
 //     thread 128 bytes): the largest allowed logit of every block of 64 and of every span of
 //     32 threads, and the span's (max, sum of exponentials) go to the workspace.  Bound by the
-//     logits' bytes: 256 x 248320 bf16 (127 MB) take 26 us, 0.72 of the copy rate; fp32 with a
-//     mask, 64 x 128256 (34 MB), 13 us, as long as four chunks a CTA take to start and drain.
+//     logits' bytes: 256 x 248320 bf16 (127 MB) take 27 us, 0.70 of the copy rate; fp32 with a
+//     mask, 64 x 128256 of which 52 rows have not ended (28 MB), 12.7 us, as long as its few
+//     chunks a CTA take to start and drain.
 //   * beam_choose_kernel, one CTA a group: the rows' lse from the spans' pairs; a bound t that at
 //     least k spans reach, the blocks of the spans that reach it, a tighter bound from those, the
 //     logits of the blocks that reach that, and their exact order.  7 us behind the stream in a

@@ -9,7 +9,8 @@
 //     copies into a ring of stages and from there to the rows that take them; no byte passes a register.  Bound
 //     by the bytes moved: caches of four layers (420 MB read, 420 written) take 153 us, 0.81 of the copy rate.
 //   * reorder_rows_kernel, for the others and for calls that move little: plain loads and stores.  A step's
-//     histories and block tables (256 rows, 4.9 MB read and written): 4.5 us in a graph, latency.  (With it alone the caches take 308 us.)
+//     histories and block tables (256 rows, 4.9 MB read and written): 4.5 us in a graph, latency.
+//     The caches take 273 us where their rows align to 8 bytes, 346 to 4, 501 to 2.
 #include "device_common.cuh"
 #include "lmh_internal.h"
 
@@ -19,7 +20,10 @@ constexpr int kRRThreads = 256;
 constexpr int kRRStates = 24;       // states of one launch
 constexpr int kRRSmem = 64 * 1024;  // staging
 constexpr int kRRSliceMax = 8192;   // bytes of a row a CTA takes at a time, at most
-constexpr int64_t kRBLeast = 16ll << 20;  // bytes of the states from which on bulk copies are taken
+// Bytes of the aligned states from which on bulk copies are taken.  Caches of 8 groups of 4 rows in place, half of whose
+// rows move, plain / bulk in a graph: 2 MB 3.4 / 3.7 us, 8 MB 4.3 / 4.2, 17 MB 7.0 / 5.0, 34 MB 10.1 / 7.6, 268 MB
+// 84 / 39; to other buffers 8 MB 4.6 / 4.6, 17 MB 8.1 / 6.1.
+constexpr int64_t kRBLeast = 16ll << 20;
 
 struct ReorderState {
   const char* src;
