@@ -22,12 +22,12 @@ def test_runs_of_ended_beams(lmh, groups, V, which, dtype):
 
 
 def _stream_ms(lmh, z, s, done):
-    """The stream kernel's shortest time of ten calls."""
+    """The stream kernel's shortest time of thirty calls."""
     from top_reduction_gb300 import lmh as L
     best = INF
     L.trace_enable(True)
     try:
-        for _ in range(10):
+        for _ in range(30):
             L.trace_reset()
             lmh.beam_select(z, s, 4, finished=done)
             best = min(best, L.trace_read("beam_stream")[1])
@@ -38,7 +38,8 @@ def _stream_ms(lmh, z, s, done):
 
 
 def test_ended_beams_cost_no_reads(lmh):
-    """50 MB of logits that one call reads and another, whose beams have all ended, does not."""
+    """50 MB of logits that one call reads and another, whose beams have all ended, does not: 0.51 to 0.60 of the time,
+    all of it the launch's; 0.83 where every CTA reads its first three chunks whatever the flags."""
     z, s = _logits(96, 128256, torch.float32, 1)
     none = torch.zeros(96, dtype=torch.uint8, device="cuda")
-    assert _stream_ms(lmh, z, s, none + 1) <= 0.6 * _stream_ms(lmh, z, s, none)
+    assert _stream_ms(lmh, z, s, none + 1) <= 0.72 * _stream_ms(lmh, z, s, none)
